@@ -400,6 +400,145 @@ uw_status uw_mlp_autotune(const uw_mlp_matrix *m, int32_t n_layers, const uint16
 uw_status uw_mlp_autotune_workspace_size(const uw_mlp_matrix *m, int32_t n_layers, int64_t batch,
                                          size_t *bytes);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a decoder layer: what stands between the compressed matmuls of
+ * a model that is being served.  The Unweight blog has no counterpart: it
+ * compresses the projections of such a layer and leaves the rest as it is.
+ * With the weights smaller, a decode step's next large read is the cache of
+ * keys and values, which is held here in 4 bits and pages.
+ * ------------------------------------------------------------------------ */
+
+/* uw_rmsnorm -- residual addition and root-mean-square norm of n rows of d:
+ *     h = bf16(x + residual)      (h = x without a residual)
+ *     y = bf16(h / sqrt(mean(h^2) + eps) * weight)
+ * The mean, the root and the products are in fp32; y is rounded to BF16 once.
+ * (Squares or products past fp32's range, |h| above 1.8e19, give 0 or NaN.)
+ *   x_dev         BF16 rows, x_stride elements apart (x_stride >= d).
+ *   residual_dev  BF16 rows to add, or NULL (then residual_out_dev is NULL too).
+ *   residual_out_dev  h (written), or NULL if it is not wanted; may be
+ *                 residual_dev or x_dev itself (in place), with that stride.
+ *   weight_dev    d BF16 values.
+ *   y_dev         BF16 rows (written), y_stride apart; may be x_dev.
+ * Any d > 0 (UW_ERR_SHAPE otherwise) up to 2^31 - 1 (UW_ERR_UNSUPPORTED); BF16
+ * pointers need 2-byte alignment, and rows of a multiple of 8 values on
+ * 16-byte boundaries run on 16-byte loads.  n = 0 does nothing. */
+uw_status uw_rmsnorm(const uint16_t *x_dev, int64_t x_stride, const uint16_t *residual_dev,
+                     int64_t residual_stride, uint16_t *residual_out_dev, int64_t residual_out_stride,
+                     const uint16_t *weight_dev, int64_t n, int64_t d, float eps, uint16_t *y_dev,
+                     int64_t y_stride, void *stream);
+
+/* uw_rmsnorm_e4m3 -- the same with y in 8 bits and a scale for each row, for
+ * 8-bit products of the caller's:
+ *     scale = max(max |y| / 448, 2^-126), q = e4m3(y / scale), y in fp32.
+ * A row that holds a value that is not finite (or products h * weight beyond
+ * fp32) comes out as NaN throughout, its scale too.
+ *   q_dev      e4m3 rows (written), q_stride bytes apart.
+ *   scale_dev  n fp32 scales (written), 4-byte aligned. */
+uw_status uw_rmsnorm_e4m3(const uint16_t *x_dev, int64_t x_stride, const uint16_t *residual_dev,
+                          int64_t residual_stride, uint16_t *residual_out_dev, int64_t residual_out_stride,
+                          const uint16_t *weight_dev, int64_t n, int64_t d, float eps, uint8_t *q_dev,
+                          int64_t q_stride, float *scale_dev, void *stream);
+
+/* The cache of keys and values of one layer, 4 bits a value, in pages.
+ *
+ * A page holds page_size tokens of every kv head.  The block of one (page,
+ * kv head), page_size * (head_dim + 8) bytes, is
+ *     K codes  page_size rows of head_dim / 2 bytes
+ *     V codes  the same
+ *     K params page_size pairs (scale, lo) of BF16
+ *     V params the same
+ * and the blocks of a page follow each other head by head, the pages page by
+ * page.  Code byte b of a row holds dimension 2b in its low and 2b + 1 in its
+ * high four bits.  A code c stands for lo + c * scale (fp32).
+ *
+ * Quantisation of one vector of head_dim BF16 values (one token, one kv head,
+ * K or V), lo and hi its smallest and largest value, in fp32:
+ *     scale = bf16((hi/2 - lo/2) / 7.5)
+ *     c     = min(max(round((x/2 - lo/2) / (scale/2)), 0), 15)   (0 if scale is 0)
+ * (round to nearest even; halved first so that no finite vector overflows).  A
+ * vector that holds a value that is not finite is stored as NaN throughout:
+ * scale = lo = NaN.
+ *
+ * Sequences: sequence s owns the tokens start[s] .. start[s + 1] - 1 of a call
+ * (its `new` tokens, possibly none) and len[s] tokens in the cache, the new
+ * ones last: new token i has position len[s] - new + i.  The token at position
+ * p lies in page table[s * table_stride + p / page_size], slot p % page_size.
+ * start, len and the table are device memory, so that a step can be captured
+ * in a CUDA graph; the kernels check what they read there: a page outside the
+ * pool, a length beyond table_width pages, a start outside the call's tokens
+ * or a negative position to append to touches nothing and is reported by
+ * uw_check_status as UW_ERR_CORRUPT.  Tokens of no sequence are left alone. */
+typedef struct {
+    void *pages_dev;          /* n_pages pages, 16-byte aligned                   */
+    const int32_t *table_dev; /* [n_seqs] rows of page numbers                    */
+    int64_t n_pages;
+    int64_t table_stride;     /* int32 elements from one sequence's row to the next */
+    int32_t table_width;      /* pages in a row                                   */
+    int32_t n_seqs;
+    int32_t kv_heads;
+    int32_t head_dim;         /* 64 or 128                                        */
+    int32_t page_size;        /* tokens: 16, 32, 64, 128 or 256                   */
+} uw_kv4_cache;
+
+/* BF16 [tokens, heads, head_dim] rows; strides in elements.  head_dim values
+ * are contiguous; dev and both strides are multiples of 16 bytes. */
+typedef struct {
+    uint16_t *dev;
+    int64_t token_stride, head_stride;
+} uw_kv4_rows;
+
+/* uw_kv4_page_bytes -- bytes of one page (all its kv heads). */
+uw_status uw_kv4_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_size, size_t *bytes);
+
+/* uw_kv4_workspace_size -- bytes of workspace of the calls below for q_heads
+ * query heads; cleared once by uw_workspace_init.  It does not grow with the
+ * sequences, their lengths or the tokens.  uw_kv4_append and uw_kv4_read use
+ * its first 256 bytes (the error word) only. */
+uw_status uw_kv4_workspace_size(const uw_kv4_cache *c, int32_t q_heads, size_t *bytes);
+
+/* uw_kv4_append -- rotate q and k by their positions and append k and v.
+ *     pairs (a, b) of a vector's first rot_dim values: (x[i], x[i + rot_dim/2])
+ *     or, with interleaved, (x[2i], x[2i+1]);
+ *     (a, b) -> bf16(a*cos[p][i] - b*sin[p][i]), bf16(b*cos[p][i] + a*sin[p][i])
+ * (fp32, each product and the sum rounded; position p as above); the other
+ * values are copied.
+ *   q         q_heads heads, read; q_out  the rotated q (written; may be q).
+ *             Both NULL with q_heads = 0: only k and v are taken.
+ *   k, v      kv_heads heads each, read.
+ *   cos_dev, sin_dev  fp32 [rope_len, rot_dim/2], or NULL with rot_dim = 0 (no
+ *             rotation).  A position at or past rope_len touches nothing and is
+ *             reported like a bad page.  rot_dim: a multiple of 16, at most
+ *             head_dim (UW_ERR_UNSUPPORTED otherwise). */
+uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start_dev, const int32_t *len_dev, int64_t n_tokens,
+                        const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *q_out, const uw_kv4_rows *k,
+                        const uw_kv4_rows *v, const float *cos_dev, const float *sin_dev, int64_t rope_len,
+                        int32_t rot_dim, int32_t interleaved, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* uw_kv4_read -- the new tokens' entries as the cache holds them: k and v
+ * [n_tokens, kv_heads, head_dim] (written) = bf16(lo + c * scale).  With
+ * start = the running sums of len it reads whole sequences. */
+uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start_dev, const int32_t *len_dev, int64_t n_tokens,
+                      const uw_kv4_rows *k, const uw_kv4_rows *v, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* uw_kv4_attention -- o = softmax(scale * q K^T) V over the cache, for the new
+ * tokens of every sequence (appended before).  Query head h reads kv head
+ * h / (q_heads / kv_heads).  A token at position p sees the keys at
+ *     max(0, p - window + 1) .. p   (causal; without: .. len - 1)
+ * (window 0: from 0).  One that sees no key gets o = 0 and lse = -inf.  What
+ * lies in a page past a sequence's length is never looked at.
+ *   q, out    q_heads heads (a multiple of kv_heads, UW_ERR_SHAPE otherwise).
+ *   lse_dev   fp32 [n_tokens, q_heads]: log(sum exp(scale q.k)) (written), or NULL.
+ *   max_new, max_len  upper bounds of the sequences' new tokens and lengths as
+ *             the host knows them (0: not known).  They only choose how the work
+ *             is split: a wrong one costs time, never the result.
+ *   softmax_scale  0 for 1 / sqrt(head_dim).
+ *   ws_dev    at least uw_kv4_workspace_size bytes.
+ * Softmax statistics and sums are fp32; the same call gives the same bits. */
+uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *start_dev, const int32_t *len_dev,
+                           int64_t n_tokens, const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *out,
+                           float *lse_dev, int64_t max_new, int64_t max_len, float softmax_scale, int32_t causal,
+                           int32_t window, void *ws_dev, size_t ws_bytes, void *stream);
+
 /* uw_check_status -- synchronise `stream`, read and clear the error word the
  * kernels record in the workspace.  Returns UW_OK, UW_ERR_CORRUPT or
  * UW_ERR_TIMEOUT (or UW_ERR_CUDA if the stream itself failed). */

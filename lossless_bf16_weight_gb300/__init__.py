@@ -17,6 +17,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libuw.so")
 
 UW_OK = 0
+UW_ERR_INVALID_ARG = 1
+UW_ERR_SHAPE = 2
 UW_ERR_BUFFER_TOO_SMALL = 3
 STATUS_NAMES = {0: "UW_OK", 1: "UW_ERR_INVALID_ARG", 2: "UW_ERR_SHAPE", 3: "UW_ERR_BUFFER_TOO_SMALL",
                 4: "UW_ERR_CORRUPT", 5: "UW_ERR_CUDA", 6: "UW_ERR_TIMEOUT", 7: "UW_ERR_UNSUPPORTED",
@@ -66,10 +68,23 @@ class Schedule(ctypes.Structure):
         return "Schedule(slots=%d, dec_ctas=%d)" % (self.slots, self.dec_ctas)
 
 
+class Kv4CacheDesc(ctypes.Structure):
+    """The 4-bit paged cache of keys and values of one layer (uw_kv4_cache)."""
+    _fields_ = [("pages_dev", ctypes.c_void_p), ("table_dev", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class Kv4Rows(ctypes.Structure):
+    """BF16 rows [tokens, heads, head_dim] with their strides in elements (uw_kv4_rows)."""
+    _fields_ = [("dev", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 # (name, restype, argtypes) of every symbol in include/uw.h
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_F32, _CACHE, _ROWS = ctypes.c_float, ctypes.POINTER(Kv4CacheDesc), ctypes.POINTER(Kv4Rows)
 SIGNATURES = [
     ("uw_compress", ctypes.c_int, [_P, _I64, _I64, _P, ctypes.POINTER(_SZ)]),
     ("uw_blob_info", ctypes.c_int, [_P, _SZ, ctypes.POINTER(Desc)]),
@@ -99,6 +114,15 @@ SIGNATURES = [
                                        ctypes.POINTER(Schedule), _P, _SZ, _P, _P]),
     ("uw_mlp_autotune_workspace_size", ctypes.c_int, [ctypes.POINTER(MlpMatrix), _I32, _I64,
                                                       ctypes.POINTER(_SZ)]),
+    ("uw_rmsnorm", ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _F32, _P, _I64, _P]),
+    ("uw_rmsnorm_e4m3", ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _F32, _P, _I64, _P, _P]),
+    ("uw_kv4_page_bytes", ctypes.c_int, [_I32, _I32, _I32, ctypes.POINTER(_SZ)]),
+    ("uw_kv4_workspace_size", ctypes.c_int, [_CACHE, _I32, ctypes.POINTER(_SZ)]),
+    ("uw_kv4_append", ctypes.c_int, [_CACHE, _P, _P, _I64, _ROWS, _I32, _ROWS, _ROWS, _ROWS, _P, _P, _I64, _I32,
+                                     _I32, _P, _SZ, _P]),
+    ("uw_kv4_read", ctypes.c_int, [_CACHE, _P, _P, _I64, _ROWS, _ROWS, _P, _SZ, _P]),
+    ("uw_kv4_attention", ctypes.c_int, [_CACHE, _P, _P, _I64, _ROWS, _I32, _ROWS, _P, _I64, _I64, _F32, _I32, _I32,
+                                        _P, _SZ, _P]),
     ("uw_check_status", ctypes.c_int, [_P, _P]),
     ("uw_selftest_bounded_wait", ctypes.c_int, [_P, _SZ, ctypes.c_uint32, _P]),
     ("uw_variant_name", ctypes.c_char_p, [_I32, _I32]),
@@ -443,6 +467,135 @@ def mlp_autotune(mats, x, y, ws, passes: int = 2, stream=None, side_stream=None)
                                   ctypes.byref(sched), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream),
                                   _side(side_stream)), "uw_mlp_autotune")
     return list(plans), sched
+
+
+# ---------------------------------------------------------------- around the matmuls of a decoder layer
+def _row_stride(t, d: int, size: int, name: str, n: int, what: str) -> int:
+    """Row stride in elements of a [n, d] (or, for one row, [d]) tensor of
+    `size`-byte elements whose rows are contiguous."""
+    if t.element_size() != size or t.shape[-1] != d or t.numel() != n * d or t.dim() > 2:
+        raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s)" % (what, name, tuple(t.shape), t.dtype))
+    if d > 1 and t.stride(-1) != 1:
+        raise UwError(UW_ERR_INVALID_ARG, "%s (%s has rows that are not contiguous)" % (what, name))
+    return t.stride(0) if t.dim() == 2 and n > 1 else d
+
+
+def rmsnorm(x, weight, y, eps: float = 1e-5, residual=None, residual_out=None, scale=None, stream=None):
+    """uw_rmsnorm: h = bf16(x + residual) into residual_out (if given), y = h / rms(h) * weight in BF16.
+    With `scale` (fp32, one for each row): uw_rmsnorm_e4m3, y holds e4m3 bytes (torch.float8_e4m3fn or uint8).
+    Rows may be strided."""
+    what = "uw_rmsnorm" if scale is None else "uw_rmsnorm_e4m3"
+    d = x.shape[-1]
+    n = x.shape[0] if x.dim() == 2 else 1
+    xs = _row_stride(x, d, 2, "x", n, what)
+    ys = _row_stride(y, d, 2 if scale is None else 1, "y", n, what)
+    rs = 0 if residual is None else _row_stride(residual, d, 2, "residual", n, what)
+    hs = 0 if residual_out is None else _row_stride(residual_out, d, 2, "residual_out", n, what)
+    _refuse(_short((weight, 2 * d, "weight")), what)
+    rp = None if residual is None else residual.data_ptr()
+    hp = None if residual_out is None else residual_out.data_ptr()
+    if scale is None:
+        _check(load().uw_rmsnorm(x.data_ptr(), xs, rp, rs, hp, hs, weight.data_ptr(), n, d, eps, y.data_ptr(), ys,
+                                 _stream(stream)), what)
+    else:
+        _refuse(_short((scale, 4 * n, "scale")), what)
+        _check(load().uw_rmsnorm_e4m3(x.data_ptr(), xs, rp, rs, hp, hs, weight.data_ptr(), n, d, eps, y.data_ptr(),
+                                      ys, scale.data_ptr(), _stream(stream)), what)
+
+
+class Kv4Cache:
+    """A layer's cache: its descriptor with the tensors behind it (made by kv4_cache)."""
+
+    def __init__(self, desc, pages, table):
+        self.desc, self.pages, self.table, self.ref = desc, pages, table, ctypes.byref(desc)
+
+
+def kv4_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
+    n = _SZ(0)
+    _check(load().uw_kv4_page_bytes(kv_heads, head_dim, page_size, ctypes.byref(n)), "uw_kv4_page_bytes")
+    return int(n.value)
+
+
+def kv4_cache(pages, table, kv_heads: int, head_dim: int, page_size: int) -> Kv4Cache:
+    """The cache in `pages` (bytes of whole pages, contiguous) with the page table
+    `table` (int32 [sequences, pages of the longest])."""
+    size = kv4_page_bytes(kv_heads, head_dim, page_size)
+    if not pages.is_contiguous() or _nbytes(pages) % size:
+        raise UwError(UW_ERR_SHAPE, "uw_kv4_cache (pages are not whole pages of %d bytes)" % size)
+    if table.dim() != 2 or table.element_size() != 4 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise UwError(UW_ERR_SHAPE, "uw_kv4_cache (table is not int32 [sequences, pages])")
+    stride = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+    d = Kv4CacheDesc(pages.data_ptr(), table.data_ptr(), _nbytes(pages) // size, stride, table.shape[1],
+                     table.shape[0], kv_heads, head_dim, page_size)
+    return Kv4Cache(d, pages, table)
+
+
+def kv4_workspace_size(cache: Kv4Cache, q_heads: int) -> int:
+    n = _SZ(0)
+    _check(load().uw_kv4_workspace_size(cache.ref, q_heads, ctypes.byref(n)), "uw_kv4_workspace_size")
+    return int(n.value)
+
+
+def _kv4_rows(t, n: int, heads: int, dim: int, name: str, what: str) -> Kv4Rows:
+    if t.dim() != 3 or t.element_size() != 2 or tuple(t.shape) != (n, heads, dim):
+        raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s, not BF16 [%d, %d, %d])" % (what, name, tuple(t.shape),
+                                                                                  t.dtype, n, heads, dim))
+    ts, hs, ds = t.stride()
+    if ds != 1:
+        raise UwError(UW_ERR_INVALID_ARG, "%s (%s: a head's values are not contiguous)" % (what, name))
+    return Kv4Rows(t.data_ptr(), ts if n > 1 else 0, hs if heads > 1 else 0)
+
+
+def _kv4_seqs(cache, start, length, what):
+    n = cache.desc.n_seqs
+    _refuse(_short((start, 4 * (n + 1), "start"), (length, 4 * n, "length")), what)
+
+
+def kv4_append(cache: Kv4Cache, start, length, q, k, v, q_out, cos, sin, ws, interleaved: bool = False, stream=None):
+    """uw_kv4_append: rotate q (into q_out; both may be None) and k, and append k and v.  Tensors
+    [tokens, heads, head_dim], strided if need be; cos and sin fp32 [positions, rotated pairs], or None."""
+    what, d = "uw_kv4_append", cache.desc
+    n = k.shape[0]
+    _kv4_seqs(cache, start, length, what)
+    kr, vr = (_kv4_rows(t, n, d.kv_heads, d.head_dim, name, what) for t, name in ((k, "k"), (v, "v")))
+    heads = 0 if q is None else q.shape[1] if q.dim() == 3 else -1
+    qr = orow = None
+    if q is not None or q_out is not None:
+        qr, orow = (_kv4_rows(t, n, heads, d.head_dim, name, what) for t, name in ((q, "q"), (q_out, "q_out")))
+    rope_len = rot = 0
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.element_size() != 4 or sin.element_size() != 4:
+            raise UwError(UW_ERR_SHAPE, "%s (cos and sin are not fp32 [positions, pairs])" % what)
+        if not (cos.is_contiguous() and sin.is_contiguous()):
+            raise UwError(UW_ERR_INVALID_ARG, "%s (cos and sin are not contiguous)" % what)
+        rope_len, rot = cos.shape[0], 2 * cos.shape[1]
+    _check(load().uw_kv4_append(cache.ref, start.data_ptr(), length.data_ptr(), n, qr, heads, orow, kr, vr,
+                                cos.data_ptr() if rot else None, sin.data_ptr() if rot else None, rope_len, rot,
+                                interleaved, ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
+
+
+def kv4_read(cache: Kv4Cache, start, length, k, v, ws, stream=None):
+    """uw_kv4_read: the new tokens' entries as BF16 into k and v [tokens, kv heads, head_dim]."""
+    what, d = "uw_kv4_read", cache.desc
+    n = k.shape[0]
+    _kv4_seqs(cache, start, length, what)
+    kr, vr = (_kv4_rows(t, n, d.kv_heads, d.head_dim, name, what) for t, name in ((k, "k"), (v, "v")))
+    _check(load().uw_kv4_read(cache.ref, start.data_ptr(), length.data_ptr(), n, kr, vr, ws.data_ptr(), _nbytes(ws),
+                              _stream(stream)), what)
+
+
+def kv4_attention(cache: Kv4Cache, start, length, q, out, ws, max_new: int = 0, max_len: int = 0,
+                  scale: float = 0.0, causal: bool = True, window: int = 0, lse=None, stream=None):
+    """uw_kv4_attention: attention of the new tokens' q [tokens, q heads, head_dim] over the cache into out."""
+    what, d = "uw_kv4_attention", cache.desc
+    n, heads = q.shape[0], q.shape[1] if q.dim() == 3 else -1
+    _kv4_seqs(cache, start, length, what)
+    qr, orow = (_kv4_rows(t, n, heads, d.head_dim, name, what) for t, name in ((q, "q"), (out, "out")))
+    if lse is not None:
+        _refuse(_short((lse, 4 * n * heads, "lse")), what)
+    _check(load().uw_kv4_attention(cache.ref, start.data_ptr(), length.data_ptr(), n, qr, heads, orow,
+                                   None if lse is None else lse.data_ptr(), max_new, max_len, scale, causal, window,
+                                   ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
 
 
 def selftest_bounded_wait(ws, tries: int, stream=None) -> None:
