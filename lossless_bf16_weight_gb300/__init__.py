@@ -164,12 +164,23 @@ def _ptr(t) -> int:
 
 
 def _stream(stream):
+    """The address of the CUDA stream to pass; None: the current one of the current device."""
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """torch.cuda.current_stream().cuda_stream without building the Stream
+    object (2.9 us a call against 0.4 us, of 3 us for a launch)."""
+    global _current_stream
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    if raw is not None:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
 
 
 def _plan_ptr(plan):
@@ -475,6 +486,8 @@ def _row_stride(t, d: int, size: int, name: str, n: int, what: str) -> int:
     `size`-byte elements whose rows are contiguous."""
     if t.element_size() != size or t.shape[-1] != d or t.numel() != n * d or t.dim() > 2:
         raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s)" % (what, name, tuple(t.shape), t.dtype))
+    if t.is_contiguous():
+        return d
     if d > 1 and t.stride(-1) != 1:
         raise UwError(UW_ERR_INVALID_ARG, "%s (%s has rows that are not contiguous)" % (what, name))
     return t.stride(0) if t.dim() == 2 and n > 1 else d
@@ -508,6 +521,7 @@ class Kv4Cache:
 
     def __init__(self, desc, pages, table):
         self.desc, self.pages, self.table, self.ref = desc, pages, table, ctypes.byref(desc)
+        self.n_seqs, self.kv_heads, self.head_dim = desc.n_seqs, desc.kv_heads, desc.head_dim
 
 
 def kv4_page_bytes(kv_heads: int, head_dim: int, page_size: int) -> int:
@@ -537,7 +551,7 @@ def kv4_workspace_size(cache: Kv4Cache, q_heads: int) -> int:
 
 
 def _kv4_rows(t, n: int, heads: int, dim: int, name: str, what: str) -> Kv4Rows:
-    if t.dim() != 3 or t.element_size() != 2 or tuple(t.shape) != (n, heads, dim):
+    if t.shape != (n, heads, dim) or t.element_size() != 2:
         raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s, not BF16 [%d, %d, %d])" % (what, name, tuple(t.shape),
                                                                                   t.dtype, n, heads, dim))
     ts, hs, ds = t.stride()
@@ -547,14 +561,17 @@ def _kv4_rows(t, n: int, heads: int, dim: int, name: str, what: str) -> Kv4Rows:
 
 
 def _kv4_seqs(cache, start, length, what):
-    n = cache.desc.n_seqs
-    _refuse(_short((start, 4 * (n + 1), "start"), (length, 4 * n, "length")), what)
+    """start and length are int32 [sequences + 1] and [sequences] at least."""
+    n = cache.n_seqs
+    if not (start.is_contiguous() and length.is_contiguous() and start.element_size() == 4 == length.element_size()
+            and start.numel() > n and length.numel() >= n):
+        _refuse("start and length are not int32 of %d and %d values" % (n + 1, n), what)
 
 
 def kv4_append(cache: Kv4Cache, start, length, q, k, v, q_out, cos, sin, ws, interleaved: bool = False, stream=None):
     """uw_kv4_append: rotate q (into q_out; both may be None) and k, and append k and v.  Tensors
     [tokens, heads, head_dim], strided if need be; cos and sin fp32 [positions, rotated pairs], or None."""
-    what, d = "uw_kv4_append", cache.desc
+    what, d = "uw_kv4_append", cache
     n = k.shape[0]
     _kv4_seqs(cache, start, length, what)
     kr, vr = (_kv4_rows(t, n, d.kv_heads, d.head_dim, name, what) for t, name in ((k, "k"), (v, "v")))
@@ -576,7 +593,7 @@ def kv4_append(cache: Kv4Cache, start, length, q, k, v, q_out, cos, sin, ws, int
 
 def kv4_read(cache: Kv4Cache, start, length, k, v, ws, stream=None):
     """uw_kv4_read: the new tokens' entries as BF16 into k and v [tokens, kv heads, head_dim]."""
-    what, d = "uw_kv4_read", cache.desc
+    what, d = "uw_kv4_read", cache
     n = k.shape[0]
     _kv4_seqs(cache, start, length, what)
     kr, vr = (_kv4_rows(t, n, d.kv_heads, d.head_dim, name, what) for t, name in ((k, "k"), (v, "v")))
@@ -587,7 +604,7 @@ def kv4_read(cache: Kv4Cache, start, length, k, v, ws, stream=None):
 def kv4_attention(cache: Kv4Cache, start, length, q, out, ws, max_new: int = 0, max_len: int = 0,
                   scale: float = 0.0, causal: bool = True, window: int = 0, lse=None, stream=None):
     """uw_kv4_attention: attention of the new tokens' q [tokens, q heads, head_dim] over the cache into out."""
-    what, d = "uw_kv4_attention", cache.desc
+    what, d = "uw_kv4_attention", cache
     n, heads = q.shape[0], q.shape[1] if q.dim() == 3 else -1
     _kv4_seqs(cache, start, length, what)
     qr, orow = (_kv4_rows(t, n, heads, d.head_dim, name, what) for t, name in ((q, "q"), (out, "out")))

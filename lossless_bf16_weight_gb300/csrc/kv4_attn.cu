@@ -1,10 +1,9 @@
-// Attention over the 4-bit paged cache, one warp for each (token, query head):
-// the keys one after the other with the running maximum and sum of their
-// softmax.  A lane holds D / 32 dimensions.
+// Entry points of the 4-bit paged cache's attention, and the checks of what the
+// cache's calls are given.
 #include <cmath>
 
 #include "kernels.h"
-#include "kv4.cuh"
+#include "kv4_attn.cuh"
 #include "kv4_host.h"
 
 namespace uw {
@@ -49,75 +48,16 @@ bool kv4_rows(const uw_kv4_rows *r, Rows *out) {
 
 namespace {
 
-struct AttnParams {
-    Kv4View v;
-    Rows q, o;
-    float *lse;
-    float scale;
-    int32_t q_heads, group, causal, window;
+// Workspace: [error word | counters | parts].
+struct Layout {
+    size_t counters, parts, total;
 };
-
-template <int D>
-__global__ void __launch_bounds__(256) kv4_attn_kernel(const AttnParams p) {
-    constexpr int N = D / 32;  // dimensions a lane
-    grid_dep_launch();
-    grid_dep_wait();
-    const Kv4View &v = p.v;
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t t = unit / p.q_heads;
-    const int h = int(unit - t * p.q_heads);
-    if (t >= v.n_tokens)
-        return;
-    const int s = kv4_find_seq(v, int(t));
-    const Seq sq = kv4_seq(v, s);
-    if (t < sq.t0 || t >= int64_t(sq.t0) + sq.n)
-        return;
-    const int32_t pos = sq.len - sq.n + (int32_t(t) - sq.t0);
-    const int32_t hi = p.causal ? pos + 1 : sq.len;
-    const int32_t lo = p.window ? max(0, pos - p.window + 1) : 0;
-    const int hk = h / p.group;
-    float q[N], o[N], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        q[i] = p.scale * bf16_lo(p.q.p[t * p.q.ts + h * p.q.hs + N * lane + i]);
-        o[i] = 0.f;
-    }
-    for (int32_t j = lo; j < hi; j++) {
-        const uint8_t *blk = kv4_block<D>(v, s, j, hk);
-        if (!blk)
-            continue;
-        const int slot = j & ((1 << v.page_log2) - 1);
-        auto load = [&](int is_v, float (&x)[N]) {
-            const uint8_t *row = blk + kv4_codes<D>(v.page_log2, slot, is_v) + N / 2 * lane;
-            const uint32_t par = *reinterpret_cast<const uint32_t *>(blk + kv4_params<D>(v.page_log2, slot, is_v));
-#pragma unroll
-            for (int i = 0; i < N; i++)
-                x[i] = fmaf(float((row[i / 2] >> (4 * (i & 1))) & 15), bf16_lo(par), bf16_hi(par));
-        };
-        float x[N], d = 0.f;
-        load(0, x);
-#pragma unroll
-        for (int i = 0; i < N; i++)
-            d = fmaf(q[i], x[i], d);
-#pragma unroll
-        for (int b = 16; b; b >>= 1)
-            d += __shfl_xor_sync(0xffffffffu, d, b);
-        const float m2 = fmaxf(m, d), old = m2 == -INFINITY ? 1.f : expf(m - m2);
-        const float e = d == -INFINITY ? 0.f : expf(d - m2);
-        load(1, x);
-        l = l * old + e;
-#pragma unroll
-        for (int i = 0; i < N; i++)
-            o[i] = o[i] * old + e * x[i];
-        m = m2;
-    }
-#pragma unroll
-    for (int i = 0; i < N; i++)
-        p.o.p[t * p.o.ts + h * p.o.hs + N * lane + i] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.f ? 0.f : o[i] / l));
-    if (p.lse && lane == 0)
-        p.lse[t * p.q_heads + h] = l == 0.f ? -INFINITY : m + logf(l);
+Layout layout(int head_dim) {
+    Layout w;
+    w.counters = 256;
+    w.parts = align_up(w.counters + 4 * size_t(kv4_decode_ctas()), 256);
+    w.total = w.parts + 4 * kv4_decode_part_floats(head_dim);
+    return w;
 }
 
 }  // namespace
@@ -142,7 +82,9 @@ extern "C" uw_status uw_kv4_workspace_size(const uw_kv4_cache *c, int32_t q_head
         return UW_ERR_INVALID_ARG;
     if (q_heads <= 0 || c->kv_heads <= 0 || q_heads % c->kv_heads)
         return UW_ERR_SHAPE;
-    *bytes = 256;
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return UW_ERR_UNSUPPORTED;
+    *bytes = layout(c->head_dim).total;
     return UW_OK;
 }
 
@@ -164,19 +106,20 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
         return UW_ERR_UNSUPPORTED;
     if (none)
         return UW_OK;
+    const Layout w = layout(c->head_dim);
+    if (ws_bytes < w.total)
+        return UW_ERR_BUFFER_TOO_SMALL;
     p.lse = lse;
-    p.scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(float(c->head_dim));
+    p.c1 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(float(c->head_dim))) * 1.44269504089f;
     p.q_heads = q_heads;
     p.group = q_heads / c->kv_heads;
     p.causal = causal != 0;
     p.window = window;
-    const int64_t blocks = (n_tokens * q_heads + 7) / 8;
-    if (blocks > 0x7fffffff)
-        return UW_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return (c->head_dim == 128 ? launch_overlapped(kv4_attn_kernel<128>, grid, dim3(256), 0, st, p)
-                               : launch_overlapped(kv4_attn_kernel<64>, grid, dim3(256), 0, st, p)) == cudaSuccess
-               ? UW_OK
-               : UW_ERR_CUDA;
+    p.rows_min = 0;
+    p.rows_max = INT64_MAX;
+    p.counters = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + w.counters);
+    p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.parts);
+    const int64_t rows = max_new * p.group;
+    const int64_t units = max_len > 0 && max_new > 0 ? (max_len / 32 + 1) * ((rows + 15) / 16 + 1) * c->kv_heads * c->n_seqs : 0;
+    return launch_kv4_decode(p, c->head_dim, rows, units, static_cast<cudaStream_t>(stream));
 }

@@ -1,0 +1,158 @@
+// What the two attention kernels over the 4-bit paged cache share: their
+// parameters, the cut of the work into equal shares, and the joining of the
+// shares of one item.
+//
+// An item is one (sequence, kv head, row tile): the rows of the tile are the
+// new tokens' query heads that read this kv head, row r = token r / group,
+// head r % group.  Its units are the key tiles that its rows can see, in
+// order (one unit, with no key in it, for an item that sees none).  All items'
+// units in a row (sequence by sequence, head by head, tile by tile) are cut
+// into gridDim.x shares of equal length, so that any mix of lengths fills the
+// GPU.  Every CTA finds its share from the lengths on the device: nothing is
+// planned on the host and a captured launch replays with other lengths.
+//
+// An item that lies in several shares is joined by the CTA that finishes last:
+// each part leaves its unnormalised output, maximum and sum in the workspace,
+// and the parts are added in their order, so the same call gives the same
+// bits whichever CTA joins.  A CTA has at most two parts of such items (the
+// end of one that began before, the beginning of one that goes on): two slots.
+#pragma once
+#include "kv4.cuh"
+
+namespace uw {
+
+struct AttnParams {
+    Kv4View v;
+    Rows q, o;
+    float *lse;
+    float c1;                 // softmax scale * log2(e)
+    int32_t q_heads, group, causal, window;
+    int64_t rows_min, rows_max;  // sequences with rows (new * group) in this range are this launch's
+    float *parts;             // [2 * gridDim.x][RB * (D + 2)]: output, maximum, sum
+    uint32_t *counters;       // [gridDim.x], left at zero
+};
+
+// Keys [lo, hi) that some row of tokens [i0, i1] of a sequence sees.
+struct KeyRange {
+    int32_t lo, hi;
+};
+__device__ __forceinline__ KeyRange visible(const AttnParams &p, const Seq &s, int i0, int i1) {
+    const int32_t before = s.len - s.n;
+    const int32_t hi = p.causal ? before + i1 + 1 : s.len;
+    const int32_t lo = p.window ? before + i0 - p.window + 1 : 0;
+    return {max(lo, 0), max(hi, 0)};
+}
+
+// One item's place in the row of units.
+struct Item {
+    int s, head, rt;
+    Seq q;
+    KeyRange keys;
+    uint64_t u0;   // its first unit
+    uint32_t n;    // its units
+};
+
+template <int RB, int T>  // rows of a row tile, keys of a unit
+struct Sched {
+    static __device__ __forceinline__ bool mine(const AttnParams &p, const Seq &s) {
+        const int64_t rows = int64_t(s.n) * p.group;
+        return rows >= p.rows_min && rows <= p.rows_max && rows > 0;
+    }
+    static __device__ __forceinline__ int row_tiles(const AttnParams &p, const Seq &s) {
+        return int((int64_t(s.n) * p.group + RB - 1) / RB);
+    }
+    static __device__ __forceinline__ KeyRange tile_keys(const AttnParams &p, const Seq &s, int rt) {
+        const int64_t r0 = int64_t(rt) * RB;
+        const int64_t r1 = min(r0 + RB, int64_t(s.n) * p.group) - 1;
+        return visible(p, s, int(r0 / p.group), int(r1 / p.group));
+    }
+    static __device__ __forceinline__ uint32_t units(const KeyRange &k) {
+        return k.hi > k.lo ? uint32_t((k.hi - 1) / T - k.lo / T + 1) : 1u;
+    }
+    // Units of one head of a sequence.
+    static __device__ __forceinline__ uint64_t seq_units(const AttnParams &p, const Seq &s) {
+        if (!mine(p, s))
+            return 0;
+        uint64_t n = 0;
+        const int rts = row_tiles(p, s);
+        for (int rt = 0; rt < rts; rt++)
+            n += units(tile_keys(p, s, rt));
+        return n;
+    }
+};
+
+// Units before each thread's block of sequences, over the CTA (kThreads
+// threads, all of them call); `total` = all units.
+template <int kThreads>
+__device__ __forceinline__ uint64_t cta_prefix(uint64_t mine, uint64_t *slots, uint64_t *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t v = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o)
+            v += u;
+    }
+    if (lane == 31)
+        slots[warp] = v;
+    __syncthreads();
+    uint64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; w++) {
+        const uint64_t t = slots[w];
+        before += w < warp ? t : 0;
+        all += t;
+    }
+    __syncthreads();
+    *total = all;
+    return before + v - mine;
+}
+
+// The share (of `workers` equal ones) that holds unit u: the last c with
+// total * c / workers <= u.
+__device__ __forceinline__ uint32_t share_of(uint64_t u, uint64_t total, uint32_t workers) {
+    return uint32_t(((u + 1) * workers - 1) / total);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// A further part of a row's softmax (maximum m2, sum l2, unnormalised output
+// o2, in log2 units) added to (m, l, o).
+__device__ __forceinline__ void join(float &m, float &l, float4 &o, float m2, float l2, float4 o2) {
+    const float top = fmaxf(m, m2);
+    const float t0 = top == -INFINITY ? 0.f : top;
+    const float f = exp2_fast(m - t0), f2 = exp2_fast(m2 - t0);
+    m = top;
+    l = fmaf(f2, l2, f * l);
+    o.x = fmaf(f2, o2.x, f * o.x);
+    o.y = fmaf(f2, o2.y, f * o.y);
+    o.z = fmaf(f2, o2.z, f * o.z);
+    o.w = fmaf(f2, o2.w, f * o.w);
+}
+
+// Four dimensions (4c ..) of row r of an item: out = o / l, and with c = 0 the lse.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnParams &p, const Item &it, int64_t r, int64_t rows, int c, float4 o,
+                                          float m, float l) {
+    if (r >= rows)
+        return;
+    const int64_t tok = it.q.t0 + r / p.group, head = int64_t(it.head) * p.group + r % p.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: o is 0 and stays 0
+    *reinterpret_cast<uint2 *>(p.o.p + tok * p.o.ts + head * p.o.hs + 4 * c) =
+        make_uint2(bf16_pack(o.x * inv, o.y * inv), bf16_pack(o.z * inv, o.w * inv));
+    if (p.lse && c == 0)
+        p.lse[tok * p.q_heads + head] = l == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(l));
+}
+
+// kv4_decode.cu
+int kv4_decode_ctas();
+size_t kv4_decode_part_floats(int head_dim);
+// rows: the most rows (new tokens * group) of a sequence, max_units: the most
+// units in all, as far as known (0: not known).
+uw_status launch_kv4_decode(const AttnParams &p, int head_dim, int64_t rows, int64_t max_units, cudaStream_t st);
+
+}  // namespace uw
