@@ -102,7 +102,7 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
         return UW_ERR_INVALID_ARG;
     if (q_heads <= 0 || q_heads % c->kv_heads)
         return UW_ERR_SHAPE;
-    if (q_heads > kKv4MaxHeads)
+    if (q_heads > kKv4MaxHeads || n_tokens * (q_heads / c->kv_heads) > 0x7fffffff)
         return UW_ERR_UNSUPPORTED;
     if (none)
         return UW_OK;
@@ -116,7 +116,7 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
     p.causal = causal != 0;
     p.window = window;
     p.rows_min = 0;
-    p.rows_max = INT64_MAX;
+    p.rows_max = INT32_MAX;
     p.counters = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + w.counters);
     p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.parts);
     const int64_t rows = max_new * p.group;

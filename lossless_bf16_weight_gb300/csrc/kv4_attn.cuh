@@ -27,7 +27,7 @@ struct AttnParams {
     float *lse;
     float c1;                 // softmax scale * log2(e)
     int32_t q_heads, group, causal, window;
-    int64_t rows_min, rows_max;  // sequences with rows (new * group) in this range are this launch's
+    int32_t rows_min, rows_max;  // sequences with rows (new * group) in this range are this launch's
     float *parts;             // [2 * gridDim.x][RB * (D + 2)]: output, maximum, sum
     uint32_t *counters;       // [gridDim.x], left at zero
 };
@@ -52,19 +52,25 @@ struct Item {
     uint32_t n;    // its units
 };
 
+// The sequence that holds a cut: its first unit and the units of one head.
+struct Found {
+    uint64_t base, per_head;
+    int32_t s;
+    Seq q;
+};
+
 template <int RB, int T>  // rows of a row tile, keys of a unit
 struct Sched {
     static __device__ __forceinline__ bool mine(const AttnParams &p, const Seq &s) {
-        const int64_t rows = int64_t(s.n) * p.group;
+        const int32_t rows = s.n * p.group;
         return rows >= p.rows_min && rows <= p.rows_max && rows > 0;
     }
     static __device__ __forceinline__ int row_tiles(const AttnParams &p, const Seq &s) {
-        return int((int64_t(s.n) * p.group + RB - 1) / RB);
+        return (s.n * p.group - 1) / RB + 1;
     }
     static __device__ __forceinline__ KeyRange tile_keys(const AttnParams &p, const Seq &s, int rt) {
-        const int64_t r0 = int64_t(rt) * RB;
-        const int64_t r1 = min(r0 + RB, int64_t(s.n) * p.group) - 1;
-        return visible(p, s, int(r0 / p.group), int(r1 / p.group));
+        const int32_t r0 = rt * RB, r1 = r0 + min(RB, s.n * p.group - r0) - 1;
+        return visible(p, s, r0 / p.group, r1 / p.group);
     }
     static __device__ __forceinline__ uint32_t units(const KeyRange &k) {
         return k.hi > k.lo ? uint32_t((k.hi - 1) / T - k.lo / T + 1) : 1u;
@@ -108,15 +114,48 @@ __device__ __forceinline__ uint64_t cta_prefix(uint64_t mine, uint64_t *slots, u
     return before + v - mine;
 }
 
+// a * b / c and a / b, in 32 bits where they fit (a 64-bit division is a
+// hundred instructions one after the other).
+__device__ __forceinline__ uint64_t mul_div(uint64_t a, uint32_t b, uint32_t c) {
+    const uint64_t ab = a * b;
+    return (ab >> 32) == 0 ? uint32_t(ab) / c : ab / c;
+}
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
+    return ((a | b) >> 32) == 0 ? uint32_t(a) / uint32_t(b) : a / b;
+}
+
 // The share (of `workers` equal ones) that holds unit u: the last c with
 // total * c / workers <= u.
 __device__ __forceinline__ uint32_t share_of(uint64_t u, uint64_t total, uint32_t workers) {
-    return uint32_t(((u + 1) * workers - 1) / total);
+    return uint32_t(divide((u + 1) * workers - 1, total));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two fp32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    return uint64_t(__float_as_uint(a)) | uint64_t(__float_as_uint(b)) << 32;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    return make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -134,13 +173,21 @@ __device__ __forceinline__ void join(float &m, float &l, float4 &o, float m2, fl
     o.w = fmaf(f2, o2.w, f * o.w);
 }
 
+// A part whose maximum is already known to be f (a factor) below the joint one.
+__device__ __forceinline__ void join_scaled(float &l, float4 &o, float f, float l2, float4 o2) {
+    l = fmaf(f, l2, l);
+    o.x = fmaf(f, o2.x, o.x);
+    o.y = fmaf(f, o2.y, o.y);
+    o.z = fmaf(f, o2.z, o.z);
+    o.w = fmaf(f, o2.w, o.w);
+}
+
 // Four dimensions (4c ..) of row r of an item: out = o / l, and with c = 0 the lse.
 template <int D>
-__device__ __forceinline__ void store_row(const AttnParams &p, const Item &it, int64_t r, int64_t rows, int c, float4 o,
-                                          float m, float l) {
-    if (r >= rows)
-        return;
-    const int64_t tok = it.q.t0 + r / p.group, head = int64_t(it.head) * p.group + r % p.group;
+__device__ __forceinline__ void store_row(const AttnParams &p, const Item &it, int r, int c, float4 o, float m,
+                                          float l) {
+    const int i = r / p.group;
+    const int64_t tok = it.q.t0 + i, head = it.head * p.group + (r - i * p.group);
     const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: o is 0 and stays 0
     *reinterpret_cast<uint2 *>(p.o.p + tok * p.o.ts + head * p.o.hs + 4 * c) =
         make_uint2(bf16_pack(o.x * inv, o.y * inv), bf16_pack(o.z * inv, o.w * inv));

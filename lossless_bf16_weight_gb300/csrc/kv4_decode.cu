@@ -17,13 +17,16 @@
 //                 offset of a key are applied to the fp32 product:
 //                 q.k = s (sum q (16 + c)) + (lo - 16 s) sum q.  Exact but for
 //                 fp32 sums: no rounded K.
-//   O^T = V^T P^T a code becomes c - 8 (one more subtraction: a sum over many
-//                 keys would lose digits to the offset), the scale goes into
-//                 the probability, p s, and the middle of the range into a sum
-//                 of its own: o = sum (p s)(c - 8) + sum p (lo + 8 s).  p s is taken
-//                 as the sum of two BF16 (a rounding and its rest), two
-//                 products for each, which the tensor cores have room for: the
-//                 result is exact to about 2^-16 before its own rounding.
+//   O^T = V^T P^T a code becomes c - 8 (one subtraction more: with an offset in
+//                 place the sum over many keys would lose digits to it), the
+//                 scale goes into the probability, p s, and the middle of the
+//                 range into a sum of its own:
+//                 o = sum (p s)(c - 8) + sum p (lo + 8 s).  p s is taken
+//                 as the sum of two BF16, a rounding and its rest, so that the
+//                 result is exact to about 2^-16 before its own rounding.  Up
+//                 to four rows leave half of the products' columns empty: the
+//                 rests go there (the same rows again) and cost nothing; more
+//                 rows take a second product.
 // The running maximum of the softmax is only raised when a score passes it by
 // 2^24 (BF16 and fp32 hold that without loss), so that a tile costs a vote
 // in place of shuffles.
@@ -48,30 +51,42 @@ constexpr int kStageBytes = kTile * (D + 8);
 template <int D>
 constexpr int kStages = D == 128 ? 3 : 5;
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-
-// 16 + c for the codes in bits 3..6 of both halves: the upper four of a
-// BF16's seven mantissa bits at 2^4.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) { return (w & 0x00780078u) | 0x41804180u; }
-// The same less 24: c - 8 (exact).
-__device__ __forceinline__ uint32_t centred_pair(uint32_t w) {
+// A value the compiler does not know, so that it stays in a register: the
+// logic operations below take their masks from registers (one instruction
+// holds one constant, and two constants would make it two).
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(code_pair(w)), "r"(0x41c041c0u));
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
+// Codes as pairs of BF16, by one logic operation each: the bits of a code are
+// the upper four of the seven mantissa bits at 2^4 (codes in bits 3..6 of both
+// halves) or the lower four at 2^7 (bits 0..3).
+struct Codes {
+    uint32_t mask3 = opaque(0x00780078u), one3 = opaque(0x41804180u);
+    uint32_t mask0 = opaque(0x000f000fu), one0 = opaque(0x43004300u);
+    uint32_t mid3 = opaque(0x41c041c0u), mid0 = opaque(0x43084308u);  // 24, 136
+    // 16 + c
+    __device__ __forceinline__ uint32_t key3(uint32_t w) const { return and_or(w, mask3, one3); }
+    // c - 8 (exact)
+    __device__ __forceinline__ uint32_t value3(uint32_t w) const { return sub2(and_or(w, mask3, one3), mid3); }
+    __device__ __forceinline__ uint32_t value0(uint32_t w) const { return sub2(and_or(w, mask0, one0), mid0); }
+};
+
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -81,7 +96,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // 8 x 8 transpose of 16-bit values across the warp.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 
@@ -109,63 +124,70 @@ template <int D, int NT>
 struct Warp {
     // D/16 pairs of dimensions of the output for 2 rows of each of NT row groups
     float o[D / 16][NT][4];
-    float m[NT][2], l[NT][2], z[NT][2];
+    float m[NT][2];
+    uint64_t l[NT], z[NT];   // sums of p and of p (lo + 8 s), for the two rows
     uint32_t q[NT][D / 16][2];
-    float qs[NT][2];
+    uint64_t qs[NT];         // sum of q
 };
 
-template <int D, int NT>
+// NT groups of eight rows; kDup (NT = 1): up to four rows, which rows 4..7 repeat.
+template <int D, int NT, bool kDup>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kernel(const AttnParams p) {
-    constexpr int RB = 8 * NT;
+    static_assert(!kDup || NT == 1, "rows repeated in one group");
+    constexpr int RB = kDup ? 4 : 8 * NT;
     constexpr int ST = kStages<D>;
     using S = Sched<RB, kTile>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t slots[kWarps];
-    __shared__ uint64_t found_base[2];
-    __shared__ int found_seq[2];
+    __shared__ Found found[2];
     __shared__ float w_m[kWarps][RB], w_l[kWarps][RB];
     __shared__ uint32_t arrived;
     grid_dep_launch();
     grid_dep_wait();
     const Kv4View &v = p.v;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_addr(smem) + warp * ST * kStageBytes<D>;
+    unsigned char *const ring = smem + warp * ST * kStageBytes<D>;
+    const uint32_t ring_at = smem_addr(ring);
 
-    // this CTA's share [ua, ub) of the units, and where it begins
+    // this CTA's share [cut 0, cut 1) of the units, and where it begins
     const int per = (v.n_seqs + kWarps * 32 - 1) / (kWarps * 32);
     const int sa = min(int(threadIdx.x) * per, v.n_seqs), sb = min(sa + per, v.n_seqs);
     uint64_t mine = 0;
-    for (int s = sa; s < sb; s++)
-        mine += S::seq_units(p, kv4_seq(v, s)) * v.heads;
+    Seq sq{0, 0, 0};
+    for (int s = sa; s < sb; s++) {
+        sq = kv4_seq(v, s);
+        mine += S::seq_units(p, sq) * v.heads;
+    }
     uint64_t total;
     const uint64_t before = cta_prefix<kWarps * 32>(mine, slots, &total);
     const uint32_t workers = uint32_t(min(total, uint64_t(gridDim.x)));
     if (blockIdx.x >= workers)
         return;
-    uint64_t cut[2] = {total * blockIdx.x / workers, total * (blockIdx.x + 1) / workers};
+    uint64_t cut[2] = {mul_div(total, blockIdx.x, workers), mul_div(total, blockIdx.x + 1, workers)};
     for (int k = 0; k < 2; k++)
         if (before <= cut[k] && cut[k] < before + mine) {
             uint64_t u = before;
             for (int s = sa; s < sb; s++) {
-                const uint64_t w = S::seq_units(p, kv4_seq(v, s)) * v.heads;
-                if (cut[k] < u + w) {
-                    found_seq[k] = s;
-                    found_base[k] = u;
+                if (per > 1)
+                    sq = kv4_seq(v, s);
+                const uint64_t w = S::seq_units(p, sq);
+                if (cut[k] < u + w * v.heads) {
+                    found[k] = Found{u, w, s, sq};
                     break;
                 }
-                u += w;
+                u += w * v.heads;
             }
         }
     __syncthreads();
     auto locate = [&](int k) {
+        const Found &f = found[k];
         Item it;
-        it.s = found_seq[k];
-        it.q = kv4_seq(v, it.s);
-        const uint64_t per_head = S::seq_units(p, it.q);
-        uint64_t rest = cut[k] - found_base[k];
-        it.head = int(rest / per_head);
-        rest -= it.head * per_head;
-        it.u0 = found_base[k] + it.head * per_head;
+        it.s = f.s;
+        it.q = f.q;
+        uint64_t rest = cut[k] - f.base;
+        it.head = int(divide(rest, f.per_head));
+        rest -= it.head * f.per_head;
+        it.u0 = f.base + it.head * f.per_head;
         for (it.rt = 0;; it.rt++) {
             it.keys = S::tile_keys(p, it.q, it.rt);
             it.n = S::units(it.keys);
@@ -183,65 +205,82 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     Item it = locate(0);
     if (whole && it.n <= kWholeUnits)
         cut[0] = it.u0;
-    if (cut[1] < total) {
+    if (cut[1] < total && whole) {
         const Item e = locate(1);
-        if (whole && e.n <= kWholeUnits)
+        if (e.n <= kWholeUnits)
             cut[1] = e.u0;
     }
+    const int64_t block = int64_t(D + 8) << v.page_log2;
+    const int mask = (1 << v.page_log2) - 1;
 
     uint64_t u = cut[0];
     while (u < cut[1]) {
         const uint32_t seg_a = uint32_t(u - it.u0), seg_b = uint32_t(min(cut[1] - it.u0, uint64_t(it.n)));
-        const int tile0 = it.keys.lo / kTile;
         const bool some = it.keys.hi > it.keys.lo;
         const int tiles = some ? int(seg_b - seg_a) : 0;
-        const int first = tile0 + int(seg_a) + warp;       // this warp's tiles: first, first + kWarps, ...
+        const int first = it.keys.lo / kTile + int(seg_a) + warp;  // this warp's tiles: first, first + kWarps, ...
         const int n_mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-        const int64_t r0 = int64_t(it.rt) * RB;
-        const int64_t rows = int64_t(it.q.n) * p.group;
+        const int r0 = it.rt * RB, rows = it.q.n * p.group;
         // keys that every row of the item sees
-        const int tok_a = int(r0 / p.group), tok_b = int((min(r0 + RB, rows) - 1) / p.group);
+        const int tok_a = r0 / p.group, tok_b = (r0 + min(RB, rows - r0) - 1) / p.group;
         const KeyRange ka = visible(p, it.q, tok_a, tok_a), kb = visible(p, it.q, tok_b, tok_b);
         const int all_lo = kb.lo, all_hi = min(ka.hi, it.q.len);
 
-        // A tile's copies.  The lane's page is that of key 16 * (lane / 16) of the tile.
+        // A tile's copies.  A tile lies in one page, or (pages of 16) its
+        // halves in two; the lane holds the page of key 16 * (lane / 16).
+        const int32_t *const table = v.table + int64_t(it.s) * v.table_stride;
         auto page_of = [&](int tile) -> int {
             const int key = tile * kTile + (lane & 16);
             if (key >= it.q.len)
                 return -1;
-            const int page = __ldg(v.table + int64_t(it.s) * v.table_stride + (key >> v.page_log2));
+            const int page = __ldg(table + (key >> v.page_log2));
             if (uint32_t(page) >= uint64_t(v.n_pages)) {
                 atomicOr(v.status, uint32_t(kStatusBadCache));
                 return -1;
             }
             return page;
         };
-        const int64_t block = int64_t(D + 8) << v.page_log2;
-        const int mask = (1 << v.page_log2) - 1;
+        const uint8_t *const base = v.pages + it.head * block;
+        const int64_t page_bytes = block * v.heads;
+        const int v_off = (D / 2) << v.page_log2;
         auto issue = [&](int tile, int page, int stage) {
-            const uint32_t dst = ring + stage * kStageBytes<D>;
+            const uint32_t dst = ring_at + stage * kStageBytes<D>;
             const int key0 = tile * kTile;
-            const uint8_t *const base = v.pages + it.head * block;
             constexpr int RC = D / 32;             // 16-byte chunks of a row
-            constexpr int RPI = 32 / RC;           // rows of one instruction
+            const uint8_t *half[2];                // codes of keys 0..15 and 16..31, the lane's chunk
+            int pages[2], slots[2];
 #pragma unroll
-            for (int j = 0; j < RC; j++) {
-                const int r = j * RPI + lane / RC, ch = lane % RC;
-                const int pg = __shfl_sync(0xffffffffu, page, r & 16);
-                const bool in = pg >= 0 && key0 + r < it.q.len;
-                const uint8_t *src = in ? base + pg * (block * v.heads) + ((key0 + r) & mask) * (D / 2) + ch * 16 : v.pages;
-                cp_async16_zfill(dst + r * (D / 2) + ch * 16, src, in ? 16u : 0u);
-                src = in ? src + ((D / 2) << v.page_log2) : v.pages;
-                cp_async16_zfill(dst + kTile * (D / 2) + r * (D / 2) + v_chunk<D>(r, ch) * 16, src, in ? 16u : 0u);
+            for (int h = 0; h < 2; h++) {
+                pages[h] = __shfl_sync(0xffffffffu, page, 16 * h);
+                slots[h] = (key0 + 16 * h) & mask;
+                half[h] = base + pages[h] * page_bytes + (slots[h] * (D / 2) + lane * 16);
             }
-            const int r = (lane & 7) * 4, is_v = (lane >> 3) & 1;
-            const int pg = __shfl_sync(0xffffffffu, page, r & 16);
+            const uint32_t to = dst + lane * 16;   // consecutive lanes, consecutive chunks
+            const uint32_t vto = dst + kTile * (D / 2) + (lane / RC) * (D / 2) + v_chunk<D>(lane / RC, lane % RC) * 16;
+            const int left = it.q.len - key0;      // keys of the tile that there are
+            const bool full = left >= kTile && (pages[0] | pages[1]) >= 0;
+            if (full) {
+#pragma unroll
+                for (int j = 0; j < RC; j++) {
+                    const uint8_t *src = half[j / (RC / 2)] + (j % (RC / 2)) * 512;
+                    cp_async16(to + j * 512, src);
+                    cp_async16(vto + j * 512, src + v_off);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < RC; j++) {
+                    const uint8_t *src = half[j / (RC / 2)] + (j % (RC / 2)) * 512;
+                    const bool in = pages[j / (RC / 2)] >= 0 && j * (32 / RC) + lane / RC < left;
+                    cp_async16_zfill(to + j * 512, in ? src : v.pages, in ? 16u : 0u);
+                    cp_async16_zfill(vto + j * 512, in ? src + v_off : v.pages, in ? 16u : 0u);
+                }
+            }
             if (lane < 16) {
-                const bool in = pg >= 0 && key0 + r < it.q.len;
-                const uint8_t *src = in ? base + pg * (block * v.heads) +
-                                              kv4_params<D>(v.page_log2, (key0 + r) & mask, is_v)
-                                        : v.pages;
-                cp_async16_zfill(dst + kTile * D + is_v * (kTile * 4) + r * 4, src, in ? 16u : 0u);
+                const int r = (lane & 7) * 4, h = (lane >> 2) & 1;
+                const bool in = (h ? pages[1] : pages[0]) >= 0 && r < left;
+                const uint8_t *src = base + (h ? pages[1] : pages[0]) * page_bytes +
+                                     kv4_params<D>(v.page_log2, (h ? slots[1] : slots[0]) + (r & 15), lane >> 3);
+                cp_async16_zfill(dst + kTile * D + lane * 16, in ? src : v.pages, in ? 16u : 0u);
             }
         };
         int page_next = n_mine > 0 ? page_of(first) : -1;
@@ -260,13 +299,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         // paired as the codes of a word come out of it: (0,4) (1,5) (2,6) (3,7).
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
-            const int64_t r = r0 + nt * 8 + g;
+            const int rr = nt * 8 + (kDup ? g & 3 : g);
             uint4 x[D / 32];
 #pragma unroll
             for (int k = 0; k < D / 32; k++)
                 x[k] = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int64_t tok = it.q.t0 + r / p.group, head = int64_t(it.head) * p.group + r % p.group;
+            if (rr < rows - r0 && n_mine > 0) {
+                const int i = (r0 + rr) / p.group;
+                const int64_t tok = it.q.t0 + i, head = it.head * p.group + (r0 + rr - i * p.group);
                 const uint4 *src = reinterpret_cast<const uint4 *>(p.q.p + tok * p.q.ts + head * p.q.hs + (D / 4) * t);
 #pragma unroll
                 for (int k = 0; k < D / 32; k++)
@@ -286,13 +326,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            w.qs[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-            w.qs[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                w.m[nt][k] = -INFINITY;
-                w.l[nt][k] = w.z[nt][k] = 0.f;
-            }
+            w.qs[nt] = pair2(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
+            w.m[nt][0] = w.m[nt][1] = -INFINITY;
+            w.l[nt] = w.z[nt] = 0;
 #pragma unroll
             for (int i = 0; i < D / 16; i++)
 #pragma unroll
@@ -300,6 +336,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                     w.o[i][nt][k] = 0.f;
         }
 
+        const Codes codes;
+        int stage = 0;
         for (int i = 0; i < n_mine; i++) {
             {
                 const int nx = i + ST - 1;
@@ -307,137 +345,187 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                 if (nx + 1 < n_mine)
                     page_next = page_of(first + (nx + 1) * kWarps);
                 if (nx < n_mine)
-                    issue(first + nx * kWarps, page, nx % ST);
+                    issue(first + nx * kWarps, page, stage == 0 ? ST - 1 : stage - 1);
                 cp_async_commit();
             }
             asm volatile("cp.async.wait_group %0;" :: "n"(ST - 1) : "memory");
             __syncwarp();
-            const uint32_t st = ring + (i % ST) * kStageBytes<D>;
+            const unsigned char *const st = ring + stage * kStageBytes<D>;
+            stage = stage + 1 == ST ? 0 : stage + 1;
             const int key0 = (first + i * kWarps) * kTile;
 
             // scores
             float sc[2][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < 2; mt++) {
+            for (int mt = 0; mt < 2; mt++)
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int k = 0; k < 4; k++)
                         sc[mt][nt][k] = 0.f;
-                uint32_t a[D / 32], b[D / 32];
-                const uint32_t row = st + (16 * mt + key_of(g)) * (D / 2) + t * (D / 8);
-                if constexpr (D == 128) {
-                    const uint4 x = lds128(row), y = lds128(row + 8 * (D / 2));
-                    a[0] = x.x, a[1] = x.y, a[2] = x.z, a[3] = x.w;
-                    b[0] = y.x, b[1] = y.y, b[2] = y.z, b[3] = y.w;
-                } else {
-                    const uint2 x = lds64(row), y = lds64(row + 8 * (D / 2));
-                    a[0] = x.x, a[1] = x.y;
-                    b[0] = y.x, b[1] = y.y;
+            uint32_t a[2][2][D / 32];  // [keys 16 mt + key_of(g), + 8][words]
+#pragma unroll
+            for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const unsigned char *row = st + (16 * mt + 8 * h + key_of(g)) * (D / 2) + t * (D / 8);
+                    if constexpr (D == 128) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(row);
+                        a[mt][h][0] = x.x, a[mt][h][1] = x.y, a[mt][h][2] = x.z, a[mt][h][3] = x.w;
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(row);
+                        a[mt][h][0] = x.x, a[mt][h][1] = x.y;
+                    }
                 }
 #pragma unroll
-                for (int k = 0; k < D / 32; k++)
+            for (int k = 0; k < D / 32; k++)
 #pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        const uint32_t a0 = code_pair(j ? a[k] >> 5 : a[k] << 3);
-                        const uint32_t a1 = code_pair(j ? b[k] >> 5 : b[k] << 3);
-                        const uint32_t a2 = code_pair(j ? a[k] >> 9 : a[k] >> 1);
-                        const uint32_t a3 = code_pair(j ? b[k] >> 9 : b[k] >> 1);
+                for (int j = 0; j < 2; j++)
+#pragma unroll
+                    for (int mt = 0; mt < 2; mt++) {
+                        const uint32_t x = a[mt][0][k], y = a[mt][1][k];
+                        const uint32_t a0 = codes.key3(j ? x >> 5 : x << 3), a1 = codes.key3(j ? y >> 5 : y << 3);
+                        const uint32_t a2 = codes.key3(j ? x >> 9 : x >> 1), a3 = codes.key3(j ? y >> 9 : y >> 1);
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++)
                             mma16816(sc[mt][nt], a0, a1, a2, a3, w.q[nt][2 * k + j][0], w.q[nt][2 * k + j][1]);
                     }
-            }
-            // sc[mt][nt][2 h + k]: key 16 mt + 8 h + key_of(g), row 8 nt + 2 t + k
-            uint32_t vpar[4];
+            // sc[mt][nt][2 h + k]: key 16 mt + 8 h + key_of(g), row 8 nt + 2 t + k.
+            // In log2 units and less the maximum: y - m = acc * a + (c * qs - m).
+            uint32_t kpar[4], vpar[4];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const uint32_t at = st + kTile * D + (8 * j + key_of(g)) * 4;
-                const uint32_t kp = lds32(at);
-                vpar[j] = lds32(at + kTile * 4);
-                const float a = bf16_lo(kp) * p.c1, c = fmaf(bf16_hi(kp), p.c1, -16.f * a);
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        float &y = sc[j >> 1][nt][2 * (j & 1) + k];
-                        y = fmaf(y, a, c * w.qs[nt][k]);
-                    }
+                const unsigned char *at = st + kTile * D + (8 * j + key_of(g)) * 4;
+                kpar[j] = *reinterpret_cast<const uint32_t *>(at);
+                vpar[j] = *reinterpret_cast<const uint32_t *>(at + kTile * 4);
             }
             const bool open = key0 < all_lo || key0 + kTile > all_hi;
-            if (open) {
+            uint64_t y[4][NT];
+            auto scores = [&]() {
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++)
+                for (int j = 0; j < 4; j++) {
+                    const float a = bf16_lo(kpar[j]) * p.c1, c = fmaf(bf16_hi(kpar[j]), p.c1, -16.f * a);
+                    const uint64_t aa = pair2(a, a), cc = pair2(c, c);
 #pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        const int64_t r = min(r0 + nt * 8 + 2 * t + k, rows - 1);
-                        const int tok = int(r / p.group);
-                        const KeyRange kr = visible(p, it.q, tok, tok);
+                    for (int nt = 0; nt < NT; nt++)
+                        y[j][nt] = fma2(pair2(sc[j >> 1][nt][2 * (j & 1)], sc[j >> 1][nt][2 * (j & 1) + 1]), aa,
+                                        fma2(cc, w.qs[nt], pair2(-w.m[nt][0], -w.m[nt][1])));
+                }
+                if (open) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        bool in[4][2];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const int row = 8 * nt + (kDup ? (2 * t + k) & 3 : 2 * t + k);
+                            const int tok = (r0 + min(row, rows - r0 - 1)) / p.group;
+                            const KeyRange kr = visible(p, it.q, tok, tok);
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                const int key = key0 + 8 * j + key_of(g);
+                                in[j][k] = key >= kr.lo && key < min(kr.hi, it.q.len);
+                            }
+                        }
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
-                            const int key = key0 + 8 * j + key_of(g);
-                            if (key < kr.lo || key >= min(kr.hi, it.q.len))
-                                sc[j >> 1][nt][2 * (j & 1) + k] = -INFINITY;
+                            const float2 f = unpair(y[j][nt]);
+                            y[j][nt] = pair2(in[j][0] ? f.x : -INFINITY, in[j][1] ? f.y : -INFINITY);
                         }
                     }
-            }
+                }
+            };
+            scores();
             // raise the maximum where a score passes it by far
+            float top[NT][2];
             bool raise = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const float top = fmaxf(fmaxf(sc[0][nt][k], sc[0][nt][2 + k]), fmaxf(sc[1][nt][k], sc[1][nt][2 + k]));
-                    raise = raise || top > w.m[nt][k] + kRaise;
-                }
+            for (int nt = 0; nt < NT; nt++) {
+                const float2 f0 = unpair(y[0][nt]), f1 = unpair(y[1][nt]), f2 = unpair(y[2][nt]), f3 = unpair(y[3][nt]);
+                top[nt][0] = fmaxf(fmaxf(f0.x, f1.x), fmaxf(f2.x, f3.x));
+                top[nt][1] = fmaxf(fmaxf(f0.y, f1.y), fmaxf(f2.y, f3.y));
+                raise = raise || fmaxf(top[nt][0], top[nt][1]) > kRaise;
+            }
             if (__any_sync(0xffffffffu, raise)) {
+                // With no maximum yet the scores are taken again, less nothing.
+                bool none = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int k = 0; k < 2; k++)
+                        none = none || w.m[nt][k] == -INFINITY;
+                const bool fresh = __any_sync(0xffffffffu, none);
+                float old[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int k = 0; k < 2; k++) {
-                        float top = fmaxf(fmaxf(sc[0][nt][k], sc[0][nt][2 + k]), fmaxf(sc[1][nt][k], sc[1][nt][2 + k]));
+                        old[nt][k] = w.m[nt][k];
+                        if (fresh)
+                            w.m[nt][k] = 0.f;
+                    }
+                if (fresh) {
+                    scores();
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        const float2 f0 = unpair(y[0][nt]), f1 = unpair(y[1][nt]), f2 = unpair(y[2][nt]),
+                                     f3 = unpair(y[3][nt]);
+                        top[nt][0] = fmaxf(fmaxf(f0.x, f1.x), fmaxf(f2.x, f3.x));
+                        top[nt][1] = fmaxf(fmaxf(f0.y, f1.y), fmaxf(f2.y, f3.y));
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    float f[2];
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        float x = top[nt][k];
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const float m2 = fmaxf(w.m[nt][k], top);
-                        const float f = m2 == -INFINITY ? 1.f : exp2_fast(w.m[nt][k] - m2);
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                        const float m2 = fmaxf(old[nt][k], x + w.m[nt][k]);
+                        f[k] = m2 == -INFINITY ? 1.f : exp2_fast(old[nt][k] - m2);
                         w.m[nt][k] = m2;
-                        w.l[nt][k] *= f;
-                        w.z[nt][k] *= f;
 #pragma unroll
                         for (int d = 0; d < D / 16; d++) {
-                            w.o[d][nt][k] *= f;
-                            w.o[d][nt][2 + k] *= f;
+                            w.o[d][nt][k] *= f[k];
+                            w.o[d][nt][2 + k] *= f[k];
                         }
                     }
+                    w.l[nt] = mul2(w.l[nt], pair2(f[0], f[1]));
+                    w.z[nt] = mul2(w.z[nt], pair2(f[0], f[1]));
+                }
+                scores();
             }
             // probabilities, as the B operand of the product with V: p s in two BF16
             uint32_t hi[2][NT][2], lo[2][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++) {
-                const float m0 = w.m[nt][0] == -INFINITY ? 0.f : w.m[nt][0];
-                const float m1 = w.m[nt][1] == -INFINITY ? 0.f : w.m[nt][1];
+            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     const float s = bf16_lo(vpar[j]), mid = fmaf(8.f, s, bf16_hi(vpar[j]));
-                    const float y0 = sc[j >> 1][nt][2 * (j & 1)], y1 = sc[j >> 1][nt][2 * (j & 1) + 1];
-                    const float p0 = exp2_fast(y0 - m0), p1 = exp2_fast(y1 - m1);
-                    w.l[nt][0] += p0;
-                    w.l[nt][1] += p1;
-                    float s0 = p0 * s, s1 = p1 * s, z0 = p0 * mid, z1 = p1 * mid;
+                    const float2 f = unpair(y[j][nt]);
+                    const uint64_t pr = pair2(exp2_fast(f.x), exp2_fast(f.y));
+                    uint64_t ps = mul2(pr, pair2(s, s));
+                    w.l[nt] = add2(w.l[nt], pr);
                     if (open) {  // a masked key's scale may be anything
-                        s0 = y0 == -INFINITY ? 0.f : s0;
-                        s1 = y1 == -INFINITY ? 0.f : s1;
-                        z0 = y0 == -INFINITY ? 0.f : z0;
-                        z1 = y1 == -INFINITY ? 0.f : z1;
+                        const float2 a = unpair(ps), b = unpair(mul2(pr, pair2(mid, mid)));
+                        const bool in0 = f.x != -INFINITY, in1 = f.y != -INFINITY;
+                        ps = pair2(in0 ? a.x : 0.f, in1 ? a.y : 0.f);
+                        w.z[nt] = add2(w.z[nt], pair2(in0 ? b.x : 0.f, in1 ? b.y : 0.f));
+                    } else {
+                        w.z[nt] = fma2(pr, pair2(mid, mid), w.z[nt]);
                     }
-                    w.z[nt][0] += z0;
-                    w.z[nt][1] += z1;
-                    const uint32_t h = bf16_pack(s0, s1);
-                    hi[j >> 1][nt][j & 1] = transpose8x8(h);
-                    lo[j >> 1][nt][j & 1] = transpose8x8(bf16_pack(s0 - bf16_lo(h), s1 - bf16_hi(h)));
+                    const float2 a = unpair(ps);
+                    const uint32_t h = bf16_pack(a.x, a.y);
+                    const float2 rest = unpair(add2(ps, pair2(-bf16_lo(h), -bf16_hi(h))));
+                    const uint32_t r = bf16_pack(rest.x, rest.y);
+                    if constexpr (kDup) {
+                        hi[j >> 1][nt][j & 1] = transpose8x8(t < 2 ? h : r);
+                    } else {
+                        hi[j >> 1][nt][j & 1] = transpose8x8(h);
+                        lo[j >> 1][nt][j & 1] = transpose8x8(r);
+                    }
                 }
-            }
             // output
 #pragma unroll
             for (int mt = 0; mt < 2; mt++) {
@@ -447,12 +535,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                 for (int j = 0; j < 4; j++) {
                     // keys of the product's rows 2t, 2t + 1, 2t + 8, 2t + 9
                     const int r = 16 * mt + 8 * (j >> 1) + key_of(2 * t + (j & 1));
-                    const uint32_t base = st + kTile * (D / 2) + r * (D / 2);
+                    const unsigned char *row = st + kTile * (D / 2) + r * (D / 2);
                     if constexpr (D == 128) {
-                        const uint2 y = lds64(base + v_chunk<D>(r, g >> 1) * 16 + (g & 1) * 8);
+                        const uint2 y = *reinterpret_cast<const uint2 *>(row + v_chunk<D>(r, g >> 1) * 16 + (g & 1) * 8);
                         x[j][0] = y.x, x[j][1] = y.y;
                     } else {
-                        x[j][0] = lds32(base + g * 4);
+                        x[j][0] = *reinterpret_cast<const uint32_t *>(row + g * 4);
                     }
                 }
 #pragma unroll
@@ -461,12 +549,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                     for (int b = 0; b < 4; b++) {
                         const uint32_t sel = b * 0x11u | (4 + b) * 0x1100u;
                         const uint32_t e = __byte_perm(x[0][k], x[1][k], sel), f = __byte_perm(x[2][k], x[3][k], sel);
-                        const uint32_t a0 = centred_pair(e << 3), a1 = centred_pair(e >> 1);
-                        const uint32_t a2 = centred_pair(f << 3), a3 = centred_pair(f >> 1);
+                        const uint32_t a0 = codes.value0(e), a1 = codes.value3(e >> 1);
+                        const uint32_t a2 = codes.value0(f), a3 = codes.value3(f >> 1);
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++) {
                             mma16816(w.o[4 * k + b][nt], a0, a1, a2, a3, hi[mt][nt][0], hi[mt][nt][1]);
-                            mma16816(w.o[4 * k + b][nt], a0, a1, a2, a3, lo[mt][nt][0], lo[mt][nt][1]);
+                            if constexpr (!kDup)
+                                mma16816(w.o[4 * k + b][nt], a0, a1, a2, a3, lo[mt][nt][0], lo[mt][nt][1]);
                         }
                     }
             }
@@ -476,38 +565,53 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
 
         // The warps' parts, joined through shared memory: each warp leaves its
         // maximum, sum and output (with the ranges' middles added) in its own ring.
-        float4 *const wo = reinterpret_cast<float4 *>(smem + warp * ST * kStageBytes<D>);
+        float4 *const wo = reinterpret_cast<float4 *>(ring);
         __syncwarp();
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+        for (int nt = 0; nt < NT; nt++) {
+            const float2 l2 = unpair(w.l[nt]), z2 = unpair(w.z[nt]);
 #pragma unroll
             for (int k = 0; k < 2; k++) {
-                float l = w.l[nt][k], z = w.z[nt][k];
+                float l = k ? l2.y : l2.x, z = k ? z2.y : z2.x;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
                     l += __shfl_xor_sync(0xffffffffu, l, o);
                     z += __shfl_xor_sync(0xffffffffu, z, o);
                 }
-                const int row = 8 * nt + 2 * t + k;
-                if (g == 0) {
-                    w_m[warp][row] = w.m[nt][k];
-                    w_l[warp][row] = l;
-                }
-                // dimensions D/8 g .. + D/8 - 1 of this row
+                float o[D / 8];  // dimensions D/8 g .. of row 8 nt + 2 t + k
 #pragma unroll
-                for (int i = 0; i < D / 32; i++)
-                    wo[part_at<D>(row, g * (D / 32) + i)] =
-                        make_float4(w.o[2 * i][nt][k] + z, w.o[2 * i][nt][2 + k] + z, w.o[2 * i + 1][nt][k] + z,
-                                    w.o[2 * i + 1][nt][2 + k] + z);
+                for (int i = 0; i < D / 16; i++) {
+                    o[2 * i] = w.o[i][nt][k];
+                    o[2 * i + 1] = w.o[i][nt][2 + k];
+                }
+                if constexpr (kDup) {  // the rests' products are in the columns four on
+#pragma unroll
+                    for (int i = 0; i < D / 8; i++)
+                        o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
+                }
+                const int row = 8 * nt + 2 * t + k;
+                if (!kDup || t < 2) {
+                    if (g == 0) {
+                        w_m[warp][row] = w.m[nt][k];
+                        w_l[warp][row] = l;
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 32; i++)
+                        wo[part_at<D>(row, g * (D / 32) + i)] =
+                            make_float4(o[4 * i] + z, o[4 * i + 1] + z, o[4 * i + 2] + z, o[4 * i + 3] + z);
+                }
             }
+        }
         __syncthreads();
 
         // This part's place among the item's, and the item's output once all are there.
         const uint32_t f = share_of(it.u0, total, workers), e = share_of(it.u0 + it.n - 1, total, workers);
         const bool alone = seg_a == 0 && seg_b == it.n;
         constexpr int F4 = RB * (D / 4);
-        float *const part = p.parts + (2 * uint64_t(blockIdx.x) + (seg_a == 0 ? 1 : 0)) * (RB * (D + 2));
-        for (int x = threadIdx.x; x < F4; x += kWarps * 32) {
+        constexpr int PF = RB * (D + 2);  // floats of a part
+        float *const part = p.parts + (2 * uint64_t(blockIdx.x) + (seg_a == 0 ? 1 : 0)) * PF;
+        const int f4 = min(rows - r0, RB) * (D / 4);  // of rows that there are
+        for (int x = threadIdx.x; x < f4; x += kWarps * 32) {
             const int row = x / (D / 4), c = x % (D / 4);
             float m = -INFINITY;
 #pragma unroll
@@ -517,17 +621,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             float l = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < kWarps; k++) {
-                const float fw = exp2_fast(w_m[k][row] - m0);
-                const float4 o = reinterpret_cast<const float4 *>(smem + k * ST * kStageBytes<D>)[part_at<D>(row, c)];
-                l = fmaf(fw, w_l[k][row], l);
-                acc.x = fmaf(fw, o.x, acc.x);
-                acc.y = fmaf(fw, o.y, acc.y);
-                acc.z = fmaf(fw, o.z, acc.z);
-                acc.w = fmaf(fw, o.w, acc.w);
-            }
+            for (int k = 0; k < kWarps; k++)
+                if (k < tiles || k == 0)
+                    join_scaled(l, acc, exp2_fast(w_m[k][row] - m0), w_l[k][row],
+                                reinterpret_cast<const float4 *>(smem + k * ST * kStageBytes<D>)[part_at<D>(row, c)]);
             if (alone) {
-                store_row<D>(p, it, r0 + row, rows, c, acc, m, l);
+                store_row<D>(p, it, r0 + row, c, acc, m, l);
             } else {
                 reinterpret_cast<float4 *>(part)[x] = acc;
                 if (c == 0) {
@@ -546,17 +645,53 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             }
             __syncthreads();
             if (arrived) {
+                // Warp w joins parts f + w, f + w + kWarps, ..., a few in flight;
+                // then the warps' results through shared memory, in their order.
                 __threadfence();
-                for (int x = threadIdx.x; x < F4; x += kWarps * 32) {
-                    const int row = x / (D / 4), c = x % (D / 4);
-                    float m = -INFINITY, l = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (uint32_t k = f; k <= e; k++) {
-                        const float *q = p.parts + (2 * uint64_t(k) + (k == f ? 1 : 0)) * (RB * (D + 2));
-                        join(m, l, acc, __ldcg(q + RB * D + row), __ldcg(q + RB * D + RB + row),
-                             __ldcg(reinterpret_cast<const float4 *>(q) + x));
+                constexpr int N = F4 / 32;
+                float m[N], l[N];
+                float4 acc[N];
+#pragma unroll
+                for (int n = 0; n < N; n++) {
+                    m[n] = -INFINITY;
+                    l[n] = 0.f;
+                    acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll 2
+                for (uint32_t k = f + warp; k <= e; k += kWarps) {
+                    const float *q = p.parts + (2 * uint64_t(k) + (k == f ? 1 : 0)) * PF;
+#pragma unroll
+                    for (int n = 0; n < N; n++) {
+                        const int x = n * 32 + lane, row = x / (D / 4);
+                        if (x < f4)
+                            join(m[n], l[n], acc[n], __ldcg(q + RB * D + row), __ldcg(q + RB * D + RB + row),
+                                 __ldcg(reinterpret_cast<const float4 *>(q) + x));
                     }
-                    store_row<D>(p, it, r0 + row, rows, c, acc, m, l);
+                }
+                float4 *const mine_o = reinterpret_cast<float4 *>(ring);
+#pragma unroll
+                for (int n = 0; n < N; n++) {
+                    const int x = n * 32 + lane, row = x / (D / 4);
+                    mine_o[x] = acc[n];
+                    if (x % (D / 4) == 0) {
+                        w_m[warp][row] = m[n];
+                        w_l[warp][row] = l[n];
+                    }
+                }
+                __syncthreads();
+                for (int x = threadIdx.x; x < f4; x += kWarps * 32) {
+                    const int row = x / (D / 4), c = x % (D / 4);
+                    float mt = -INFINITY, lt = 0.f;
+                    float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < kWarps; k++)
+                        mt = fmaxf(mt, w_m[k][row]);
+                    const float m0 = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+                    for (int k = 0; k < kWarps; k++)
+                        join_scaled(lt, ot, exp2_fast(w_m[k][row] - m0), w_l[k][row],
+                                    reinterpret_cast<const float4 *>(smem + k * ST * kStageBytes<D>)[x]);
+                    store_row<D>(p, it, r0 + row, c, ot, mt, lt);
                 }
             }
         }
@@ -580,12 +715,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kDup>
 uw_status launch(const AttnParams &p, int ctas, cudaStream_t st) {
     constexpr size_t smem = size_t(kWarps) * kStages<D> * kStageBytes<D>;
-    if (!ensure_smem(kv4_decode_kernel<D, NT>, smem))
+    if (!ensure_smem(kv4_decode_kernel<D, NT, kDup>, smem))
         return UW_ERR_CUDA;
-    return launch_overlapped(kv4_decode_kernel<D, NT>, dim3(unsigned(ctas)), dim3(kWarps * 32), smem, st, p) ==
+    return launch_overlapped(kv4_decode_kernel<D, NT, kDup>, dim3(unsigned(ctas)), dim3(kWarps * 32), smem, st, p) ==
                    cudaSuccess
                ? UW_OK
                : UW_ERR_CUDA;
@@ -597,17 +732,15 @@ int kv4_decode_ctas() { return 2 * sm_count(); }
 
 size_t kv4_decode_part_floats(int head_dim) { return 2 * size_t(kv4_decode_ctas()) * 16 * (head_dim + 2); }
 
-// Eight rows a tile where no sequence has more (one new token of up to eight
-// heads a group), sixteen otherwise.
 uw_status launch_kv4_decode(const AttnParams &p, int head_dim, int64_t rows, int64_t max_units, cudaStream_t st) {
-    const bool wide = rows == 0 || rows > 8;
+    const bool dup = rows > 0 && rows <= 4, wide = rows == 0 || rows > 8;
     int64_t ctas = wide ? kv4_decode_ctas() / 2 : kv4_decode_ctas();
     if (max_units > 0)
         ctas = std::min(ctas, max_units);
     const int n = int(ctas);
     if (head_dim == 128)
-        return wide ? launch<128, 2>(p, n, st) : launch<128, 1>(p, n, st);
-    return wide ? launch<64, 2>(p, n, st) : launch<64, 1>(p, n, st);
+        return wide ? launch<128, 2, false>(p, n, st) : dup ? launch<128, 1, true>(p, n, st) : launch<128, 1, false>(p, n, st);
+    return wide ? launch<64, 2, false>(p, n, st) : dup ? launch<64, 1, true>(p, n, st) : launch<64, 1, false>(p, n, st);
 }
 
 }  // namespace uw
