@@ -5,7 +5,7 @@
 // An item is one (sequence, kv head, row tile): the rows of the tile are the
 // new tokens' query heads that read this kv head, row r = token r / group,
 // head r % group.  Its units are the key tiles that its rows can see, in
-// order (one unit, with no key in it, for an item that sees none).  All items'
+// order, and a few more for what an item costs however short it is.  All items'
 // units in a row (sequence by sequence, head by head, tile by tile) are cut
 // into gridDim.x shares of equal length, so that any mix of lengths fills the
 // GPU.  Every CTA finds its share from the lengths on the device: nothing is
@@ -59,7 +59,7 @@ struct Found {
     Seq q;
 };
 
-template <int RB, int T>  // rows of a row tile, keys of a unit
+template <int RB, int T, int kCost>  // rows of a row tile, keys of a unit, units an item costs beyond its tiles
 struct Sched {
     static __device__ __forceinline__ bool mine(const AttnParams &p, const Seq &s) {
         const int32_t rows = s.n * p.group;
@@ -73,7 +73,7 @@ struct Sched {
         return visible(p, s, r0 / p.group, r1 / p.group);
     }
     static __device__ __forceinline__ uint32_t units(const KeyRange &k) {
-        return k.hi > k.lo ? uint32_t((k.hi - 1) / T - k.lo / T + 1) : 1u;
+        return kCost + (k.hi > k.lo ? uint32_t((k.hi - 1) / T - k.lo / T + 1) : 0u);
     }
     // Units of one head of a sequence.
     static __device__ __forceinline__ uint64_t seq_units(const AttnParams &p, const Seq &s) {
@@ -182,12 +182,13 @@ __device__ __forceinline__ void join_scaled(float &l, float4 &o, float f, float 
     o.w = fmaf(f, o2.w, o.w);
 }
 
-// Four dimensions (4c ..) of row r of an item: out = o / l, and with c = 0 the lse.
+// Four dimensions (4c ..) of row r of the items of a sequence (first token t0)
+// and kv head: out = o / l, and with c = 0 the lse.
 template <int D>
-__device__ __forceinline__ void store_row(const AttnParams &p, const Item &it, int r, int c, float4 o, float m,
+__device__ __forceinline__ void store_row(const AttnParams &p, int t0, int kv_head, int r, int c, float4 o, float m,
                                           float l) {
     const int i = r / p.group;
-    const int64_t tok = it.q.t0 + i, head = it.head * p.group + (r - i * p.group);
+    const int64_t tok = t0 + i, head = kv_head * p.group + (r - i * p.group);
     const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: o is 0 and stays 0
     *reinterpret_cast<uint2 *>(p.o.p + tok * p.o.ts + head * p.o.hs + 4 * c) =
         make_uint2(bf16_pack(o.x * inv, o.y * inv), bf16_pack(o.z * inv, o.w * inv));

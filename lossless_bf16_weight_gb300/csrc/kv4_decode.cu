@@ -12,15 +12,13 @@
 // more than one and the codes are the A operand straight from shared memory
 // registers; tcgen05 would pad the rows to 64 or 128 and needs its operands
 // written out as BF16.
-//   S^T = K Q^T   a code c becomes BF16 16 + c by one logic operation (its
-//                 bits are the upper mantissa bits of 16), and the scale and
-//                 offset of a key are applied to the fp32 product:
-//                 q.k = s (sum q (16 + c)) + (lo - 16 s) sum q.  Exact but for
+//   S^T = K Q^T   a code is a BF16 as it stands (see Codes: one logic operation
+//                 for two), and the scale and offset of a key are applied to
+//                 the fp32 product: q.k = s sum q c + lo sum q.  Exact but for
 //                 fp32 sums: no rounded K.
-//   O^T = V^T P^T a code becomes c - 8 (one subtraction more: with an offset in
-//                 place the sum over many keys would lose digits to it), the
-//                 scale goes into the probability, p s, and the middle of the
-//                 range into a sum of its own:
+//   O^T = V^T P^T a code becomes c - 8 (one subtraction more: the sum over many
+//                 keys would lose digits to the offset), the scale goes into the
+//                 probability, p s, and the middle of the range into a sum of its own:
 //                 o = sum (p s)(c - 8) + sum p (lo + 8 s).  p s is taken
 //                 as the sum of two BF16, a rounding and its rest, so that the
 //                 result is exact to about 2^-16 before its own rounding.  Up
@@ -44,7 +42,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTile = 32;            // keys of a unit
 constexpr float kRaise = 24.f;       // log2 headroom of a probability
-constexpr uint32_t kWholeUnits = 32; // items up to this many units are not cut while shares are short
+constexpr int kItemCost = 8;         // what an item costs beyond its tiles, in tiles (its join, a partly used round)
+constexpr uint32_t kWholeUnits = 32 + kItemCost;  // items up to this many units are not cut while shares are short
 
 template <int D>
 constexpr int kStageBytes = kTile * (D + 8);
@@ -52,16 +51,10 @@ template <int D>
 constexpr int kStages = D == 128 ? 3 : 5;
 
 // A value the compiler does not know, so that it stays in a register: the
-// logic operations below take their masks from registers (one instruction
-// holds one constant, and two constants would make it two).
+// logic operations below take their masks from registers.
 __device__ __forceinline__ uint32_t opaque(uint32_t v) {
     uint32_t r;
     asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
     return r;
 }
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
@@ -69,20 +62,31 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t mul2_bf16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
-// Codes as pairs of BF16, by one logic operation each: the bits of a code are
-// the upper four of the seven mantissa bits at 2^4 (codes in bits 3..6 of both
-// halves) or the lower four at 2^7 (bits 0..3).
+// Codes as pairs of BF16: bits 0..7 of a BF16 on their own are the integer n
+// they spell, times 2^-133 (subnormal below 128, the first normal binade
+// from there).  So a code in bits 0..3 of a half is c, one in bits 4..7 is 16 c,
+// in units of 2^-133, with no shift and no conversion; the queries and
+// probabilities they meet are scaled up by kQUp and kPUp.
 struct Codes {
-    uint32_t mask3 = opaque(0x00780078u), one3 = opaque(0x41804180u);
-    uint32_t mask0 = opaque(0x000f000fu), one0 = opaque(0x43004300u);
-    uint32_t mid3 = opaque(0x41c041c0u), mid0 = opaque(0x43084308u);  // 24, 136
-    // 16 + c
-    __device__ __forceinline__ uint32_t key3(uint32_t w) const { return and_or(w, mask3, one3); }
-    // c - 8 (exact)
-    __device__ __forceinline__ uint32_t value3(uint32_t w) const { return sub2(and_or(w, mask3, one3), mid3); }
-    __device__ __forceinline__ uint32_t value0(uint32_t w) const { return sub2(and_or(w, mask0, one0), mid0); }
+    uint32_t mask0 = opaque(0x000f000fu), mask4 = opaque(0x00f000f0u);
+    uint32_t mid0 = opaque(0x00080008u), mid4 = opaque(0x00800080u);
+    // c and 16 c
+    __device__ __forceinline__ uint32_t low(uint32_t w) const { return w & mask0; }
+    __device__ __forceinline__ uint32_t high(uint32_t w) const { return w & mask4; }
+    // c - 8 and 16 (c - 8), exact
+    __device__ __forceinline__ uint32_t low_mid(uint32_t w) const { return sub2(w & mask0, mid0); }
+    __device__ __forceinline__ uint32_t high_mid(uint32_t w) const { return sub2(w & mask4, mid4); }
 };
+constexpr uint32_t kQUpLow = 0x57805780u, kQUpHigh = 0x55805580u;  // 2^48, and 2^44 for the codes times 16
+constexpr float kQDown = 3.8685626e25f;                            // 2^85 = 2^133 / 2^48
+constexpr float kPUp = 1.8446744e19f;                              // 2^64
+constexpr float kPDownLow = 5.9029581e20f, kPDownHigh = 3.6893488e19f;  // 2^69 = 2^133 / 2^64, 2^65
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -130,18 +134,94 @@ struct Warp {
     uint64_t qs[NT];         // sum of q
 };
 
+// A CTA's part of one item: tiles first .. first + tiles - 1 (none for an item
+// that sees no key), units [a, b) of its n (the last kItemCost of which are no tiles).
+struct Seg {
+    uint64_t u0;
+    int32_t s, head, rt, t0, tokens, len;
+    int32_t first, tiles;
+    uint32_t a, b, n;
+    int32_t all_lo, all_hi;  // keys that every row sees
+};
+constexpr int kSegs = 32;
+
+// Warp 0 lists the segments from unit u (in item it) up to unit `end`, at most
+// kSegs of them; returns the unit after them and leaves `it` there.  The
+// sequences' lengths are read 32 at a time.
+template <int RB>
+__device__ __forceinline__ uint64_t list_segments(const AttnParams &p, Item &it, uint64_t u, uint64_t end, Seg *segs,
+                                                  int *count) {
+    using S = Sched<RB, kTile, kItemCost>;
+    const int lane = threadIdx.x & 31;
+    int base = it.s, n = 0;
+    Seq next = base + lane < p.v.n_seqs ? kv4_seq(p.v, base + lane) : Seq{0, 0, 0};
+    while (u < end && n < kSegs) {
+        if (lane == 0) {
+            Seg g;
+            const int tiles = it.keys.hi > it.keys.lo ? int(it.n) - kItemCost : 0;
+            g.u0 = it.u0;
+            g.s = it.s;
+            g.head = it.head;
+            g.rt = it.rt;
+            g.t0 = it.q.t0;
+            g.tokens = it.q.n;
+            g.len = it.q.len;
+            g.n = it.n;
+            g.a = uint32_t(u - it.u0);
+            g.b = uint32_t(min(end - it.u0, uint64_t(it.n)));
+            g.first = it.keys.lo / kTile + int(g.a);
+            g.tiles = max(0, min(int(g.b), tiles) - int(g.a));
+            const int r0 = it.rt * RB, r1 = r0 + min(RB, it.q.n * p.group - r0) - 1;
+            const int i0 = r0 / p.group, i1 = r1 / p.group;
+            g.all_lo = visible(p, it.q, i1, i1).lo;
+            g.all_hi = min(visible(p, it.q, i0, i0).hi, it.q.len);
+            segs[n] = g;
+        }
+        n++;
+        u = min(end, it.u0 + it.n);
+        if (u == it.u0 + it.n && u < end) {
+            it.u0 = u;
+            if (++it.rt == S::row_tiles(p, it.q)) {
+                it.rt = 0;
+                if (++it.head == p.v.heads) {
+                    it.head = 0;
+                    do {
+                        if (++it.s - base == 32) {
+                            base = it.s;
+                            next = base + lane < p.v.n_seqs ? kv4_seq(p.v, base + lane) : Seq{0, 0, 0};
+                        }
+                        it.q.t0 = __shfl_sync(0xffffffffu, next.t0, it.s - base);
+                        it.q.n = __shfl_sync(0xffffffffu, next.n, it.s - base);
+                        it.q.len = __shfl_sync(0xffffffffu, next.len, it.s - base);
+                    } while (!S::mine(p, it.q));
+                }
+            }
+            it.keys = S::tile_keys(p, it.q, it.rt);
+            it.n = S::units(it.keys);
+        }
+    }
+    if (lane == 0)
+        *count = n;
+    return u;
+}
+
 // NT groups of eight rows; kDup (NT = 1): up to four rows, which rows 4..7 repeat.
 template <int D, int NT, bool kDup>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kernel(const AttnParams p) {
     static_assert(!kDup || NT == 1, "rows repeated in one group");
     constexpr int RB = kDup ? 4 : 8 * NT;
     constexpr int ST = kStages<D>;
-    using S = Sched<RB, kTile>;
+    using S = Sched<RB, kTile, kItemCost>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t slots[kWarps];
     __shared__ Found found[2];
     __shared__ float w_m[kWarps][RB], w_l[kWarps][RB];
-    __shared__ uint32_t arrived;
+    __shared__ Seg segs[kSegs], pend[2];
+    __shared__ int listed, w_at[kWarps];
+    __shared__ uint64_t listed_to;
+    __shared__ uint32_t arrived[2], from[2], to_part[2];
+    constexpr int F4 = RB * (D / 4);
+    constexpr int PF = RB * (D + 2);  // floats of a part
     grid_dep_launch();
     grid_dep_wait();
     const Kv4View &v = p.v;
@@ -153,10 +233,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     const int per = (v.n_seqs + kWarps * 32 - 1) / (kWarps * 32);
     const int sa = min(int(threadIdx.x) * per, v.n_seqs), sb = min(sa + per, v.n_seqs);
     uint64_t mine = 0;
-    Seq sq{0, 0, 0};
+    Seq seq{0, 0, 0};
     for (int s = sa; s < sb; s++) {
-        sq = kv4_seq(v, s);
-        mine += S::seq_units(p, sq) * v.heads;
+        seq = kv4_seq(v, s);
+        mine += S::seq_units(p, seq) * v.heads;
     }
     uint64_t total;
     const uint64_t before = cta_prefix<kWarps * 32>(mine, slots, &total);
@@ -169,10 +249,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             uint64_t u = before;
             for (int s = sa; s < sb; s++) {
                 if (per > 1)
-                    sq = kv4_seq(v, s);
-                const uint64_t w = S::seq_units(p, sq);
+                    seq = kv4_seq(v, s);
+                const uint64_t w = S::seq_units(p, seq);
                 if (cut[k] < u + w * v.heads) {
-                    found[k] = Found{u, w, s, sq};
+                    found[k] = Found{u, w, s, seq};
                     break;
                 }
                 u += w * v.heads;
@@ -201,7 +281,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     // While a share is at most a tile for each warp, an item of a few tiles
     // a warp is taken whole: a cut through it would cost a round trip through
     // the workspace.
-    const bool whole = total <= uint64_t(kWarps) * gridDim.x;
+    const bool whole = total <= uint64_t(kWarps + kItemCost) * gridDim.x;
     Item it = locate(0);
     if (whole && it.n <= kWholeUnits)
         cut[0] = it.u0;
@@ -210,54 +290,51 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         if (e.n <= kWholeUnits)
             cut[1] = e.u0;
     }
-    const int64_t block = int64_t(D + 8) << v.page_log2;
+    const int64_t block = int64_t(D + 8) << v.page_log2, page_bytes = block * v.heads;
     const int mask = (1 << v.page_log2) - 1;
+    const int v_off = (D / 2) << v.page_log2;
 
-    uint64_t u = cut[0];
-    while (u < cut[1]) {
-        const uint32_t seg_a = uint32_t(u - it.u0), seg_b = uint32_t(min(cut[1] - it.u0, uint64_t(it.n)));
-        const bool some = it.keys.hi > it.keys.lo;
-        const int tiles = some ? int(seg_b - seg_a) : 0;
-        const int first = it.keys.lo / kTile + int(seg_a) + warp;  // this warp's tiles: first, first + kWarps, ...
-        const int n_mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-        const int r0 = it.rt * RB, rows = it.q.n * p.group;
-        // keys that every row of the item sees
-        const int tok_a = r0 / p.group, tok_b = (r0 + min(RB, rows - r0) - 1) / p.group;
-        const KeyRange ka = visible(p, it.q, tok_a, tok_a), kb = visible(p, it.q, tok_b, tok_b);
-        const int all_lo = kb.lo, all_hi = min(ka.hi, it.q.len);
-
-        // A tile's copies.  A tile lies in one page, or (pages of 16) its
-        // halves in two; the lane holds the page of key 16 * (lane / 16).
-        const int32_t *const table = v.table + int64_t(it.s) * v.table_stride;
-        auto page_of = [&](int tile) -> int {
-            const int key = tile * kTile + (lane & 16);
-            if (key >= it.q.len)
-                return -1;
-            const int page = __ldg(table + (key >> v.page_log2));
-            if (uint32_t(page) >= uint64_t(v.n_pages)) {
-                atomicOr(v.status, uint32_t(kStatusBadCache));
-                return -1;
-            }
-            return page;
-        };
-        const uint8_t *const base = v.pages + it.head * block;
-        const int64_t page_bytes = block * v.heads;
-        const int v_off = (D / 2) << v.page_log2;
-        auto issue = [&](int tile, int page, int stage) {
+    // The warp's next tile to copy: segment, tile, and the lane's page (that of
+    // key 16 * (lane / 16) of the tile, which may lie in two pages of 16).  It
+    // runs ahead of the products through all listed segments, so that the
+    // copies go on while a segment is joined.
+    int nx_seg = 0, nx_tile = 0, nx_page = -1, n_segs = 0;
+    auto next_page = [&]() {
+        const Seg &sg = segs[nx_seg];
+        const int key = min(nx_tile * kTile + (lane & 16), sg.len - 1);  // (the first key's where there is no other)
+        nx_page = __ldg(v.table + int64_t(sg.s) * v.table_stride + (key >> v.page_log2));
+    };
+    // From segment nx_seg on, the first one with a tile for this warp.
+    auto next_seg = [&]() {
+        while (nx_seg < n_segs && segs[nx_seg].tiles <= warp)
+            nx_seg++;
+        if (nx_seg < n_segs) {
+            nx_tile = segs[nx_seg].first + warp;
+            next_page();
+        }
+    };
+    auto issue = [&](int stage) {
+        if (nx_seg < n_segs) {
+            const Seg &sg = segs[nx_seg];
             const uint32_t dst = ring_at + stage * kStageBytes<D>;
-            const int key0 = tile * kTile;
+            const int key0 = nx_tile * kTile;
+            const uint8_t *const base = v.pages + sg.head * block;
             constexpr int RC = D / 32;             // 16-byte chunks of a row
             const uint8_t *half[2];                // codes of keys 0..15 and 16..31, the lane's chunk
             int pages[2], slots[2];
+            if (uint32_t(nx_page) >= uint32_t(v.n_pages)) {  // (looked at here, not where it is loaded)
+                atomicOr(v.status, uint32_t(kStatusBadCache));
+                nx_page = -1;
+            }
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                pages[h] = __shfl_sync(0xffffffffu, page, 16 * h);
+                pages[h] = __shfl_sync(0xffffffffu, nx_page, 16 * h);
                 slots[h] = (key0 + 16 * h) & mask;
                 half[h] = base + pages[h] * page_bytes + (slots[h] * (D / 2) + lane * 16);
             }
             const uint32_t to = dst + lane * 16;   // consecutive lanes, consecutive chunks
             const uint32_t vto = dst + kTile * (D / 2) + (lane / RC) * (D / 2) + v_chunk<D>(lane / RC, lane % RC) * 16;
-            const int left = it.q.len - key0;      // keys of the tile that there are
+            const int left = sg.len - key0;        // keys of the tile that there are
             const bool full = left >= kTile && (pages[0] | pages[1]) >= 0;
             if (full) {
 #pragma unroll
@@ -282,17 +359,42 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                                      kv4_params<D>(v.page_log2, (h ? slots[1] : slots[0]) + (r & 15), lane >> 3);
                 cp_async16_zfill(dst + kTile * D + lane * 16, in ? src : v.pages, in ? 16u : 0u);
             }
-        };
-        int page_next = n_mine > 0 ? page_of(first) : -1;
-#pragma unroll
-        for (int s = 0; s < ST - 1; s++) {
-            const int page = page_next;
-            if (s + 1 < n_mine)
-                page_next = page_of(first + (s + 1) * kWarps);
-            if (s < n_mine)
-                issue(first + s * kWarps, page, s);
-            cp_async_commit();
+            nx_tile += kWarps;
+            if (nx_tile - sg.first < sg.tiles) {
+                next_page();
+            } else {
+                nx_seg++;
+                next_seg();
+            }
         }
+        cp_async_commit();
+    };
+
+    const Codes codes;
+    const float c1_up = p.c1 * kQDown;
+    int n_pend = 0;  // parts of cut items, arrived together at the end
+    int stage = 0;   // the ring's next stage to use; the one before it is free
+    uint64_t u = cut[0];
+    while (u < cut[1]) {
+        if (warp == 0) {
+            const uint64_t to = list_segments<RB>(p, it, u, cut[1], segs, &listed);
+            if (lane == 0)
+                listed_to = to;
+        }
+        __syncthreads();
+        u = listed_to;
+        n_segs = listed;
+        nx_seg = 0;
+        next_seg();
+        for (int s = 0; s < ST - 1; s++)
+            issue((stage + s) % ST);
+
+        for (int sgi = 0; sgi < n_segs; sgi++) {
+        const Seg &sg = segs[sgi];
+        const int n_mine = sg.tiles > warp ? (sg.tiles - warp + kWarps - 1) / kWarps : 0;
+        const int r0 = sg.rt * RB, rows = sg.tokens * p.group;
+        const int all_lo = sg.all_lo, all_hi = sg.all_hi;
+        const Seq sq{sg.t0, sg.tokens, sg.len};
 
         Warp<D, NT> w;
         // Queries: lane (g, t) holds row g of each group, dimensions D/4 t .. + D/4 - 1,
@@ -306,7 +408,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                 x[k] = make_uint4(0, 0, 0, 0);
             if (rr < rows - r0 && n_mine > 0) {
                 const int i = (r0 + rr) / p.group;
-                const int64_t tok = it.q.t0 + i, head = it.head * p.group + (r0 + rr - i * p.group);
+                const int64_t tok = sg.t0 + i, head = sg.head * p.group + (r0 + rr - i * p.group);
                 const uint4 *src = reinterpret_cast<const uint4 *>(p.q.p + tok * p.q.ts + head * p.q.hs + (D / 4) * t);
 #pragma unroll
                 for (int k = 0; k < D / 32; k++)
@@ -315,10 +417,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < D / 32; k++) {
-                w.q[nt][2 * k][0] = __byte_perm(x[k].x, x[k].z, 0x5410);
-                w.q[nt][2 * k][1] = __byte_perm(x[k].x, x[k].z, 0x7632);
-                w.q[nt][2 * k + 1][0] = __byte_perm(x[k].y, x[k].w, 0x5410);
-                w.q[nt][2 * k + 1][1] = __byte_perm(x[k].y, x[k].w, 0x7632);
+                w.q[nt][2 * k][0] = mul2_bf16(__byte_perm(x[k].x, x[k].z, 0x5410), kQUpLow);
+                w.q[nt][2 * k][1] = mul2_bf16(__byte_perm(x[k].x, x[k].z, 0x7632), kQUpHigh);
+                w.q[nt][2 * k + 1][0] = mul2_bf16(__byte_perm(x[k].y, x[k].w, 0x5410), kQUpLow);
+                w.q[nt][2 * k + 1][1] = mul2_bf16(__byte_perm(x[k].y, x[k].w, 0x7632), kQUpHigh);
                 const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
                 for (int i = 0; i < 4; i++)
@@ -336,23 +438,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                     w.o[i][nt][k] = 0.f;
         }
 
-        const Codes codes;
-        int stage = 0;
         for (int i = 0; i < n_mine; i++) {
-            {
-                const int nx = i + ST - 1;
-                const int page = page_next;
-                if (nx + 1 < n_mine)
-                    page_next = page_of(first + (nx + 1) * kWarps);
-                if (nx < n_mine)
-                    issue(first + nx * kWarps, page, stage == 0 ? ST - 1 : stage - 1);
-                cp_async_commit();
-            }
+            issue(stage == 0 ? ST - 1 : stage - 1);
             asm volatile("cp.async.wait_group %0;" :: "n"(ST - 1) : "memory");
             __syncwarp();
             const unsigned char *const st = ring + stage * kStageBytes<D>;
             stage = stage + 1 == ST ? 0 : stage + 1;
-            const int key0 = (first + i * kWarps) * kTile;
+            const int key0 = (sg.first + warp + i * kWarps) * kTile;
 
             // scores
             float sc[2][NT][4];
@@ -383,9 +475,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int mt = 0; mt < 2; mt++) {
-                        const uint32_t x = a[mt][0][k], y = a[mt][1][k];
-                        const uint32_t a0 = codes.key3(j ? x >> 5 : x << 3), a1 = codes.key3(j ? y >> 5 : y << 3);
-                        const uint32_t a2 = codes.key3(j ? x >> 9 : x >> 1), a3 = codes.key3(j ? y >> 9 : y >> 1);
+                        const uint32_t x = j ? a[mt][0][k] >> 8 : a[mt][0][k], y = j ? a[mt][1][k] >> 8 : a[mt][1][k];
+                        const uint32_t a0 = codes.low(x), a1 = codes.low(y), a2 = codes.high(x), a3 = codes.high(y);
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++)
                             mma16816(sc[mt][nt], a0, a1, a2, a3, w.q[nt][2 * k + j][0], w.q[nt][2 * k + j][1]);
@@ -404,7 +495,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             auto scores = [&]() {
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const float a = bf16_lo(kpar[j]) * p.c1, c = fmaf(bf16_hi(kpar[j]), p.c1, -16.f * a);
+                    const float a = bf16_lo(kpar[j]) * c1_up, c = bf16_hi(kpar[j]) * p.c1;
                     const uint64_t aa = pair2(a, a), cc = pair2(c, c);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
@@ -419,11 +510,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                         for (int k = 0; k < 2; k++) {
                             const int row = 8 * nt + (kDup ? (2 * t + k) & 3 : 2 * t + k);
                             const int tok = (r0 + min(row, rows - r0 - 1)) / p.group;
-                            const KeyRange kr = visible(p, it.q, tok, tok);
+                            const KeyRange kr = visible(p, sq, tok, tok);
 #pragma unroll
                             for (int j = 0; j < 4; j++) {
                                 const int key = key0 + 8 * j + key_of(g);
-                                in[j][k] = key >= kr.lo && key < min(kr.hi, it.q.len);
+                                in[j][k] = key >= kr.lo && key < min(kr.hi, sq.len);
                             }
                         }
 #pragma unroll
@@ -502,7 +593,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const float s = bf16_lo(vpar[j]), mid = fmaf(8.f, s, bf16_hi(vpar[j]));
+                    const float s = bf16_lo(vpar[j]) * kPUp, mid = fmaf(8.f / kPUp, s, bf16_hi(vpar[j]));
                     const float2 f = unpair(y[j][nt]);
                     const uint64_t pr = pair2(exp2_fast(f.x), exp2_fast(f.y));
                     uint64_t ps = mul2(pr, pair2(s, s));
@@ -549,8 +640,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                     for (int b = 0; b < 4; b++) {
                         const uint32_t sel = b * 0x11u | (4 + b) * 0x1100u;
                         const uint32_t e = __byte_perm(x[0][k], x[1][k], sel), f = __byte_perm(x[2][k], x[3][k], sel);
-                        const uint32_t a0 = codes.value0(e), a1 = codes.value3(e >> 1);
-                        const uint32_t a2 = codes.value0(f), a3 = codes.value3(f >> 1);
+                        const uint32_t a0 = codes.low_mid(e), a1 = codes.high_mid(e);
+                        const uint32_t a2 = codes.low_mid(f), a3 = codes.high_mid(f);
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++) {
                             mma16816(w.o[4 * k + b][nt], a0, a1, a2, a3, hi[mt][nt][0], hi[mt][nt][1]);
@@ -561,11 +652,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             }
             __syncwarp();
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-
         // The warps' parts, joined through shared memory: each warp leaves its
-        // maximum, sum and output (with the ranges' middles added) in its own ring.
-        float4 *const wo = reinterpret_cast<float4 *>(ring);
+        // maximum, sum and output (with the ranges' middles added) in its ring's
+        // free stage (sixteen rows: in an area of their own).
+        unsigned char *const mine_at = NT == 1 ? ring + (stage == 0 ? ST - 1 : stage - 1) * kStageBytes<D>
+                                               : smem + kWarps * ST * kStageBytes<D> + warp * (RB * D * 4);
+        if (lane == 0)
+            w_at[warp] = int(mine_at - smem);
+        float4 *const wo = reinterpret_cast<float4 *>(mine_at);
         __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
@@ -581,8 +675,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                 float o[D / 8];  // dimensions D/8 g .. of row 8 nt + 2 t + k
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) {
-                    o[2 * i] = w.o[i][nt][k];
-                    o[2 * i + 1] = w.o[i][nt][2 + k];
+                    o[2 * i] = w.o[i][nt][k] * kPDownLow;
+                    o[2 * i + 1] = w.o[i][nt][2 + k] * kPDownHigh;
                 }
                 if constexpr (kDup) {  // the rests' products are in the columns four on
 #pragma unroll
@@ -604,12 +698,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         }
         __syncthreads();
 
-        // This part's place among the item's, and the item's output once all are there.
-        const uint32_t f = share_of(it.u0, total, workers), e = share_of(it.u0 + it.n - 1, total, workers);
-        const bool alone = seg_a == 0 && seg_b == it.n;
-        constexpr int F4 = RB * (D / 4);
-        constexpr int PF = RB * (D + 2);  // floats of a part
-        float *const part = p.parts + (2 * uint64_t(blockIdx.x) + (seg_a == 0 ? 1 : 0)) * PF;
+        const bool alone = sg.a == 0 && sg.b == sg.n;
+        float *const part = p.parts + (2 * uint64_t(blockIdx.x) + (sg.a == 0 ? 1 : 0)) * PF;
         const int f4 = min(rows - r0, RB) * (D / 4);  // of rows that there are
         for (int x = threadIdx.x; x < f4; x += kWarps * 32) {
             const int row = x / (D / 4), c = x % (D / 4);
@@ -622,11 +712,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kWarps; k++)
-                if (k < tiles || k == 0)
-                    join_scaled(l, acc, exp2_fast(w_m[k][row] - m0), w_l[k][row],
-                                reinterpret_cast<const float4 *>(smem + k * ST * kStageBytes<D>)[part_at<D>(row, c)]);
+                join_scaled(l, acc, exp2_fast(w_m[k][row] - m0), w_l[k][row],
+                            reinterpret_cast<const float4 *>(smem + w_at[k])[part_at<D>(row, c)]);
             if (alone) {
-                store_row<D>(p, it, r0 + row, c, acc, m, l);
+                store_row<D>(p, sg.t0, sg.head, r0 + row, c, acc, m, l);
             } else {
                 reinterpret_cast<float4 *>(part)[x] = acc;
                 if (c == 0) {
@@ -636,88 +725,93 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             }
         }
         if (!alone) {
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                arrived = atomicAdd(p.counters + f, 1u) == e - f;
-                if (arrived)
-                    p.counters[f] = 0;  // ready for the next call
-            }
-            __syncthreads();
-            if (arrived) {
-                // Warp w joins parts f + w, f + w + kWarps, ..., a few in flight;
-                // then the warps' results through shared memory, in their order.
-                __threadfence();
-                constexpr int N = F4 / 32;
-                float m[N], l[N];
-                float4 acc[N];
-#pragma unroll
-                for (int n = 0; n < N; n++) {
-                    m[n] = -INFINITY;
-                    l[n] = 0.f;
-                    acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll 2
-                for (uint32_t k = f + warp; k <= e; k += kWarps) {
-                    const float *q = p.parts + (2 * uint64_t(k) + (k == f ? 1 : 0)) * PF;
-#pragma unroll
-                    for (int n = 0; n < N; n++) {
-                        const int x = n * 32 + lane, row = x / (D / 4);
-                        if (x < f4)
-                            join(m[n], l[n], acc[n], __ldcg(q + RB * D + row), __ldcg(q + RB * D + RB + row),
-                                 __ldcg(reinterpret_cast<const float4 *>(q) + x));
-                    }
-                }
-                float4 *const mine_o = reinterpret_cast<float4 *>(ring);
-#pragma unroll
-                for (int n = 0; n < N; n++) {
-                    const int x = n * 32 + lane, row = x / (D / 4);
-                    mine_o[x] = acc[n];
-                    if (x % (D / 4) == 0) {
-                        w_m[warp][row] = m[n];
-                        w_l[warp][row] = l[n];
-                    }
-                }
-                __syncthreads();
-                for (int x = threadIdx.x; x < f4; x += kWarps * 32) {
-                    const int row = x / (D / 4), c = x % (D / 4);
-                    float mt = -INFINITY, lt = 0.f;
-                    float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int k = 0; k < kWarps; k++)
-                        mt = fmaxf(mt, w_m[k][row]);
-                    const float m0 = mt == -INFINITY ? 0.f : mt;
-#pragma unroll
-                    for (int k = 0; k < kWarps; k++)
-                        join_scaled(lt, ot, exp2_fast(w_m[k][row] - m0), w_l[k][row],
-                                    reinterpret_cast<const float4 *>(smem + k * ST * kStageBytes<D>)[x]);
-                    store_row<D>(p, it, r0 + row, c, ot, mt, lt);
-                }
-            }
+            if (threadIdx.x == 0)
+                pend[n_pend] = sg;
+            n_pend++;
         }
-        __syncthreads();  // the rings are free again
+        __syncthreads();  // the free stages are free again
+        }
+    }
+    if (n_pend == 0)
+        return;
 
-        u += seg_b - seg_a;
-        if (u < cut[1]) {
-            it.u0 += it.n;
-            if (++it.rt == S::row_tiles(p, it.q)) {
-                it.rt = 0;
-                if (++it.head == v.heads) {
-                    it.head = 0;
-                    do
-                        it.q = kv4_seq(v, ++it.s);
-                    while (!S::mine(p, it.q));
-                }
-            }
-            it.keys = S::tile_keys(p, it.q, it.rt);
-            it.n = S::units(it.keys);
+    // The cut items of this share (at most two): whoever arrives last joins the
+    // parts.  Warp w joins parts f + w, f + w + kWarps, ..., a few in flight; then
+    // the warps' results through shared memory, in their order.
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < n_pend) {
+        const Seg &sg = pend[threadIdx.x];
+        const uint32_t f = share_of(sg.u0, total, workers), e = share_of(sg.u0 + sg.n - 1, total, workers);
+        const bool last = atomicAdd(p.counters + f, 1u) == e - f;
+        if (last)
+            p.counters[f] = 0;  // ready for the next call
+        arrived[threadIdx.x] = last;
+        from[threadIdx.x] = f;
+        to_part[threadIdx.x] = e;
+    }
+    __syncthreads();
+    for (int k = 0; k < n_pend; k++) {
+        if (!arrived[k])
+            continue;
+        __threadfence();
+        const Seg &sg = pend[k];
+        const uint32_t f = from[k], e = to_part[k];
+        const int r0 = sg.rt * RB;
+        const int f4 = min(sg.tokens * p.group - r0, RB) * (D / 4);
+        constexpr int N = F4 / 32;
+        float m[N], l[N];
+        float4 acc[N];
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            m[n] = -INFINITY;
+            l[n] = 0.f;
+            acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+#pragma unroll 2
+        for (uint32_t x0 = f + warp; x0 <= e; x0 += kWarps) {
+            const float *q = p.parts + (2 * uint64_t(x0) + (x0 == f ? 1 : 0)) * PF;
+#pragma unroll
+            for (int n = 0; n < N; n++) {
+                const int x = n * 32 + lane, row = x / (D / 4);
+                if (x < f4)
+                    join(m[n], l[n], acc[n], __ldcg(q + RB * D + row), __ldcg(q + RB * D + RB + row),
+                         __ldcg(reinterpret_cast<const float4 *>(q) + x));
+            }
+        }
+        float4 *const mine_o = reinterpret_cast<float4 *>(ring);
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const int x = n * 32 + lane, row = x / (D / 4);
+            mine_o[x] = acc[n];
+            if (x % (D / 4) == 0) {
+                w_m[warp][row] = m[n];
+                w_l[warp][row] = l[n];
+            }
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < f4; x += kWarps * 32) {
+            const int row = x / (D / 4), c = x % (D / 4);
+            float mt = -INFINITY, lt = 0.f;
+            float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; w++)
+                mt = fmaxf(mt, w_m[w][row]);
+            const float m0 = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++)
+                join_scaled(lt, ot, exp2_fast(w_m[w][row] - m0), w_l[w][row],
+                            reinterpret_cast<const float4 *>(smem + w * ST * kStageBytes<D>)[x]);
+            store_row<D>(p, sg.t0, sg.head, r0 + row, c, ot, mt, lt);
+        }
+        __syncthreads();
     }
 }
 
 template <int D, int NT, bool kDup>
 uw_status launch(const AttnParams &p, int ctas, cudaStream_t st) {
-    constexpr size_t smem = size_t(kWarps) * kStages<D> * kStageBytes<D>;
+    constexpr size_t smem = size_t(kWarps) * (kStages<D> * kStageBytes<D> + (NT == 1 ? 0 : 8 * NT * D * 4));
     if (!ensure_smem(kv4_decode_kernel<D, NT, kDup>, smem))
         return UW_ERR_CUDA;
     return launch_overlapped(kv4_decode_kernel<D, NT, kDup>, dim3(unsigned(ctas)), dim3(kWarps * 32), smem, st, p) ==
