@@ -113,6 +113,7 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
     p.c1 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(float(c->head_dim))) * 1.44269504089f;
     p.q_heads = q_heads;
     p.group = q_heads / c->kv_heads;
+    p.by_group = Divisor(uint32_t(p.group));
     p.causal = causal != 0;
     p.window = window;
     p.rows_min = 0;

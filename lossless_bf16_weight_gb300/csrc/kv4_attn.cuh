@@ -1,4 +1,4 @@
-// What the two attention kernels over the 4-bit paged cache share: their
+// What the attention kernels over the 4-bit paged cache share: their
 // parameters, the cut of the work into equal shares, and the joining of the
 // shares of one item.
 //
@@ -7,19 +7,31 @@
 // head r % group.  Its units are the key tiles that its rows can see, in
 // order, and a few more for what an item costs however short it is.  All items'
 // units in a row (sequence by sequence, head by head, tile by tile) are cut
-// into gridDim.x shares of equal length, so that any mix of lengths fills the
-// GPU.  Every CTA finds its share from the lengths on the device: nothing is
-// planned on the host and a captured launch replays with other lengths.
+// into shares of equal length, so that any mix of lengths fills the GPU.  Every
+// CTA finds its share from the lengths on the device: nothing is planned on
+// the host and a captured launch replays with other lengths.
 //
 // An item that lies in several shares is joined by the CTA that finishes last:
 // each part leaves its unnormalised output, maximum and sum in the workspace,
 // and the parts are added in their order, so the same call gives the same
-// bits whichever CTA joins.  A CTA has at most two parts of such items (the
-// end of one that began before, the beginning of one that goes on): two slots.
+// bits whichever CTA joins.  A share has at most two parts of such items (the
+// end of one that began before, the beginning of one that goes on).
 #pragma once
 #include "kv4.cuh"
 
 namespace uw {
+
+// Division by a number that the host knows: n / d for 0 <= n < 2^31 as
+// n * ceil(2^(31 + s) / d) >> (31 + s) with 2^s >= d.
+struct Divisor {
+    uint32_t d, mul, shift;
+    explicit Divisor(uint32_t d = 1) : d(d), shift(31) {
+        while ((1ull << (shift - 31)) < d)
+            shift++;
+        mul = uint32_t(((1ull << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ int of(int n) const { return int((uint64_t(uint32_t(n)) * mul) >> shift); }
+};
 
 struct AttnParams {
     Kv4View v;
@@ -27,8 +39,9 @@ struct AttnParams {
     float *lse;
     float c1;                 // softmax scale * log2(e)
     int32_t q_heads, group, causal, window;
+    Divisor by_group;
     int32_t rows_min, rows_max;  // sequences with rows (new * group) in this range are this launch's
-    float *parts;             // [2 * gridDim.x][RB * (D + 2)]: output, maximum, sum
+    float *parts;             // parts of RB * (D + 2) floats: output, maximum, sum
     uint32_t *counters;       // [gridDim.x], left at zero
 };
 
@@ -48,15 +61,9 @@ struct Item {
     int s, head, rt;
     Seq q;
     KeyRange keys;
-    uint64_t u0;   // its first unit
-    uint32_t n;    // its units
-};
-
-// The sequence that holds a cut: its first unit and the units of one head.
-struct Found {
-    uint64_t base, per_head;
-    int32_t s;
-    Seq q;
+    uint64_t u0;     // its first unit
+    uint32_t tiles;  // its key tiles: the first of its units
+    uint32_t n;      // its units
 };
 
 template <int RB, int T, int kCost>  // rows of a row tile, keys of a unit, units an item costs beyond its tiles
@@ -70,10 +77,10 @@ struct Sched {
     }
     static __device__ __forceinline__ KeyRange tile_keys(const AttnParams &p, const Seq &s, int rt) {
         const int32_t r0 = rt * RB, r1 = r0 + min(RB, s.n * p.group - r0) - 1;
-        return visible(p, s, r0 / p.group, r1 / p.group);
+        return visible(p, s, p.by_group.of(r0), p.by_group.of(r1));
     }
-    static __device__ __forceinline__ uint32_t units(const KeyRange &k) {
-        return kCost + (k.hi > k.lo ? uint32_t((k.hi - 1) / T - k.lo / T + 1) : 0u);
+    static __device__ __forceinline__ uint32_t tiles(const KeyRange &k) {
+        return k.hi > k.lo ? uint32_t((k.hi - 1) / T - k.lo / T + 1) : 0u;
     }
     // Units of one head of a sequence.
     static __device__ __forceinline__ uint64_t seq_units(const AttnParams &p, const Seq &s) {
@@ -82,16 +89,37 @@ struct Sched {
         uint64_t n = 0;
         const int rts = row_tiles(p, s);
         for (int rt = 0; rt < rts; rt++)
-            n += units(tile_keys(p, s, rt));
+            n += kCost + tiles(tile_keys(p, s, rt));
         return n;
+    }
+    static __device__ __forceinline__ void set_tile(const AttnParams &p, Item &it, int rt) {
+        it.rt = rt;
+        it.keys = tile_keys(p, it.q, rt);
+        it.tiles = tiles(it.keys);
+        it.n = kCost + it.tiles;
     }
 };
 
-// Units before each thread's block of sequences, over the CTA (kThreads
-// threads, all of them call); `total` = all units.
+// The row of units as a CTA of kThreads threads sees it: thread i stands for
+// the sequences [i * per, (i + 1) * per), before[i] units come before them.
 template <int kThreads>
-__device__ __forceinline__ uint64_t cta_prefix(uint64_t mine, uint64_t *slots, uint64_t *total) {
+struct Row {
+    uint64_t before[kThreads], sums[kThreads / 32];
+    Seq seq[kThreads];  // with per = 1: the sequence
+};
+
+// Fills the row (all threads call); returns all units.
+template <class S, int kThreads>
+__device__ __forceinline__ uint64_t build_row(const AttnParams &p, Row<kThreads> &row) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (p.v.n_seqs + kThreads - 1) / kThreads;
+    const int a = min(int(threadIdx.x) * per, p.v.n_seqs), b = min(a + per, p.v.n_seqs);
+    uint64_t mine = 0;
+    for (int s = a; s < b; s++) {
+        const Seq q = kv4_seq(p.v, s);
+        mine += S::seq_units(p, q) * p.v.heads;
+        row.seq[threadIdx.x] = q;
+    }
     uint64_t v = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -100,18 +128,18 @@ __device__ __forceinline__ uint64_t cta_prefix(uint64_t mine, uint64_t *slots, u
             v += u;
     }
     if (lane == 31)
-        slots[warp] = v;
+        row.sums[warp] = v;
     __syncthreads();
-    uint64_t before = 0, all = 0;
+    uint64_t before = v - mine, all = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; w++) {
-        const uint64_t t = slots[w];
+        const uint64_t t = row.sums[w];
         before += w < warp ? t : 0;
         all += t;
     }
+    row.before[threadIdx.x] = before;
     __syncthreads();
-    *total = all;
-    return before + v - mine;
+    return all;
 }
 
 // a * b / c and a / b, in 32 bits where they fit (a 64-bit division is a
@@ -122,6 +150,44 @@ __device__ __forceinline__ uint64_t mul_div(uint64_t a, uint32_t b, uint32_t c) 
 }
 __device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
     return ((a | b) >> 32) == 0 ? uint32_t(a) / uint32_t(b) : a / b;
+}
+
+// The item that holds unit u (of fewer than all); a warp calls.
+template <class S, int kThreads>
+__device__ __forceinline__ Item locate(const AttnParams &p, const Row<kThreads> &row, uint64_t u) {
+    const int lane = threadIdx.x & 31;
+    const int per = (p.v.n_seqs + kThreads - 1) / kThreads;
+    int i = -1;  // the last thread with before <= u
+#pragma unroll 1
+    for (int k = 0; k < kThreads / 32 && 32 * k * per < p.v.n_seqs; k++)
+        i += __popc(__ballot_sync(0xffffffffu, row.before[32 * k + lane] <= u));
+    Item it;
+    it.s = i * per;
+    uint64_t rest = u - row.before[i], per_head;
+    it.u0 = row.before[i];
+    if (per == 1) {
+        it.q = row.seq[i];
+        per_head = S::seq_units(p, it.q);
+    } else {
+        for (;; it.s++) {
+            it.q = kv4_seq(p.v, it.s);
+            per_head = S::seq_units(p, it.q);
+            if (rest < per_head * p.v.heads)
+                break;
+            rest -= per_head * p.v.heads;
+            it.u0 += per_head * p.v.heads;
+        }
+    }
+    it.head = int(divide(rest, per_head));
+    rest -= it.head * per_head;
+    it.u0 += it.head * per_head;
+    for (int rt = 0;; rt++) {
+        S::set_tile(p, it, rt);
+        if (rest < it.n)
+            return it;
+        rest -= it.n;
+        it.u0 += it.n;
+    }
 }
 
 // The share (of `workers` equal ones) that holds unit u: the last c with
@@ -187,12 +253,29 @@ __device__ __forceinline__ void join_scaled(float &l, float4 &o, float f, float 
 template <int D>
 __device__ __forceinline__ void store_row(const AttnParams &p, int t0, int kv_head, int r, int c, float4 o, float m,
                                           float l) {
-    const int i = r / p.group;
+    const int i = p.by_group.of(r);
     const int64_t tok = t0 + i, head = kv_head * p.group + (r - i * p.group);
     const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: o is 0 and stays 0
     *reinterpret_cast<uint2 *>(p.o.p + tok * p.o.ts + head * p.o.hs + 4 * c) =
         make_uint2(bf16_pack(o.x * inv, o.y * inv), bf16_pack(o.z * inv, o.w * inv));
     if (p.lse && c == 0)
+        p.lse[tok * p.q_heads + head] = l == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(l));
+}
+
+// The same for N dimensions from d0 on.
+template <int N>
+__device__ __forceinline__ void store_dims(const AttnParams &p, int t0, int kv_head, int r, int d0, const float (&o)[N],
+                                           float m, float l) {
+    const int i = p.by_group.of(r);
+    const int64_t tok = t0 + i, head = kv_head * p.group + (r - i * p.group);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint4 *const dst = reinterpret_cast<uint4 *>(p.o.p + tok * p.o.ts + head * p.o.hs + d0);
+#pragma unroll
+    for (int k = 0; k < N / 8; k++)
+        dst[k] = make_uint4(bf16_pack(o[8 * k] * inv, o[8 * k + 1] * inv), bf16_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                            bf16_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                            bf16_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+    if (p.lse && d0 == 0)
         p.lse[tok * p.q_heads + head] = l == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(l));
 }
 

@@ -3,9 +3,11 @@
 //
 // Bound by memory: every cached vector is read once for all rows that share
 // it, D / 2 + 4 bytes.  A CTA of eight warps takes an equal share of all key
-// tiles (kv4_attn.cuh); in it a warp takes every eighth tile of 32 keys and
-// keeps a ring of tiles in flight by itself (cp.async, no CTA barrier), so
-// that about 100 KB an SM are on their way.
+// tiles (kv4_attn.cuh), and each of its warps an equal share of that, which it
+// works through by itself: a ring of tiles in flight (cp.async) runs on from
+// item to item, an item that lies in one warp's share is written out by that
+// warp, and only the items that the cuts between warps and CTAs go through
+// are joined at the end, first in the CTA, then through the workspace.
 //
 // The products run on mma.sync.m16n8k16 with keys (and dimensions) on the
 // 16-row side and 8 rows of queries on the other, so that 8 rows cost no
@@ -42,8 +44,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTile = 32;            // keys of a unit
 constexpr float kRaise = 24.f;       // log2 headroom of a probability
-constexpr int kItemCost = 8;         // what an item costs beyond its tiles, in tiles (its join, a partly used round)
-constexpr uint32_t kWholeUnits = 32 + kItemCost;  // items up to this many units are not cut while shares are short
+constexpr int kItemCost = 1;         // what an item costs a warp beyond its tiles, in tiles
+constexpr uint32_t kWholeTiles = 32; // items up to this many tiles are not cut between CTAs while shares are short
 
 template <int D>
 constexpr int kStageBytes = kTile * (D + 8);
@@ -116,14 +118,6 @@ __device__ __forceinline__ int v_chunk(int r, int ch) {
     return D == 128 ? ch ^ (((r >> 2) & 1) << 1) : ch;
 }
 
-// Where float4 c of a row lies in a warp's part: the four pairs of rows that
-// are written together exchange their places against bank conflicts.
-template <int D>
-__device__ __forceinline__ int part_at(int row, int c) {
-    constexpr int N = D / 32;
-    return row * (D / 4) + (c ^ (((row & 7) >> 1) & (N - 1)));
-}
-
 template <int D, int NT>
 struct Warp {
     // D/16 pairs of dimensions of the output for 2 rows of each of NT row groups
@@ -134,59 +128,63 @@ struct Warp {
     uint64_t qs[NT];         // sum of q
 };
 
-// A CTA's part of one item: tiles first .. first + tiles - 1 (none for an item
-// that sees no key), units [a, b) of its n (the last kItemCost of which are no tiles).
+// A warp's part of one item: tiles first .. first + tiles - 1.
 struct Seg {
     uint64_t u0;
     int32_t s, head, rt, t0, tokens, len;
-    int32_t first, tiles;
-    uint32_t a, b, n;
-    int32_t all_lo, all_hi;  // keys that every row sees
+    int32_t first, tiles, of;  // `of`: the item's tiles
+    int32_t all_lo, all_hi;    // keys that every row sees
 };
-constexpr int kSegs = 32;
+constexpr int kSegs = 8;
 
-// Warp 0 lists the segments from unit u (in item it) up to unit `end`, at most
-// kSegs of them; returns the unit after them and leaves `it` there.  The
-// sequences' lengths are read 32 at a time.
-template <int RB>
+// The warp lists the segments of the units from u (in item `it`) up to `end`,
+// at most kSegs of them; returns the unit after them and leaves `it` there.
+// An item's last units, which are no tiles, are nobody's; one that sees no
+// key at all is a segment without tiles of the warp that has its first unit.
+// The sequences' lengths are read 32 at a time.
+template <class S, int RB>
 __device__ __forceinline__ uint64_t list_segments(const AttnParams &p, Item &it, uint64_t u, uint64_t end, Seg *segs,
                                                   int *count) {
-    using S = Sched<RB, kTile, kItemCost>;
     const int lane = threadIdx.x & 31;
     int base = it.s, n = 0;
-    Seq next = base + lane < p.v.n_seqs ? kv4_seq(p.v, base + lane) : Seq{0, 0, 0};
+    Seq next{0, 0, 0};
+    bool loaded = false;
     while (u < end && n < kSegs) {
-        if (lane == 0) {
-            Seg g;
-            const int tiles = it.keys.hi > it.keys.lo ? int(it.n) - kItemCost : 0;
-            g.u0 = it.u0;
-            g.s = it.s;
-            g.head = it.head;
-            g.rt = it.rt;
-            g.t0 = it.q.t0;
-            g.tokens = it.q.n;
-            g.len = it.q.len;
-            g.n = it.n;
-            g.a = uint32_t(u - it.u0);
-            g.b = uint32_t(min(end - it.u0, uint64_t(it.n)));
-            g.first = it.keys.lo / kTile + int(g.a);
-            g.tiles = max(0, min(int(g.b), tiles) - int(g.a));
-            const int r0 = it.rt * RB, r1 = r0 + min(RB, it.q.n * p.group - r0) - 1;
-            const int i0 = r0 / p.group, i1 = r1 / p.group;
-            g.all_lo = visible(p, it.q, i1, i1).lo;
-            g.all_hi = min(visible(p, it.q, i0, i0).hi, it.q.len);
-            segs[n] = g;
+        const uint32_t a = uint32_t(u - it.u0), b = uint32_t(min(end - it.u0, uint64_t(it.n)));
+        const int tiles = int(min(b, it.tiles)) - int(a);
+        if (tiles > 0 || (it.tiles == 0 && a == 0)) {
+            if (lane == 0) {
+                Seg g;
+                g.u0 = it.u0;
+                g.s = it.s;
+                g.head = it.head;
+                g.rt = it.rt;
+                g.t0 = it.q.t0;
+                g.tokens = it.q.n;
+                g.len = it.q.len;
+                g.first = it.keys.lo / kTile + int(a);
+                g.tiles = max(tiles, 0);
+                g.of = int(it.tiles);
+                const int r0 = it.rt * RB, r1 = r0 + min(RB, it.q.n * p.group - r0) - 1;
+                const int i0 = p.by_group.of(r0), i1 = p.by_group.of(r1);
+                g.all_lo = visible(p, it.q, i1, i1).lo;
+                g.all_hi = min(visible(p, it.q, i0, i0).hi, it.q.len);
+                segs[n] = g;
+            }
+            n++;
         }
-        n++;
-        u = min(end, it.u0 + it.n);
-        if (u == it.u0 + it.n && u < end) {
+        u = it.u0 + b;
+        if (u < end) {  // the next item
             it.u0 = u;
-            if (++it.rt == S::row_tiles(p, it.q)) {
-                it.rt = 0;
+            int rt = it.rt + 1;
+            if (rt == S::row_tiles(p, it.q)) {
+                rt = 0;
                 if (++it.head == p.v.heads) {
                     it.head = 0;
                     do {
-                        if (++it.s - base == 32) {
+                        if (!loaded || ++it.s - base == 32) {
+                            it.s += loaded ? 0 : 1;
+                            loaded = true;
                             base = it.s;
                             next = base + lane < p.v.n_seqs ? kv4_seq(p.v, base + lane) : Seq{0, 0, 0};
                         }
@@ -196,14 +194,20 @@ __device__ __forceinline__ uint64_t list_segments(const AttnParams &p, Item &it,
                     } while (!S::mine(p, it.q));
                 }
             }
-            it.keys = S::tile_keys(p, it.q, it.rt);
-            it.n = S::units(it.keys);
+            S::set_tile(p, it, rt);
         }
     }
-    if (lane == 0)
-        *count = n;
+    *count = n;
+    __syncwarp();
     return u;
 }
+
+// A part of an item that waits to be joined.
+struct Part {
+    const float *at;  // its floats; null: none
+    uint64_t u0;
+    int32_t rt, t0, tokens, head, tiles, of;
+};
 
 // NT groups of eight rows; kDup (NT = 1): up to four rows, which rows 4..7 repeat.
 template <int D, int NT, bool kDup>
@@ -211,110 +215,65 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     static_assert(!kDup || NT == 1, "rows repeated in one group");
     constexpr int RB = kDup ? 4 : 8 * NT;
     constexpr int ST = kStages<D>;
+    constexpr int PF = RB * (D + 2);  // floats of a part
     using S = Sched<RB, kTile, kItemCost>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t slots[kWarps];
-    __shared__ Found found[2];
-    __shared__ float w_m[kWarps][RB], w_l[kWarps][RB];
-    __shared__ Seg segs[kSegs], pend[2];
-    __shared__ int listed, w_at[kWarps];
-    __shared__ uint64_t listed_to;
+    __shared__ Row<kWarps * 32> row_of_units;
+    __shared__ Seg all_segs[kWarps][kSegs];
+    __shared__ Part parts[2 * kWarps], pend[2];
+    __shared__ float row_m[RB], row_l[RB];
     __shared__ uint32_t arrived[2], from[2], to_part[2];
-    constexpr int F4 = RB * (D / 4);
-    constexpr int PF = RB * (D + 2);  // floats of a part
     grid_dep_launch();
     grid_dep_wait();
     const Kv4View &v = p.v;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     unsigned char *const ring = smem + warp * ST * kStageBytes<D>;
     const uint32_t ring_at = smem_addr(ring);
+    if (lane < 2)
+        parts[2 * warp + lane].at = nullptr;
+    if (threadIdx.x < 2)
+        pend[threadIdx.x].at = nullptr;
 
-    // this CTA's share [cut 0, cut 1) of the units, and where it begins
-    const int per = (v.n_seqs + kWarps * 32 - 1) / (kWarps * 32);
-    const int sa = min(int(threadIdx.x) * per, v.n_seqs), sb = min(sa + per, v.n_seqs);
-    uint64_t mine = 0;
-    Seq seq{0, 0, 0};
-    for (int s = sa; s < sb; s++) {
-        seq = kv4_seq(v, s);
-        mine += S::seq_units(p, seq) * v.heads;
-    }
-    uint64_t total;
-    const uint64_t before = cta_prefix<kWarps * 32>(mine, slots, &total);
+    // this CTA's share [cut 0, cut 1) of the units, and this warp's of that
+    const uint64_t total = build_row<S>(p, row_of_units);
     const uint32_t workers = uint32_t(min(total, uint64_t(gridDim.x)));
     if (blockIdx.x >= workers)
         return;
     uint64_t cut[2] = {mul_div(total, blockIdx.x, workers), mul_div(total, blockIdx.x + 1, workers)};
-    for (int k = 0; k < 2; k++)
-        if (before <= cut[k] && cut[k] < before + mine) {
-            uint64_t u = before;
-            for (int s = sa; s < sb; s++) {
-                if (per > 1)
-                    seq = kv4_seq(v, s);
-                const uint64_t w = S::seq_units(p, seq);
-                if (cut[k] < u + w * v.heads) {
-                    found[k] = Found{u, w, s, seq};
-                    break;
-                }
-                u += w * v.heads;
-            }
-        }
-    __syncthreads();
-    auto locate = [&](int k) {
-        const Found &f = found[k];
-        Item it;
-        it.s = f.s;
-        it.q = f.q;
-        uint64_t rest = cut[k] - f.base;
-        it.head = int(divide(rest, f.per_head));
-        rest -= it.head * f.per_head;
-        it.u0 = f.base + it.head * f.per_head;
-        for (it.rt = 0;; it.rt++) {
-            it.keys = S::tile_keys(p, it.q, it.rt);
-            it.n = S::units(it.keys);
-            if (rest < it.n)
-                break;
-            rest -= it.n;
-            it.u0 += it.n;
-        }
-        return it;
-    };
-    // While a share is at most a tile for each warp, an item of a few tiles
-    // a warp is taken whole: a cut through it would cost a round trip through
+    // While a share is about a tile for each warp, an item of a few tiles a
+    // warp is taken whole: a cut through it would cost a round trip through
     // the workspace.
-    const bool whole = total <= uint64_t(kWarps + kItemCost) * gridDim.x;
-    Item it = locate(0);
-    if (whole && it.n <= kWholeUnits)
-        cut[0] = it.u0;
-    if (cut[1] < total && whole) {
-        const Item e = locate(1);
-        if (e.n <= kWholeUnits)
-            cut[1] = e.u0;
+    const bool snap = total <= uint64_t(kWarps + kItemCost) * gridDim.x;
+    uint64_t u = 0, u_end = 0;
+    Item it{};
+#pragma unroll 1
+    for (int k = snap ? 0 : 2; k < 3; k++) {
+        if (k == 2) {
+            u = cut[0] + (cut[1] - cut[0]) * warp / kWarps;
+            u_end = cut[0] + (cut[1] - cut[0]) * (warp + 1) / kWarps;
+            if (u == u_end)
+                break;
+        }
+        const uint64_t at = k == 0 ? cut[0] : k == 1 ? cut[1] : u;
+        if (at == total)
+            continue;
+        it = locate<S>(p, row_of_units, at);
+        if (k < 2 && it.tiles <= kWholeTiles)
+            cut[k] = it.u0;
     }
+    Seg *const segs = all_segs[warp];
     const int64_t block = int64_t(D + 8) << v.page_log2, page_bytes = block * v.heads;
     const int mask = (1 << v.page_log2) - 1;
     const int v_off = (D / 2) << v.page_log2;
 
     // The warp's next tile to copy: segment, tile, and the lane's page (that of
     // key 16 * (lane / 16) of the tile, which may lie in two pages of 16).  It
-    // runs ahead of the products through all listed segments, so that the
-    // copies go on while a segment is joined.
-    int nx_seg = 0, nx_tile = 0, nx_page = -1, n_segs = 0;
-    auto next_page = [&]() {
-        const Seg &sg = segs[nx_seg];
-        const int key = min(nx_tile * kTile + (lane & 16), sg.len - 1);  // (the first key's where there is no other)
-        nx_page = __ldg(v.table + int64_t(sg.s) * v.table_stride + (key >> v.page_log2));
-    };
-    // From segment nx_seg on, the first one with a tile for this warp.
-    auto next_seg = [&]() {
-        while (nx_seg < n_segs && segs[nx_seg].tiles <= warp)
-            nx_seg++;
-        if (nx_seg < n_segs) {
-            nx_tile = segs[nx_seg].first + warp;
-            next_page();
-        }
-    };
+    // runs ahead of the products through all listed segments.
+    // A list of segments starts with nx_seg = -1: the first call only finds the
+    // first tile.
+    int nx_seg = -1, nx_tile = 0, nx_end = 0, nx_page = -1, n_segs = 0;
     auto issue = [&](int stage) {
-        if (nx_seg < n_segs) {
+        if (nx_seg >= 0 && nx_seg < n_segs) {
             const Seg &sg = segs[nx_seg];
             const uint32_t dst = ring_at + stage * kStageBytes<D>;
             const int key0 = nx_tile * kTile;
@@ -359,39 +318,33 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                                      kv4_params<D>(v.page_log2, (h ? slots[1] : slots[0]) + (r & 15), lane >> 3);
                 cp_async16_zfill(dst + kTile * D + lane * 16, in ? src : v.pages, in ? 16u : 0u);
             }
-            nx_tile += kWarps;
-            if (nx_tile - sg.first < sg.tiles) {
-                next_page();
-            } else {
-                nx_seg++;
-                next_seg();
-            }
         }
         cp_async_commit();
+        if (++nx_tile >= nx_end) {
+            do
+                nx_seg++;
+            while (nx_seg < n_segs && segs[nx_seg].tiles == 0);
+            if (nx_seg >= n_segs)
+                return;
+            nx_tile = segs[nx_seg].first;
+            nx_end = nx_tile + segs[nx_seg].tiles;
+        }
+        const Seg &sg = segs[nx_seg];
+        const int key = min(nx_tile * kTile + (lane & 16), sg.len - 1);  // (the last key's where there is no other)
+        nx_page = __ldg(v.table + int64_t(sg.s) * v.table_stride + (key >> v.page_log2));
     };
 
     const Codes codes;
     const float c1_up = p.c1 * kQDown;
-    int n_pend = 0;  // parts of cut items, arrived together at the end
-    int stage = 0;   // the ring's next stage to use; the one before it is free
-    uint64_t u = cut[0];
-    while (u < cut[1]) {
-        if (warp == 0) {
-            const uint64_t to = list_segments<RB>(p, it, u, cut[1], segs, &listed);
-            if (lane == 0)
-                listed_to = to;
-        }
-        __syncthreads();
-        u = listed_to;
-        n_segs = listed;
-        nx_seg = 0;
-        next_seg();
-        for (int s = 0; s < ST - 1; s++)
-            issue((stage + s) % ST);
-
+    int stage = 0;  // the ring's next stage to use
+    while (u < u_end) {
+        u = list_segments<S, RB>(p, it, u, u_end, segs, &n_segs);
+        nx_seg = -1;
+        nx_end = 0;
+        int fill = stage == 0 ? ST - 1 : stage - 1, calls = ST + 1;
         for (int sgi = 0; sgi < n_segs; sgi++) {
         const Seg &sg = segs[sgi];
-        const int n_mine = sg.tiles > warp ? (sg.tiles - warp + kWarps - 1) / kWarps : 0;
+        const int n_mine = sg.tiles;
         const int r0 = sg.rt * RB, rows = sg.tokens * p.group;
         const int all_lo = sg.all_lo, all_hi = sg.all_hi;
         const Seq sq{sg.t0, sg.tokens, sg.len};
@@ -407,7 +360,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             for (int k = 0; k < D / 32; k++)
                 x[k] = make_uint4(0, 0, 0, 0);
             if (rr < rows - r0 && n_mine > 0) {
-                const int i = (r0 + rr) / p.group;
+                const int i = p.by_group.of(r0 + rr);
                 const int64_t tok = sg.t0 + i, head = sg.head * p.group + (r0 + rr - i * p.group);
                 const uint4 *src = reinterpret_cast<const uint4 *>(p.q.p + tok * p.q.ts + head * p.q.hs + (D / 4) * t);
 #pragma unroll
@@ -439,12 +392,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         }
 
         for (int i = 0; i < n_mine; i++) {
-            issue(stage == 0 ? ST - 1 : stage - 1);
+            for (; calls > 0; calls--) {  // the ring's fill at first, then a tile for a tile
+                issue(fill);
+                fill = fill + 1 == ST ? 0 : fill + 1;
+            }
+            calls = 1;
             asm volatile("cp.async.wait_group %0;" :: "n"(ST - 1) : "memory");
             __syncwarp();
             const unsigned char *const st = ring + stage * kStageBytes<D>;
             stage = stage + 1 == ST ? 0 : stage + 1;
-            const int key0 = (sg.first + warp + i * kWarps) * kTile;
+            const int key0 = (sg.first + i) * kTile;
 
             // scores
             float sc[2][NT][4];
@@ -509,7 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
 #pragma unroll
                         for (int k = 0; k < 2; k++) {
                             const int row = 8 * nt + (kDup ? (2 * t + k) & 3 : 2 * t + k);
-                            const int tok = (r0 + min(row, rows - r0 - 1)) / p.group;
+                            const int tok = p.by_group.of(r0 + min(row, rows - r0 - 1));
                             const KeyRange kr = visible(p, sq, tok, tok);
 #pragma unroll
                             for (int j = 0; j < 4; j++) {
@@ -652,15 +609,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             }
             __syncwarp();
         }
-        // The warps' parts, joined through shared memory: each warp leaves its
-        // maximum, sum and output (with the ranges' middles added) in its ring's
-        // free stage (sixteen rows: in an area of their own).
-        unsigned char *const mine_at = NT == 1 ? ring + (stage == 0 ? ST - 1 : stage - 1) * kStageBytes<D>
-                                               : smem + kWarps * ST * kStageBytes<D> + warp * (RB * D * 4);
-        if (lane == 0)
-            w_at[warp] = int(mine_at - smem);
-        float4 *const wo = reinterpret_cast<float4 *>(mine_at);
-        __syncwarp();
+        // A whole item is written out; a part of one goes to the workspace, or
+        // (the warp's last) to its ring.
+        const bool whole = sg.tiles == sg.of;
+        const bool last = u == u_end && sgi == n_segs - 1;
+        float *part = nullptr;
+        if (!whole) {
+            if (last) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();
+            }
+            part = last ? reinterpret_cast<float *>(ring)
+                        : p.parts + (2 * uint64_t(gridDim.x) + blockIdx.x * kWarps + warp) * PF;
+            if (lane == 0)
+                parts[2 * warp + last] = Part{part, sg.u0, sg.rt, sg.t0, sg.tokens, sg.head, sg.tiles, sg.of};
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
             const float2 l2 = unpair(w.l[nt]), z2 = unpair(w.z[nt]);
@@ -683,67 +646,96 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                     for (int i = 0; i < D / 8; i++)
                         o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
                 }
-                const int row = 8 * nt + 2 * t + k;
-                if (!kDup || t < 2) {
-                    if (g == 0) {
-                        w_m[warp][row] = w.m[nt][k];
-                        w_l[warp][row] = l;
-                    }
 #pragma unroll
-                    for (int i = 0; i < D / 32; i++)
-                        wo[part_at<D>(row, g * (D / 32) + i)] =
-                            make_float4(o[4 * i] + z, o[4 * i + 1] + z, o[4 * i + 2] + z, o[4 * i + 3] + z);
+                for (int i = 0; i < D / 8; i++)
+                    o[i] += z;
+                const int row = 8 * nt + 2 * t + k;
+                if ((!kDup || t < 2) && r0 + row < rows) {
+                    if (whole) {
+                        store_dims<D / 8>(p, sg.t0, sg.head, r0 + row, (D / 8) * g, o, w.m[nt][k], l);
+                    } else {
+                        float4 *const dst = reinterpret_cast<float4 *>(part) + row * (D / 4) + g * (D / 32);
+#pragma unroll
+                        for (int i = 0; i < D / 32; i++)
+                            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        if (g == 0) {
+                            part[RB * D + row] = w.m[nt][k];
+                            part[RB * D + RB + row] = l;
+                        }
+                    }
                 }
             }
         }
-        __syncthreads();
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
 
-        const bool alone = sg.a == 0 && sg.b == sg.n;
-        float *const part = p.parts + (2 * uint64_t(blockIdx.x) + (sg.a == 0 ? 1 : 0)) * PF;
-        const int f4 = min(rows - r0, RB) * (D / 4);  // of rows that there are
-        for (int x = threadIdx.x; x < f4; x += kWarps * 32) {
-            const int row = x / (D / 4), c = x % (D / 4);
-            float m = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kWarps; k++)
-                m = fmaxf(m, w_m[k][row]);
+    // Items that the cuts between the warps go through: consecutive parts of
+    // one item are joined, in their order, and written out or, if the CTA does
+    // not have all of the item, left in the workspace.  Lane i of every warp looks
+    // at part i: a group begins where the item is not the part's before.
+    {
+        const bool has = lane < 2 * kWarps && parts[lane & (2 * kWarps - 1)].at;
+        const uint64_t id = has ? parts[lane].u0 : 0;
+        const uint32_t some = __ballot_sync(0xffffffffu, has);
+        const uint32_t under = some & ((1u << lane) - 1u);
+        const uint64_t id_before = __shfl_sync(0xffffffffu, id, under ? 31 - __clz(under) : 0);
+        uint32_t heads = __ballot_sync(0xffffffffu, has && (under == 0 || id_before != id));
+        const int n = __popc(heads) * (RB * D / 4);
+        int at_group = 0;
+        for (int idx = threadIdx.x; idx < n; idx += kWarps * 32) {
+            for (; at_group < idx / (RB * D / 4); at_group++)
+                heads &= heads - 1;
+            const int a = __ffs(heads) - 1, x = idx % (RB * D / 4), row = x / (D / 4);
+            const uint32_t later = heads & (heads - 1);
+            const int b = later ? __ffs(later) - 1 : 2 * kWarps;
+            const Part &head = parts[a];
+            const int r0 = head.rt * RB;
+            if (row >= head.tokens * p.group - r0)
+                continue;
+            float m = -INFINITY, l = 0.f;
+            int tiles = 0;
+            for (int k = a; k < b; k++)
+                if (some >> k & 1) {
+                    m = fmaxf(m, parts[k].at[RB * D + row]);
+                    tiles += parts[k].tiles;
+                }
             const float m0 = m == -INFINITY ? 0.f : m;
-            float l = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kWarps; k++)
-                join_scaled(l, acc, exp2_fast(w_m[k][row] - m0), w_l[k][row],
-                            reinterpret_cast<const float4 *>(smem + w_at[k])[part_at<D>(row, c)]);
-            if (alone) {
-                store_row<D>(p, sg.t0, sg.head, r0 + row, c, acc, m, l);
+            for (int k = a; k < b; k++)
+                if (some >> k & 1) {
+                    const float *q = parts[k].at;
+                    join_scaled(l, acc, exp2_fast(q[RB * D + row] - m0), q[RB * D + RB + row],
+                                reinterpret_cast<const float4 *>(q)[x]);
+                }
+            const int c = x % (D / 4);
+            if (tiles == head.of) {
+                store_row<D>(p, head.t0, head.head, r0 + row, c, acc, m, l);
             } else {
+                const int first = cut[0] > head.u0 ? 0 : 1;  // ends an item, or begins one
+                float *const part = p.parts + (2 * uint64_t(blockIdx.x) + first) * PF;
                 reinterpret_cast<float4 *>(part)[x] = acc;
                 if (c == 0) {
                     part[RB * D + row] = m;
                     part[RB * D + RB + row] = l;
                 }
+                if (x == 0) {
+                    pend[first] = head;
+                    pend[first].at = part;
+                }
             }
         }
-        if (!alone) {
-            if (threadIdx.x == 0)
-                pend[n_pend] = sg;
-            n_pend++;
-        }
-        __syncthreads();  // the free stages are free again
-        }
     }
-    if (n_pend == 0)
-        return;
-
-    // The cut items of this share (at most two): whoever arrives last joins the
-    // parts.  Warp w joins parts f + w, f + w + kWarps, ..., a few in flight; then
-    // the warps' results through shared memory, in their order.
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __threadfence();
     __syncthreads();
-    if (threadIdx.x < n_pend) {
-        const Seg &sg = pend[threadIdx.x];
-        const uint32_t f = share_of(sg.u0, total, workers), e = share_of(sg.u0 + sg.n - 1, total, workers);
+    if (pend[0].at == nullptr && pend[1].at == nullptr)
+        return;
+
+    // Items that go on in other CTAs: whoever arrives last joins the parts.
+    if (threadIdx.x < 2 && pend[threadIdx.x].at) {
+        const Part &sg = pend[threadIdx.x];
+        const uint32_t f = share_of(sg.u0, total, workers), e = share_of(sg.u0 + sg.of - 1, total, workers);
         const bool last = atomicAdd(p.counters + f, 1u) == e - f;
         if (last)
             p.counters[f] = 0;  // ready for the next call
@@ -752,58 +744,71 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         to_part[threadIdx.x] = e;
     }
     __syncthreads();
-    for (int k = 0; k < n_pend; k++) {
-        if (!arrived[k])
+    for (int k = 0; k < 2; k++) {
+        if (pend[k].at == nullptr || !arrived[k])
             continue;
         __threadfence();
-        const Seg &sg = pend[k];
-        const uint32_t f = from[k], e = to_part[k];
-        const int r0 = sg.rt * RB;
-        const int f4 = min(sg.tokens * p.group - r0, RB) * (D / 4);
-        constexpr int N = F4 / 32;
-        float m[N], l[N];
-        float4 acc[N];
-#pragma unroll
-        for (int n = 0; n < N; n++) {
-            m[n] = -INFINITY;
-            l[n] = 0.f;
-            acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // First every part's maximum and sum, from which its weight; then the
+        // outputs, many in flight: thread x takes float4 x of every second (or
+        // fourth, ...) part, and the threads of one float4 are added in their order.
+        const Part &sg = pend[k];
+        const uint32_t f = from[k];
+        const int n = int(to_part[k] - f) + 1;
+        const int r0 = sg.rt * RB, real = min(sg.tokens * p.group - r0, RB);
+        const int f4 = real * (D / 4);
+        auto part_of = [&](int i) { return p.parts + (2 * uint64_t(f + i) + (i == 0 ? 1 : 0)) * PF; };
+        float *const wt = reinterpret_cast<float *>(smem);             // [n][RB] weights
+        float *const sums = wt + n * RB;                               // [n][RB] sums, then outputs
+        for (int i = threadIdx.x; i < n * RB; i += kWarps * 32) {
+            const bool in = i % RB < real;
+            wt[i] = in ? __ldcg(part_of(i / RB) + RB * D + i % RB) : -INFINITY;
+            sums[i] = in ? __ldcg(part_of(i / RB) + RB * D + RB + i % RB) : 0.f;
         }
-#pragma unroll 2
-        for (uint32_t x0 = f + warp; x0 <= e; x0 += kWarps) {
-            const float *q = p.parts + (2 * uint64_t(x0) + (x0 == f ? 1 : 0)) * PF;
-#pragma unroll
-            for (int n = 0; n < N; n++) {
-                const int x = n * 32 + lane, row = x / (D / 4);
-                if (x < f4)
-                    join(m[n], l[n], acc[n], __ldcg(q + RB * D + row), __ldcg(q + RB * D + RB + row),
-                         __ldcg(reinterpret_cast<const float4 *>(q) + x));
+        __syncthreads();
+        if (threadIdx.x < RB) {
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; i++)
+                m = fmaxf(m, wt[i * RB + threadIdx.x]);
+            const float m0 = m == -INFINITY ? 0.f : m;
+            for (int i = 0; i < n; i++) {
+                const float w = exp2_fast(wt[i * RB + threadIdx.x] - m0);
+                wt[i * RB + threadIdx.x] = w;
+                l = fmaf(w, sums[i * RB + threadIdx.x], l);
             }
+            row_m[threadIdx.x] = m;
+            row_l[threadIdx.x] = l;
         }
-        float4 *const mine_o = reinterpret_cast<float4 *>(ring);
-#pragma unroll
-        for (int n = 0; n < N; n++) {
-            const int x = n * 32 + lane, row = x / (D / 4);
-            mine_o[x] = acc[n];
-            if (x % (D / 4) == 0) {
-                w_m[warp][row] = m[n];
-                w_l[warp][row] = l[n];
+        __syncthreads();
+        constexpr int F4 = RB * (D / 4);
+        constexpr int kSplit = F4 < kWarps * 32 ? kWarps * 32 / F4 : 1;
+        float4 *const outs = reinterpret_cast<float4 *>(smem + (2 * n * RB * 4 + 15) / 16 * 16);
+        for (int x = threadIdx.x % F4; x < f4; x += kWarps * 32 / kSplit) {
+            const int row = x / (D / 4), s0 = threadIdx.x / F4 % kSplit;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int i = s0; i < n; i += kSplit) {
+                const float w = wt[i * RB + row];
+                const float4 o = __ldcg(reinterpret_cast<const float4 *>(part_of(i)) + x);
+                acc.x = fmaf(w, o.x, acc.x);
+                acc.y = fmaf(w, o.y, acc.y);
+                acc.z = fmaf(w, o.z, acc.z);
+                acc.w = fmaf(w, o.w, acc.w);
             }
+            outs[s0 * F4 + x] = acc;
         }
         __syncthreads();
         for (int x = threadIdx.x; x < f4; x += kWarps * 32) {
-            const int row = x / (D / 4), c = x % (D / 4);
-            float mt = -INFINITY, lt = 0.f;
-            float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int row = x / (D / 4);
+            float4 acc = outs[x];
 #pragma unroll
-            for (int w = 0; w < kWarps; w++)
-                mt = fmaxf(mt, w_m[w][row]);
-            const float m0 = mt == -INFINITY ? 0.f : mt;
-#pragma unroll
-            for (int w = 0; w < kWarps; w++)
-                join_scaled(lt, ot, exp2_fast(w_m[w][row] - m0), w_l[w][row],
-                            reinterpret_cast<const float4 *>(smem + w * ST * kStageBytes<D>)[x]);
-            store_row<D>(p, sg.t0, sg.head, r0 + row, c, ot, mt, lt);
+            for (int s0 = 1; s0 < kSplit; s0++) {
+                const float4 o = outs[s0 * F4 + x];
+                acc.x += o.x;
+                acc.y += o.y;
+                acc.z += o.z;
+                acc.w += o.w;
+            }
+            store_row<D>(p, sg.t0, sg.head, r0 + row, x % (D / 4), acc, row_m[row], row_l[row]);
         }
         __syncthreads();
     }
@@ -811,7 +816,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
 
 template <int D, int NT, bool kDup>
 uw_status launch(const AttnParams &p, int ctas, cudaStream_t st) {
-    constexpr size_t smem = size_t(kWarps) * (kStages<D> * kStageBytes<D> + (NT == 1 ? 0 : 8 * NT * D * 4));
+    static_assert(8 * NT * (D + 2) * 4 <= kStages<D> * kStageBytes<D>, "a part fits a ring");
+    constexpr size_t smem = size_t(kWarps) * kStages<D> * kStageBytes<D>;
     if (!ensure_smem(kv4_decode_kernel<D, NT, kDup>, smem))
         return UW_ERR_CUDA;
     return launch_overlapped(kv4_decode_kernel<D, NT, kDup>, dim3(unsigned(ctas)), dim3(kWarps * 32), smem, st, p) ==
@@ -824,7 +830,7 @@ uw_status launch(const AttnParams &p, int ctas, cudaStream_t st) {
 
 int kv4_decode_ctas() { return 2 * sm_count(); }
 
-size_t kv4_decode_part_floats(int head_dim) { return 2 * size_t(kv4_decode_ctas()) * 16 * (head_dim + 2); }
+size_t kv4_decode_part_floats(int head_dim) { return (2 + kWarps) * size_t(kv4_decode_ctas()) * 16 * (head_dim + 2); }
 
 uw_status launch_kv4_decode(const AttnParams &p, int head_dim, int64_t rows, int64_t max_units, cudaStream_t st) {
     const bool dup = rows > 0 && rows <= 4, wide = rows == 0 || rows > 8;
