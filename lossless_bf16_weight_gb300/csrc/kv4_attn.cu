@@ -48,15 +48,22 @@ bool kv4_rows(const uw_kv4_rows *r, Rows *out) {
 
 namespace {
 
-// Workspace: [error word | counters | parts].
+// Sequences with up to so many rows (new tokens x query heads of a kv head)
+// take the kernel for few rows.
+constexpr int kFewRows = 64;
+
+// Workspace: [error word | counters and parts of the kernel for few rows | the
+// same of the other].
 struct Layout {
-    size_t counters, parts, total;
+    size_t few_counters, few_parts, many_counters, many_parts, total;
 };
 Layout layout(int head_dim) {
     Layout w;
-    w.counters = 256;
-    w.parts = align_up(w.counters + 4 * size_t(kv4_decode_ctas()), 256);
-    w.total = w.parts + 4 * kv4_decode_part_floats(head_dim);
+    w.few_counters = 256;
+    w.few_parts = align_up(w.few_counters + 4 * size_t(kv4_decode_ctas()), 256);
+    w.many_counters = align_up(w.few_parts + 4 * kv4_decode_part_floats(head_dim), 256);
+    w.many_parts = align_up(w.many_counters + 4 * size_t(kv4_prefill_ctas()), 256);
+    w.total = w.many_parts + 4 * kv4_prefill_part_floats(head_dim);
     return w;
 }
 
@@ -116,11 +123,29 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
     p.by_group = Divisor(uint32_t(p.group));
     p.causal = causal != 0;
     p.window = window;
-    p.rows_min = 0;
-    p.rows_max = INT32_MAX;
-    p.counters = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + w.counters);
-    p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.parts);
+    uint8_t *const wsb = static_cast<uint8_t *>(ws);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Which sequences take which kernel is decided on the device by their rows;
+    // the host's bounds only leave out a launch that has none, and a wrong bound
+    // leaves all sequences to the kernel that is launched.
     const int64_t rows = max_new * p.group;
-    const int64_t units = max_len > 0 && max_new > 0 ? (max_len / 32 + 1) * ((rows + 15) / 16 + 1) * c->kv_heads * c->n_seqs : 0;
-    return launch_kv4_decode(p, c->head_dim, rows, units, static_cast<cudaStream_t>(stream));
+    const bool few = rows == 0 || rows <= kFewRows || c->n_seqs > 1, many = rows == 0 || rows > kFewRows;
+    if (few) {
+        p.rows_min = 0;
+        p.rows_max = many ? kFewRows : INT32_MAX;
+        p.counters = reinterpret_cast<uint32_t *>(wsb + w.few_counters);
+        p.parts = reinterpret_cast<float *>(wsb + w.few_parts);
+        const int64_t units = max_len > 0 && !many ? (max_len / 32 + 2) * (rows / 8 + 1) * c->kv_heads * c->n_seqs : 0;
+        const uw_status r = launch_kv4_decode(p, c->head_dim, many ? 0 : rows, units, st);
+        if (r != UW_OK)
+            return r;
+    }
+    if (many) {
+        p.rows_min = few ? kFewRows + 1 : 0;
+        p.rows_max = INT32_MAX;
+        p.counters = reinterpret_cast<uint32_t *>(wsb + w.many_counters);
+        p.parts = reinterpret_cast<float *>(wsb + w.many_parts);
+        return launch_kv4_prefill(p, c->head_dim, st);
+    }
+    return UW_OK;
 }

@@ -68,6 +68,7 @@ struct Item {
 
 template <int RB, int T, int kCost>  // rows of a row tile, keys of a unit, units an item costs beyond its tiles
 struct Sched {
+    static constexpr int kRows = RB, kKeys = T;
     static __device__ __forceinline__ bool mine(const AttnParams &p, const Seq &s) {
         const int32_t rows = s.n * p.group;
         return rows >= p.rows_min && rows <= p.rows_max && rows > 0;
@@ -82,7 +83,8 @@ struct Sched {
     static __device__ __forceinline__ uint32_t tiles(const KeyRange &k) {
         return k.hi > k.lo ? uint32_t((k.hi - 1) / T - k.lo / T + 1) : 0u;
     }
-    // Units of one head of a sequence.
+    // Units of one head of a sequence: by one thread, and by a warp that
+    // shares its row tiles.
     static __device__ __forceinline__ uint64_t seq_units(const AttnParams &p, const Seq &s) {
         if (!mine(p, s))
             return 0;
@@ -91,6 +93,19 @@ struct Sched {
         for (int rt = 0; rt < rts; rt++)
             n += kCost + tiles(tile_keys(p, s, rt));
         return n;
+    }
+    static __device__ __forceinline__ uint64_t seq_units_warp(const AttnParams &p, const Seq &s) {
+        if (!mine(p, s))
+            return 0;
+        uint64_t n = 0;
+        const int rts = row_tiles(p, s);
+        for (int rt = threadIdx.x & 31; rt < rts; rt += 32)
+            n += kCost + tiles(tile_keys(p, s, rt));
+        if (rts > 1)
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                n += __shfl_xor_sync(0xffffffffu, n, o);
+        return rts > 1 ? n : __shfl_sync(0xffffffffu, n, 0);
     }
     static __device__ __forceinline__ void set_tile(const AttnParams &p, Item &it, int rt) {
         it.rt = rt;
@@ -108,17 +123,40 @@ struct Row {
     Seq seq[kThreads];  // with per = 1: the sequence
 };
 
-// Fills the row (all threads call); returns all units.
-template <class S, int kThreads>
+// Fills the row (all threads call); returns all units.  kWide: a warp for
+// each sequence, its lanes for the row tiles, where sequences have many;
+// otherwise a thread for each sequence.
+template <class S, int kThreads, bool kWide>
 __device__ __forceinline__ uint64_t build_row(const AttnParams &p, Row<kThreads> &row) {
+    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.v.n_seqs + kThreads - 1) / kThreads;
-    const int a = min(int(threadIdx.x) * per, p.v.n_seqs), b = min(a + per, p.v.n_seqs);
     uint64_t mine = 0;
-    for (int s = a; s < b; s++) {
-        const Seq q = kv4_seq(p.v, s);
-        mine += S::seq_units(p, q) * p.v.heads;
-        row.seq[threadIdx.x] = q;
+    if constexpr (kWide) {
+        row.before[threadIdx.x] = 0;
+        __syncthreads();
+        for (int s0 = 0; s0 < p.v.n_seqs; s0 += kThreads) {
+            const int own = s0 + warp + lane * kWarps;  // the lane's sequence, of this warp's 32
+            const Seq q = own < p.v.n_seqs ? kv4_seq(p.v, own) : Seq{0, 0, 0};
+            if (own < p.v.n_seqs)
+                row.seq[own % kThreads] = q;
+            for (int k = 0; k < 32 && s0 + warp + k * kWarps < p.v.n_seqs; k++) {
+                const Seq one{__shfl_sync(0xffffffffu, q.t0, k), __shfl_sync(0xffffffffu, q.n, k),
+                              __shfl_sync(0xffffffffu, q.len, k)};
+                const uint64_t u = S::seq_units_warp(p, one) * p.v.heads;
+                if (lane == 0 && u)
+                    atomicAdd(reinterpret_cast<unsigned long long *>(&row.before[(s0 + warp + k * kWarps) / per]), u);
+            }
+        }
+        __syncthreads();
+        mine = row.before[threadIdx.x];
+    } else {
+        const int a = min(int(threadIdx.x) * per, p.v.n_seqs), b = min(a + per, p.v.n_seqs);
+        for (int s = a; s < b; s++) {
+            const Seq q = kv4_seq(p.v, s);
+            mine += S::seq_units(p, q) * p.v.heads;
+            row.seq[threadIdx.x] = q;
+        }
     }
     uint64_t v = mine;
 #pragma unroll
@@ -132,7 +170,7 @@ __device__ __forceinline__ uint64_t build_row(const AttnParams &p, Row<kThreads>
     __syncthreads();
     uint64_t before = v - mine, all = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; w++) {
+    for (int w = 0; w < kWarps; w++) {
         const uint64_t t = row.sums[w];
         before += w < warp ? t : 0;
         all += t;
@@ -167,11 +205,11 @@ __device__ __forceinline__ Item locate(const AttnParams &p, const Row<kThreads> 
     it.u0 = row.before[i];
     if (per == 1) {
         it.q = row.seq[i];
-        per_head = S::seq_units(p, it.q);
+        per_head = S::seq_units_warp(p, it.q);
     } else {
         for (;; it.s++) {
             it.q = kv4_seq(p.v, it.s);
-            per_head = S::seq_units(p, it.q);
+            per_head = S::seq_units_warp(p, it.q);
             if (rest < per_head * p.v.heads)
                 break;
             rest -= per_head * p.v.heads;
@@ -181,13 +219,106 @@ __device__ __forceinline__ Item locate(const AttnParams &p, const Row<kThreads> 
     it.head = int(divide(rest, per_head));
     rest -= it.head * per_head;
     it.u0 += it.head * per_head;
-    for (int rt = 0;; rt++) {
-        S::set_tile(p, it, rt);
-        if (rest < it.n)
+    // its row tile: 32 of them at a time
+    const int rts = S::row_tiles(p, it.q);
+    for (int rt0 = 0;; rt0 += 32) {
+        const int rt = rt0 + lane;
+        uint32_t n = 0;
+        if (rt < rts) {
+            S::set_tile(p, it, rt);
+            n = it.n;
+        }
+        uint64_t upto = n;
+        if (rts > 1)
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o)
+                    upto += x;
+            }
+        const uint32_t past = __ballot_sync(0xffffffffu, rt < rts && rest < upto);
+        if (past) {
+            const int at = __ffs(past) - 1;
+            it.u0 += __shfl_sync(0xffffffffu, upto - n, at);
+            S::set_tile(p, it, rt0 + at);
             return it;
-        rest -= it.n;
-        it.u0 += it.n;
+        }
+        const uint64_t all = __shfl_sync(0xffffffffu, upto, 31);
+        rest -= all;
+        it.u0 += all;
     }
+}
+
+// A share's part of one item: tiles first .. first + tiles - 1.
+struct Seg {
+    uint64_t u0;
+    int32_t s, head, rt, t0, tokens, len;
+    int32_t first, tiles, of;  // `of`: the item's tiles
+    int32_t all_lo, all_hi;    // keys that every row sees
+};
+// A warp lists the segments of the units from u (in item `it`) up to `end`,
+// at most kMost of them; returns the unit after them and leaves `it` there.
+// An item's last units, which are no tiles, are nobody's; one that sees no
+// key at all is a segment without tiles of the share that has its first unit.
+// The sequences' lengths are read 32 at a time.
+template <class S, int kMost>
+__device__ __forceinline__ uint64_t list_segments(const AttnParams &p, Item &it, uint64_t u, uint64_t end, Seg *segs,
+                                                  int *count) {
+    const int lane = threadIdx.x & 31;
+    int base = it.s, n = 0;
+    Seq next{0, 0, 0};
+    bool loaded = false;
+    while (u < end && n < kMost) {
+        const uint32_t a = uint32_t(u - it.u0), b = uint32_t(min(end - it.u0, uint64_t(it.n)));
+        const int tiles = int(min(b, it.tiles)) - int(a);
+        if (tiles > 0 || (it.tiles == 0 && a == 0)) {
+            if (lane == 0) {
+                Seg g;
+                g.u0 = it.u0;
+                g.s = it.s;
+                g.head = it.head;
+                g.rt = it.rt;
+                g.t0 = it.q.t0;
+                g.tokens = it.q.n;
+                g.len = it.q.len;
+                g.first = it.keys.lo / S::kKeys + int(a);
+                g.tiles = max(tiles, 0);
+                g.of = int(it.tiles);
+                const int r0 = it.rt * S::kRows, r1 = r0 + min(S::kRows, it.q.n * p.group - r0) - 1;
+                const int i0 = p.by_group.of(r0), i1 = p.by_group.of(r1);
+                g.all_lo = visible(p, it.q, i1, i1).lo;
+                g.all_hi = min(visible(p, it.q, i0, i0).hi, it.q.len);
+                segs[n] = g;
+            }
+            n++;
+        }
+        u = it.u0 + b;
+        if (u < end) {  // the next item
+            it.u0 = u;
+            int rt = it.rt + 1;
+            if (rt == S::row_tiles(p, it.q)) {
+                rt = 0;
+                if (++it.head == p.v.heads) {
+                    it.head = 0;
+                    do {
+                        if (!loaded || ++it.s - base == 32) {
+                            it.s += loaded ? 0 : 1;
+                            loaded = true;
+                            base = it.s;
+                            next = base + lane < p.v.n_seqs ? kv4_seq(p.v, base + lane) : Seq{0, 0, 0};
+                        }
+                        it.q.t0 = __shfl_sync(0xffffffffu, next.t0, it.s - base);
+                        it.q.n = __shfl_sync(0xffffffffu, next.n, it.s - base);
+                        it.q.len = __shfl_sync(0xffffffffu, next.len, it.s - base);
+                    } while (!S::mine(p, it.q));
+                }
+            }
+            S::set_tile(p, it, rt);
+        }
+    }
+    *count = n;
+    __syncwarp();
+    return u;
 }
 
 // The share (of `workers` equal ones) that holds unit u: the last c with
@@ -285,5 +416,9 @@ size_t kv4_decode_part_floats(int head_dim);
 // rows: the most rows (new tokens * group) of a sequence, max_units: the most
 // units in all, as far as known (0: not known).
 uw_status launch_kv4_decode(const AttnParams &p, int head_dim, int64_t rows, int64_t max_units, cudaStream_t st);
+// kv4_prefill.cu
+int kv4_prefill_ctas();
+size_t kv4_prefill_part_floats(int head_dim);
+uw_status launch_kv4_prefill(const AttnParams &p, int head_dim, cudaStream_t st);
 
 }  // namespace uw

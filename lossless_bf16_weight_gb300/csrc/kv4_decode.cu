@@ -34,6 +34,7 @@
 
 #include "kernels.h"
 #include "kv4_attn.cuh"
+#include "kv4_codes.cuh"
 #include "kv4_host.h"
 #include "tc.cuh"
 
@@ -51,44 +52,6 @@ template <int D>
 constexpr int kStageBytes = kTile * (D + 8);
 template <int D>
 constexpr int kStages = D == 128 ? 3 : 5;
-
-// A value the compiler does not know, so that it stays in a register: the
-// logic operations below take their masks from registers.
-__device__ __forceinline__ uint32_t opaque(uint32_t v) {
-    uint32_t r;
-    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t mul2_bf16(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// Codes as pairs of BF16: bits 0..7 of a BF16 on their own are the integer n
-// they spell, times 2^-133 (subnormal below 128, the first normal binade
-// from there).  So a code in bits 0..3 of a half is c, one in bits 4..7 is 16 c,
-// in units of 2^-133, with no shift and no conversion; the queries and
-// probabilities they meet are scaled up by kQUp and kPUp.
-struct Codes {
-    uint32_t mask0 = opaque(0x000f000fu), mask4 = opaque(0x00f000f0u);
-    uint32_t mid0 = opaque(0x00080008u), mid4 = opaque(0x00800080u);
-    // c and 16 c
-    __device__ __forceinline__ uint32_t low(uint32_t w) const { return w & mask0; }
-    __device__ __forceinline__ uint32_t high(uint32_t w) const { return w & mask4; }
-    // c - 8 and 16 (c - 8), exact
-    __device__ __forceinline__ uint32_t low_mid(uint32_t w) const { return sub2(w & mask0, mid0); }
-    __device__ __forceinline__ uint32_t high_mid(uint32_t w) const { return sub2(w & mask4, mid4); }
-};
-constexpr uint32_t kQUpLow = 0x57805780u, kQUpHigh = 0x55805580u;  // 2^48, and 2^44 for the codes times 16
-constexpr float kQDown = 3.8685626e25f;                            // 2^85 = 2^133 / 2^48
-constexpr float kPUp = 1.8446744e19f;                              // 2^64
-constexpr float kPDownLow = 5.9029581e20f, kPDownHigh = 3.6893488e19f;  // 2^69 = 2^133 / 2^64, 2^65
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -128,79 +91,7 @@ struct Warp {
     uint64_t qs[NT];         // sum of q
 };
 
-// A warp's part of one item: tiles first .. first + tiles - 1.
-struct Seg {
-    uint64_t u0;
-    int32_t s, head, rt, t0, tokens, len;
-    int32_t first, tiles, of;  // `of`: the item's tiles
-    int32_t all_lo, all_hi;    // keys that every row sees
-};
-constexpr int kSegs = 8;
-
-// The warp lists the segments of the units from u (in item `it`) up to `end`,
-// at most kSegs of them; returns the unit after them and leaves `it` there.
-// An item's last units, which are no tiles, are nobody's; one that sees no
-// key at all is a segment without tiles of the warp that has its first unit.
-// The sequences' lengths are read 32 at a time.
-template <class S, int RB>
-__device__ __forceinline__ uint64_t list_segments(const AttnParams &p, Item &it, uint64_t u, uint64_t end, Seg *segs,
-                                                  int *count) {
-    const int lane = threadIdx.x & 31;
-    int base = it.s, n = 0;
-    Seq next{0, 0, 0};
-    bool loaded = false;
-    while (u < end && n < kSegs) {
-        const uint32_t a = uint32_t(u - it.u0), b = uint32_t(min(end - it.u0, uint64_t(it.n)));
-        const int tiles = int(min(b, it.tiles)) - int(a);
-        if (tiles > 0 || (it.tiles == 0 && a == 0)) {
-            if (lane == 0) {
-                Seg g;
-                g.u0 = it.u0;
-                g.s = it.s;
-                g.head = it.head;
-                g.rt = it.rt;
-                g.t0 = it.q.t0;
-                g.tokens = it.q.n;
-                g.len = it.q.len;
-                g.first = it.keys.lo / kTile + int(a);
-                g.tiles = max(tiles, 0);
-                g.of = int(it.tiles);
-                const int r0 = it.rt * RB, r1 = r0 + min(RB, it.q.n * p.group - r0) - 1;
-                const int i0 = p.by_group.of(r0), i1 = p.by_group.of(r1);
-                g.all_lo = visible(p, it.q, i1, i1).lo;
-                g.all_hi = min(visible(p, it.q, i0, i0).hi, it.q.len);
-                segs[n] = g;
-            }
-            n++;
-        }
-        u = it.u0 + b;
-        if (u < end) {  // the next item
-            it.u0 = u;
-            int rt = it.rt + 1;
-            if (rt == S::row_tiles(p, it.q)) {
-                rt = 0;
-                if (++it.head == p.v.heads) {
-                    it.head = 0;
-                    do {
-                        if (!loaded || ++it.s - base == 32) {
-                            it.s += loaded ? 0 : 1;
-                            loaded = true;
-                            base = it.s;
-                            next = base + lane < p.v.n_seqs ? kv4_seq(p.v, base + lane) : Seq{0, 0, 0};
-                        }
-                        it.q.t0 = __shfl_sync(0xffffffffu, next.t0, it.s - base);
-                        it.q.n = __shfl_sync(0xffffffffu, next.n, it.s - base);
-                        it.q.len = __shfl_sync(0xffffffffu, next.len, it.s - base);
-                    } while (!S::mine(p, it.q));
-                }
-            }
-            S::set_tile(p, it, rt);
-        }
-    }
-    *count = n;
-    __syncwarp();
-    return u;
-}
+constexpr int kSegs = 8;  // segments a warp lists at once
 
 // A part of an item that waits to be joined.
 struct Part {
@@ -235,7 +126,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         pend[threadIdx.x].at = nullptr;
 
     // this CTA's share [cut 0, cut 1) of the units, and this warp's of that
-    const uint64_t total = build_row<S>(p, row_of_units);
+    const uint64_t total = build_row<S, kWarps * 32, false>(p, row_of_units);
     const uint32_t workers = uint32_t(min(total, uint64_t(gridDim.x)));
     if (blockIdx.x >= workers)
         return;
@@ -338,7 +229,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     const float c1_up = p.c1 * kQDown;
     int stage = 0;  // the ring's next stage to use
     while (u < u_end) {
-        u = list_segments<S, RB>(p, it, u, u_end, segs, &n_segs);
+        u = list_segments<S, kSegs>(p, it, u, u_end, segs, &n_segs);
         nx_seg = -1;
         nx_end = 0;
         int fill = stage == 0 ? ST - 1 : stage - 1, calls = ST + 1;

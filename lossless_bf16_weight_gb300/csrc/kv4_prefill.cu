@@ -1,0 +1,629 @@
+// Attention over the 4-bit paged cache for sequences with many rows (new
+// tokens x query heads of a kv head): prompts and their chunks.
+//
+// Bound by the tensor cores and by what stands around them: every key of an
+// item is unpacked once for 256 rows, and every score takes its exponential.
+// One persistent CTA an SM takes an equal share of all (256 rows x 128 keys)
+// steps (kv4_attn.cuh).  Warp roles:
+//   softmax   warps 0-3 and 4-7: one thread a row of the upper and lower 128
+//             rows.  It reads its row of S from tensor memory, applies the keys'
+//             scales and offsets and the mask, takes the exponentials and writes
+//             P s (BF16) over S, where the second product reads it; at the end
+//             of an item it writes the row's output.
+//   unpack    warps 8-11: codes from global memory (loaded a tile ahead) to BF16
+//             tiles in shared memory, K as [keys][dims], V transposed as
+//             [dims][keys], both K-major for the tensor cores; the scales and
+//             offsets; the queries of an item.
+//   MMA       warp 12, one thread: S = Q K^T and O += (P s) V with
+//             tcgen05.mma, 128 rows each, in the order S0 S1 | PV0 S0' PV1 S1' | ...,
+//             so that one half's softmax runs beside the other half's products.
+// Both products take the codes as they are (Codes in kv4_codes.cuh: integers in units
+// of 2^-133, no rounded K or V), the queries and probabilities scaled up
+// against them.  The running maximum is only raised when a score passes it by
+// 2^24, so that O is rarely rescaled.
+#include <cmath>
+
+#include "kernels.h"
+#include "kv4_attn.cuh"
+#include "kv4_codes.cuh"
+#include "tc.cuh"
+
+namespace uw {
+
+namespace {
+
+constexpr int kRows = 256, kKeys = 128;
+constexpr int kSoftmax = 256, kUnpack = 128;          // threads; 13 warps leave each 128 registers
+constexpr int kThreads = kSoftmax + kUnpack + 32;
+constexpr int kItemCost = 3;                          // what an item costs beyond its steps, in steps
+constexpr int kSegs = 32;
+constexpr int kStages = 2, kParStages = 4;
+constexpr float kRaise = 24.f;                        // log2 headroom of a probability
+constexpr uint32_t kTmemCols = 512;
+
+enum Bar {
+    kQFull, kQEmpty, kKFull, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages,
+    kParFull = kVEmpty + kStages, kSFull = kParFull + kParStages, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+    kBars = kPvDone + 2
+};
+
+struct Shared {
+    uint64_t bars[kBars];
+    uint64_t listed_to;
+    Seg segs[kSegs];
+    float qs[2][kRows];                    // sums of the queries, of this item and the next
+    float4 kpar[kParStages][kKeys / 2];    // (a, a', b, b') of two keys: y = a (q.c) + b sum q
+    float4 vpar[kParStages][kKeys / 2];    // (s, s', mid, mid')
+    Row<kThreads> row;
+    uint32_t tmem, dead, arrived;
+    int n_segs;
+};
+
+template <int D>
+constexpr uint32_t kTileBytes = kKeys * D * 2;  // 128 rows of Q, 128 keys of K, D dimensions of V
+template <int D>
+constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * size_t(kTileBytes<D>);
+
+// A wait that every thread of a role makes at the same place.  One that runs
+// out marks the kernel dead: all later waits return at once, every role
+// walks through its remaining steps without waiting, and the status word tells.
+__device__ __forceinline__ void wait(Shared &sh, uint32_t bar, uint32_t parity, uint32_t *status) {
+    if (*reinterpret_cast<volatile uint32_t *>(&sh.dead))
+        return;
+    if (!mbar_wait(bar, parity, status, kStatusTimeout))
+        *reinterpret_cast<volatile uint32_t *>(&sh.dead) = 1;
+}
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Byte offset of 16-byte chunk c (8 values) of row r in a tile of `rows` rows:
+// blocks of 64 values, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_at(int r, int c, int rows) {
+    return uint32_t(c >> 3) * uint32_t(rows) * 128u + sw128_offset(uint32_t(r), uint32_t(c & 7));
+}
+
+template <int D>
+__device__ __forceinline__ void mma_role(const AttnParams &p, Shared &sh, uint32_t bars, uint32_t q_at, uint32_t k_at,
+                                         uint32_t v_at, uint32_t &steps, uint32_t (&cnt)[2], uint32_t &items) {
+    constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys), kIdO = idesc_bf16_f32(128, D);
+    const uint32_t tm = sh.tmem;
+    auto score = [&](int half, uint32_t step) {
+        const uint32_t k = k_at + (step % kStages) * kTileBytes<D>, q = q_at + half * kTileBytes<D>;
+#pragma unroll
+        for (int i = 0; i < D / 16; i++)
+            mma_bf16(tm + half * kKeys, sdesc_sw128(q + (i / 4) * (128 * 128) + (i % 4) * 32),
+                     sdesc_sw128(k + (i / 4) * (kKeys * 128) + (i % 4) * 32), kIdS, i > 0);
+        mma_commit(bars + 8 * (kSFull + half));
+    };
+    auto output = [&](int half, uint32_t step, bool more) {
+        const uint32_t v = v_at + (step % kStages) * kTileBytes<D>;
+#pragma unroll
+        for (int i = 0; i < kKeys / 16; i++)
+            mma_ts(tm + 256 + half * D, tm + half * kKeys + i * 8,
+                   sdesc_sw128(v + (i / 4) * (D * 128) + (i % 4) * 32), kIdO, more || i > 0);
+        mma_commit(bars + 8 * (kPvDone + half));
+    };
+    for (int s = 0; s < sh.n_segs; s++) {
+        const Seg &sg = sh.segs[s];
+        if (sg.tiles == 0)
+            continue;
+        const bool two = sg.tokens * p.group - sg.rt * kRows > 128;
+        wait(sh, bars + 8 * kQFull, items & 1, p.v.status);
+        items++;
+        for (int j = 0; j <= sg.tiles; j++, steps += j <= sg.tiles) {
+            // the scores of step j beside the outputs of step j - 1
+            const uint32_t step = steps, before = steps - 1;
+            const bool scores = j < sg.tiles, outputs = j > 0;
+            if (outputs) {
+                wait(sh, bars + 8 * kPFull, cnt[0] & 1, p.v.status);
+                wait(sh, bars + 8 * (kVFull + before % kStages), (before / kStages) & 1, p.v.status);
+                tc_fence_after();
+                output(0, before, j > 1);
+                cnt[0]++;
+            }
+            if (scores) {
+                wait(sh, bars + 8 * (kKFull + step % kStages), (step / kStages) & 1, p.v.status);
+                tc_fence_after();
+                score(0, step);
+            }
+            if (two) {
+                if (outputs) {
+                    wait(sh, bars + 8 * (kPFull + 1), cnt[1] & 1, p.v.status);
+                    tc_fence_after();
+                    output(1, before, j > 1);
+                    cnt[1]++;
+                }
+                if (scores)
+                    score(1, step);
+            }
+            if (outputs)
+                mma_commit(bars + 8 * (kVEmpty + before % kStages));
+            if (scores)
+                mma_commit(bars + 8 * (kKEmpty + step % kStages));
+            if (j == sg.tiles - 1)
+                mma_commit(bars + 8 * kQEmpty);
+        }
+    }
+    // every commit has arrived before the barriers go
+    if (steps > 0)
+        wait(sh, bars + 8 * (kVEmpty + (steps - 1) % kStages), ((steps - 1) / kStages) & 1, p.v.status);
+}
+
+template <int D>
+__device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uint32_t bars, uint32_t q_at,
+                                            uint32_t k_at, uint32_t v_at, uint32_t &steps, uint32_t &items) {
+    const Kv4View &v = p.v;
+    const int t = threadIdx.x - kSoftmax, lane = t & 31;
+    const Codes codes;
+    const int64_t block = int64_t(D + 8) << v.page_log2, page_bytes = block * v.heads;
+    const int mask = (1 << v.page_log2) - 1;
+    // K: a key; V: a word (8 dimensions) of 8 keys, VT times
+    constexpr int KC = D / 32;            // 16-byte chunks of a packed row
+    constexpr int VW = D / 8;             // words of a packed row
+    constexpr int VT = kKeys / 8 * VW / kUnpack, KG = kUnpack / VW;
+    const int key = t, vw = t % VW, kg = t / VW;
+    // Order of a V word's bytes and halves of a byte, so that eight lanes
+    // write eight different rows (mod 8) at a time.
+    uint32_t sel[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const uint32_t b = (j + vw) & 3;
+        sel[j] = b * 0x11u | (4 + b) * 0x1100u;
+    }
+    const bool odd_first = (vw >> 2) & 1;
+    const uint32_t m_a = odd_first ? codes.mask4 : codes.mask0, m_b = odd_first ? codes.mask0 : codes.mask4;
+    const uint32_t c_a = odd_first ? codes.mid4 : codes.mid0, c_b = odd_first ? codes.mid0 : codes.mid4;
+    const float a_up = p.c1 * kQDown;
+    for (int s = 0; s < sh.n_segs; s++) {
+        const Seg &sg = sh.segs[s];
+        if (sg.tiles == 0)
+            continue;
+        const int r0 = sg.rt * kRows, rows = sg.tokens * p.group;
+        const uint8_t *const base = v.pages + sg.head * block;
+        const int32_t *const table = v.table + int64_t(sg.s) * v.table_stride;
+        uint4 rk[KC];
+        uint32_t rv[VT][8], rp[2];
+        auto page_of = [&](int at) { return __ldg(table + (min(at, sg.len - 1) >> v.page_log2)); };
+        auto check = [&](int page) {
+            if (uint32_t(page) < uint32_t(v.n_pages))
+                return page;
+            atomicOr(v.status, uint32_t(kStatusBadCache));
+            return -1;
+        };
+        auto load = [&](int key0, int pk, const int (&pv)[VT]) {
+            pk = check(pk);
+            const int ka = key0 + key;
+#pragma unroll
+            for (int i = 0; i < KC; i++)
+                rk[i] = make_uint4(0, 0, 0, 0);
+            rp[0] = rp[1] = 0;
+            if (pk >= 0 && ka < sg.len) {
+                const uint8_t *b = base + pk * page_bytes;
+                const uint4 *src = reinterpret_cast<const uint4 *>(b + (ka & mask) * (D / 2));
+#pragma unroll
+                for (int i = 0; i < KC; i++)
+                    rk[i] = __ldg(src + i);
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    rp[i] = __ldg(reinterpret_cast<const uint32_t *>(b + kv4_params<D>(v.page_log2, ka & mask, i)));
+            }
+#pragma unroll
+            for (int n = 0; n < VT; n++) {
+                const int va = key0 + 8 * (kg + n * KG), pg = check(pv[n]);
+                const uint8_t *b = base + pg * page_bytes + kv4_codes<D>(v.page_log2, va & mask, 1) + vw * 4;
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    rv[n][i] = pg >= 0 && va + i < sg.len ? __ldg(reinterpret_cast<const uint32_t *>(b + i * (D / 2))) : 0u;
+            }
+        };
+        const int first = sg.first * kKeys;
+        int pk, pv[VT];
+        auto pages = [&](int key0) {
+            pk = page_of(key0 + key);
+#pragma unroll
+            for (int n = 0; n < VT; n++)
+                pv[n] = page_of(key0 + 8 * (kg + n * KG));
+        };
+        pages(first);
+
+        // queries: a thread writes two rows, in the order the codes of a word come out in
+        wait(sh, bars + 8 * kQEmpty, (items & 1) ^ 1, v.status);
+        for (int rr = t; rr < kRows; rr += kUnpack) {
+            const bool in = rr < rows - r0;
+            const int i = p.by_group.of(in ? r0 + rr : 0);
+            const int64_t tok = sg.t0 + i, head = sg.head * p.group + (r0 + rr - i * p.group);
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q.p + tok * p.q.ts + head * p.q.hs);
+            const uint32_t to = q_at + (rr >> 7) * kTileBytes<D>;
+            float sum = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; c++) {
+                const uint4 x = in ? src[c] : make_uint4(0, 0, 0, 0);
+                const uint32_t a[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    sum += bf16_lo(a[k]) + bf16_hi(a[k]);
+                sts128(to + tile_at(rr & 127, c, 128), mul2_bf16(__byte_perm(x.x, x.z, 0x5410), kQUpLow),
+                       mul2_bf16(__byte_perm(x.x, x.z, 0x7632), kQUpHigh),
+                       mul2_bf16(__byte_perm(x.y, x.w, 0x5410), kQUpLow),
+                       mul2_bf16(__byte_perm(x.y, x.w, 0x7632), kQUpHigh));
+            }
+            sh.qs[items & 1][rr] = sum;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bars + 8 * kQFull);
+        items++;
+
+        load(first, pk, pv);
+        if (sg.tiles > 1)
+            pages(first + kKeys);
+        for (int j = 0; j < sg.tiles; j++, steps++) {
+            const uint32_t stage = steps % kStages, turn = (steps / kStages) & 1, par = steps % kParStages;
+            uint4 ck[KC];
+            uint32_t cv[VT][8];
+            const uint32_t cp[2] = {rp[0], rp[1]};
+#pragma unroll
+            for (int i = 0; i < KC; i++)
+                ck[i] = rk[i];
+#pragma unroll
+            for (int n = 0; n < VT; n++)
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    cv[n][i] = rv[n][i];
+            if (j + 1 < sg.tiles) {
+                load(first + (j + 1) * kKeys, pk, pv);
+                if (j + 2 < sg.tiles)
+                    pages(first + (j + 2) * kKeys);
+            }
+            {
+                float *const kd = reinterpret_cast<float *>(sh.kpar[par]) + (key >> 1) * 4 + (key & 1);
+                float *const vd = reinterpret_cast<float *>(sh.vpar[par]) + (key >> 1) * 4 + (key & 1);
+                kd[0] = bf16_lo(cp[0]) * a_up;
+                kd[2] = bf16_hi(cp[0]) * p.c1;
+                vd[0] = bf16_lo(cp[1]) * kPUp;
+                vd[2] = fmaf(8.f, bf16_lo(cp[1]), bf16_hi(cp[1]));
+            }
+            wait(sh, bars + 8 * (kKEmpty + stage), turn ^ 1, v.status);
+            const uint32_t kt = k_at + stage * kTileBytes<D>;
+#pragma unroll
+            for (int i = 0; i < KC; i++) {
+                const uint32_t a[4] = {ck[i].x, ck[i].y, ck[i].z, ck[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const uint32_t y = a[k] >> 8;
+                    sts128(kt + tile_at(key, i * 4 + k, kKeys), codes.low(a[k]), codes.high(a[k]),
+                           codes.low(y), codes.high(y));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bars + 8 * (kKFull + stage));
+                mbar_arrive(bars + 8 * (kParFull + par));
+            }
+            wait(sh, bars + 8 * (kVEmpty + stage), turn ^ 1, v.status);
+            const uint32_t vt = v_at + stage * kTileBytes<D>;
+#pragma unroll
+            for (int n = 0; n < VT; n++)
+#pragma unroll
+                for (int jj = 0; jj < 4; jj++) {
+                    uint32_t e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        e[i] = __byte_perm(cv[n][2 * i], cv[n][2 * i + 1], sel[jj]);
+                    const int d = 8 * vw + 2 * ((jj + vw) & 3), c = kg + n * KG;
+                    sts128(vt + tile_at(d + odd_first, c, D), sub2(e[0] & m_a, c_a), sub2(e[1] & m_a, c_a),
+                           sub2(e[2] & m_a, c_a), sub2(e[3] & m_a, c_a));
+                    sts128(vt + tile_at(d + !odd_first, c, D), sub2(e[0] & m_b, c_b), sub2(e[1] & m_b, c_b),
+                           sub2(e[2] & m_b, c_b), sub2(e[3] & m_b, c_b));
+                }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bars + 8 * (kVFull + stage));
+        }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, uint32_t bars, uint64_t total,
+                                             uint32_t workers, uint64_t cut0, uint32_t &steps, uint32_t &items,
+                                             uint32_t &cnt) {
+    constexpr int PF = kRows * (D + 2);
+    const int half = threadIdx.x >> 7, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+    const uint32_t s_tm = sh.tmem + lanes + half * kKeys, o_tm = sh.tmem + lanes + 256 + half * D;
+    for (int sgi = 0; sgi < sh.n_segs; sgi++) {
+        const Seg &sg = sh.segs[sgi];
+        const int r0 = sg.rt * kRows, rows = sg.tokens * p.group;
+        const int r = r0 + int(threadIdx.x);
+        const bool active = r0 + 128 * half < rows;  // this half has rows
+        const Seq sq{sg.t0, sg.tokens, sg.len};
+        float m = -INFINITY;
+        uint64_t l2 = 0, z2 = 0;
+        for (int j = 0; j < sg.tiles; j++) {
+            const uint32_t step = steps + j, par = step % kParStages;
+            if (!active)
+                continue;
+            const int key0 = (sg.first + j) * kKeys;
+            wait(sh, bars + 8 * (kParFull + par), (step / kParStages) & 1, p.v.status);
+            const float qsum = sh.qs[items & 1][threadIdx.x];
+            const uint64_t qs = pair2(qsum, qsum);
+            wait(sh, bars + 8 * (kSFull + half), cnt & 1, p.v.status);
+            tc_fence_after();
+            const bool open = key0 < sg.all_lo || key0 + kKeys > sg.all_hi;
+            int lo = 0, hi = kKeys;  // the row's keys in this tile
+            if (open) {
+                const int i = p.by_group.of(min(r, rows - 1));
+                const KeyRange kr = visible(p, sq, i, i);
+                lo = kr.lo - key0;
+                hi = min(kr.hi, sg.len) - key0;
+            }
+            const ulonglong2 *const kp = reinterpret_cast<const ulonglong2 *>(sh.kpar[par]);
+            const ulonglong2 *const vp = reinterpret_cast<const ulonglong2 *>(sh.vpar[par]);
+#pragma unroll 1
+            for (int c = 0; c < kKeys / 32; c++) {
+                uint32_t x[32];
+                tmem_ld32(s_tm + 32 * c, x);
+                tmem_ld_wait();
+                uint64_t y[16];
+                const float m0 = m == -INFINITY ? 0.f : m;
+                const uint64_t mm = pair2(-m0, -m0);
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const ulonglong2 ab = kp[16 * c + i];
+                    y[i] = fma2(pair2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), ab.x, fma2(ab.y, qs, mm));
+                }
+                if (open) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const float2 f = unpair(y[i]);
+                        const int k = 32 * c + 2 * i;
+                        y[i] = pair2(k >= lo && k < hi ? f.x : -INFINITY, k + 1 >= lo && k + 1 < hi ? f.y : -INFINITY);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const float2 f = unpair(y[i]);
+                    top = fmaxf(top, fmaxf(f.x, f.y));
+                }
+                if (__any_sync(0xffffffffu, top > kRaise || (m == -INFINITY && top > -INFINITY))) {
+                    // Raise the maximum: what the row has so far is scaled down, its
+                    // probabilities of this tile among it.
+                    const float m2 = fmaxf(m, m0 + top);
+                    const float m20 = m2 == -INFINITY ? 0.f : m2;
+                    const float f = m == -INFINITY ? 0.f : exp2_fast(m - m20);
+                    const uint64_t ff = pair2(f, f), d = pair2(m0 - m20, m0 - m20);
+                    l2 = mul2(l2, ff);
+                    z2 = mul2(z2, ff);
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        y[i] = add2(y[i], d);
+                    tmem_st_wait();
+                    for (int c2 = 0; c2 < c; c2++) {
+                        uint32_t w[16];
+                        tmem_ld16(s_tm + 16 * c2, w);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            w[i] = bf16_pack(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
+                        tmem_st16(s_tm + 16 * c2, w);
+                    }
+                    if (j > 0) {
+                        wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
+                        tc_fence_after();
+                        for (int d0 = 0; d0 < D; d0 += 16) {
+                            uint32_t w[16];
+                            tmem_ld16(o_tm + d0, w);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; i++)
+                                w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                            tmem_st16(o_tm + d0, w);
+                        }
+                    }
+                    m = m2;
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const ulonglong2 sm = vp[16 * c + i];
+                    const float2 f = unpair(y[i]);
+                    const uint64_t pr = pair2(exp2_fast(f.x), exp2_fast(f.y));
+                    l2 = add2(l2, pr);
+                    uint64_t ps = mul2(pr, sm.x);
+                    if (open) {  // a masked key's scale may be anything
+                        const float2 a = unpair(ps), b = unpair(mul2(pr, sm.y));
+                        const bool in0 = f.x != -INFINITY, in1 = f.y != -INFINITY;
+                        ps = pair2(in0 ? a.x : 0.f, in1 ? a.y : 0.f);
+                        z2 = add2(z2, pair2(in0 ? b.x : 0.f, in1 ? b.y : 0.f));
+                    } else {
+                        z2 = fma2(pr, sm.y, z2);
+                    }
+                    const float2 a = unpair(ps);
+                    pk[i] = bf16_pack(a.x, a.y);
+                }
+                tmem_st16(s_tm + 16 * c, pk);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bars + 8 * (kPFull + half));
+            cnt++;
+        }
+        steps += sg.tiles;
+        items += sg.tiles > 0;
+
+        // the row's output
+        const float2 lf = unpair(l2), zf = unpair(z2);
+        const float l = lf.x + lf.y, z = zf.x + zf.y;
+        const bool whole = sg.tiles == sg.of, valued = active && sg.tiles > 0;
+        const int slot = cut0 > sg.u0 ? 0 : 1;
+        float *const part = p.parts + (2 * uint64_t(blockIdx.x) + slot) * PF;
+        if (valued) {
+            wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
+            tc_fence_after();
+        }
+        if (active) {
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 16) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    w[i] = 0;
+                if (valued) {
+                    tmem_ld16(o_tm + d0, w);
+                    tmem_ld_wait();
+                }
+                float o[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    o[i] = fmaf(__uint_as_float(w[i]), i & 1 ? kPDownHigh : kPDownLow, z);
+                if (r < rows) {
+                    if (whole) {
+                        store_dims<16>(p, sg.t0, sg.head, r, d0, o, m, l);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            reinterpret_cast<float4 *>(part)[(d0 / 4 + i) * kRows + threadIdx.x] =
+                                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+            }
+            if (!whole) {
+                part[kRows * D + threadIdx.x] = m;
+                part[kRows * D + kRows + threadIdx.x] = l;
+            }
+        }
+        if (!whole) {
+            // An item that goes on in other CTAs: whoever arrives last joins the parts.
+            const uint32_t f = share_of(sg.u0, total, workers), e = share_of(sg.u0 + sg.of - 1, total, workers);
+            __threadfence();
+            softmax_sync();
+            if (threadIdx.x == 0) {
+                sh.arrived = atomicAdd(p.counters + f, 1u) == e - f;
+                if (sh.arrived)
+                    p.counters[f] = 0;  // ready for the next call
+            }
+            softmax_sync();
+            if (sh.arrived && r < rows) {
+                __threadfence();
+                auto at = [&](uint32_t i) { return p.parts + (2 * uint64_t(i) + (i == f ? 1 : 0)) * PF; };
+                float mt = -INFINITY, lt = 0.f;
+                for (uint32_t i = f; i <= e; i++)
+                    mt = fmaxf(mt, __ldcg(at(i) + kRows * D + threadIdx.x));
+                const float m0 = mt == -INFINITY ? 0.f : mt;
+                for (uint32_t i = f; i <= e; i++)
+                    lt = fmaf(exp2_fast(__ldcg(at(i) + kRows * D + threadIdx.x) - m0),
+                              __ldcg(at(i) + kRows * D + kRows + threadIdx.x), lt);
+#pragma unroll 1
+                for (int d0 = 0; d0 < D; d0 += 16) {
+                    float o[16];
+#pragma unroll
+                    for (int k = 0; k < 16; k++)
+                        o[k] = 0.f;
+                    for (uint32_t i = f; i <= e; i++) {
+                        const float w = exp2_fast(__ldcg(at(i) + kRows * D + threadIdx.x) - m0);
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(at(i)) + (d0 / 4 + k) * kRows + threadIdx.x);
+                            o[4 * k] = fmaf(w, x.x, o[4 * k]);
+                            o[4 * k + 1] = fmaf(w, x.y, o[4 * k + 1]);
+                            o[4 * k + 2] = fmaf(w, x.z, o[4 * k + 2]);
+                            o[4 * k + 3] = fmaf(w, x.w, o[4 * k + 3]);
+                        }
+                    }
+                    store_dims<16>(p, sg.t0, sg.head, r, d0, o, mt, lt);
+                }
+            }
+            softmax_sync();  // sh.arrived is read
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const AttnParams p) {
+    using S = Sched<kRows, kKeys, kItemCost>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Shared sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t raw = smem_addr(smem_raw), q_at = (raw + 1023u) & ~1023u;
+    const uint32_t k_at = q_at + 2 * kTileBytes<D>, v_at = k_at + kStages * kTileBytes<D>;
+    const uint32_t bars = smem_addr(sh.bars);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; i++) {
+            uint32_t n = 1;  // a commit
+            if (i == kQFull || (i >= kKFull && i < kKEmpty) || (i >= kVFull && i < kVEmpty) ||
+                (i >= kParFull && i < kSFull))
+                n = kUnpack / 32;
+            else if (i >= kPFull && i < kPvDone)
+                n = 4;
+            mbar_init(bars + 8 * i, n);
+        }
+        mbar_init_fence();
+        sh.dead = 0;
+    }
+    grid_dep_launch();
+    grid_dep_wait();
+    const uint64_t total = build_row<S, kThreads, true>(p, sh.row);
+    const uint32_t workers = uint32_t(min(total, uint64_t(gridDim.x)));
+    if (blockIdx.x >= workers)
+        return;
+    if (warp == kThreads / 32 - 1)
+        tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
+    uint64_t u = mul_div(total, blockIdx.x, workers);
+    const uint64_t cut0 = u, cut1 = mul_div(total, blockIdx.x + 1, workers);
+    Item it{};
+    if (warp == 0)
+        it = locate<S>(p, sh.row, u);
+    uint32_t steps = 0, items = 0, cnt[2] = {0, 0}, own = 0;
+    tc_fence_before();
+    while (u < cut1) {
+        if (warp == 0) {
+            int n;
+            const uint64_t to = list_segments<S, kSegs>(p, it, u, cut1, sh.segs, &n);
+            if (lane == 0) {
+                sh.listed_to = to;
+                sh.n_segs = n;
+            }
+        }
+        __syncthreads();
+        tc_fence_after();
+        u = sh.listed_to;
+        if (warp < kSoftmax / 32)
+            softmax_role<D>(p, sh, bars, total, workers, cut0, steps, items, own);
+        else if (warp < (kSoftmax + kUnpack) / 32)
+            unpack_role<D>(p, sh, bars, q_at, k_at, v_at, steps, items);
+        else if (lane == 0)
+            mma_role<D>(p, sh, bars, q_at, k_at, v_at, steps, cnt, items);
+        __syncthreads();
+    }
+    if (warp == kThreads / 32 - 1)
+        tmem_dealloc(sh.tmem, kTmemCols);
+}
+
+template <int D>
+uw_status launch(const AttnParams &p, int ctas, cudaStream_t st) {
+    if (!ensure_smem(kv4_prefill_kernel<D>, kSmem<D>))
+        return UW_ERR_CUDA;
+    return launch_overlapped(kv4_prefill_kernel<D>, dim3(unsigned(ctas)), dim3(kThreads), kSmem<D>, st, p) ==
+                   cudaSuccess
+               ? UW_OK
+               : UW_ERR_CUDA;
+}
+
+}  // namespace
+
+int kv4_prefill_ctas() { return sm_count(); }
+
+size_t kv4_prefill_part_floats(int head_dim) { return 2 * size_t(kv4_prefill_ctas()) * kRows * (head_dim + 2); }
+
+uw_status launch_kv4_prefill(const AttnParams &p, int head_dim, cudaStream_t st) {
+    const int n = kv4_prefill_ctas();
+    return head_dim == 128 ? launch<128>(p, n, st) : launch<64>(p, n, st);
+}
+
+}  // namespace uw
