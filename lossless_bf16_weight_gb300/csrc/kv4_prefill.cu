@@ -5,11 +5,11 @@
 // item is unpacked once for 256 rows, and every score takes its exponential.
 // One persistent CTA an SM takes an equal share of all (256 rows x 128 keys)
 // steps (kv4_attn.cuh).  Warp roles:
-//   softmax   warps 0-3 and 4-7: one thread a row of the upper and lower 128
-//             rows.  It reads its row of S from tensor memory, applies the keys'
-//             scales and offsets and the mask, takes the exponentials and writes
-//             P s (BF16) over S, where the second product reads it; at the end
-//             of an item it writes the row's output.
+//   softmax   warps 0-3 and 4-7: the upper and lower 128 rows, 32 a warp.  They
+//             read S from tensor memory, apply the keys' scales and offsets and
+//             the mask, take the exponentials and write P s (BF16) over S, where
+//             the second product reads it; at the end of an item they write
+//             the rows' output.
 //   unpack    warps 8-11: codes from global memory (loaded a tile ahead) to BF16
 //             tiles in shared memory, K as [keys][dims], V transposed as
 //             [dims][keys], both K-major for the tensor cores; the scales and
@@ -22,6 +22,7 @@
 // against them.  The running maximum is only raised when a score passes it by
 // 2^24, so that O is rarely rescaled.
 #include <cmath>
+#include <type_traits>
 
 #include "kernels.h"
 #include "kv4_attn.cuh"
@@ -331,7 +332,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                                              uint32_t workers, uint64_t cut0, uint32_t &steps, uint32_t &items,
                                              uint32_t &cnt) {
     constexpr int PF = kRows * (D + 2);
-    const int half = threadIdx.x >> 7, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = threadIdx.x >> 7, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t s_tm = sh.tmem + lanes + half * kKeys, o_tm = sh.tmem + lanes + 256 + half * D;
     for (int sgi = 0; sgi < sh.n_segs; sgi++) {
@@ -340,113 +341,168 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
         const int r = r0 + int(threadIdx.x);
         const bool active = r0 + 128 * half < rows;  // this half has rows
         const Seq sq{sg.t0, sg.tokens, sg.len};
-        float m = -INFINITY;
-        uint64_t l2 = 0, z2 = 0;
+        // The warp's 32 rows lie like the rows of a matrix product's fragment: a
+        // thread has rows g + 8 i (i < 4) and of them the key pairs 8 k + 2 t, so that a
+        // pair's scales and offsets are read once for four rows.
+        float m[4], qsum[4];
+        uint64_t l2[4], z2[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            m[i] = -INFINITY;
+            l2[i] = z2[i] = 0;
+        }
         for (int j = 0; j < sg.tiles; j++) {
             const uint32_t step = steps + j, par = step % kParStages;
             if (!active)
                 continue;
             const int key0 = (sg.first + j) * kKeys;
             wait(sh, bars + 8 * (kParFull + par), (step / kParStages) & 1, p.v.status);
-            const float qsum = sh.qs[items & 1][threadIdx.x];
-            const uint64_t qs = pair2(qsum, qsum);
+            if (j == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    qsum[i] = sh.qs[items & 1][32 * warp + g + 8 * i];
+            }
             wait(sh, bars + 8 * (kSFull + half), cnt & 1, p.v.status);
             tc_fence_after();
             const bool open = key0 < sg.all_lo || key0 + kKeys > sg.all_hi;
-            int lo = 0, hi = kKeys;  // the row's keys in this tile
-            if (open) {
-                const int i = p.by_group.of(min(r, rows - 1));
-                const KeyRange kr = visible(p, sq, i, i);
-                lo = kr.lo - key0;
-                hi = min(kr.hi, sg.len) - key0;
-            }
-            const ulonglong2 *const kp = reinterpret_cast<const ulonglong2 *>(sh.kpar[par]);
-            const ulonglong2 *const vp = reinterpret_cast<const ulonglong2 *>(sh.vpar[par]);
+            auto tile = [&](auto masked) {
+                constexpr bool kOpen = decltype(masked)::value;
+                int lo[4], hi[4];  // the rows' keys in this tile, less the thread's first
+                if constexpr (kOpen) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int tok = p.by_group.of(min(r0 + 32 * warp + g + 8 * i, rows - 1));
+                        const KeyRange kr = visible(p, sq, tok, tok);
+                        lo[i] = kr.lo - key0 - 2 * t;
+                        hi[i] = min(kr.hi, sg.len) - key0 - 2 * t;
+                    }
+                }
+                const ulonglong2 *const kp = reinterpret_cast<const ulonglong2 *>(sh.kpar[par]) + t;
+                const ulonglong2 *const vp = reinterpret_cast<const ulonglong2 *>(sh.vpar[par]) + t;
 #pragma unroll 1
-            for (int c = 0; c < kKeys / 32; c++) {
-                uint32_t x[32];
-                tmem_ld32(s_tm + 32 * c, x);
-                tmem_ld_wait();
-                uint64_t y[16];
-                const float m0 = m == -INFINITY ? 0.f : m;
-                const uint64_t mm = pair2(-m0, -m0);
-                float top = -INFINITY;
+                for (int c = 0; c < kKeys / 32; c++) {
+                    uint32_t x[32];  // [16 rows' half][key group][row g, g + 8][pair]
+                    tmem_ld_16x256_x4(s_tm + 32 * c, x);
+                    tmem_ld_16x256_x4(s_tm + 32 * c + (16u << 16), x + 16);
+                    tmem_ld_wait();
+                    uint64_t y[4][4];  // [row][key group]
+                    float top[4];
+                    uint64_t qs[4], mm[4];
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const ulonglong2 ab = kp[16 * c + i];
-                    y[i] = fma2(pair2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), ab.x, fma2(ab.y, qs, mm));
-                }
-                if (open) {
-#pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const float2 f = unpair(y[i]);
-                        const int k = 32 * c + 2 * i;
-                        y[i] = pair2(k >= lo && k < hi ? f.x : -INFINITY, k + 1 >= lo && k + 1 < hi ? f.y : -INFINITY);
+                    for (int i = 0; i < 4; i++) {
+                        const float m0 = m[i] == -INFINITY ? 0.f : -m[i];
+                        qs[i] = pair2(qsum[i], qsum[i]);
+                        mm[i] = pair2(m0, m0);
+                        top[i] = -INFINITY;
                     }
-                }
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const float2 f = unpair(y[i]);
-                    top = fmaxf(top, fmaxf(f.x, f.y));
-                }
-                if (__any_sync(0xffffffffu, top > kRaise || (m == -INFINITY && top > -INFINITY))) {
-                    // Raise the maximum: what the row has so far is scaled down, its
-                    // probabilities of this tile among it.
-                    const float m2 = fmaxf(m, m0 + top);
-                    const float m20 = m2 == -INFINITY ? 0.f : m2;
-                    const float f = m == -INFINITY ? 0.f : exp2_fast(m - m20);
-                    const uint64_t ff = pair2(f, f), d = pair2(m0 - m20, m0 - m20);
-                    l2 = mul2(l2, ff);
-                    z2 = mul2(z2, ff);
+                    for (int k = 0; k < 4; k++) {
+                        const ulonglong2 ab = kp[16 * c + 4 * k];
 #pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        y[i] = add2(y[i], d);
-                    tmem_st_wait();
-                    for (int c2 = 0; c2 < c; c2++) {
-                        uint32_t w[16];
-                        tmem_ld16(s_tm + 16 * c2, w);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; i++)
-                            w[i] = bf16_pack(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
-                        tmem_st16(s_tm + 16 * c2, w);
-                    }
-                    if (j > 0) {
-                        wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
-                        tc_fence_after();
-                        for (int d0 = 0; d0 < D; d0 += 16) {
-                            uint32_t w[16];
-                            tmem_ld16(o_tm + d0, w);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; i++)
-                                w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-                            tmem_st16(o_tm + d0, w);
+                        for (int i = 0; i < 4; i++) {
+                            const uint32_t *const w = x + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
+                            y[i][k] = fma2(pair2(__uint_as_float(w[0]), __uint_as_float(w[1])), ab.x,
+                                           fma2(ab.y, qs[i], mm[i]));
+                            if constexpr (kOpen) {
+                                const float2 f = unpair(y[i][k]);
+                                const int at = 32 * c + 8 * k;
+                                y[i][k] = pair2(at >= lo[i] && at < hi[i] ? f.x : -INFINITY,
+                                                at + 1 >= lo[i] && at + 1 < hi[i] ? f.y : -INFINITY);
+                            }
+                            const float2 f = unpair(y[i][k]);
+                            top[i] = fmaxf(top[i], fmaxf(f.x, f.y));
                         }
                     }
-                    m = m2;
-                }
-                uint32_t pk[16];
+                    bool raise = false;
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const ulonglong2 sm = vp[16 * c + i];
-                    const float2 f = unpair(y[i]);
-                    const uint64_t pr = pair2(exp2_fast(f.x), exp2_fast(f.y));
-                    l2 = add2(l2, pr);
-                    uint64_t ps = mul2(pr, sm.x);
-                    if (open) {  // a masked key's scale may be anything
-                        const float2 a = unpair(ps), b = unpair(mul2(pr, sm.y));
-                        const bool in0 = f.x != -INFINITY, in1 = f.y != -INFINITY;
-                        ps = pair2(in0 ? a.x : 0.f, in1 ? a.y : 0.f);
-                        z2 = add2(z2, pair2(in0 ? b.x : 0.f, in1 ? b.y : 0.f));
-                    } else {
-                        z2 = fma2(pr, sm.y, z2);
+                    for (int i = 0; i < 4; i++)
+                        raise = raise || top[i] > kRaise || (m[i] == -INFINITY && top[i] > -INFINITY);
+                    if (__any_sync(0xffffffffu, raise)) {
+                        // Raise the maxima: what the rows have so far is scaled down, their
+                        // probabilities of this tile among it.
+                        float f[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+                            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+                            const float m0 = m[i] == -INFINITY ? 0.f : m[i];
+                            const float m2 = fmaxf(m[i], m0 + top[i]), m20 = m2 == -INFINITY ? 0.f : m2;
+                            f[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - m20);
+                            const uint64_t ff = pair2(f[i], f[i]), d = pair2(m0 - m20, m0 - m20);
+                            l2[i] = mul2(l2[i], ff);
+                            z2[i] = mul2(z2[i], ff);
+#pragma unroll
+                            for (int k = 0; k < 4; k++)
+                                y[i][k] = add2(y[i][k], d);
+                            m[i] = m2;
+                        }
+                        tmem_st_wait();
+#pragma unroll 1
+                        for (int c2 = 0; c2 < 2 * c; c2++) {
+                            const uint32_t at = s_tm + 16 * (c2 >> 1) + (uint32_t(16 * (c2 & 1)) << 16);
+                            const float fa = c2 & 1 ? f[2] : f[0], fb = c2 & 1 ? f[3] : f[1];
+                            uint32_t w[8];
+                            tmem_ld_16x128_x4(at, w);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                w[2 * i] = bf16_pack(bf16_lo(w[2 * i]) * fa, bf16_hi(w[2 * i]) * fa);
+                                w[2 * i + 1] = bf16_pack(bf16_lo(w[2 * i + 1]) * fb, bf16_hi(w[2 * i + 1]) * fb);
+                            }
+                            tmem_st_16x128_x4(at, w);
+                        }
+                        if (j > 0) {
+                            // the output has a row a thread
+                            float fo = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const float o = __shfl_sync(0xffffffffu, f[i], 4 * (lane & 7));
+                                fo = (lane >> 3) == i ? o : fo;
+                            }
+                            wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int d0 = 0; d0 < D; d0 += 16) {
+                                uint32_t w[16];
+                                tmem_ld16(o_tm + d0, w);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; i++)
+                                    w[i] = __float_as_uint(__uint_as_float(w[i]) * fo);
+                                tmem_st16(o_tm + d0, w);
+                            }
+                        }
                     }
-                    const float2 a = unpair(ps);
-                    pk[i] = bf16_pack(a.x, a.y);
+                    uint32_t pk[16];  // [16 rows' half][key group][row g, g + 8]
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const ulonglong2 sm = vp[16 * c + 4 * k];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const float2 f = unpair(y[i][k]);
+                            const uint64_t pr = pair2(exp2_fast(f.x), exp2_fast(f.y));
+                            l2[i] = add2(l2[i], pr);
+                            uint64_t ps = mul2(pr, sm.x);
+                            if constexpr (kOpen) {  // a masked key's scale may be anything
+                                const float2 a = unpair(ps), b = unpair(mul2(pr, sm.y));
+                                const bool in0 = f.x != -INFINITY, in1 = f.y != -INFINITY;
+                                ps = pair2(in0 ? a.x : 0.f, in1 ? a.y : 0.f);
+                                z2[i] = add2(z2[i], pair2(in0 ? b.x : 0.f, in1 ? b.y : 0.f));
+                            } else {
+                                z2[i] = fma2(pr, sm.y, z2[i]);
+                            }
+                            const float2 a = unpair(ps);
+                            pk[8 * (i >> 1) + 2 * k + (i & 1)] = bf16_pack(a.x, a.y);
+                        }
+                    }
+                    tmem_st_16x128_x4(s_tm + 16 * c, pk);
+                    tmem_st_16x128_x4(s_tm + 16 * c + (16u << 16), pk + 8);
                 }
-                tmem_st16(s_tm + 16 * c, pk);
-            }
+            };
+            if (open)
+                tile(std::true_type());
+            else
+                tile(std::false_type());
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -457,9 +513,27 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
         steps += sg.tiles;
         items += sg.tiles > 0;
 
-        // the row's output
-        const float2 lf = unpair(l2), zf = unpair(z2);
-        const float l = lf.x + lf.y, z = zf.x + zf.y;
+        // From here on a thread has one row: its maximum and sums from the four
+        // threads that had them.
+        float row_m = 0.f, l = 0.f, z = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 lf = unpair(l2[i]), zf = unpair(z2[i]);
+            float ls = lf.x + lf.y, zs = zf.x + zf.y;
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                ls += __shfl_xor_sync(0xffffffffu, ls, o);
+                zs += __shfl_xor_sync(0xffffffffu, zs, o);
+            }
+            const float mi = __shfl_sync(0xffffffffu, m[i], 4 * (lane & 7));
+            ls = __shfl_sync(0xffffffffu, ls, 4 * (lane & 7));
+            zs = __shfl_sync(0xffffffffu, zs, 4 * (lane & 7));
+            if ((lane >> 3) == i) {
+                row_m = mi;
+                l = ls;
+                z = zs;
+            }
+        }
         const bool whole = sg.tiles == sg.of, valued = active && sg.tiles > 0;
         const int slot = cut0 > sg.u0 ? 0 : 1;
         float *const part = p.parts + (2 * uint64_t(blockIdx.x) + slot) * PF;
@@ -484,7 +558,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                     o[i] = fmaf(__uint_as_float(w[i]), i & 1 ? kPDownHigh : kPDownLow, z);
                 if (r < rows) {
                     if (whole) {
-                        store_dims<16>(p, sg.t0, sg.head, r, d0, o, m, l);
+                        store_dims<16>(p, sg.t0, sg.head, r, d0, o, row_m, l);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; i++)
@@ -494,7 +568,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                 }
             }
             if (!whole) {
-                part[kRows * D + threadIdx.x] = m;
+                part[kRows * D + threadIdx.x] = row_m;
                 part[kRows * D + kRows + threadIdx.x] = l;
             }
         }
