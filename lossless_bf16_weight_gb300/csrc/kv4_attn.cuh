@@ -335,10 +335,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // Two fp32 values in one 64-bit register: one instruction for both.
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
-    return uint64_t(__float_as_uint(a)) | uint64_t(__float_as_uint(b)) << 32;
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
 __device__ __forceinline__ float2 unpair(uint64_t v) {
-    return make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;

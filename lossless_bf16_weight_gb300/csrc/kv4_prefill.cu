@@ -14,9 +14,10 @@
 //             tiles in shared memory, K as [keys][dims], V transposed as
 //             [dims][keys], both K-major for the tensor cores; the scales and
 //             offsets; the queries of an item.
-//   MMA       warp 12, one thread: S = Q K^T and O += (P s) V with
-//             tcgen05.mma, 128 rows each, in the order S0 S1 | PV0 S0' PV1 S1' | ...,
-//             so that one half's softmax runs beside the other half's products.
+//   MMA       warp 12, one elected thread (the rest of the warp walks along, which
+//             keeps descriptors and addresses in uniform registers): S = Q K^T and O += (P s) V with
+//             tcgen05.mma, 128 rows and half a step's keys each: while the softmax
+//             works on one half of the keys, the products of the other half run.
 // Both products take the codes as they are (Codes in kv4_codes.cuh: integers in units
 // of 2^-133, no rounded K or V), the queries and probabilities scaled up
 // against them.  The running maximum is only raised when a score passes it by
@@ -44,8 +45,9 @@ constexpr uint32_t kTmemCols = 512;
 
 enum Bar {
     kQFull, kQEmpty, kKFull, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages,
-    kParFull = kVEmpty + kStages, kSFull = kParFull + kParStages, kPFull = kSFull + 2, kPvDone = kPFull + 2,
-    kBars = kPvDone + 2
+    kParFull = kVEmpty + kStages,
+    kSFull = kParFull + kParStages, kPFull = kSFull + 4,  // [rows' half][keys' half]
+    kPvDone = kPFull + 4, kBars = kPvDone + 4
 };
 
 struct Shared {
@@ -69,7 +71,7 @@ constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * size_t(kTileBytes<D>);
 // out marks the kernel dead: all later waits return at once, every role
 // walks through its remaining steps without waiting, and the status word tells.
 __device__ __forceinline__ void wait(Shared &sh, uint32_t bar, uint32_t parity, uint32_t *status) {
-    if (*reinterpret_cast<volatile uint32_t *>(&sh.dead))
+    if (mbar_try_wait(bar, parity) || *reinterpret_cast<volatile uint32_t *>(&sh.dead))
         return;
     if (!mbar_wait(bar, parity, status, kStatusTimeout))
         *reinterpret_cast<volatile uint32_t *>(&sh.dead) = 1;
@@ -86,23 +88,38 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c, int rows) {
 template <int D>
 __device__ __forceinline__ void mma_role(const AttnParams &p, Shared &sh, uint32_t bars, uint32_t q_at, uint32_t k_at,
                                          uint32_t v_at, uint32_t &steps, uint32_t (&cnt)[2], uint32_t &items) {
-    constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys), kIdO = idesc_bf16_f32(128, D);
+    constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys / 2), kIdO = idesc_bf16_f32(128, D);
     const uint32_t tm = sh.tmem;
-    auto score = [&](int half, uint32_t step) {
-        const uint32_t k = k_at + (step % kStages) * kTileBytes<D>, q = q_at + half * kTileBytes<D>;
+    // Descriptors of the tiles; a step of 16 values along the product adds 32
+    // bytes, the next block of 64 values `rows` * 128 (both in units of 16 bytes).
+    const uint64_t q_desc = sdesc_sw128(q_at), k_desc = sdesc_sw128(k_at), v_desc = sdesc_sw128(v_at);
+    auto at = [](int i, int rows) { return uint64_t((i / 4) * (rows * 8) + (i % 4) * 2); };
+    // Scores of 128 rows and half a step's keys, and the output of the same.
+    auto score = [&](int half, uint32_t step, int h) {
+        const uint64_t q = q_desc + half * (kTileBytes<D> >> 4);
+        const uint64_t k = k_desc + (step % kStages) * (kTileBytes<D> >> 4) + h * (kKeys / 2 * 8);
+        if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < D / 16; i++)
-            mma_bf16(tm + half * kKeys, sdesc_sw128(q + (i / 4) * (128 * 128) + (i % 4) * 32),
-                     sdesc_sw128(k + (i / 4) * (kKeys * 128) + (i % 4) * 32), kIdS, i > 0);
-        mma_commit(bars + 8 * (kSFull + half));
+            for (int i = 0; i < D / 16; i++)
+                mma_bf16(tm + half * kKeys + h * (kKeys / 2), q + at(i, 128), k + at(i, kKeys), kIdS, i > 0);
+            mma_commit(bars + 8 * (kSFull + 2 * half + h));
+        }
+        __syncwarp();
     };
-    auto output = [&](int half, uint32_t step, bool more) {
-        const uint32_t v = v_at + (step % kStages) * kTileBytes<D>;
+    auto output = [&](int half, uint32_t step, int h, bool more) {
+        const uint64_t v = v_desc + (step % kStages) * (kTileBytes<D> >> 4) + h * (D * 8);
+        if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < kKeys / 16; i++)
-            mma_ts(tm + 256 + half * D, tm + half * kKeys + i * 8,
-                   sdesc_sw128(v + (i / 4) * (D * 128) + (i % 4) * 32), kIdO, more || i > 0);
-        mma_commit(bars + 8 * (kPvDone + half));
+            for (int i = 0; i < kKeys / 32; i++)
+                mma_ts(tm + 256 + half * D, tm + half * kKeys + h * (kKeys / 2) + i * 8, v + 2 * i, kIdO, more || i > 0);
+            mma_commit(bars + 8 * (kPvDone + 2 * half + h));
+        }
+        __syncwarp();
+    };
+    auto commit = [&](int bar) {
+        if (elect_one())
+            mma_commit(bars + 8 * bar);
+        __syncwarp();
     };
     for (int s = 0; s < sh.n_segs; s++) {
         const Seg &sg = sh.segs[s];
@@ -111,39 +128,39 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Shared &sh, uint32
         const bool two = sg.tokens * p.group - sg.rt * kRows > 128;
         wait(sh, bars + 8 * kQFull, items & 1, p.v.status);
         items++;
-        for (int j = 0; j <= sg.tiles; j++, steps += j <= sg.tiles) {
-            // the scores of step j beside the outputs of step j - 1
-            const uint32_t step = steps, before = steps - 1;
+        // Step j's scores beside step j - 1's outputs, by halves of the keys: while
+        // the softmax of one half runs, the other half's products do.
+        for (int j = 0; j <= sg.tiles; j++) {
+            const uint32_t step = steps + j, before = step - 1;
             const bool scores = j < sg.tiles, outputs = j > 0;
-            if (outputs) {
-                wait(sh, bars + 8 * kPFull, cnt[0] & 1, p.v.status);
-                wait(sh, bars + 8 * (kVFull + before % kStages), (before / kStages) & 1, p.v.status);
-                tc_fence_after();
-                output(0, before, j > 1);
-                cnt[0]++;
-            }
-            if (scores) {
+            if (scores)
                 wait(sh, bars + 8 * (kKFull + step % kStages), (step / kStages) & 1, p.v.status);
-                tc_fence_after();
-                score(0, step);
-            }
-            if (two) {
+            if (outputs)
+                wait(sh, bars + 8 * (kVFull + before % kStages), (before / kStages) & 1, p.v.status);
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                const int h = x >> 1, half = x & 1;
+                if (half && !two)
+                    continue;
                 if (outputs) {
-                    wait(sh, bars + 8 * (kPFull + 1), cnt[1] & 1, p.v.status);
+                    wait(sh, bars + 8 * (kPFull + 2 * half + h), cnt[half] & 1, p.v.status);
                     tc_fence_after();
-                    output(1, before, j > 1);
-                    cnt[1]++;
+                    output(half, before, h, j > 1 || h > 0);
+                    cnt[half] += h;
                 }
-                if (scores)
-                    score(1, step);
+                if (scores) {
+                    tc_fence_after();
+                    score(half, step, h);
+                }
             }
             if (outputs)
-                mma_commit(bars + 8 * (kVEmpty + before % kStages));
+                commit(kVEmpty + before % kStages);
             if (scores)
-                mma_commit(bars + 8 * (kKEmpty + step % kStages));
+                commit(kKEmpty + step % kStages);
             if (j == sg.tiles - 1)
-                mma_commit(bars + 8 * kQEmpty);
+                commit(kQEmpty);
         }
+        steps += sg.tiles;
     }
     // every commit has arrived before the barriers go
     if (steps > 0)
@@ -362,8 +379,6 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                 for (int i = 0; i < 4; i++)
                     qsum[i] = sh.qs[items & 1][32 * warp + g + 8 * i];
             }
-            wait(sh, bars + 8 * (kSFull + half), cnt & 1, p.v.status);
-            tc_fence_after();
             const bool open = key0 < sg.all_lo || key0 + kKeys > sg.all_hi;
             auto tile = [&](auto masked) {
                 constexpr bool kOpen = decltype(masked)::value;
@@ -381,6 +396,11 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                 const ulonglong2 *const vp = reinterpret_cast<const ulonglong2 *>(sh.vpar[par]) + t;
 #pragma unroll 1
                 for (int c = 0; c < kKeys / 32; c++) {
+                    const int h = c >> 1;  // the half of the keys, whose P lies over its scores
+                    if ((c & 1) == 0) {
+                        wait(sh, bars + 8 * (kSFull + 2 * half + h), cnt & 1, p.v.status);
+                        tc_fence_after();
+                    }
                     uint32_t x[32];  // [16 rows' half][key group][row g, g + 8][pair]
                     tmem_ld_16x256_x4(s_tm + 32 * c, x);
                     tmem_ld_16x256_x4(s_tm + 32 * c + (16u << 16), x + 16);
@@ -438,8 +458,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                         }
                         tmem_st_wait();
 #pragma unroll 1
-                        for (int c2 = 0; c2 < 2 * c; c2++) {
-                            const uint32_t at = s_tm + 16 * (c2 >> 1) + (uint32_t(16 * (c2 & 1)) << 16);
+                        for (int c2 = 0; c2 < 2 * (c & 1); c2++) {  // not yet handed over: this half's first
+                            const uint32_t at = s_tm + 64 * h + (uint32_t(16 * c2) << 16);
                             const float fa = c2 & 1 ? f[2] : f[0], fb = c2 & 1 ? f[3] : f[1];
                             uint32_t w[8];
                             tmem_ld_16x128_x4(at, w);
@@ -451,7 +471,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                             }
                             tmem_st_16x128_x4(at, w);
                         }
-                        if (j > 0) {
+                        if (j > 0 || h > 0) {
                             // the output has a row a thread
                             float fo = 0.f;
 #pragma unroll
@@ -459,7 +479,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                                 const float o = __shfl_sync(0xffffffffu, f[i], 4 * (lane & 7));
                                 fo = (lane >> 3) == i ? o : fo;
                             }
-                            wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
+                            wait(sh, bars + 8 * (kPvDone + 2 * half + (h ^ 1)), (cnt + h - 1) & 1, p.v.status);
                             tc_fence_after();
 #pragma unroll 1
                             for (int d0 = 0; d0 < D; d0 += 16) {
@@ -495,19 +515,22 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                             pk[8 * (i >> 1) + 2 * k + (i & 1)] = bf16_pack(a.x, a.y);
                         }
                     }
-                    tmem_st_16x128_x4(s_tm + 16 * c, pk);
-                    tmem_st_16x128_x4(s_tm + 16 * c + (16u << 16), pk + 8);
+                    const uint32_t to = s_tm + 64 * h + 16 * (c & 1);
+                    tmem_st_16x128_x4(to, pk);
+                    tmem_st_16x128_x4(to + (16u << 16), pk + 8);
+                    if (c & 1) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bars + 8 * (kPFull + 2 * half + h));
+                    }
                 }
             };
             if (open)
                 tile(std::true_type());
             else
                 tile(std::false_type());
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bars + 8 * (kPFull + half));
             cnt++;
         }
         steps += sg.tiles;
@@ -538,7 +561,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
         const int slot = cut0 > sg.u0 ? 0 : 1;
         float *const part = p.parts + (2 * uint64_t(blockIdx.x) + slot) * PF;
         if (valued) {
-            wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
+            wait(sh, bars + 8 * (kPvDone + 2 * half + 1), (cnt - 1) & 1, p.v.status);
             tc_fence_after();
         }
         if (active) {
@@ -623,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const AttnPara
     using S = Sched<kRows, kKeys, kItemCost>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Shared sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t raw = smem_addr(smem_raw), q_at = (raw + 1023u) & ~1023u;
     const uint32_t k_at = q_at + 2 * kTileBytes<D>, v_at = k_at + kStages * kTileBytes<D>;
     const uint32_t bars = smem_addr(sh.bars);
@@ -671,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const AttnPara
             softmax_role<D>(p, sh, bars, total, workers, cut0, steps, items, own);
         else if (warp < (kSoftmax + kUnpack) / 32)
             unpack_role<D>(p, sh, bars, q_at, k_at, v_at, steps, items);
-        else if (lane == 0)
+        else
             mma_role<D>(p, sh, bars, q_at, k_at, v_at, steps, cnt, items);
         __syncthreads();
     }
