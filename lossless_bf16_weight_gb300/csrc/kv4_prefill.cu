@@ -20,8 +20,9 @@
 //             works on one half of the keys, the products of the other half run.
 // Both products take the codes as they are (Codes in kv4_codes.cuh: integers in units
 // of 2^-133, no rounded K or V), the queries and probabilities scaled up
-// against them.  The running maximum is only raised when a score passes it by
-// 2^24, so that O is rarely rescaled.
+// against them.  The running maximum is only raised when the probabilities of
+// 64 keys add up to more than 2^24 (BF16 and fp32 hold that without
+// loss), so that no score is compared and O is rarely rescaled.
 #include <cmath>
 #include <type_traits>
 
@@ -35,12 +36,12 @@ namespace uw {
 namespace {
 
 constexpr int kRows = 256, kKeys = 128;
-constexpr int kSoftmax = 256, kUnpack = 128;          // threads; 13 warps leave each 128 registers
-constexpr int kThreads = kSoftmax + kUnpack + 32;
+constexpr int kSoftmax = 256, kUnpack = 128;          // threads
+constexpr int kThreads = kSoftmax + kUnpack + 128;    // and a warpgroup whose first warp issues the products
 constexpr int kItemCost = 3;                          // what an item costs beyond its steps, in steps
 constexpr int kSegs = 32;
 constexpr int kStages = 2, kParStages = 4;
-constexpr float kRaise = 24.f;                        // log2 headroom of a probability
+constexpr float kRaise = 16777216.f;                  // 2^24: headroom of the probabilities of 64 keys
 constexpr uint32_t kTmemCols = 512;
 
 enum Bar {
@@ -191,6 +192,15 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
     const bool odd_first = (vw >> 2) & 1;
     const uint32_t m_a = odd_first ? codes.mask4 : codes.mask0, m_b = odd_first ? codes.mask0 : codes.mask4;
     const uint32_t c_a = odd_first ? codes.mid4 : codes.mid0, c_b = odd_first ? codes.mid0 : codes.mid4;
+    // Where the word's even (or odd) dimension of byte j goes in a V tile; the
+    // other one is the next row (or the one before): 128 bytes and one chunk
+    // bit on, both by exclusive or.  A second task lies a block of 64 keys on.
+    static_assert(VT == 1 || KG == 8, "a thread's tasks lie in the same place of their blocks");
+    uint32_t v_to[4];
+    constexpr uint32_t v_flip = 128u ^ 16u;
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        v_to[j] = tile_at(8 * vw + 2 * ((j + vw) & 3) + odd_first, kg, D);
     const float a_up = p.c1 * kQDown;
     for (int s = 0; s < sh.n_segs; s++) {
         const Seg &sg = sh.segs[s];
@@ -201,48 +211,63 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
         const int32_t *const table = v.table + int64_t(sg.s) * v.table_stride;
         uint4 rk[KC];
         uint32_t rv[VT][8], rp[2];
-        auto page_of = [&](int at) { return __ldg(table + (min(at, sg.len - 1) >> v.page_log2)); };
-        auto check = [&](int page) {
-            if (uint32_t(page) < uint32_t(v.n_pages))
-                return page;
-            atomicOr(v.status, uint32_t(kStatusBadCache));
-            return -1;
-        };
-        auto load = [&](int key0, int pk, const int (&pv)[VT]) {
-            pk = check(pk);
-            const int ka = key0 + key;
-#pragma unroll
-            for (int i = 0; i < KC; i++)
-                rk[i] = make_uint4(0, 0, 0, 0);
-            rp[0] = rp[1] = 0;
-            if (pk >= 0 && ka < sg.len) {
-                const uint8_t *b = base + pk * page_bytes;
-                const uint4 *src = reinterpret_cast<const uint4 *>(b + (ka & mask) * (D / 2));
-#pragma unroll
-                for (int i = 0; i < KC; i++)
-                    rk[i] = __ldg(src + i);
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-                    rp[i] = __ldg(reinterpret_cast<const uint32_t *>(b + kv4_params<D>(v.page_log2, ka & mask, i)));
-            }
-#pragma unroll
-            for (int n = 0; n < VT; n++) {
-                const int va = key0 + 8 * (kg + n * KG), pg = check(pv[n]);
-                const uint8_t *b = base + pg * page_bytes + kv4_codes<D>(v.page_log2, va & mask, 1) + vw * 4;
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    rv[n][i] = pg >= 0 && va + i < sg.len ? __ldg(reinterpret_cast<const uint32_t *>(b + i * (D / 2))) : 0u;
-            }
-        };
-        const int first = sg.first * kKeys;
         int pk, pv[VT];
+        auto page_of = [&](int at) { return __ldg(table + (min(at, sg.len - 1) >> v.page_log2)); };
         auto pages = [&](int key0) {
             pk = page_of(key0 + key);
 #pragma unroll
             for (int n = 0; n < VT; n++)
                 pv[n] = page_of(key0 + 8 * (kg + n * KG));
         };
+        auto bad = [&](int page) {
+            if (uint32_t(page) < uint32_t(v.n_pages))
+                return false;
+            atomicOr(v.status, uint32_t(kStatusBadCache));
+            return true;
+        };
+        // A key or eight keys of V that are not there are zeros; pages are
+        // looked at here, a tile after they were loaded.
+        auto load_k = [&](int key0) {
+            const int at = key0 + key;
+#pragma unroll
+            for (int i = 0; i < KC; i++)
+                rk[i] = make_uint4(0, 0, 0, 0);
+            rp[0] = rp[1] = 0;
+            if (!bad(pk) && at < sg.len) {
+                const uint8_t *b = base + pk * page_bytes;
+                const uint4 *src = reinterpret_cast<const uint4 *>(b + (at & mask) * (D / 2));
+#pragma unroll
+                for (int i = 0; i < KC; i++)
+                    rk[i] = __ldg(src + i);
+                const uint8_t *par = b + kv4_params<D>(v.page_log2, at & mask, 0);
+                rp[0] = __ldg(reinterpret_cast<const uint32_t *>(par));
+                rp[1] = __ldg(reinterpret_cast<const uint32_t *>(par + (4 << v.page_log2)));
+            }
+        };
+        auto load_v = [&](int key0) {
+#pragma unroll
+            for (int n = 0; n < VT; n++) {
+                const int at = key0 + 8 * (kg + n * KG);
+                const uint8_t *b = base + pv[n] * page_bytes + kv4_codes<D>(v.page_log2, at & mask, 1) + vw * 4;
+                if (!bad(pv[n]) && at + 8 <= sg.len) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        rv[n][i] = __ldg(reinterpret_cast<const uint32_t *>(b + i * (D / 2)));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        rv[n][i] = uint32_t(pv[n]) < uint32_t(v.n_pages) && at + i < sg.len
+                                       ? __ldg(reinterpret_cast<const uint32_t *>(b + i * (D / 2)))
+                                       : 0u;
+                }
+            }
+        };
+        const int first = sg.first * kKeys;
         pages(first);
+        load_k(first);
+        load_v(first);
+        if (sg.tiles > 1)
+            pages(first + kKeys);
 
         // queries: a thread writes two rows, in the order the codes of a word come out in
         wait(sh, bars + 8 * kQEmpty, (items & 1) ^ 1, v.status);
@@ -273,40 +298,22 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
             mbar_arrive(bars + 8 * kQFull);
         items++;
 
-        load(first, pk, pv);
-        if (sg.tiles > 1)
-            pages(first + kKeys);
         for (int j = 0; j < sg.tiles; j++, steps++) {
             const uint32_t stage = steps % kStages, turn = (steps / kStages) & 1, par = steps % kParStages;
-            uint4 ck[KC];
-            uint32_t cv[VT][8];
-            const uint32_t cp[2] = {rp[0], rp[1]};
-#pragma unroll
-            for (int i = 0; i < KC; i++)
-                ck[i] = rk[i];
-#pragma unroll
-            for (int n = 0; n < VT; n++)
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    cv[n][i] = rv[n][i];
-            if (j + 1 < sg.tiles) {
-                load(first + (j + 1) * kKeys, pk, pv);
-                if (j + 2 < sg.tiles)
-                    pages(first + (j + 2) * kKeys);
-            }
+            const bool more = j + 1 < sg.tiles;
             {
                 float *const kd = reinterpret_cast<float *>(sh.kpar[par]) + (key >> 1) * 4 + (key & 1);
                 float *const vd = reinterpret_cast<float *>(sh.vpar[par]) + (key >> 1) * 4 + (key & 1);
-                kd[0] = bf16_lo(cp[0]) * a_up;
-                kd[2] = bf16_hi(cp[0]) * p.c1;
-                vd[0] = bf16_lo(cp[1]) * kPUp;
-                vd[2] = fmaf(8.f, bf16_lo(cp[1]), bf16_hi(cp[1]));
+                kd[0] = bf16_lo(rp[0]) * a_up;
+                kd[2] = bf16_hi(rp[0]) * p.c1;
+                vd[0] = bf16_lo(rp[1]) * kPUp;
+                vd[2] = fmaf(8.f, bf16_lo(rp[1]), bf16_hi(rp[1]));
             }
             wait(sh, bars + 8 * (kKEmpty + stage), turn ^ 1, v.status);
             const uint32_t kt = k_at + stage * kTileBytes<D>;
 #pragma unroll
             for (int i = 0; i < KC; i++) {
-                const uint32_t a[4] = {ck[i].x, ck[i].y, ck[i].z, ck[i].w};
+                const uint32_t a[4] = {rk[i].x, rk[i].y, rk[i].z, rk[i].w};
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const uint32_t y = a[k] >> 8;
@@ -320,6 +327,8 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
                 mbar_arrive(bars + 8 * (kKFull + stage));
                 mbar_arrive(bars + 8 * (kParFull + par));
             }
+            if (more)
+                load_k(first + (j + 1) * kKeys);
             wait(sh, bars + 8 * (kVEmpty + stage), turn ^ 1, v.status);
             const uint32_t vt = v_at + stage * kTileBytes<D>;
 #pragma unroll
@@ -329,13 +338,17 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
                     uint32_t e[4];
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        e[i] = __byte_perm(cv[n][2 * i], cv[n][2 * i + 1], sel[jj]);
-                    const int d = 8 * vw + 2 * ((jj + vw) & 3), c = kg + n * KG;
-                    sts128(vt + tile_at(d + odd_first, c, D), sub2(e[0] & m_a, c_a), sub2(e[1] & m_a, c_a),
-                           sub2(e[2] & m_a, c_a), sub2(e[3] & m_a, c_a));
-                    sts128(vt + tile_at(d + !odd_first, c, D), sub2(e[0] & m_b, c_b), sub2(e[1] & m_b, c_b),
-                           sub2(e[2] & m_b, c_b), sub2(e[3] & m_b, c_b));
+                        e[i] = __byte_perm(rv[n][2 * i], rv[n][2 * i + 1], sel[jj]);
+                    const uint32_t to = vt + v_to[jj] + n * (D * 128);
+                    sts128(to, sub2(e[0] & m_a, c_a), sub2(e[1] & m_a, c_a), sub2(e[2] & m_a, c_a), sub2(e[3] & m_a, c_a));
+                    sts128(to ^ v_flip, sub2(e[0] & m_b, c_b), sub2(e[1] & m_b, c_b), sub2(e[2] & m_b, c_b),
+                           sub2(e[3] & m_b, c_b));
                 }
+            if (more) {
+                load_v(first + (j + 1) * kKeys);
+                if (j + 2 < sg.tiles)
+                    pages(first + (j + 2) * kKeys);
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
@@ -361,12 +374,14 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
         // The warp's 32 rows lie like the rows of a matrix product's fragment: a
         // thread has rows g + 8 i (i < 4) and of them the key pairs 8 k + 2 t, so that a
         // pair's scales and offsets are read once for four rows.
-        float m[4], qsum[4];
+        float m[4], lim[4];      // maximum; the sum of 64 keys' probabilities from which it is raised
+        uint64_t mm[4], qs[4];   // less the maximum, and the sum of q, in pairs
         uint64_t l2[4], z2[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             m[i] = -INFINITY;
-            l2[i] = z2[i] = 0;
+            lim[i] = -1.f;       // no maximum yet: any sum
+            l2[i] = z2[i] = mm[i] = qs[i] = 0;
         }
         for (int j = 0; j < sg.tiles; j++) {
             const uint32_t step = steps + j, par = step % kParStages;
@@ -376,8 +391,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
             wait(sh, bars + 8 * (kParFull + par), (step / kParStages) & 1, p.v.status);
             if (j == 0) {
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    qsum[i] = sh.qs[items & 1][32 * warp + g + 8 * i];
+                for (int i = 0; i < 4; i++) {
+                    const float q = sh.qs[items & 1][32 * warp + g + 8 * i];
+                    qs[i] = pair2(q, q);
+                }
             }
             const bool open = key0 < sg.all_lo || key0 + kKeys > sg.all_hi;
             auto tile = [&](auto masked) {
@@ -395,136 +412,134 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                 const ulonglong2 *const kp = reinterpret_cast<const ulonglong2 *>(sh.kpar[par]) + t;
                 const ulonglong2 *const vp = reinterpret_cast<const ulonglong2 *>(sh.vpar[par]) + t;
 #pragma unroll 1
-                for (int c = 0; c < kKeys / 32; c++) {
-                    const int h = c >> 1;  // the half of the keys, whose P lies over its scores
-                    if ((c & 1) == 0) {
-                        wait(sh, bars + 8 * (kSFull + 2 * half + h), cnt & 1, p.v.status);
-                        tc_fence_after();
-                    }
-                    uint32_t x[32];  // [16 rows' half][key group][row g, g + 8][pair]
-                    tmem_ld_16x256_x4(s_tm + 32 * c, x);
-                    tmem_ld_16x256_x4(s_tm + 32 * c + (16u << 16), x + 16);
-                    tmem_ld_wait();
-                    uint64_t y[4][4];  // [row][key group]
-                    float top[4];
-                    uint64_t qs[4], mm[4];
+                for (int h = 0; h < 2; h++) {  // halves of the keys; P of one lies over its scores
+                    wait(sh, bars + 8 * (kSFull + 2 * half + h), cnt & 1, p.v.status);
+                    tc_fence_after();
+                    uint64_t y[4][8], sum[4];  // [row][key group]: scores, then probabilities
+                    for (bool again = false;; again = true) {
+                        uint32_t x[64];  // [32 keys][16 rows' half][key group][row g, g + 8][pair]
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const float m0 = m[i] == -INFINITY ? 0.f : -m[i];
-                        qs[i] = pair2(qsum[i], qsum[i]);
-                        mm[i] = pair2(m0, m0);
-                        top[i] = -INFINITY;
-                    }
+                        for (int c = 0; c < 4; c++)
+                            tmem_ld_16x256_x4(s_tm + 64 * h + 32 * (c >> 1) + (uint32_t(16 * (c & 1)) << 16), x + 16 * c);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const ulonglong2 ab = kp[16 * c + 4 * k];
+                        for (int k = 0; k < 8; k++) {
+                            const ulonglong2 ab = kp[32 * h + 4 * k];
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const uint32_t *const w = x + 32 * (k >> 2) + 16 * (i >> 1) + 4 * (k & 3) + 2 * (i & 1);
+                                y[i][k] = fma2(pair2(__uint_as_float(w[0]), __uint_as_float(w[1])), ab.x,
+                                               fma2(ab.y, qs[i], mm[i]));
+                                if constexpr (kOpen) {
+                                    const float2 f = unpair(y[i][k]);
+                                    const int at = 64 * h + 8 * k;
+                                    y[i][k] = pair2(at >= lo[i] && at < hi[i] ? f.x : -INFINITY,
+                                                    at + 1 >= lo[i] && at + 1 < hi[i] ? f.y : -INFINITY);
+                                }
+                            }
+                        }
+                        if (again) {
+                            // Raise the maxima to those of these keys: what the rows have so far
+                            // is scaled down.
+                            float f[4];
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                float top = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < 8; k++) {
+                                    const float2 v = unpair(y[i][k]);
+                                    top = fmaxf(top, fmaxf(v.x, v.y));
+                                }
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                                const float m0 = m[i] == -INFINITY ? 0.f : m[i];
+                                const float m2 = fmaxf(m[i], m0 + top), m20 = m2 == -INFINITY ? 0.f : m2;
+                                f[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - m20);
+                                const uint64_t ff = pair2(f[i], f[i]), d = pair2(m0 - m20, m0 - m20);
+                                l2[i] = mul2(l2[i], ff);
+                                z2[i] = mul2(z2[i], ff);
+#pragma unroll
+                                for (int k = 0; k < 8; k++)
+                                    y[i][k] = add2(y[i][k], d);
+                                m[i] = m2;
+                                mm[i] = pair2(-m20, -m20);
+                                lim[i] = m2 == -INFINITY ? -1.f : kRaise;
+                            }
+                            if (j > 0 || h > 0) {
+                                // the output has a row a thread
+                                float fo = 0.f;
+#pragma unroll
+                                for (int i = 0; i < 4; i++) {
+                                    const float o = __shfl_sync(0xffffffffu, f[i], 4 * (lane & 7));
+                                    fo = (lane >> 3) == i ? o : fo;
+                                }
+                                wait(sh, bars + 8 * (kPvDone + 2 * half + (h ^ 1)), (cnt + h - 1) & 1, p.v.status);
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int d0 = 0; d0 < D; d0 += 16) {
+                                    uint32_t w[16];
+                                    tmem_ld16(o_tm + d0, w);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int i = 0; i < 16; i++)
+                                        w[i] = __float_as_uint(__uint_as_float(w[i]) * fo);
+                                    tmem_st16(o_tm + d0, w);
+                                }
+                            }
+                        }
+                        uint64_t pr[4][8];
+                        bool raise = false;
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
-                            const uint32_t *const w = x + 16 * (i >> 1) + 4 * k + 2 * (i & 1);
-                            y[i][k] = fma2(pair2(__uint_as_float(w[0]), __uint_as_float(w[1])), ab.x,
-                                           fma2(ab.y, qs[i], mm[i]));
-                            if constexpr (kOpen) {
+#pragma unroll
+                            for (int k = 0; k < 8; k++) {
                                 const float2 f = unpair(y[i][k]);
-                                const int at = 32 * c + 8 * k;
-                                y[i][k] = pair2(at >= lo[i] && at < hi[i] ? f.x : -INFINITY,
-                                                at + 1 >= lo[i] && at + 1 < hi[i] ? f.y : -INFINITY);
+                                pr[i][k] = pair2(exp2_fast(f.x), exp2_fast(f.y));
                             }
-                            const float2 f = unpair(y[i][k]);
-                            top[i] = fmaxf(top[i], fmaxf(f.x, f.y));
+                            sum[i] = add2(add2(add2(pr[i][0], pr[i][1]), add2(pr[i][2], pr[i][3])),
+                                          add2(add2(pr[i][4], pr[i][5]), add2(pr[i][6], pr[i][7])));
+                            const float2 f = unpair(sum[i]);
+                            raise = raise || f.x + f.y > lim[i];
                         }
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+#pragma unroll
+                            for (int k = 0; k < 8; k++)
+                                y[i][k] = pr[i][k];
+                        if (again || !__any_sync(0xffffffffu, raise))
+                            break;
                     }
-                    bool raise = false;
+                    uint32_t pk[32];  // [32 keys][16 rows' half][key group][row g, g + 8]
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        raise = raise || top[i] > kRaise || (m[i] == -INFINITY && top[i] > -INFINITY);
-                    if (__any_sync(0xffffffffu, raise)) {
-                        // Raise the maxima: what the rows have so far is scaled down, their
-                        // probabilities of this tile among it.
-                        float f[4];
+                        l2[i] = add2(l2[i], sum[i]);
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        const ulonglong2 sm = vp[32 * h + 4 * k];
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
-                            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-                            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-                            const float m0 = m[i] == -INFINITY ? 0.f : m[i];
-                            const float m2 = fmaxf(m[i], m0 + top[i]), m20 = m2 == -INFINITY ? 0.f : m2;
-                            f[i] = m[i] == -INFINITY ? 0.f : exp2_fast(m[i] - m20);
-                            const uint64_t ff = pair2(f[i], f[i]), d = pair2(m0 - m20, m0 - m20);
-                            l2[i] = mul2(l2[i], ff);
-                            z2[i] = mul2(z2[i], ff);
-#pragma unroll
-                            for (int k = 0; k < 4; k++)
-                                y[i][k] = add2(y[i][k], d);
-                            m[i] = m2;
-                        }
-                        tmem_st_wait();
-#pragma unroll 1
-                        for (int c2 = 0; c2 < 2 * (c & 1); c2++) {  // not yet handed over: this half's first
-                            const uint32_t at = s_tm + 64 * h + (uint32_t(16 * c2) << 16);
-                            const float fa = c2 & 1 ? f[2] : f[0], fb = c2 & 1 ? f[3] : f[1];
-                            uint32_t w[8];
-                            tmem_ld_16x128_x4(at, w);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                w[2 * i] = bf16_pack(bf16_lo(w[2 * i]) * fa, bf16_hi(w[2 * i]) * fa);
-                                w[2 * i + 1] = bf16_pack(bf16_lo(w[2 * i + 1]) * fb, bf16_hi(w[2 * i + 1]) * fb);
-                            }
-                            tmem_st_16x128_x4(at, w);
-                        }
-                        if (j > 0 || h > 0) {
-                            // the output has a row a thread
-                            float fo = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const float o = __shfl_sync(0xffffffffu, f[i], 4 * (lane & 7));
-                                fo = (lane >> 3) == i ? o : fo;
-                            }
-                            wait(sh, bars + 8 * (kPvDone + 2 * half + (h ^ 1)), (cnt + h - 1) & 1, p.v.status);
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int d0 = 0; d0 < D; d0 += 16) {
-                                uint32_t w[16];
-                                tmem_ld16(o_tm + d0, w);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 16; i++)
-                                    w[i] = __float_as_uint(__uint_as_float(w[i]) * fo);
-                                tmem_st16(o_tm + d0, w);
-                            }
-                        }
-                    }
-                    uint32_t pk[16];  // [16 rows' half][key group][row g, g + 8]
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const ulonglong2 sm = vp[16 * c + 4 * k];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const float2 f = unpair(y[i][k]);
-                            const uint64_t pr = pair2(exp2_fast(f.x), exp2_fast(f.y));
-                            l2[i] = add2(l2[i], pr);
-                            uint64_t ps = mul2(pr, sm.x);
+                            uint64_t ps = mul2(y[i][k], sm.x);
                             if constexpr (kOpen) {  // a masked key's scale may be anything
-                                const float2 a = unpair(ps), b = unpair(mul2(pr, sm.y));
-                                const bool in0 = f.x != -INFINITY, in1 = f.y != -INFINITY;
+                                const int at = 64 * h + 8 * k;
+                                const float2 a = unpair(ps), b = unpair(mul2(y[i][k], sm.y));
+                                const bool in0 = at >= lo[i] && at < hi[i], in1 = at + 1 >= lo[i] && at + 1 < hi[i];
                                 ps = pair2(in0 ? a.x : 0.f, in1 ? a.y : 0.f);
                                 z2[i] = add2(z2[i], pair2(in0 ? b.x : 0.f, in1 ? b.y : 0.f));
                             } else {
-                                z2[i] = fma2(pr, sm.y, z2[i]);
+                                z2[i] = fma2(y[i][k], sm.y, z2[i]);
                             }
                             const float2 a = unpair(ps);
-                            pk[8 * (i >> 1) + 2 * k + (i & 1)] = bf16_pack(a.x, a.y);
+                            pk[16 * (k >> 2) + 8 * (i >> 1) + 2 * (k & 3) + (i & 1)] = bf16_pack(a.x, a.y);
                         }
                     }
-                    const uint32_t to = s_tm + 64 * h + 16 * (c & 1);
-                    tmem_st_16x128_x4(to, pk);
-                    tmem_st_16x128_x4(to + (16u << 16), pk + 8);
-                    if (c & 1) {
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(bars + 8 * (kPFull + 2 * half + h));
-                    }
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        tmem_st_16x128_x4(s_tm + 64 * h + 16 * (c >> 1) + (uint32_t(16 * (c & 1)) << 16), pk + 8 * c);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bars + 8 * (kPFull + 2 * half + h));
                 }
             };
             if (open)
@@ -671,32 +686,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const AttnPara
         return;
     if (warp == kThreads / 32 - 1)
         tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
-    uint64_t u = mul_div(total, blockIdx.x, workers);
-    const uint64_t cut0 = u, cut1 = mul_div(total, blockIdx.x + 1, workers);
-    Item it{};
-    if (warp == 0)
-        it = locate<S>(p, sh.row, u);
-    uint32_t steps = 0, items = 0, cnt[2] = {0, 0}, own = 0;
+    const uint64_t cut0 = mul_div(total, blockIdx.x, workers), cut1 = mul_div(total, blockIdx.x + 1, workers);
+    // From here on every role walks through the lists of segments by itself;
+    // barrier 0 stands before and after a list's work.  Registers a thread by
+    // warpgroup: 2 x 184 + 88 + 56 = 4 x 128, the launch's.
     tc_fence_before();
-    while (u < cut1) {
-        if (warp == 0) {
-            int n;
-            const uint64_t to = list_segments<S, kSegs>(p, it, u, cut1, sh.segs, &n);
-            if (lane == 0) {
-                sh.listed_to = to;
-                sh.n_segs = n;
+    if (warp < kSoftmax / 32) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        Item it{};
+        if (warp == 0)
+            it = locate<S>(p, sh.row, cut0);
+        uint32_t steps = 0, items = 0, cnt = 0;
+        for (uint64_t u = cut0; u < cut1;) {
+            if (warp == 0) {
+                int n;
+                const uint64_t to = list_segments<S, kSegs>(p, it, u, cut1, sh.segs, &n);
+                if (lane == 0) {
+                    sh.listed_to = to;
+                    sh.n_segs = n;
+                }
             }
+            __syncthreads();
+            tc_fence_after();
+            u = sh.listed_to;
+            softmax_role<D>(p, sh, bars, total, workers, cut0, steps, items, cnt);
+            __syncthreads();
         }
-        __syncthreads();
-        tc_fence_after();
-        u = sh.listed_to;
-        if (warp < kSoftmax / 32)
-            softmax_role<D>(p, sh, bars, total, workers, cut0, steps, items, own);
-        else if (warp < (kSoftmax + kUnpack) / 32)
+    } else if (warp < (kSoftmax + kUnpack) / 32) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        uint32_t steps = 0, items = 0;
+        for (uint64_t u = cut0; u < cut1;) {
+            __syncthreads();
+            u = sh.listed_to;
             unpack_role<D>(p, sh, bars, q_at, k_at, v_at, steps, items);
-        else
-            mma_role<D>(p, sh, bars, q_at, k_at, v_at, steps, cnt, items);
-        __syncthreads();
+            __syncthreads();
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        uint32_t steps = 0, items = 0, cnt[2] = {0, 0};
+        for (uint64_t u = cut0; u < cut1;) {
+            __syncthreads();
+            tc_fence_after();
+            u = sh.listed_to;
+            if (warp == (kSoftmax + kUnpack) / 32)
+                mma_role<D>(p, sh, bars, q_at, k_at, v_at, steps, cnt, items);
+            __syncthreads();
+        }
     }
     if (warp == kThreads / 32 - 1)
         tmem_dealloc(sh.tmem, kTmemCols);
