@@ -264,10 +264,6 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
         };
         const int first = sg.first * kKeys;
         pages(first);
-        load_k(first);
-        load_v(first);
-        if (sg.tiles > 1)
-            pages(first + kKeys);
 
         // queries: a thread writes two rows, in the order the codes of a word come out in
         wait(sh, bars + 8 * kQEmpty, (items & 1) ^ 1, v.status);
@@ -278,7 +274,7 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q.p + tok * p.q.ts + head * p.q.hs);
             const uint32_t to = q_at + (rr >> 7) * kTileBytes<D>;
             float sum = 0.f;
-#pragma unroll 4
+#pragma unroll 8
             for (int c = 0; c < D / 8; c++) {
                 const uint4 x = in ? src[c] : make_uint4(0, 0, 0, 0);
                 const uint32_t a[4] = {x.x, x.y, x.z, x.w};
@@ -297,6 +293,10 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
         if (lane == 0)
             mbar_arrive(bars + 8 * kQFull);
         items++;
+        load_k(first);
+        load_v(first);
+        if (sg.tiles > 1)
+            pages(first + kKeys);
 
         for (int j = 0; j < sg.tiles; j++, steps++) {
             const uint32_t stage = steps % kStages, turn = (steps / kStages) & 1, par = steps % kParStages;
@@ -689,10 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const AttnPara
     const uint64_t cut0 = mul_div(total, blockIdx.x, workers), cut1 = mul_div(total, blockIdx.x + 1, workers);
     // From here on every role walks through the lists of segments by itself;
     // barrier 0 stands before and after a list's work.  Registers a thread by
-    // warpgroup: 2 x 184 + 88 + 56 = 4 x 128, the launch's.
+    // warpgroup: 2 x 176 + 104 + 56 = 4 x 128, the launch's.
     tc_fence_before();
     if (warp < kSoftmax / 32) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         Item it{};
         if (warp == 0)
             it = locate<S>(p, sh.row, cut0);
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const AttnPara
             __syncthreads();
         }
     } else if (warp < (kSoftmax + kUnpack) / 32) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         uint32_t steps = 0, items = 0;
         for (uint64_t u = cut0; u < cut1;) {
             __syncthreads();
