@@ -1,5 +1,6 @@
 // Entry points of the 4-bit paged cache's attention, and the checks of what the
 // cache's calls are given.
+#include <algorithm>
 #include <cmath>
 
 #include "kernels.h"
@@ -49,8 +50,12 @@ bool kv4_rows(const uw_kv4_rows *r, Rows *out) {
 namespace {
 
 // Sequences with up to so many rows (new tokens x query heads of a kv head)
-// take the kernel for few rows.
-constexpr int kFewRows = 64;
+// take the kernel for few rows.  Measured with 8 kv heads of 128, that kernel and
+// the other: 16 sequences of 4096 keys, 16 rows 44 and 86 us, 32 rows 69 and 86,
+// 64 rows 119 and 87; one sequence of 8192 keys, 64 rows 34 and 48: with few steps
+// (256 rows x 128 keys) in all, what the other kernel takes to start decides.
+constexpr int kFewRows = 32, kFewRowsShort = 64;
+constexpr int64_t kShortSteps = 1024;
 
 // Workspace: [error word | counters and parts of the kernel for few rows | the
 // same of the other].
@@ -129,19 +134,22 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
     // the host's bounds only leave out a launch that has none, and a wrong bound
     // leaves all sequences to the kernel that is launched.
     const int64_t rows = max_new * p.group;
-    const bool few = rows == 0 || rows <= kFewRows || c->n_seqs > 1, many = rows == 0 || rows > kFewRows;
+    const bool few_steps = max_len > 0 && (max_len + 127) / 128 * c->kv_heads * c->n_seqs <= kShortSteps;
+    const int few_rows = few_steps ? kFewRowsShort : kFewRows;
+    const bool few = rows == 0 || rows <= few_rows || c->n_seqs > 1, many = rows == 0 || rows > few_rows;
     if (few) {
         p.rows_min = 0;
-        p.rows_max = many ? kFewRows : INT32_MAX;
+        p.rows_max = many ? few_rows : INT32_MAX;
         p.counters = reinterpret_cast<uint32_t *>(wsb + w.few_counters);
         p.parts = reinterpret_cast<float *>(wsb + w.few_parts);
         const int64_t units = max_len > 0 && !many ? (max_len / 32 + 2) * (rows / 8 + 1) * c->kv_heads * c->n_seqs : 0;
-        const uw_status r = launch_kv4_decode(p, c->head_dim, many ? 0 : rows, units, st);
+        // beside prompts most of the other sequences have one new token
+        const uw_status r = launch_kv4_decode(p, c->head_dim, many ? std::max(p.group, 5) : rows, units, st);
         if (r != UW_OK)
             return r;
     }
     if (many) {
-        p.rows_min = few ? kFewRows + 1 : 0;
+        p.rows_min = few ? few_rows + 1 : 0;
         p.rows_max = INT32_MAX;
         p.counters = reinterpret_cast<uint32_t *>(wsb + w.many_counters);
         p.parts = reinterpret_cast<float *>(wsb + w.many_parts);

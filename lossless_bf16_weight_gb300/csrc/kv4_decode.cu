@@ -135,22 +135,35 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     // warp is taken whole: a cut through it would cost a round trip through
     // the workspace.
     const bool snap = total <= uint64_t(kWarps + kItemCost) * gridDim.x;
-    uint64_t u = 0, u_end = 0;
+    uint64_t u = cut[0], u_end = cut[1];
     Item it{};
+    bool found = false;  // `it` holds unit u
 #pragma unroll 1
     for (int k = snap ? 0 : 2; k < 3; k++) {
+        const uint64_t end = it.u0 + it.n;
+        if (k == 1) {
+            if (cut[1] == total || cut[1] == end)
+                continue;
+            if (cut[1] < end) {  // in the same item
+                cut[1] = it.tiles <= kWholeTiles ? it.u0 : cut[1];
+                continue;
+            }
+        }
         if (k == 2) {
+            if (cut[0] == cut[1])
+                return;
             u = cut[0] + (cut[1] - cut[0]) * warp / kWarps;
             u_end = cut[0] + (cut[1] - cut[0]) * (warp + 1) / kWarps;
-            if (u == u_end)
+            if (u == u_end || (found && u >= it.u0 && u < end))
                 break;
         }
-        const uint64_t at = k == 0 ? cut[0] : k == 1 ? cut[1] : u;
-        if (at == total)
-            continue;
-        it = locate<S>(p, row_of_units, at);
-        if (k < 2 && it.tiles <= kWholeTiles)
-            cut[k] = it.u0;
+        const Item at = locate<S>(p, row_of_units, k == 1 ? cut[1] : u);
+        if (k < 2 && at.tiles <= kWholeTiles)
+            cut[k] = at.u0;
+        if (k != 1) {
+            it = at;
+            found = true;
+        }
     }
     Seg *const segs = all_segs[warp];
     const int64_t block = int64_t(D + 8) << v.page_log2, page_bytes = block * v.heads;
@@ -618,10 +631,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             }
         }
     }
-    __threadfence();
     __syncthreads();
     if (pend[0].at == nullptr && pend[1].at == nullptr)
         return;
+    __threadfence();
+    __syncthreads();
 
     // Items that go on in other CTAs: whoever arrives last joins the parts.
     if (threadIdx.x < 2 && pend[threadIdx.x].at) {
