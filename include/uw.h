@@ -505,7 +505,7 @@ uw_status uw_kv4_workspace_size(const uw_kv4_cache *c, int32_t q_heads, size_t *
  *   q         q_heads heads, read; q_out  the rotated q (written; may be q).
  *             Both NULL with q_heads = 0: only k and v are taken.
  *   k, v      kv_heads heads each, read.
- *   cos_dev, sin_dev  fp32 [rope_len, rot_dim/2], or NULL with rot_dim = 0 (no
+ *   cos_dev, sin_dev  fp32 [rope_len, rot_dim/2], 16-byte aligned, or NULL with rot_dim = 0 (no
  *             rotation).  A position at or past rope_len touches nothing and is
  *             reported like a bad page.  rot_dim: a multiple of 16, at most
  *             head_dim (UW_ERR_UNSUPPORTED otherwise). */

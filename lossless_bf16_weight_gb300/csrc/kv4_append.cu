@@ -3,17 +3,18 @@
 //           vector (one token, one kv head) and writes codes and params
 //   read    the new tokens' entries as BF16
 //
-// Both move little per token (48 vectors of 256 bytes for 32 + 2 x 8 heads of
-// 128), so they are bound by latency for a decode step and by memory for
-// prompts.  A vector belongs to D / 8 lanes, 16 bytes each; a warp takes
-// 32 / (D / 8) heads of one token at a time, `chunk` times, so that the
-// token's place and its row of the rotation table are found once for all of
-// them.  Minimum and maximum are joined by shuffles within the vector's lanes.
+// A decode step moves little (48 vectors of 256 bytes a token for 32 + 2 x 8
+// heads of 128): its time is latency.  For prompts instructions and memory are
+// about even.  A vector belongs to D / 8 lanes, 16 bytes each; a warp takes q heads
+// of one token, or k and v heads, 32 / (D / 8) at a time, and finds the token's
+// place and its row of the rotation table once for all of them.  Minimum and
+// maximum are joined by shuffles within the vector's lanes.
 //
-// The rotation rounds each product and the sum (no fused multiply-add), so
-// that the same inputs give the same codes as the formula computed step by
-// step in fp32; a code is a step function, and a last-bit difference before
-// it could show as a whole step after it.
+// The rotation rounds each product and the sum (no fused multiply-add), and the
+// quotient of the quantisation is correctly rounded, so that the same inputs
+// give the same codes as the formula computed step by step in fp32; a code is a
+// step function, and a last-bit difference before it could show as a whole step
+// after it.
 #include "kernels.h"
 #include "kv4.cuh"
 #include "kv4_host.h"
@@ -27,64 +28,118 @@ struct AppendParams {
     Rows q, qo, k, vv;
     const float *cos, *sin;
     int64_t rope_len;
-    int32_t q_heads, rot, interleaved, chunk;
+    int32_t q_heads, rot, interleaved;
+    int32_t q_units, kv_units;    // warps a token: of q heads, and of k and v heads
+    int32_t q_rounds, kv_rounds;  // heads such a warp takes one after the other (times 32 / (D / 8))
 };
 
-template <int D>
-__device__ __forceinline__ float vec_min(float x) {
-#pragma unroll
-    for (int o = D / 16; o; o >>= 1)
-        x = fminf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+constexpr int kAhead = 4;  // vectors of q a lane has on their way
+
+// Smaller halves of two pairs of BF16; NaN wherever one is.
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// Codes and params of eight values of a vector of D, whose lanes are
-// together; all 32 lanes call.  Returns the lane's eight codes.
+// a / b correctly rounded, from r = 1 / b correctly rounded: two corrections
+// of a r by its remainder (Markstein, IBM J. Res. Dev. 34, 1990).  For the
+// quotients of quantise(), 0 .. 16 or so, with neither b nor r near the ends of
+// fp32's range.
+__device__ __forceinline__ float divide_by(float a, float b, float r) {
+    float q = a * r;
+    q = fmaf(fmaf(-q, b, a), r, q);
+    return fmaf(fmaf(-q, b, a), r, q);
+}
+
+// Codes and params of eight values (pairs of BF16) of a vector of D, whose lanes
+// are together; all 32 lanes call.  Returns the lane's eight codes.
 template <int D>
-__device__ __forceinline__ uint32_t quantise(const float (&f)[8], uint32_t *params) {
-    float lo = f[0], hi = f[0];
-    bool finite = true;
+__device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[4], uint32_t *params) {
+    constexpr uint32_t kSigns = 0x80008000u;
+    // (smallest value, largest with its sign turned) as a pair
+    const uint32_t l = min2(min2(x[0], x[1]), min2(x[2], x[3]));
+    const uint32_t h = min2(min2(x[0] ^ kSigns, x[1] ^ kSigns), min2(x[2] ^ kSigns, x[3] ^ kSigns));
+    uint32_t ends = min2(__byte_perm(l, h, 0x5410), __byte_perm(l, h, 0x7632));
 #pragma unroll
-    for (int k = 0; k < 8; k++) {
-        lo = fminf(lo, f[k]);
-        hi = fmaxf(hi, f[k]);
-        finite = finite && fabsf(f[k]) <= 3.4e38f;
-    }
-    lo = vec_min<D>(lo);
-    hi = -vec_min<D>(-hi);
-    const float bad = -vec_min<D>(finite ? 0.f : -1.f);
-    if (bad > 0.f) {
+    for (int o = D / 16; o; o >>= 1)
+        ends = min2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+    const float lo = bf16_lo(ends), hi = -bf16_hi(ends);
+    // halves: hi - lo of two finite values may not be finite
+    const float lo2 = 0.5f * lo, range2 = 0.5f * hi - lo2;
+    if (!(range2 <= 3.4e38f)) {  // a value that is not finite
         *params = 0x7fc07fc0u;
         return 0u;
     }
-    // halves: hi - lo of two finite values may not be finite
-    const float lo2 = 0.5f * lo;
-    const uint32_t sb = bf16_pack((0.5f * hi - lo2) / 7.5f, lo);
+    const uint32_t sb = bf16_pack(range2 / 7.5f, lo);
     const float s2 = 0.5f * bf16_lo(sb);
     *params = sb;
+    if (!(s2 > 0.f))
+        return 0u;
     uint32_t codes = 0u;
+    if (s2 > 1e-30f && s2 < 1e30f) {
+        // Quotients from 0 to 15.06 (the scale is within 2^-8 of its value), so no
+        // clamping; the integer they round to is read off the sum with 1.5 * 2^23.
+        constexpr float kRound = 12582912.f;
+        const float r = __frcp_rn(s2);
+        constexpr uint32_t kOff = 0x4B400000u * 0x11111111u;  // the sums' other bits, as they add up
 #pragma unroll
-    for (int k = 0; k < 8; k++) {
-        const float c = s2 > 0.f ? rintf((0.5f * f[k] - lo2) / s2) : 0.f;
-        codes |= uint32_t(fminf(fmaxf(c, 0.f), 15.f)) << (4 * k);
+        for (int k = 7; k >= 0; k--) {
+            const float f = k & 1 ? bf16_hi(x[k / 2]) : bf16_lo(x[k / 2]);
+            codes = codes * 16u + __float_as_uint(divide_by(fmaf(0.5f, f, -lo2), s2, r) + kRound);
+        }
+        codes -= kOff;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const float f = k & 1 ? bf16_hi(x[k / 2]) : bf16_lo(x[k / 2]);
+            codes |= uint32_t(fminf(fmaxf(rintf((0.5f * f - lo2) / s2), 0.f), 15.f)) << (4 * k);
+        }
     }
     return codes;
 }
 
+// A lane's share of a token's rotation: its eight values are one side of
+// eight pairs (half split: the other side lies rot / 2 values on or back), or four
+// whole pairs (interleaved).
+struct Rotation {
+    float c[8], s[8];  // cosines and sines (half split: with the sign of the side)
+    int other;         // half split: where the other side's values are, from the own
+    bool on, interleaved;
+};
+
+// Rotated values of a lane: own ones in a, the other side's in b.  Each product
+// and the sum rounded (scalar instructions: ptxas fuses packed ones).
+__device__ __forceinline__ void rotate(const Rotation &r, uint32_t (&a)[4], const uint4 &other) {
+    if (!r.on)
+        return;
+    const uint32_t b[4] = {other.x, other.y, other.z, other.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float u = bf16_lo(a[k]), w = bf16_hi(a[k]);
+        if (r.interleaved)
+            a[k] = bf16_pack(__fsub_rn(__fmul_rn(u, r.c[k]), __fmul_rn(w, r.s[k])),
+                             __fadd_rn(__fmul_rn(w, r.c[k]), __fmul_rn(u, r.s[k])));
+        else
+            a[k] = bf16_pack(__fadd_rn(__fmul_rn(u, r.c[2 * k]), __fmul_rn(bf16_lo(b[k]), r.s[2 * k])),
+                             __fadd_rn(__fmul_rn(w, r.c[2 * k + 1]), __fmul_rn(bf16_hi(b[k]), r.s[2 * k + 1])));
+    }
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p) {
     constexpr int L = D / 8;       // lanes of a vector
     constexpr int G = 32 / L;      // vectors a warp takes at once
     grid_dep_launch();
     grid_dep_wait();
     const Kv4View &v = p.v;
     const int lane = threadIdx.x & 31, c = lane % L;
-    const int total = p.q_heads + 2 * v.heads;
-    const int per_token = (total + G * p.chunk - 1) / (G * p.chunk);
-    const int64_t unit = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t t = unit / per_token;
+    const uint32_t per_token = uint32_t(p.q_units + p.kv_units);
+    const uint64_t unit = uint64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t t = (unit >> 32) ? unit / per_token : uint32_t(unit) / per_token;
     if (t >= v.n_tokens)
         return;
+    const int part = int(unit - uint64_t(t) * per_token);
     const int s = kv4_find_seq(v, int(t));
     const Seq q = kv4_seq(v, s);
     if (t < q.t0 || t >= int64_t(q.t0) + q.n)
@@ -95,85 +150,89 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendParams p) {
             atomicOr(v.status, uint32_t(kStatusBadCache));
         return;
     }
-    // The lane's share of the rotation: its eight values are one side of
-    // eight pairs (half split: the partner's lie rot / 2 values on or back),
-    // or four whole pairs (interleaved).
     const int half = p.rot / 2, i0 = 8 * c;
-    const bool rotated = i0 < p.rot, second = !p.interleaved && i0 >= half;
-    float cs[8], sn[8];
-    if (rotated) {
+    Rotation r;
+    r.on = i0 < p.rot;
+    r.interleaved = p.interleaved;
+    r.other = 0;
+    if (r.on) {
         const int64_t row = int64_t(pos) * half;
         if (p.interleaved) {
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                cs[k] = __ldg(p.cos + row + 4 * c + k);
-                sn[k] = __ldg(p.sin + row + 4 * c + k);
-            }
+            const float4 cs = *reinterpret_cast<const float4 *>(p.cos + row + 4 * c);
+            const float4 sn = *reinterpret_cast<const float4 *>(p.sin + row + 4 * c);
+            r.c[0] = cs.x, r.c[1] = cs.y, r.c[2] = cs.z, r.c[3] = cs.w;
+            r.s[0] = sn.x, r.s[1] = sn.y, r.s[2] = sn.z, r.s[3] = sn.w;
         } else {
+            const bool second = i0 >= half;
+            const float sign = second ? 1.f : -1.f;
             const int j = second ? i0 - half : i0;
+            r.other = second ? -half : half;
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                cs[k] = __ldg(p.cos + row + j + k);
-                sn[k] = __ldg(p.sin + row + j + k);
+            for (int k = 0; k < 2; k++) {
+                const float4 cs = *reinterpret_cast<const float4 *>(p.cos + row + j + 4 * k);
+                const float4 sn = *reinterpret_cast<const float4 *>(p.sin + row + j + 4 * k);
+                r.c[4 * k] = cs.x, r.c[4 * k + 1] = cs.y, r.c[4 * k + 2] = cs.z, r.c[4 * k + 3] = cs.w;
+                r.s[4 * k] = sign * sn.x, r.s[4 * k + 1] = sign * sn.y;
+                r.s[4 * k + 2] = sign * sn.z, r.s[4 * k + 3] = sign * sn.w;
             }
         }
     }
-    const int partner = p.interleaved || !rotated ? lane : second ? lane - half / 8 : lane + half / 8;
-    const int slot = pos & ((1 << v.page_log2) - 1);
 
-    const int h0 = int(unit - t * per_token) * G * p.chunk + lane / L;
-    for (int ci = 0; ci < p.chunk; ci++) {
-        const int h = h0 + ci * G;
-        const bool mine = h < total;
-        // q heads first, then k, then v
-        const int kind = h < p.q_heads ? 0 : h < p.q_heads + v.heads ? 1 : 2;
-        const int hk = kind == 0 ? h : kind == 1 ? h - p.q_heads : h - p.q_heads - v.heads;
-        const Rows &src = kind == 0 ? p.q : kind == 1 ? p.k : p.vv;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (mine)
-            x = *reinterpret_cast<const uint4 *>(src.p + t * src.ts + hk * src.hs + i0);
-        uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4];
+    if (part < p.q_units) {
+        // q: the other side's values are read like the own ones (the same cache
+        // line), before anything is written: q_out may be q
+        const int h0 = part * p.q_rounds * G + lane / L;
+        const uint16_t *src = p.q.p + t * p.q.ts + h0 * p.q.hs + i0;
+        uint16_t *dst = p.qo.p + t * p.qo.ts + h0 * p.qo.hs + i0;
+        for (int n0 = 0; n0 < p.q_rounds; n0 += kAhead) {
+            uint4 x[kAhead], o[kAhead];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            b[k] = __shfl_sync(0xffffffffu, a[k], partner);
-        if (kind != 2 && rotated) {
-            if (p.interleaved) {
+            for (int n = 0; n < kAhead; n++) {
+                const bool in = n0 + n < p.q_rounds && h0 + (n0 + n) * G < p.q_heads;
+                const uint16_t *at = src + int64_t(n0 + n) * G * p.q.hs;
+                x[n] = in ? *reinterpret_cast<const uint4 *>(at) : make_uint4(0, 0, 0, 0);
+                o[n] = in && !r.interleaved ? *reinterpret_cast<const uint4 *>(at + r.other) : make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const float u = bf16_lo(a[k]), w = bf16_hi(a[k]);
-                    a[k] = bf16_pack(__fsub_rn(__fmul_rn(u, cs[k]), __fmul_rn(w, sn[k])),
-                                     __fadd_rn(__fmul_rn(w, cs[k]), __fmul_rn(u, sn[k])));
-                }
-            } else {
-                // first side: a c - b s; second side: a c + b s (a its own value, b the partner's)
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const float s0 = second ? sn[2 * k] : -sn[2 * k], s1 = second ? sn[2 * k + 1] : -sn[2 * k + 1];
-                    a[k] = bf16_pack(__fadd_rn(__fmul_rn(bf16_lo(a[k]), cs[2 * k]), __fmul_rn(bf16_lo(b[k]), s0)),
-                                     __fadd_rn(__fmul_rn(bf16_hi(a[k]), cs[2 * k + 1]), __fmul_rn(bf16_hi(b[k]), s1)));
-                }
+            for (int n = 0; n < kAhead; n++) {
+                uint32_t a[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+                rotate(r, a, o[n]);
+                if (n0 + n < p.q_rounds && h0 + (n0 + n) * G < p.q_heads)
+                    *reinterpret_cast<uint4 *>(dst + int64_t(n0 + n) * G * p.qo.hs) = make_uint4(a[0], a[1], a[2], a[3]);
             }
         }
-        if (kind == 0 && mine)
-            *reinterpret_cast<uint4 *>(p.qo.p + t * p.qo.ts + hk * p.qo.hs + i0) = make_uint4(a[0], a[1], a[2], a[3]);
-        if (__ballot_sync(0xffffffffu, mine && kind != 0)) {
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                f[2 * k] = bf16_lo(a[k]);
-                f[2 * k + 1] = bf16_hi(a[k]);
-            }
-            uint32_t params;
-            const uint32_t codes = quantise<D>(f, &params);
-            if (mine && kind != 0) {
-                uint8_t *blk = kv4_block<D>(v, s, pos, hk);
-                if (blk) {
-                    const int is_v = kind == 2;
-                    *reinterpret_cast<uint32_t *>(blk + kv4_codes<D>(v.page_log2, slot, is_v) + 4 * c) = codes;
-                    if (c == 0)
-                        *reinterpret_cast<uint32_t *>(blk + kv4_params<D>(v.page_log2, slot, is_v)) = params;
-                }
-            }
+        return;
+    }
+    // k heads, then v heads
+    uint8_t *const page = kv4_block<D>(v, s, pos, 0);  // the token's page, block of head 0
+    if (!page)
+        return;
+    const int slot = pos & ((1 << v.page_log2) - 1);
+    const int64_t block = int64_t(D + 8) << v.page_log2;
+    const int j0 = (part - p.q_units) * p.kv_rounds * G + lane / L;
+#pragma unroll 2
+    for (int n = 0; n < p.kv_rounds; n++) {
+        const int j = j0 + n * G;
+        if (j - lane / L >= 2 * v.heads)
+            break;
+        const bool mine = j < 2 * v.heads, is_v = j >= v.heads;
+        const int h = is_v ? j - v.heads : j;
+        const Rows &src = is_v ? p.vv : p.k;
+        const uint16_t *at = src.p + t * src.ts + h * src.hs + i0;
+        const bool turn = mine && !is_v && r.on;
+        const uint4 x = mine ? *reinterpret_cast<const uint4 *>(at) : make_uint4(0, 0, 0, 0);
+        const uint4 o = turn && !r.interleaved ? *reinterpret_cast<const uint4 *>(at + r.other) : make_uint4(0, 0, 0, 0);
+        uint32_t a[4] = {x.x, x.y, x.z, x.w};
+        if (turn)
+            rotate(r, a, o);
+        uint32_t params;
+        const uint32_t codes = quantise<D>(a, &params);
+        if (mine) {
+            uint8_t *const blk = page + h * block;
+            *reinterpret_cast<uint32_t *>(blk + kv4_codes<D>(v.page_log2, slot, is_v) + 4 * c) = codes;
+            if (c == 0)
+                *reinterpret_cast<uint32_t *>(blk + kv4_params<D>(v.page_log2, slot, is_v)) = params;
         }
     }
 }
@@ -201,15 +260,18 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View v, const Ro
         return;
     }
     const int slot = pos & ((1 << v.page_log2) - 1);
+    const int64_t block = int64_t(D + 8) << v.page_log2;
+    const uint8_t *const page = kv4_block<D>(v, s, pos, 0);
     const int h0 = int(unit - t * per_token) * G * chunk + lane / L;
+#pragma unroll 4
     for (int ci = 0; ci < chunk; ci++) {
         const int h = h0 + ci * G;
         if (h >= total)
             break;
         const int is_v = h >= v.heads, hk = is_v ? h - v.heads : h;
-        const uint8_t *blk = kv4_block<D>(v, s, pos, hk);
-        if (!blk)
+        if (!page)
             continue;
+        const uint8_t *blk = page + hk * block;
         const uint32_t codes = *reinterpret_cast<const uint32_t *>(blk + kv4_codes<D>(v.page_log2, slot, is_v) + 4 * c);
         const uint32_t par = *reinterpret_cast<const uint32_t *>(blk + kv4_params<D>(v.page_log2, slot, is_v));
         const float scale = bf16_lo(par), lo = bf16_hi(par);
@@ -223,13 +285,13 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View v, const Ro
     }
 }
 
-// Heads a warp takes one after the other: enough warps for two per scheduler
-// come first, fewer and longer ones after that.
-int heads_per_warp(int64_t tokens, int rounds) {
-    int chunk = 1;
-    while (chunk < rounds && tokens * ((rounds + 2 * chunk - 1) / (2 * chunk)) >= 152 * 4 * 2)
-        chunk *= 2;
-    return chunk;
+// Vectors a warp takes one after the other (up to `most`) of the `all` of a token:
+// warps for two per scheduler come first, longer ones after that.
+int rounds_of(int64_t tokens, int all, int most) {
+    int n = 1;
+    while (2 * n <= most && n < all && tokens * ((all + 2 * n - 1) / (2 * n)) >= 152 * 4 * 2)
+        n *= 2;
+    return n;
 }
 
 }  // namespace
@@ -251,7 +313,7 @@ extern "C" uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start, 
         return UW_ERR_INVALID_ARG;
     if (rot_dim % 16 || rot_dim > c->head_dim || q_heads > kKv4MaxHeads)
         return UW_ERR_UNSUPPORTED;
-    if ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) & 3)
+    if ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) & 15)
         return UW_ERR_INVALID_ARG;
     if (p.v.n_tokens == 0)
         return UW_OK;
@@ -263,9 +325,12 @@ extern "C" uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start, 
     p.q_heads = q_heads;
     p.rot = rot_dim;
     p.interleaved = interleaved != 0;
-    const int g = c->head_dim == 128 ? 2 : 4, rounds = (q_heads + 2 * c->kv_heads + g - 1) / g;
-    p.chunk = heads_per_warp(n_tokens, rounds);
-    const int64_t units = n_tokens * ((rounds + p.chunk - 1) / p.chunk);
+    const int g = c->head_dim == 128 ? 2 : 4, q_all = (q_heads + g - 1) / g, kv_all = (2 * c->kv_heads + g - 1) / g;
+    p.q_rounds = rounds_of(n_tokens, q_all, 16);
+    p.kv_rounds = rounds_of(n_tokens, kv_all, 8);
+    p.q_units = (q_all + p.q_rounds - 1) / p.q_rounds;
+    p.kv_units = (kv_all + p.kv_rounds - 1) / p.kv_rounds;
+    const int64_t units = n_tokens * (p.q_units + p.kv_units);
     if (units > int64_t(8) * 0x7fffffff)
         return UW_ERR_UNSUPPORTED;
     const dim3 grid(unsigned((units + 7) / 8));
@@ -290,7 +355,7 @@ extern "C" uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start, co
     if (!kv4_rows(k, &ko) || !kv4_rows(v, &vo))
         return UW_ERR_INVALID_ARG;
     const int g = c->head_dim == 128 ? 2 : 4, rounds = (2 * c->kv_heads + g - 1) / g;
-    const int chunk = heads_per_warp(n_tokens, rounds);
+    const int chunk = rounds_of(n_tokens, rounds, 8);
     const int64_t units = n_tokens * ((rounds + chunk - 1) / chunk);
     if (units > int64_t(8) * 0x7fffffff)
         return UW_ERR_UNSUPPORTED;
