@@ -5,9 +5,9 @@
 // Memory bound: a row is read once, kept in registers as fp32 through the
 // sum of squares, and written once.  Rows on 16-byte boundaries with a
 // multiple of 8 values up to kMaxVecDim run on 16-byte loads: one warp a row
-// up to 1024 values (no barrier; 8 rows a CTA), one CTA a row above.  Other
-// rows (odd sizes, unaligned strides, longer rows) are walked value by value
-// and read again in place of being kept.
+// up to 1024 values (no barrier; 8 rows a CTA), one CTA a row above.  Rows of
+// other sizes, strides or alignments are read value by value, and longer ones
+// read again in place of being kept.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -74,33 +74,35 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float a, float b) {
 
 // The 8-bit form of a row from u = h * w (exact in fp32: 8 x 8 significant
 // bits) and its largest magnitude.  1 / rms stands in y and in the scale and
-// cancels in y / scale = u / (max |u| / 448), so a code depends on two
+// cancels in y / scale = u * (448 / max |u|), so a code depends on two
 // roundings only.  A row whose scale is the smallest (max |y| below 448 *
-// 2^-126) divides y itself; one that is not finite, or whose u is not, has a
+// 2^-126) takes y times 2^126; one that is not finite, or whose u is not, has a
 // NaN scale.
 struct RowScale {
-    float scale, mul, div;
+    float scale, a, b;
     __device__ __forceinline__ RowScale(float top, float rstd) {
         const float own = top * rstd / kE4m3Max;
         scale = max_nan(own, kMinScale);
-        const bool least = own <= kMinScale;
-        mul = least ? rstd : 1.f;
-        div = own <= INFINITY ? (least ? kMinScale : top / kE4m3Max) : scale;
+        const bool least = own <= kMinScale, small = top < 1e-30f;  // 448 / top beyond fp32
+        a = least ? rstd : small ? 1.f / top : kE4m3Max / top;
+        b = least ? 1.f / kMinScale : small ? kE4m3Max : 1.f;
+        if (!(own <= INFINITY))
+            a = scale;
     }
-    __device__ __forceinline__ float of(float u) const { return u * mul / div; }
+    __device__ __forceinline__ float of(float u) const { return u * a * b; }
 };
 
-// Eight values of a row in fp32: load x (+ r, rounded to BF16 and stored to h).
-__device__ __forceinline__ void load8(const NormParams &p, int64_t row, int64_t i, float (&f)[8]) {
-    const uint4 xv = *reinterpret_cast<const uint4 *>(p.x + row * p.xs + i);
+// Eight values of h in fp32: x, or with a residual x + r rounded to BF16 and
+// stored.
+__device__ __forceinline__ void add8(const NormParams &p, int64_t row, int64_t i, const uint4 &xv, const uint4 &rv,
+                                     float (&f)[8]) {
     uint32_t a[4] = {xv.x, xv.y, xv.z, xv.w};
     if (p.r) {
-        const uint4 rv = *reinterpret_cast<const uint4 *>(p.r + row * p.rs + i);
         const uint32_t b[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
         for (int k = 0; k < 4; k++)
             a[k] = bf16_pack(bf16_lo(a[k]) + bf16_lo(b[k]), bf16_hi(a[k]) + bf16_hi(b[k]));
-        if (p.h)
+        if (p.h && i < p.d)
             *reinterpret_cast<uint4 *>(p.h + row * p.hs + i) = make_uint4(a[0], a[1], a[2], a[3]);
     }
 #pragma unroll
@@ -115,17 +117,22 @@ template <int V, bool k8, bool kWarp>
 __device__ __forceinline__ void norm_row(const NormParams &p, int64_t row, int t, int T, float *slots) {
     float f[V][8];
     float ss = 0.f;
+    // all loads before the first store, which could otherwise not pass it
+    uint4 xv[V], w[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
         const int64_t i = 8 * (int64_t(v) * T + t);
-        if (i < p.d) {
-            load8(p, row, i, f[v]);
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-                ss = fmaf(f[v][k], f[v][k], ss);
-        }
+        xv[v] = i < p.d ? *reinterpret_cast<const uint4 *>(p.x + row * p.xs + i) : make_uint4(0, 0, 0, 0);
+        w[v] = i < p.d && p.r ? *reinterpret_cast<const uint4 *>(p.r + row * p.rs + i) : make_uint4(0, 0, 0, 0);
     }
-    uint4 w[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        const int64_t i = 8 * (int64_t(v) * T + t);
+        add8(p, row, i, xv[v], w[v], f[v]);
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            ss = fmaf(f[v][k], f[v][k], ss);
+    }
 #pragma unroll
     for (int v = 0; v < V; v++) {
         const int64_t i = 8 * (int64_t(v) * T + t);
@@ -191,9 +198,75 @@ __global__ void __launch_bounds__(512) norm_cta_kernel(const NormParams p) {
     norm_row<V, k8, false>(p, blockIdx.x, threadIdx.x, blockDim.x, slots);
 }
 
-// Any size, stride and alignment: the row is walked value by value, and
-// h (or x) read again for the second and third pass (by the thread that
-// wrote it).
+// Rows whose size, stride or alignment is not one of 16-byte loads, up to V
+// values a thread: the same with single values, thread t of T having t, t + T, ...
+template <int V, bool k8>
+__global__ void __launch_bounds__(512) norm_odd_kernel(const NormParams p) {
+    __shared__ float slots[64];
+    grid_dep_launch();
+    grid_dep_wait();
+    const int64_t row = blockIdx.x;
+    const int d = int(p.d), T = blockDim.x;
+    const uint16_t *x = p.x + row * p.xs, *r = p.r ? p.r + row * p.rs : nullptr;
+    uint16_t *h = p.h ? p.h + row * p.hs : nullptr;
+    // all loads before the first store, which could otherwise not pass it
+    float f[V], w[V], ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        const int i = v * T + int(threadIdx.x);
+        f[v] = i < d ? bf16_lo(x[i]) : 0.f;
+    }
+    if (r) {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int i = v * T + int(threadIdx.x);
+            w[v] = i < d ? bf16_lo(r[i]) : 0.f;
+        }
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int i = v * T + int(threadIdx.x);
+            const __nv_bfloat16 b = __float2bfloat16_rn(f[v] + w[v]);
+            if (h && i < d)
+                h[i] = __bfloat16_as_ushort(b);
+            f[v] = __bfloat162float(b);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        const int i = v * T + int(threadIdx.x);
+        w[v] = i < d ? bf16_lo(p.w[i]) : 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++)
+        ss = fmaf(f[v], f[v], ss);
+    const float rstd = rsqrtf(cta_reduce<false>(ss, slots) / float(d) + p.eps);
+    float top = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        const int i = v * T + int(threadIdx.x);
+        if (i < d) {
+            f[v] *= w[v];
+            if constexpr (k8)
+                top = max_nan(top, fabsf(f[v]));
+            else
+                static_cast<uint16_t *>(p.y)[row * p.ys + i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[v] * rstd));
+        }
+    }
+    if constexpr (k8) {
+        const RowScale s(cta_reduce<true>(top, slots + 32), rstd);
+        if (threadIdx.x == 0)
+            p.scale[row] = s.scale;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const int i = v * T + int(threadIdx.x);
+            if (i < d)
+                static_cast<uint8_t *>(p.y)[row * p.ys + i] = to_e4m3(s.of(f[v]));
+        }
+    }
+}
+
+// Longer rows of any kind: the row is walked value by value, and x and r read
+// again for the second and third pass.
 template <bool k8>
 __global__ void __launch_bounds__(512) norm_any_kernel(const NormParams p) {
     __shared__ float slots[64];
@@ -236,7 +309,14 @@ __global__ void __launch_bounds__(512) norm_any_kernel(const NormParams p) {
 
 template <bool k8>
 cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t st) {
-    if (!vec || p.d > kMaxVecDim)
+    if (!vec && p.d <= kMaxVecDim) {
+        const int v = p.d <= 8 * 512 ? 8 : p.d <= 16 * 512 ? 16 : 32;
+        const dim3 grid(unsigned(p.n)), block(unsigned((p.d + 32 * v - 1) / (32 * v) * 32));
+        return v == 8    ? launch_overlapped(norm_odd_kernel<8, k8>, grid, block, 0, st, p)
+               : v == 16 ? launch_overlapped(norm_odd_kernel<16, k8>, grid, block, 0, st, p)
+                         : launch_overlapped(norm_odd_kernel<32, k8>, grid, block, 0, st, p);
+    }
+    if (p.d > kMaxVecDim)
         return launch_overlapped(norm_any_kernel<k8>, dim3(unsigned(p.n)), dim3(512), 0, st, p);
     const int vecs = int(p.d / 8);
     if (p.d <= kWarpDim) {
