@@ -97,15 +97,16 @@ struct Sched {
     static __device__ __forceinline__ uint64_t seq_units_warp(const AttnParams &p, const Seq &s) {
         if (!mine(p, s))
             return 0;
-        uint64_t n = 0;
         const int rts = row_tiles(p, s);
+        if (rts == 1)
+            return kCost + tiles(tile_keys(p, s, 0));
+        uint64_t n = 0;
         for (int rt = threadIdx.x & 31; rt < rts; rt += 32)
             n += kCost + tiles(tile_keys(p, s, rt));
-        if (rts > 1)
 #pragma unroll
-            for (int o = 16; o; o >>= 1)
-                n += __shfl_xor_sync(0xffffffffu, n, o);
-        return rts > 1 ? n : __shfl_sync(0xffffffffu, n, 0);
+        for (int o = 16; o; o >>= 1)
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+        return n;
     }
     static __device__ __forceinline__ void set_tile(const AttnParams &p, Item &it, int rt) {
         it.rt = rt;
@@ -219,8 +220,12 @@ __device__ __forceinline__ Item locate(const AttnParams &p, const Row<kThreads> 
     it.head = int(divide(rest, per_head));
     rest -= it.head * per_head;
     it.u0 += it.head * per_head;
-    // its row tile: 32 of them at a time
     const int rts = S::row_tiles(p, it.q);
+    if (rts == 1) {
+        S::set_tile(p, it, 0);
+        return it;
+    }
+    // its row tile: 32 of them at a time
     for (int rt0 = 0;; rt0 += 32) {
         const int rt = rt0 + lane;
         uint32_t n = 0;
@@ -229,13 +234,12 @@ __device__ __forceinline__ Item locate(const AttnParams &p, const Row<kThreads> 
             n = it.n;
         }
         uint64_t upto = n;
-        if (rts > 1)
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o)
-                    upto += x;
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o)
+                upto += x;
+        }
         const uint32_t past = __ballot_sync(0xffffffffu, rt < rts && rest < upto);
         if (past) {
             const int at = __ffs(past) - 1;

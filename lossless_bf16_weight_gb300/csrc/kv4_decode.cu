@@ -598,20 +598,24 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             const int r0 = head.rt * RB;
             if (row >= head.tokens * p.group - r0)
                 continue;
-            float m = -INFINITY, l = 0.f;
+            // every part's place in the loops is known, so that their loads go out together
+            const uint32_t in = some & ((2u << (b - 1)) - (1u << a));
+            float w[2 * kWarps], m = -INFINITY, l = 0.f;
             int tiles = 0;
-            for (int k = a; k < b; k++)
-                if (some >> k & 1) {
-                    m = fmaxf(m, parts[k].at[RB * D + row]);
-                    tiles += parts[k].tiles;
-                }
+#pragma unroll
+            for (int k = 0; k < 2 * kWarps; k++) {
+                const Part &part = parts[in >> k & 1 ? k : a];
+                w[k] = in >> k & 1 ? part.at[RB * D + row] : -INFINITY;
+                tiles += in >> k & 1 ? part.tiles : 0;
+                m = fmaxf(m, w[k]);
+            }
             const float m0 = m == -INFINITY ? 0.f : m;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = a; k < b; k++)
-                if (some >> k & 1) {
+#pragma unroll
+            for (int k = 0; k < 2 * kWarps; k++)
+                if (in >> k & 1) {
                     const float *q = parts[k].at;
-                    join_scaled(l, acc, exp2_fast(q[RB * D + row] - m0), q[RB * D + RB + row],
-                                reinterpret_cast<const float4 *>(q)[x]);
+                    join_scaled(l, acc, exp2_fast(w[k] - m0), q[RB * D + RB + row], reinterpret_cast<const float4 *>(q)[x]);
                 }
             const int c = x % (D / 4);
             if (tiles == head.of) {
@@ -670,18 +674,26 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             sums[i] = in ? __ldcg(part_of(i / RB) + RB * D + RB + i % RB) : 0.f;
         }
         __syncthreads();
-        if (threadIdx.x < RB) {
+        for (int row = warp; row < real; row += kWarps) {  // a warp a row, a lane a part
             float m = -INFINITY, l = 0.f;
-            for (int i = 0; i < n; i++)
-                m = fmaxf(m, wt[i * RB + threadIdx.x]);
+            for (int i = lane; i < n; i += 32)
+                m = fmaxf(m, wt[i * RB + row]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float m0 = m == -INFINITY ? 0.f : m;
-            for (int i = 0; i < n; i++) {
-                const float w = exp2_fast(wt[i * RB + threadIdx.x] - m0);
-                wt[i * RB + threadIdx.x] = w;
-                l = fmaf(w, sums[i * RB + threadIdx.x], l);
+            for (int i = lane; i < n; i += 32) {
+                const float w = exp2_fast(wt[i * RB + row] - m0);
+                wt[i * RB + row] = w;
+                l = fmaf(w, sums[i * RB + row], l);
             }
-            row_m[threadIdx.x] = m;
-            row_l[threadIdx.x] = l;
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) {
+                row_m[row] = m;
+                row_l[row] = l;
+            }
         }
         __syncthreads();
         constexpr int F4 = RB * (D / 4);
