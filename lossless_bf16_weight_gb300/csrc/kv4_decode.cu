@@ -74,11 +74,20 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // takes from one lane group fall on different halves of the banks.
 __device__ __forceinline__ int key_of(int k) { return k ^ ((k >> 1) & 1); }
 
-// Where 16-byte chunk ch of V row r lies in its row (D = 128: rows 4..7 of
-// eight have their halves exchanged, against bank conflicts of the 8-byte loads).
+// Where 16-byte chunk ch of V row r lies in its row: the same chunk of eight
+// consecutive rows falls on all banks.
 template <int D>
 __device__ __forceinline__ int v_chunk(int r, int ch) {
-    return D == 128 ? ch ^ (((r >> 2) & 1) << 1) : ch;
+    return ch ^ ((r >> (D == 128 ? 1 : 2)) & (D / 32 - 1));
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed: lane (g, t) gets rows 2t
+// and 2t + 1 of column g of each; lane 8 i + r gives the address of row r of matrix i.
+__device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
 }
 
 template <int D, int NT>
@@ -304,6 +313,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             asm volatile("cp.async.wait_group %0;" :: "n"(ST - 1) : "memory");
             __syncwarp();
             const unsigned char *const st = ring + stage * kStageBytes<D>;
+            const uint32_t st_at = ring_at + stage * kStageBytes<D>;
             stage = stage + 1 == ST ? 0 : stage + 1;
             const int key0 = (sg.first + i) * kTile;
 
@@ -480,37 +490,29 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                 }
             // output
 #pragma unroll
-            for (int mt = 0; mt < 2; mt++) {
-                constexpr int VW = D / 64;  // 32-bit words of a row for one lane
-                uint32_t x[4][VW];
+            for (int mt = 0; mt < 2; mt++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    // keys of the product's rows 2t, 2t + 1, 2t + 8, 2t + 9
-                    const int r = 16 * mt + 8 * (j >> 1) + key_of(2 * t + (j & 1));
-                    const unsigned char *row = st + kTile * (D / 2) + r * (D / 2);
-                    if constexpr (D == 128) {
-                        const uint2 y = *reinterpret_cast<const uint2 *>(row + v_chunk<D>(r, g >> 1) * 16 + (g & 1) * 8);
-                        x[j][0] = y.x, x[j][1] = y.y;
-                    } else {
-                        x[j][0] = *reinterpret_cast<const uint32_t *>(row + g * 4);
-                    }
-                }
+                for (int c = 0; c < D / 64; c++) {
+                    // x[2 e + h]: keys 8 h + 2t, + 1, the four codes 4 g .. of chunk 2 c + e
+                    uint32_t x[4];
+                    const int r = 16 * mt + (lane & 8) + key_of(lane & 7);
+                    ldmatrix_t(x, st_at + kTile * (D / 2) + r * (D / 2) + v_chunk<D>(r, 2 * c + (lane >> 4)) * 16);
 #pragma unroll
-                for (int k = 0; k < VW; k++)
+                    for (int e = 0; e < 2; e++)
 #pragma unroll
-                    for (int b = 0; b < 4; b++) {
-                        const uint32_t sel = b * 0x11u | (4 + b) * 0x1100u;
-                        const uint32_t e = __byte_perm(x[0][k], x[1][k], sel), f = __byte_perm(x[2][k], x[3][k], sel);
-                        const uint32_t a0 = codes.low_mid(e), a1 = codes.high_mid(e);
-                        const uint32_t a2 = codes.low_mid(f), a3 = codes.high_mid(f);
+                        for (int j = 0; j < 2; j++) {
+                            const uint32_t y = j ? x[2 * e] >> 8 : x[2 * e], z = j ? x[2 * e + 1] >> 8 : x[2 * e + 1];
+                            const uint32_t a0 = codes.low_mid(y), a1 = codes.high_mid(y);
+                            const uint32_t a2 = codes.low_mid(z), a3 = codes.high_mid(z);
 #pragma unroll
-                        for (int nt = 0; nt < NT; nt++) {
-                            mma16816(w.o[4 * k + b][nt], a0, a1, a2, a3, hi[mt][nt][0], hi[mt][nt][1]);
-                            if constexpr (!kDup)
-                                mma16816(w.o[4 * k + b][nt], a0, a1, a2, a3, lo[mt][nt][0], lo[mt][nt][1]);
+                            for (int nt = 0; nt < NT; nt++) {
+                                float(&o)[4] = w.o[4 * c + 2 * e + j][nt];
+                                mma16816(o, a0, a1, a2, a3, hi[mt][nt][0], hi[mt][nt][1]);
+                                if constexpr (!kDup)
+                                    mma16816(o, a0, a1, a2, a3, lo[mt][nt][0], lo[mt][nt][1]);
+                            }
                         }
-                    }
-            }
+                }
             __syncwarp();
         }
         // A whole item is written out; a part of one goes to the workspace, or
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                     l += __shfl_xor_sync(0xffffffffu, l, o);
                     z += __shfl_xor_sync(0xffffffffu, z, o);
                 }
-                float o[D / 8];  // dimensions D/8 g .. of row 8 nt + 2 t + k
+                float o[D / 8];  // o[4 c + i]: dimension 32 c + 4 g + i of row 8 nt + 2 t + k
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) {
                     o[2 * i] = w.o[i][nt][k] * kPDownLow;
@@ -556,12 +558,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                 const int row = 8 * nt + 2 * t + k;
                 if ((!kDup || t < 2) && r0 + row < rows) {
                     if (whole) {
-                        store_dims<D / 8>(p, sg.t0, sg.head, r0 + row, (D / 8) * g, o, w.m[nt][k], l);
-                    } else {
-                        float4 *const dst = reinterpret_cast<float4 *>(part) + row * (D / 4) + g * (D / 32);
 #pragma unroll
                         for (int i = 0; i < D / 32; i++)
-                            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            store_row<D>(p, sg.t0, sg.head, r0 + row, 8 * i + g,
+                                         make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]), w.m[nt][k], l);
+                    } else {
+                        float4 *const dst = reinterpret_cast<float4 *>(part) + row * (D / 4) + g;
+#pragma unroll
+                        for (int i = 0; i < D / 32; i++)
+                            dst[8 * i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         if (g == 0) {
                             part[RB * D + row] = w.m[nt][k];
                             part[RB * D + RB + row] = l;
