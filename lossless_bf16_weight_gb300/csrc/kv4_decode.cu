@@ -69,16 +69,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-// The key of a tile that row k of a product's 16 stands for: with rows 2, 3
-// (mod 4) exchanged, the eight rows of a K load and the rows that a V load
-// takes from one lane group fall on different halves of the banks.
-__device__ __forceinline__ int key_of(int k) { return k ^ ((k >> 1) & 1); }
-
-// Where 16-byte chunk ch of V row r lies in its row: the same chunk of eight
-// consecutive rows falls on all banks.
+// A product's 16 keys: row 8 h + i of product mt stands for key 4 i + 2 mt + h
+// of the tile, so that a lane's four keys (i = g) and their scales and offsets
+// lie side by side.  Rows of codes lie in 128-byte lines, several to a line,
+// and the 16-byte chunks of a line are exchanged by turn(row / 4): the rows
+// 4 i + .. of eight (or, for the wider loads of K, of a phase's) lanes are then
+// on different banks.
 template <int D>
-__device__ __forceinline__ int v_chunk(int r, int ch) {
-    return ch ^ ((r >> (D == 128 ? 1 : 2)) & (D / 32 - 1));
+__device__ __forceinline__ uint32_t turn(uint32_t i) {
+    return (D == 128 ? (i & 1) << 2 | i >> 1 : i << 1 | i >> 2) & 7;
 }
 
 // Four 8 x 8 matrices of 16-bit values, transposed: lane (g, t) gets rows 2t
@@ -175,76 +174,63 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         }
     }
     Seg *const segs = all_segs[warp];
-    const int64_t block = int64_t(D + 8) << v.page_log2, page_bytes = block * v.heads;
+    const int64_t block = int64_t(D + 8) << v.page_log2;
+    const uint32_t page_bytes = uint32_t(block) * v.heads;  // (at most 65536 heads of 34816 bytes)
     const int mask = (1 << v.page_log2) - 1;
-    const int v_off = (D / 2) << v.page_log2;
+    const uint32_t v_off = (D / 2) << v.page_log2;
 
-    // The warp's next tile to copy: segment, tile, and the lane's page (that of
-    // key 16 * (lane / 16) of the tile, which may lie in two pages of 16).  It
-    // runs ahead of the products through all listed segments.
-    // A list of segments starts with nx_seg = -1: the first call only finds the
-    // first tile.
-    int nx_seg = -1, nx_tile = 0, nx_end = 0, nx_page = -1, n_segs = 0;
+    // The warp's next tile to copy runs ahead of the products through all listed
+    // segments.  Lanes 0..15 copy its keys 0..15, the others the rest (which may
+    // lie in another page of 16): nx_key is the lane's first, nx_page its page.  A
+    // tile's keys are always copied in full, they are there in the page; what
+    // no row sees is left out of the sums.
+    int n_segs = 0, nx_seg = 0, nx_tiles = 0, nx_key = 0, nx_last = 0, nx_page = 0;
+    const uint8_t *nx_base = nullptr;
+    const int32_t *nx_table = nullptr;
+    bool bad = false;
+    auto next_seg = [&]() {
+        while (nx_seg < n_segs && segs[nx_seg].tiles == 0)
+            nx_seg++;
+        if (nx_seg == n_segs)
+            return;
+        const Seg &sg = segs[nx_seg++];
+        nx_tiles = sg.tiles;
+        nx_key = sg.first * kTile + (lane & 16);
+        nx_last = sg.len - 1;
+        nx_base = v.pages + (sg.head * block + (lane & 15) * 16);
+        nx_table = v.table + int64_t(sg.s) * v.table_stride;
+        nx_page = __ldg(nx_table + (min(nx_key, nx_last) >> v.page_log2));
+    };
+    constexpr int RC = D / 32;  // 16-byte chunks of a row
+    const uint32_t first_row = (lane & 16) + (lane & 15) / RC;
+    const uint32_t to0 = ((first_row * RC + lane % RC) ^ turn<D>(first_row >> 2)) * 16;
+    const uint32_t par_off = kv4_params<D>(v.page_log2, 0, (lane >> 2) & 1) - (lane & 12) * 16;  // from the lane's codes
+    const uint32_t par_to = kTile * D + ((lane & 4) ? kTile * 4 : 0) + ((lane & 16) ? 64 : 0) + (lane & 3) * 16;
     auto issue = [&](int stage) {
-        if (nx_seg >= 0 && nx_seg < n_segs) {
-            const Seg &sg = segs[nx_seg];
+        if (nx_tiles > 0) {
             const uint32_t dst = ring_at + stage * kStageBytes<D>;
-            const int key0 = nx_tile * kTile;
-            const uint8_t *const base = v.pages + sg.head * block;
-            constexpr int RC = D / 32;             // 16-byte chunks of a row
-            const uint8_t *half[2];                // codes of keys 0..15 and 16..31, the lane's chunk
-            int pages[2], slots[2];
-            if (uint32_t(nx_page) >= uint32_t(v.n_pages)) {  // (looked at here, not where it is loaded)
-                atomicOr(v.status, uint32_t(kStatusBadCache));
-                nx_page = -1;
-            }
+            const bool ok = uint32_t(nx_page) < uint64_t(v.n_pages);  // (looked at here, not where it is loaded)
+            bad = bad || !ok;
+            const uint32_t slot = nx_key & mask, bytes = ok ? 16 : 0;
+            const uint8_t *const page = nx_base + uint64_t(ok ? nx_page : 0) * page_bytes;
+            const uint8_t *const src = page + slot * (D / 2);
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                pages[h] = __shfl_sync(0xffffffffu, nx_page, 16 * h);
-                slots[h] = (key0 + 16 * h) & mask;
-                half[h] = base + pages[h] * page_bytes + (slots[h] * (D / 2) + lane * 16);
+            for (int j = 0; j < RC; j++) {
+                // rows first_row + 16 / RC j; what that does to their turn
+                constexpr uint32_t kStep = D == 128 ? 1 : 2;
+                const uint32_t to = dst + (to0 ^ (turn<D>(kStep * j) * 16)) + j * 256;
+                cp_async16_zfill(to, src + j * 256, bytes);
+                cp_async16_zfill(to + kTile * (D / 2), src + (v_off + j * 256), bytes);
             }
-            const uint32_t to = dst + lane * 16;   // consecutive lanes, consecutive chunks
-            const uint32_t vto = dst + kTile * (D / 2) + (lane / RC) * (D / 2) + v_chunk<D>(lane / RC, lane % RC) * 16;
-            const int left = sg.len - key0;        // keys of the tile that there are
-            const bool full = left >= kTile && (pages[0] | pages[1]) >= 0;
-            if (full) {
-#pragma unroll
-                for (int j = 0; j < RC; j++) {
-                    const uint8_t *src = half[j / (RC / 2)] + (j % (RC / 2)) * 512;
-                    cp_async16(to + j * 512, src);
-                    cp_async16(vto + j * 512, src + v_off);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < RC; j++) {
-                    const uint8_t *src = half[j / (RC / 2)] + (j % (RC / 2)) * 512;
-                    const bool in = pages[j / (RC / 2)] >= 0 && j * (32 / RC) + lane / RC < left;
-                    cp_async16_zfill(to + j * 512, in ? src : v.pages, in ? 16u : 0u);
-                    cp_async16_zfill(vto + j * 512, in ? src + v_off : v.pages, in ? 16u : 0u);
-                }
-            }
-            if (lane < 16) {
-                const int r = (lane & 7) * 4, h = (lane >> 2) & 1;
-                const bool in = (h ? pages[1] : pages[0]) >= 0 && r < left;
-                const uint8_t *src = base + (h ? pages[1] : pages[0]) * page_bytes +
-                                     kv4_params<D>(v.page_log2, (h ? slots[1] : slots[0]) + (r & 15), lane >> 3);
-                cp_async16_zfill(dst + kTile * D + lane * 16, in ? src : v.pages, in ? 16u : 0u);
-            }
+            if ((lane & 8) == 0)
+                cp_async16_zfill(dst + par_to, page + (slot * 4 + par_off), bytes);
+            nx_key += kTile;
+            if (--nx_tiles == 0)
+                next_seg();
+            else
+                nx_page = __ldg(nx_table + (min(nx_key, nx_last) >> v.page_log2));
         }
         cp_async_commit();
-        if (++nx_tile >= nx_end) {
-            do
-                nx_seg++;
-            while (nx_seg < n_segs && segs[nx_seg].tiles == 0);
-            if (nx_seg >= n_segs)
-                return;
-            nx_tile = segs[nx_seg].first;
-            nx_end = nx_tile + segs[nx_seg].tiles;
-        }
-        const Seg &sg = segs[nx_seg];
-        const int key = min(nx_tile * kTile + (lane & 16), sg.len - 1);  // (the last key's where there is no other)
-        nx_page = __ldg(v.table + int64_t(sg.s) * v.table_stride + (key >> v.page_log2));
     };
 
     const Codes codes;
@@ -252,9 +238,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     int stage = 0;  // the ring's next stage to use
     while (u < u_end) {
         u = list_segments<S, kSegs>(p, it, u, u_end, segs, &n_segs);
-        nx_seg = -1;
-        nx_end = 0;
-        int fill = stage == 0 ? ST - 1 : stage - 1, calls = ST + 1;
+        nx_seg = 0;
+        next_seg();
+        int fill = stage, calls = ST;
         for (int sgi = 0; sgi < n_segs; sgi++) {
         const Seg &sg = segs[sgi];
         const int n_mine = sg.tiles;
@@ -326,41 +312,39 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
 #pragma unroll
                     for (int k = 0; k < 4; k++)
                         sc[mt][nt][k] = 0.f;
-            uint32_t a[2][2][D / 32];  // [keys 16 mt + key_of(g), + 8][words]
+            uint32_t a[4][D / 32];  // [key 4 g + j][words]
 #pragma unroll
-            for (int mt = 0; mt < 2; mt++)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const unsigned char *row = st + (16 * mt + 8 * h + key_of(g)) * (D / 2) + t * (D / 8);
-                    if constexpr (D == 128) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(row);
-                        a[mt][h][0] = x.x, a[mt][h][1] = x.y, a[mt][h][2] = x.z, a[mt][h][3] = x.w;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(row);
-                        a[mt][h][0] = x.x, a[mt][h][1] = x.y;
-                    }
+            for (int j = 0; j < 4; j++) {
+                // row 4 g + j, bytes D / 8 t ..
+                const uint32_t s0 = D == 128 ? g * 16 + (t ^ turn<D>(g)) : g * 8 + ((t >> 1) ^ turn<D>(g));
+                const unsigned char *at =
+                    st + ((s0 * 16) ^ (D == 128 ? (j & 1) * 64 : j * 32)) + (D == 128 ? (j >> 1) * 128 : (t & 1) * 8);
+                if constexpr (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(at);
+                    a[j][0] = x.x, a[j][1] = x.y, a[j][2] = x.z, a[j][3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                    a[j][0] = x.x, a[j][1] = x.y;
                 }
+            }
 #pragma unroll
             for (int k = 0; k < D / 32; k++)
 #pragma unroll
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int mt = 0; mt < 2; mt++) {
-                        const uint32_t x = j ? a[mt][0][k] >> 8 : a[mt][0][k], y = j ? a[mt][1][k] >> 8 : a[mt][1][k];
+                        const uint32_t x = j ? a[2 * mt][k] >> 8 : a[2 * mt][k];
+                        const uint32_t y = j ? a[2 * mt + 1][k] >> 8 : a[2 * mt + 1][k];
                         const uint32_t a0 = codes.low(x), a1 = codes.low(y), a2 = codes.high(x), a3 = codes.high(y);
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++)
                             mma16816(sc[mt][nt], a0, a1, a2, a3, w.q[nt][2 * k + j][0], w.q[nt][2 * k + j][1]);
                     }
-            // sc[mt][nt][2 h + k]: key 16 mt + 8 h + key_of(g), row 8 nt + 2 t + k.
+            // sc[mt][nt][2 h + k]: key 4 g + 2 mt + h, row 8 nt + 2 t + k.
             // In log2 units and less the maximum: y - m = acc * a + (c * qs - m).
-            uint32_t kpar[4], vpar[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const unsigned char *at = st + kTile * D + (8 * j + key_of(g)) * 4;
-                kpar[j] = *reinterpret_cast<const uint32_t *>(at);
-                vpar[j] = *reinterpret_cast<const uint32_t *>(at + kTile * 4);
-            }
+            const uint4 kp = *reinterpret_cast<const uint4 *>(st + kTile * D + g * 16);
+            const uint4 vp = *reinterpret_cast<const uint4 *>(st + kTile * (D + 4) + g * 16);
+            const uint32_t kpar[4] = {kp.x, kp.y, kp.z, kp.w}, vpar[4] = {vp.x, vp.y, vp.z, vp.w};
             const bool open = key0 < all_lo || key0 + kTile > all_hi;
             uint64_t y[4][NT];
             auto scores = [&]() {
@@ -384,7 +368,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                             const KeyRange kr = visible(p, sq, tok, tok);
 #pragma unroll
                             for (int j = 0; j < 4; j++) {
-                                const int key = key0 + 8 * j + key_of(g);
+                                const int key = key0 + 4 * g + j;
                                 in[j][k] = key >= kr.lo && key < min(kr.hi, sq.len);
                             }
                         }
@@ -493,10 +477,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             for (int mt = 0; mt < 2; mt++)
 #pragma unroll
                 for (int c = 0; c < D / 64; c++) {
-                    // x[2 e + h]: keys 8 h + 2t, + 1, the four codes 4 g .. of chunk 2 c + e
+                    // x[2 e + h]: rows 8 h + 2t, + 1, the four codes 4 g .. of chunk 2 c + e
                     uint32_t x[4];
-                    const int r = 16 * mt + (lane & 8) + key_of(lane & 7);
-                    ldmatrix_t(x, st_at + kTile * (D / 2) + r * (D / 2) + v_chunk<D>(r, 2 * c + (lane >> 4)) * 16);
+                    const uint32_t i = lane & 7, h = (lane >> 3) & 1, e0 = lane >> 4;
+                    const uint32_t s0 = D == 128 ? i * 16 + ((h * 4 + e0) ^ turn<D>(i)) : i * 8 + ((h * 2 + e0) ^ turn<D>(i));
+                    ldmatrix_t(x, st_at + kTile * (D / 2) + ((s0 * 16) ^ (D == 128 ? c * 32 : mt * 64)) +
+                                      (D == 128 ? mt * 128 : 0));
 #pragma unroll
                     for (int e = 0; e < 2; e++)
 #pragma unroll
@@ -578,6 +564,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (bad)
+        atomicOr(v.status, uint32_t(kStatusBadCache));
     __syncthreads();
 
     // Items that the cuts between the warps go through: consecutive parts of
