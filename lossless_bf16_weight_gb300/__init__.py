@@ -188,7 +188,7 @@ def _plan_ptr(plan):
 
 
 def _nbytes(t) -> int:
-    return t.nbytes if isinstance(t, np.ndarray) else t.numel() * t.element_size()
+    return t.nbytes
 
 
 def _contiguous(t) -> bool:
@@ -481,10 +481,13 @@ def mlp_autotune(mats, x, y, ws, passes: int = 2, stream=None, side_stream=None)
 
 
 # ---------------------------------------------------------------- around the matmuls of a decoder layer
-def _row_stride(t, d: int, size: int, name: str, n: int, what: str) -> int:
+def _row_stride(t, shape, size: int, name: str, what: str) -> int:
     """Row stride in elements of a [n, d] (or, for one row, [d]) tensor of
     `size`-byte elements whose rows are contiguous."""
-    if t.element_size() != size or t.shape[-1] != d or t.numel() != n * d or t.dim() > 2:
+    if t.shape == shape and t.itemsize == size and t.is_contiguous():
+        return shape[-1]
+    d, n = shape[-1], shape[0] if len(shape) == 2 else 1
+    if t.itemsize != size or t.shape[-1] != d or t.numel() != n * d or t.dim() > 2:
         raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s)" % (what, name, tuple(t.shape), t.dtype))
     if t.is_contiguous():
         return d
@@ -498,15 +501,17 @@ def rmsnorm(x, weight, y, eps: float = 1e-5, residual=None, residual_out=None, s
     With `scale` (fp32, one for each row): uw_rmsnorm_e4m3, y holds e4m3 bytes (torch.float8_e4m3fn or uint8).
     Rows may be strided."""
     what = "uw_rmsnorm" if scale is None else "uw_rmsnorm_e4m3"
-    d = x.shape[-1]
-    n = x.shape[0] if x.dim() == 2 else 1
-    xs = _row_stride(x, d, 2, "x", n, what)
-    ys = _row_stride(y, d, 2 if scale is None else 1, "y", n, what)
-    rs = 0 if residual is None else _row_stride(residual, d, 2, "residual", n, what)
-    hs = 0 if residual_out is None else _row_stride(residual_out, d, 2, "residual_out", n, what)
+    shape = x.shape
+    d, n = shape[-1], shape[0] if len(shape) == 2 else 1
+    xs = _row_stride(x, shape, 2, "x", what)
+    ys = _row_stride(y, shape, 2 if scale is None else 1, "y", what)
+    rp = hp = None
+    rs = hs = 0
+    if residual is not None:
+        rp, rs = residual.data_ptr(), _row_stride(residual, shape, 2, "residual", what)
+    if residual_out is not None:
+        hp, hs = residual_out.data_ptr(), _row_stride(residual_out, shape, 2, "residual_out", what)
     _refuse(_short((weight, 2 * d, "weight")), what)
-    rp = None if residual is None else residual.data_ptr()
-    hp = None if residual_out is None else residual_out.data_ptr()
     if scale is None:
         _check(load().uw_rmsnorm(x.data_ptr(), xs, rp, rs, hp, hs, weight.data_ptr(), n, d, eps, y.data_ptr(), ys,
                                  _stream(stream)), what)
@@ -551,7 +556,7 @@ def kv4_workspace_size(cache: Kv4Cache, q_heads: int) -> int:
 
 
 def _kv4_rows(t, n: int, heads: int, dim: int, name: str, what: str) -> Kv4Rows:
-    if t.shape != (n, heads, dim) or t.element_size() != 2:
+    if t.shape != (n, heads, dim) or t.itemsize != 2:
         raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s, not BF16 [%d, %d, %d])" % (what, name, tuple(t.shape),
                                                                                   t.dtype, n, heads, dim))
     ts, hs, ds = t.stride()
@@ -563,8 +568,8 @@ def _kv4_rows(t, n: int, heads: int, dim: int, name: str, what: str) -> Kv4Rows:
 def _kv4_seqs(cache, start, length, what):
     """start and length are int32 [sequences + 1] and [sequences] at least."""
     n = cache.n_seqs
-    if not (start.is_contiguous() and length.is_contiguous() and start.element_size() == 4 == length.element_size()
-            and start.numel() > n and length.numel() >= n):
+    if not (start.is_contiguous() and length.is_contiguous() and start.itemsize == 4 == length.itemsize and start.numel() > n
+            and length.numel() >= n):
         _refuse("start and length are not int32 of %d and %d values" % (n + 1, n), what)
 
 
@@ -574,18 +579,21 @@ def kv4_append(cache: Kv4Cache, start, length, q, k, v, q_out, cos, sin, ws, int
     what, d = "uw_kv4_append", cache
     n = k.shape[0]
     _kv4_seqs(cache, start, length, what)
-    kr, vr = (_kv4_rows(t, n, d.kv_heads, d.head_dim, name, what) for t, name in ((k, "k"), (v, "v")))
+    kr = _kv4_rows(k, n, d.kv_heads, d.head_dim, "k", what)
+    vr = _kv4_rows(v, n, d.kv_heads, d.head_dim, "v", what)
     heads = 0 if q is None else q.shape[1] if q.dim() == 3 else -1
     qr = orow = None
     if q is not None or q_out is not None:
-        qr, orow = (_kv4_rows(t, n, heads, d.head_dim, name, what) for t, name in ((q, "q"), (q_out, "q_out")))
+        qr = _kv4_rows(q, n, heads, d.head_dim, "q", what)
+        orow = _kv4_rows(q_out, n, heads, d.head_dim, "q_out", what)
     rope_len = rot = 0
     if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape or cos.element_size() != 4 or sin.element_size() != 4:
+        rope = cos.shape
+        if len(rope) != 2 or rope != sin.shape or cos.itemsize != 4 or sin.itemsize != 4:
             raise UwError(UW_ERR_SHAPE, "%s (cos and sin are not fp32 [positions, pairs])" % what)
         if not (cos.is_contiguous() and sin.is_contiguous()):
             raise UwError(UW_ERR_INVALID_ARG, "%s (cos and sin are not contiguous)" % what)
-        rope_len, rot = cos.shape[0], 2 * cos.shape[1]
+        rope_len, rot = rope[0], 2 * rope[1]
     _check(load().uw_kv4_append(cache.ref, start.data_ptr(), length.data_ptr(), n, qr, heads, orow, kr, vr,
                                 cos.data_ptr() if rot else None, sin.data_ptr() if rot else None, rope_len, rot,
                                 interleaved, ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
@@ -596,7 +604,8 @@ def kv4_read(cache: Kv4Cache, start, length, k, v, ws, stream=None):
     what, d = "uw_kv4_read", cache
     n = k.shape[0]
     _kv4_seqs(cache, start, length, what)
-    kr, vr = (_kv4_rows(t, n, d.kv_heads, d.head_dim, name, what) for t, name in ((k, "k"), (v, "v")))
+    kr = _kv4_rows(k, n, d.kv_heads, d.head_dim, "k", what)
+    vr = _kv4_rows(v, n, d.kv_heads, d.head_dim, "v", what)
     _check(load().uw_kv4_read(cache.ref, start.data_ptr(), length.data_ptr(), n, kr, vr, ws.data_ptr(), _nbytes(ws),
                               _stream(stream)), what)
 
@@ -607,7 +616,8 @@ def kv4_attention(cache: Kv4Cache, start, length, q, out, ws, max_new: int = 0, 
     what, d = "uw_kv4_attention", cache
     n, heads = q.shape[0], q.shape[1] if q.dim() == 3 else -1
     _kv4_seqs(cache, start, length, what)
-    qr, orow = (_kv4_rows(t, n, heads, d.head_dim, name, what) for t, name in ((q, "q"), (out, "out")))
+    qr = _kv4_rows(q, n, heads, d.head_dim, "q", what)
+    orow = _kv4_rows(out, n, heads, d.head_dim, "out", what)
     if lse is not None:
         _refuse(_short((lse, 4 * n * heads, "lse")), what)
     _check(load().uw_kv4_attention(cache.ref, start.data_ptr(), length.data_ptr(), n, qr, heads, orow,
