@@ -33,7 +33,7 @@ struct AppendParams {
     int32_t q_rounds, kv_rounds;  // heads such a warp takes one after the other (times 32 / (D / 8))
 };
 
-constexpr int kAhead = 4;  // vectors of q a lane has on their way
+constexpr int kAhead = 2;  // vectors a lane has on their way
 
 // Smaller halves of two pairs of BF16; NaN wherever one is.
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
@@ -104,7 +104,6 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[4], uint32_t *p
 // whole pairs (interleaved).
 struct Rotation {
     float c[8], s[8];  // cosines and sines (half split: with the sign of the side)
-    int other;         // half split: where the other side's values are, from the own
     bool on, interleaved;
 };
 
@@ -140,6 +139,33 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
     if (t >= v.n_tokens)
         return;
     const int part = int(unit - uint64_t(t) * per_token);
+    // The unit's vectors: q heads, or k heads and then v heads.  They are loaded
+    // before the token is looked up, a group of kAhead at a time, and with them the
+    // other sides of their pairs (the same cache lines), before anything is
+    // written: q_out may be q.
+    const bool of_q = part < p.q_units;
+    const int rounds = of_q ? p.q_rounds : p.kv_rounds, all = of_q ? p.q_heads : 2 * v.heads;
+    const int j0 = (of_q ? part : part - p.q_units) * rounds * G + lane / L;
+    const int half = p.rot / 2, i0 = 8 * c;
+    Rotation r;
+    r.on = i0 < p.rot;
+    r.interleaved = p.interleaved;
+    const bool second = i0 >= half;
+    const int other = second ? -half : half;  // half split: where the other side's values are, from the own
+    uint4 x[kAhead], o[kAhead];
+    auto fetch = [&](int n0) {
+#pragma unroll
+        for (int n = 0; n < kAhead; n++) {
+            const int j = j0 + (n0 + n) * G;
+            const bool in = n0 + n < rounds && j < all, is_v = !of_q && j >= v.heads;
+            const Rows &src = of_q ? p.q : is_v ? p.vv : p.k;
+            const uint16_t *at = src.p + t * src.ts + (is_v ? j - v.heads : j) * src.hs + i0;
+            x[n] = in ? *reinterpret_cast<const uint4 *>(at) : make_uint4(0, 0, 0, 0);
+            o[n] = in && !is_v && r.on && !r.interleaved ? *reinterpret_cast<const uint4 *>(at + other)
+                                                         : make_uint4(0, 0, 0, 0);
+        }
+    };
+    fetch(0);
     const int s = kv4_find_seq(v, int(t));
     const Seq q = kv4_seq(v, s);
     if (t < q.t0 || t >= int64_t(q.t0) + q.n)
@@ -150,11 +176,6 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
             atomicOr(v.status, uint32_t(kStatusBadCache));
         return;
     }
-    const int half = p.rot / 2, i0 = 8 * c;
-    Rotation r;
-    r.on = i0 < p.rot;
-    r.interleaved = p.interleaved;
-    r.other = 0;
     if (r.on) {
         const int64_t row = int64_t(pos) * half;
         if (p.interleaved) {
@@ -163,10 +184,8 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
             r.c[0] = cs.x, r.c[1] = cs.y, r.c[2] = cs.z, r.c[3] = cs.w;
             r.s[0] = sn.x, r.s[1] = sn.y, r.s[2] = sn.z, r.s[3] = sn.w;
         } else {
-            const bool second = i0 >= half;
             const float sign = second ? 1.f : -1.f;
             const int j = second ? i0 - half : i0;
-            r.other = second ? -half : half;
 #pragma unroll
             for (int k = 0; k < 2; k++) {
                 const float4 cs = *reinterpret_cast<const float4 *>(p.cos + row + j + 4 * k);
@@ -178,62 +197,51 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
         }
     }
 
-    if (part < p.q_units) {
-        // q: the other side's values are read like the own ones (the same cache
-        // line), before anything is written: q_out may be q
-        const int h0 = part * p.q_rounds * G + lane / L;
-        const uint16_t *src = p.q.p + t * p.q.ts + h0 * p.q.hs + i0;
-        uint16_t *dst = p.qo.p + t * p.qo.ts + h0 * p.qo.hs + i0;
-        for (int n0 = 0; n0 < p.q_rounds; n0 += kAhead) {
-            uint4 x[kAhead], o[kAhead];
-#pragma unroll
-            for (int n = 0; n < kAhead; n++) {
-                const bool in = n0 + n < p.q_rounds && h0 + (n0 + n) * G < p.q_heads;
-                const uint16_t *at = src + int64_t(n0 + n) * G * p.q.hs;
-                x[n] = in ? *reinterpret_cast<const uint4 *>(at) : make_uint4(0, 0, 0, 0);
-                o[n] = in && !r.interleaved ? *reinterpret_cast<const uint4 *>(at + r.other) : make_uint4(0, 0, 0, 0);
-            }
+    if (of_q) {
+        uint16_t *const dst = p.qo.p + t * p.qo.ts + j0 * p.qo.hs + i0;
+        for (int n0 = 0;;) {
             __syncwarp();
 #pragma unroll
             for (int n = 0; n < kAhead; n++) {
                 uint32_t a[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
                 rotate(r, a, o[n]);
-                if (n0 + n < p.q_rounds && h0 + (n0 + n) * G < p.q_heads)
+                if (n0 + n < rounds && j0 + (n0 + n) * G < all)
                     *reinterpret_cast<uint4 *>(dst + int64_t(n0 + n) * G * p.qo.hs) = make_uint4(a[0], a[1], a[2], a[3]);
             }
+            n0 += kAhead;
+            if (n0 >= rounds)
+                return;
+            fetch(n0);
         }
-        return;
     }
-    // k heads, then v heads
     uint8_t *const page = kv4_block<D>(v, s, pos, 0);  // the token's page, block of head 0
     if (!page)
         return;
     const int slot = pos & ((1 << v.page_log2) - 1);
     const int64_t block = int64_t(D + 8) << v.page_log2;
-    const int j0 = (part - p.q_units) * p.kv_rounds * G + lane / L;
-#pragma unroll 2
-    for (int n = 0; n < p.kv_rounds; n++) {
-        const int j = j0 + n * G;
-        if (j - lane / L >= 2 * v.heads)
-            break;
-        const bool mine = j < 2 * v.heads, is_v = j >= v.heads;
-        const int h = is_v ? j - v.heads : j;
-        const Rows &src = is_v ? p.vv : p.k;
-        const uint16_t *at = src.p + t * src.ts + h * src.hs + i0;
-        const bool turn = mine && !is_v && r.on;
-        const uint4 x = mine ? *reinterpret_cast<const uint4 *>(at) : make_uint4(0, 0, 0, 0);
-        const uint4 o = turn && !r.interleaved ? *reinterpret_cast<const uint4 *>(at + r.other) : make_uint4(0, 0, 0, 0);
-        uint32_t a[4] = {x.x, x.y, x.z, x.w};
-        if (turn)
-            rotate(r, a, o);
-        uint32_t params;
-        const uint32_t codes = quantise<D>(a, &params);
-        if (mine) {
-            uint8_t *const blk = page + h * block;
-            *reinterpret_cast<uint32_t *>(blk + kv4_codes<D>(v.page_log2, slot, is_v) + 4 * c) = codes;
-            if (c == 0)
-                *reinterpret_cast<uint32_t *>(blk + kv4_params<D>(v.page_log2, slot, is_v)) = params;
+    for (int n0 = 0;;) {
+#pragma unroll
+        for (int n = 0; n < kAhead; n++) {
+            const int j = j0 + (n0 + n) * G;
+            if (n0 + n >= rounds || j - lane / L >= all)
+                return;
+            const bool is_v = j >= v.heads;
+            uint32_t a[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+            if (!is_v)
+                rotate(r, a, o[n]);
+            uint32_t params;
+            const uint32_t codes = quantise<D>(a, &params);
+            if (j < all) {
+                uint8_t *const blk = page + (is_v ? j - v.heads : j) * block;
+                *reinterpret_cast<uint32_t *>(blk + kv4_codes<D>(v.page_log2, slot, is_v) + 4 * c) = codes;
+                if (c == 0)
+                    *reinterpret_cast<uint32_t *>(blk + kv4_params<D>(v.page_log2, slot, is_v)) = params;
+            }
         }
+        n0 += kAhead;
+        if (n0 >= rounds)
+            return;
+        fetch(n0);
     }
 }
 
