@@ -31,6 +31,7 @@ struct AppendParams {
     int32_t q_heads, rot, interleaved;
     int32_t q_units, kv_units;    // warps a token: of q heads, and of k and v heads
     int32_t q_rounds, kv_rounds;  // heads such a warp takes one after the other (times 32 / (D / 8))
+    float minus_zero;             // -0, which the compiler does not know (rotate())
 };
 
 constexpr int kAhead = 2;  // vectors a lane has on their way
@@ -42,14 +43,14 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// a / b correctly rounded, from r = 1 / b correctly rounded: two corrections
+// a / b correctly rounded (two quotients at once), from -b and r = 1 / b correctly rounded: two corrections
 // of a r by its remainder (Markstein, IBM J. Res. Dev. 34, 1990).  For the
 // quotients of quantise(), 0 .. 16 or so, with neither b nor r near the ends of
 // fp32's range.
-__device__ __forceinline__ float divide_by(float a, float b, float r) {
-    float q = a * r;
-    q = fmaf(fmaf(-q, b, a), r, q);
-    return fmaf(fmaf(-q, b, a), r, q);
+__device__ __forceinline__ uint64_t divide_by(uint64_t a, uint64_t minus_b, uint64_t r) {
+    uint64_t q = mul2(a, r);
+    q = fma2(fma2(q, minus_b, a), r, q);
+    return fma2(fma2(q, minus_b, a), r, q);
 }
 
 // Codes and params of eight values (pairs of BF16) of a vector of D, whose lanes
@@ -81,12 +82,15 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[4], uint32_t *p
         // Quotients from 0 to 15.06 (the scale is within 2^-8 of its value), so no
         // clamping; the integer they round to is read off the sum with 1.5 * 2^23.
         constexpr float kRound = 12582912.f;
-        const float r = __frcp_rn(s2);
+        const float rcp = __frcp_rn(s2);
+        const uint64_t r = pair2(rcp, rcp), minus_s2 = pair2(-s2, -s2), minus_lo2 = pair2(-lo2, -lo2);
+        const uint64_t a_half = pair2(0.5f, 0.5f), round = pair2(kRound, kRound);
         constexpr uint32_t kOff = 0x4B400000u * 0x11111111u;  // the sums' other bits, as they add up
 #pragma unroll
-        for (int k = 7; k >= 0; k--) {
-            const float f = k & 1 ? bf16_hi(x[k / 2]) : bf16_lo(x[k / 2]);
-            codes = codes * 16u + __float_as_uint(divide_by(fmaf(0.5f, f, -lo2), s2, r) + kRound);
+        for (int k = 3; k >= 0; k--) {
+            const uint64_t f = fma2(a_half, pair2(bf16_lo(x[k]), bf16_hi(x[k])), minus_lo2);
+            const float2 n = unpair(add2(divide_by(f, minus_s2, r), round));
+            codes = (codes * 16u + __float_as_uint(n.y)) * 16u + __float_as_uint(n.x);
         }
         codes -= kOff;
     } else {
@@ -103,25 +107,24 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[4], uint32_t *p
 // eight pairs (half split: the other side lies rot / 2 values on or back), or four
 // whole pairs (interleaved).
 struct Rotation {
-    float c[8], s[8];  // cosines and sines (half split: with the sign of the side)
+    uint64_t c[4], s[4];  // cosines and sines of two values each, the sines with the sign of the side
     bool on, interleaved;
 };
 
-// Rotated values of a lane: own ones in a, the other side's in b.  Each product
-// and the sum rounded (scalar instructions: ptxas fuses packed ones).
-__device__ __forceinline__ void rotate(const Rotation &r, uint32_t (&a)[4], const uint4 &other) {
+// Rotated values of a lane, own c + other s: own ones in a, the other side's in
+// b (half split).  Each product is rounded and then the sum: a product is a
+// fused multiply-add to a -0 that comes with the call, as the assembler joins
+// a plain product, and one with a -0 that it sees, with the sum.
+__device__ __forceinline__ void rotate(const Rotation &r, uint64_t zero, uint32_t (&a)[4], const uint4 &other) {
     if (!r.on)
         return;
     const uint32_t b[4] = {other.x, other.y, other.z, other.w};
 #pragma unroll
     for (int k = 0; k < 4; k++) {
         const float u = bf16_lo(a[k]), w = bf16_hi(a[k]);
-        if (r.interleaved)
-            a[k] = bf16_pack(__fsub_rn(__fmul_rn(u, r.c[k]), __fmul_rn(w, r.s[k])),
-                             __fadd_rn(__fmul_rn(w, r.c[k]), __fmul_rn(u, r.s[k])));
-        else
-            a[k] = bf16_pack(__fadd_rn(__fmul_rn(u, r.c[2 * k]), __fmul_rn(bf16_lo(b[k]), r.s[2 * k])),
-                             __fadd_rn(__fmul_rn(w, r.c[2 * k + 1]), __fmul_rn(bf16_hi(b[k]), r.s[2 * k + 1])));
+        const uint64_t o = r.interleaved ? pair2(w, u) : pair2(bf16_lo(b[k]), bf16_hi(b[k]));
+        const float2 y = unpair(add2(fma2(pair2(u, w), r.c[k], zero), fma2(o, r.s[k], zero)));
+        a[k] = bf16_pack(y.x, y.y);
     }
 }
 
@@ -181,8 +184,9 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
         if (p.interleaved) {
             const float4 cs = *reinterpret_cast<const float4 *>(p.cos + row + 4 * c);
             const float4 sn = *reinterpret_cast<const float4 *>(p.sin + row + 4 * c);
-            r.c[0] = cs.x, r.c[1] = cs.y, r.c[2] = cs.z, r.c[3] = cs.w;
-            r.s[0] = sn.x, r.s[1] = sn.y, r.s[2] = sn.z, r.s[3] = sn.w;
+            r.c[0] = pair2(cs.x, cs.x), r.c[1] = pair2(cs.y, cs.y), r.c[2] = pair2(cs.z, cs.z), r.c[3] = pair2(cs.w, cs.w);
+            r.s[0] = pair2(-sn.x, sn.x), r.s[1] = pair2(-sn.y, sn.y);
+            r.s[2] = pair2(-sn.z, sn.z), r.s[3] = pair2(-sn.w, sn.w);
         } else {
             const float sign = second ? 1.f : -1.f;
             const int j = second ? i0 - half : i0;
@@ -190,13 +194,13 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
             for (int k = 0; k < 2; k++) {
                 const float4 cs = *reinterpret_cast<const float4 *>(p.cos + row + j + 4 * k);
                 const float4 sn = *reinterpret_cast<const float4 *>(p.sin + row + j + 4 * k);
-                r.c[4 * k] = cs.x, r.c[4 * k + 1] = cs.y, r.c[4 * k + 2] = cs.z, r.c[4 * k + 3] = cs.w;
-                r.s[4 * k] = sign * sn.x, r.s[4 * k + 1] = sign * sn.y;
-                r.s[4 * k + 2] = sign * sn.z, r.s[4 * k + 3] = sign * sn.w;
+                r.c[2 * k] = pair2(cs.x, cs.y), r.c[2 * k + 1] = pair2(cs.z, cs.w);
+                r.s[2 * k] = pair2(sign * sn.x, sign * sn.y), r.s[2 * k + 1] = pair2(sign * sn.z, sign * sn.w);
             }
         }
     }
 
+    const uint64_t zero = pair2(p.minus_zero, p.minus_zero);
     if (of_q) {
         uint16_t *const dst = p.qo.p + t * p.qo.ts + j0 * p.qo.hs + i0;
         for (int n0 = 0;;) {
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
 #pragma unroll
             for (int n = 0; n < kAhead; n++) {
                 uint32_t a[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-                rotate(r, a, o[n]);
+                rotate(r, zero, a, o[n]);
                 if (n0 + n < rounds && j0 + (n0 + n) * G < all)
                     *reinterpret_cast<uint4 *>(dst + int64_t(n0 + n) * G * p.qo.hs) = make_uint4(a[0], a[1], a[2], a[3]);
             }
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
             const bool is_v = j >= v.heads;
             uint32_t a[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
             if (!is_v)
-                rotate(r, a, o[n]);
+                rotate(r, zero, a, o[n]);
             uint32_t params;
             const uint32_t codes = quantise<D>(a, &params);
             if (j < all) {
@@ -333,6 +337,7 @@ extern "C" uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start, 
     p.q_heads = q_heads;
     p.rot = rot_dim;
     p.interleaved = interleaved != 0;
+    p.minus_zero = -0.f;
     const int g = c->head_dim == 128 ? 2 : 4, q_all = (q_heads + g - 1) / g, kv_all = (2 * c->kv_heads + g - 1) / g;
     p.q_rounds = rounds_of(n_tokens, q_all, 16);
     p.kv_rounds = rounds_of(n_tokens, kv_all, 8);

@@ -337,48 +337,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// Two fp32 values in one 64-bit register: one instruction for both.
-__device__ __forceinline__ uint64_t pair2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// A further part of a row's softmax (maximum m2, sum l2, unnormalised output
-// o2, in log2 units) added to (m, l, o).
-__device__ __forceinline__ void join(float &m, float &l, float4 &o, float m2, float l2, float4 o2) {
-    const float top = fmaxf(m, m2);
-    const float t0 = top == -INFINITY ? 0.f : top;
-    const float f = exp2_fast(m - t0), f2 = exp2_fast(m2 - t0);
-    m = top;
-    l = fmaf(f2, l2, f * l);
-    o.x = fmaf(f2, o2.x, f * o.x);
-    o.y = fmaf(f2, o2.y, f * o.y);
-    o.z = fmaf(f2, o2.z, f * o.z);
-    o.w = fmaf(f2, o2.w, f * o.w);
-}
-
-// A part whose maximum is already known to be f (a factor) below the joint one.
+// A further part of a row (sum l2, unnormalised output o2) added to (l, o),
+// scaled down by f to the joint maximum.
 __device__ __forceinline__ void join_scaled(float &l, float4 &o, float f, float l2, float4 o2) {
     l = fmaf(f, l2, l);
     o.x = fmaf(f, o2.x, o.x);
