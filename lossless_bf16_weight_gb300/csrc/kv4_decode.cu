@@ -650,9 +650,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         if (pend[k].at == nullptr || !arrived[k])
             continue;
         __threadfence();
-        // First every part's maximum and sum, from which its weight; then the
-        // outputs, many in flight: thread x takes float4 x of every second (or
-        // fourth, ...) part, and the threads of one float4 are added in their order.
+        // Every part's maximum and sum give its weight; the outputs are on their
+        // way meanwhile: thread x takes float4 x of every second (or fourth, ...)
+        // part, and the threads of one float4 are added in their order.
         const Part &sg = pend[k];
         const uint32_t f = from[k];
         const int n = int(to_part[k] - f) + 1;
@@ -666,44 +666,63 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             wt[i] = in ? __ldcg(part_of(i / RB) + RB * D + i % RB) : -INFINITY;
             sums[i] = in ? __ldcg(part_of(i / RB) + RB * D + RB + i % RB) : 0.f;
         }
-        __syncthreads();
-        for (int row = warp; row < real; row += kWarps) {  // a warp a row, a lane a part
-            float m = -INFINITY, l = 0.f;
-            for (int i = lane; i < n; i += 32)
-                m = fmaxf(m, wt[i * RB + row]);
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float m0 = m == -INFINITY ? 0.f : m;
-            for (int i = lane; i < n; i += 32) {
-                const float w = exp2_fast(wt[i * RB + row] - m0);
-                wt[i * RB + row] = w;
-                l = fmaf(w, sums[i * RB + row], l);
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (lane == 0) {
-                row_m[row] = m;
-                row_l[row] = l;
-            }
-        }
-        __syncthreads();
         constexpr int F4 = RB * (D / 4);
-        constexpr int kSplit = F4 < kWarps * 32 ? kWarps * 32 / F4 : 1;
+        constexpr int kSplit = F4 < kWarps * 32 ? kWarps * 32 / F4 : 1, kTurns = F4 * kSplit / (kWarps * 32);
+        constexpr int kHeld = 16;
         float4 *const outs = reinterpret_cast<float4 *>(smem + (2 * n * RB * 4 + 15) / 16 * 16);
-        for (int x = threadIdx.x % F4; x < f4; x += kWarps * 32 / kSplit) {
-            const int row = x / (D / 4), s0 = threadIdx.x / F4 % kSplit;
+        const int s0 = threadIdx.x / F4 % kSplit;
+#pragma unroll
+        for (int turn = 0; turn < kTurns; turn++) {
+            const int x = threadIdx.x % F4 + turn * (kWarps * 32), row = x / (D / 4);
+            float4 held[kHeld];
+#pragma unroll
+            for (int h = 0; h < kHeld; h++) {
+                const int i = s0 + h * kSplit;
+                held[h] = x < f4 && i < n ? __ldcg(reinterpret_cast<const float4 *>(part_of(i)) + x)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (turn == 0) {
+                __syncthreads();
+                for (int row = warp; row < real; row += kWarps) {  // a warp a row, a lane a part
+                    float m = -INFINITY, l = 0.f;
+                    for (int i = lane; i < n; i += 32)
+                        m = fmaxf(m, wt[i * RB + row]);
+#pragma unroll
+                    for (int o = 16; o; o >>= 1)
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const float m0 = m == -INFINITY ? 0.f : m;
+                    for (int i = lane; i < n; i += 32) {
+                        const float w = exp2_fast(wt[i * RB + row] - m0);
+                        wt[i * RB + row] = w;
+                        l = fmaf(w, sums[i * RB + row], l);
+                    }
+#pragma unroll
+                    for (int o = 16; o; o >>= 1)
+                        l += __shfl_xor_sync(0xffffffffu, l, o);
+                    if (lane == 0) {
+                        row_m[row] = m;
+                        row_l[row] = l;
+                    }
+                }
+                __syncthreads();
+            }
+            if (x >= f4)
+                continue;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int i = s0; i < n; i += kSplit) {
+            auto add = [&](int i, const float4 &o) {
                 const float w = wt[i * RB + row];
-                const float4 o = __ldcg(reinterpret_cast<const float4 *>(part_of(i)) + x);
                 acc.x = fmaf(w, o.x, acc.x);
                 acc.y = fmaf(w, o.y, acc.y);
                 acc.z = fmaf(w, o.z, acc.z);
                 acc.w = fmaf(w, o.w, acc.w);
-            }
+            };
+#pragma unroll
+            for (int h = 0; h < kHeld; h++)
+                if (s0 + h * kSplit < n)
+                    add(s0 + h * kSplit, held[h]);
+#pragma unroll 8
+            for (int i = s0 + kHeld * kSplit; i < n; i += kSplit)
+                add(i, __ldcg(reinterpret_cast<const float4 *>(part_of(i)) + x));
             outs[s0 * F4 + x] = acc;
         }
         __syncthreads();
