@@ -51,8 +51,8 @@ namespace {
 
 // Sequences with up to so many rows (new tokens x query heads of a kv head)
 // take the kernel for few rows.  Measured with 8 kv heads of 128, that kernel and
-// the other: 16 sequences of 4096 keys, 16 rows 44 and 86 us, 32 rows 69 and 86,
-// 64 rows 119 and 87; one sequence of 8192 keys, 64 rows 34 and 48: with few steps
+// the other: 16 sequences of 4096 keys, 16 rows 41 and 82 us, 32 rows 65 and 81,
+// 64 rows 110 and 83; one sequence of 8192 keys, 64 rows 29 and 48: with few steps
 // (256 rows x 128 keys) in all, what the other kernel takes to start decides.
 constexpr int kFewRows = 32, kFewRowsShort = 64;
 constexpr int64_t kShortSteps = 1024;

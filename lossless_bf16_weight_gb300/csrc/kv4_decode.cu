@@ -1,8 +1,11 @@
 // Attention over the 4-bit paged cache for sequences with few rows (new
 // tokens x query heads of a kv head): single tokens, drafted tokens.
 //
-// Bound by memory: every cached vector is read once for all rows that share
-// it, D / 2 + 4 bytes.  A CTA of eight warps takes an equal share of all key
+// Every cached vector is read once for all rows that share it, D / 2 + 4 bytes,
+// so memory is the floor; what bounds the kernel is what a warp does with 32 keys
+// of 128 (4352 bytes): 555 instructions, 160 of them the logic that takes the
+// codes apart and 64 the subtractions of their middle, at 0.62 instructions a
+// cycle.  A CTA of eight warps takes an equal share of all key
 // tiles (kv4_attn.cuh), and each of its warps an equal share of that, which it
 // works through by itself: a ring of tiles in flight (cp.async) runs on from
 // item to item, an item that lies in one warp's share is written out by that
@@ -18,10 +21,13 @@
 //                 for two), and the scale and offset of a key are applied to
 //                 the fp32 product: q.k = s sum q c + lo sum q.  Exact but for
 //                 fp32 sums: no rounded K.
-//   O^T = V^T P^T a code becomes c - 8 (one subtraction more: the sum over many
-//                 keys would lose digits to the offset), the scale goes into the
-//                 probability, p s, and the middle of the range into a sum of its own:
-//                 o = sum (p s)(c - 8) + sum p (lo + 8 s).  p s is taken
+//   O^T = V^T P^T the codes of two keys come side by side out of a transposing
+//                 matrix load.  A code becomes c - 8 (one subtraction more: without
+//                 it the sum over many keys would lose digits to the offset, and
+//                 subtracting 8 sum p s from the products in fp32 left 2^-24 of a
+//                 large p where a value is exactly zero), the scale goes into the
+//                 probability, p s, and the middle of the range into a sum of its
+//                 own: o = sum (p s)(c - 8) + sum p (lo + 8 s).  p s is taken
 //                 as the sum of two BF16, a rounding and its rest, so that the
 //                 result is exact to about 2^-16 before its own rounding.  Up
 //                 to four rows leave half of the products' columns empty: the
@@ -30,7 +36,16 @@
 // The running maximum of the softmax is only raised when a score passes it by
 // 2^24 (BF16 and fp32 hold that without loss), so that a tile costs a vote
 // in place of shuffles.
+//
+// Measured, 32 query and 8 kv heads of 128:
+//   one token, 131072 keys        @LONG
+//   64 tokens, 100 to 8192 keys   38 us (2.9 TB/s)
+//   one token, 290 keys           8.6 us
+// A call's first 6 us go to finding the shares and the first loads, its last
+// 6 to the joins, whose steps wait for one another's loads.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kernels.h"
 #include "kv4_attn.cuh"
@@ -45,8 +60,17 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTile = 32;            // keys of a unit
 constexpr float kRaise = 24.f;       // log2 headroom of a probability
-constexpr int kItemCost = 1;         // what an item costs a warp beyond its tiles, in tiles
-constexpr uint32_t kWholeTiles = 32; // items up to this many tiles are not cut between CTAs while shares are short
+// What an item costs a warp beyond its tiles (queries, output), in tiles: 64
+// tokens of 100 to 8192 keys 45.8 us with none, 40.5 with 1, 38.4 with 2, 37.8 with 3, 38.0 with 4.
+constexpr int kItemCost = 3;
+// Items up to this many tiles are not cut between CTAs while shares are short:
+// one token of 290 keys 11.2 us if they are, 8.6 if not.
+constexpr uint32_t kWholeTiles = 32;
+// Sequences of more than eight rows are taken sixteen at a time (each key
+// unpacked once for all, but one CTA an SM) only if there are more units (32 keys
+// x 8 rows) than this: 16 x 4 new tokens, 4096 keys 41 us against 46 by eights,
+// 1 x 4 new tokens, 8192 keys 18.9 us against 17.7, 7 x 5 drafted tokens 18.1 against 15.1.
+constexpr int64_t kNarrow = 32768;
 
 template <int D>
 constexpr int kStageBytes = kTile * (D + 8);
@@ -108,7 +132,8 @@ struct Part {
     int32_t rt, t0, tokens, head, tiles, of;
 };
 
-// NT groups of eight rows; kDup (NT = 1): up to four rows, which rows 4..7 repeat.
+// NT groups of eight rows; kDup (NT = 1): up to four rows, which rows 4..7 repeat
+// (one token, 131072 keys 40.6 us, with a second product for the rests 44.2).
 template <int D, int NT, bool kDup>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kernel(const AttnParams p) {
     static_assert(!kDup || NT == 1, "rows repeated in one group");
@@ -204,7 +229,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     constexpr int RC = D / 32;  // 16-byte chunks of a row
     const uint32_t first_row = (lane & 16) + (lane & 15) / RC;
     const uint32_t to0 = ((first_row * RC + lane % RC) ^ turn<D>(first_row >> 2)) * 16;
-    const uint32_t par_off = kv4_params<D>(v.page_log2, 0, (lane >> 2) & 1) - (lane & 12) * 16;  // from the lane's codes
+    // scales and offsets: from the lane's first codes
+    const uint32_t par_off = kv4_params<D>(v.page_log2, 0, (lane >> 2) & 1) - (lane & 12) * 16;
     const uint32_t par_to = kTile * D + ((lane & 4) ? kTile * 4 : 0) + ((lane & 16) ? 64 : 0) + (lane & 3) * 16;
     auto issue = [&](int stage) {
         if (nx_tiles > 0) {
@@ -242,325 +268,326 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         next_seg();
         int fill = stage, calls = ST;
         for (int sgi = 0; sgi < n_segs; sgi++) {
-        const Seg &sg = segs[sgi];
-        const int n_mine = sg.tiles;
-        const int r0 = sg.rt * RB, rows = sg.tokens * p.group;
-        const int all_lo = sg.all_lo, all_hi = sg.all_hi;
-        const Seq sq{sg.t0, sg.tokens, sg.len};
+            const Seg &sg = segs[sgi];
+            const int n_mine = sg.tiles;
+            const int r0 = sg.rt * RB, rows = sg.tokens * p.group;
+            const int all_lo = sg.all_lo, all_hi = sg.all_hi;
+            const Seq sq{sg.t0, sg.tokens, sg.len};
 
-        Warp<D, NT> w;
-        // Queries: lane (g, t) holds row g of each group, dimensions D/4 t .. + D/4 - 1,
-        // paired as the codes of a word come out of it: (0,4) (1,5) (2,6) (3,7).
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-            const int rr = nt * 8 + (kDup ? g & 3 : g);
-            uint4 x[D / 32];
-#pragma unroll
-            for (int k = 0; k < D / 32; k++)
-                x[k] = make_uint4(0, 0, 0, 0);
-            if (rr < rows - r0 && n_mine > 0) {
-                const int i = p.by_group.of(r0 + rr);
-                const int64_t tok = sg.t0 + i, head = sg.head * p.group + (r0 + rr - i * p.group);
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q.p + tok * p.q.ts + head * p.q.hs + (D / 4) * t);
-#pragma unroll
-                for (int k = 0; k < D / 32; k++)
-                    x[k] = src[k];
-            }
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 32; k++) {
-                w.q[nt][2 * k][0] = mul2_bf16(__byte_perm(x[k].x, x[k].z, 0x5410), kQUpLow);
-                w.q[nt][2 * k][1] = mul2_bf16(__byte_perm(x[k].x, x[k].z, 0x7632), kQUpHigh);
-                w.q[nt][2 * k + 1][0] = mul2_bf16(__byte_perm(x[k].y, x[k].w, 0x5410), kQUpLow);
-                w.q[nt][2 * k + 1][1] = mul2_bf16(__byte_perm(x[k].y, x[k].w, 0x7632), kQUpHigh);
-                const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    sum += bf16_lo(a[i]) + bf16_hi(a[i]);
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            w.qs[nt] = pair2(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
-            w.m[nt][0] = w.m[nt][1] = -INFINITY;
-            w.l[nt] = w.z[nt] = 0;
-#pragma unroll
-            for (int i = 0; i < D / 16; i++)
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    w.o[i][nt][k] = 0.f;
-        }
-
-        for (int i = 0; i < n_mine; i++) {
-            for (; calls > 0; calls--) {  // the ring's fill at first, then a tile for a tile
-                issue(fill);
-                fill = fill + 1 == ST ? 0 : fill + 1;
-            }
-            calls = 1;
-            asm volatile("cp.async.wait_group %0;" :: "n"(ST - 1) : "memory");
-            __syncwarp();
-            const unsigned char *const st = ring + stage * kStageBytes<D>;
-            const uint32_t st_at = ring_at + stage * kStageBytes<D>;
-            stage = stage + 1 == ST ? 0 : stage + 1;
-            const int key0 = (sg.first + i) * kTile;
-
-            // scores
-            float sc[2][NT][4];
-#pragma unroll
-            for (int mt = 0; mt < 2; mt++)
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        sc[mt][nt][k] = 0.f;
-            uint32_t a[4][D / 32];  // [key 4 g + j][words]
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                // row 4 g + j, bytes D / 8 t ..
-                const uint32_t s0 = D == 128 ? g * 16 + (t ^ turn<D>(g)) : g * 8 + ((t >> 1) ^ turn<D>(g));
-                const unsigned char *at =
-                    st + ((s0 * 16) ^ (D == 128 ? (j & 1) * 64 : j * 32)) + (D == 128 ? (j >> 1) * 128 : (t & 1) * 8);
-                if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(at);
-                    a[j][0] = x.x, a[j][1] = x.y, a[j][2] = x.z, a[j][3] = x.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(at);
-                    a[j][0] = x.x, a[j][1] = x.y;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < D / 32; k++)
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-#pragma unroll
-                    for (int mt = 0; mt < 2; mt++) {
-                        const uint32_t x = j ? a[2 * mt][k] >> 8 : a[2 * mt][k];
-                        const uint32_t y = j ? a[2 * mt + 1][k] >> 8 : a[2 * mt + 1][k];
-                        const uint32_t a0 = codes.low(x), a1 = codes.low(y), a2 = codes.high(x), a3 = codes.high(y);
-#pragma unroll
-                        for (int nt = 0; nt < NT; nt++)
-                            mma16816(sc[mt][nt], a0, a1, a2, a3, w.q[nt][2 * k + j][0], w.q[nt][2 * k + j][1]);
-                    }
-            // sc[mt][nt][2 h + k]: key 4 g + 2 mt + h, row 8 nt + 2 t + k.
-            // In log2 units and less the maximum: y - m = acc * a + (c * qs - m).
-            const uint4 kp = *reinterpret_cast<const uint4 *>(st + kTile * D + g * 16);
-            const uint4 vp = *reinterpret_cast<const uint4 *>(st + kTile * (D + 4) + g * 16);
-            const uint32_t kpar[4] = {kp.x, kp.y, kp.z, kp.w}, vpar[4] = {vp.x, vp.y, vp.z, vp.w};
-            const bool open = key0 < all_lo || key0 + kTile > all_hi;
-            uint64_t y[4][NT];
-            auto scores = [&]() {
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const float a = bf16_lo(kpar[j]) * c1_up, c = bf16_hi(kpar[j]) * p.c1;
-                    const uint64_t aa = pair2(a, a), cc = pair2(c, c);
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
-                        y[j][nt] = fma2(pair2(sc[j >> 1][nt][2 * (j & 1)], sc[j >> 1][nt][2 * (j & 1) + 1]), aa,
-                                        fma2(cc, w.qs[nt], pair2(-w.m[nt][0], -w.m[nt][1])));
-                }
-                if (open) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++) {
-                        bool in[4][2];
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const int row = 8 * nt + (kDup ? (2 * t + k) & 3 : 2 * t + k);
-                            const int tok = p.by_group.of(r0 + min(row, rows - r0 - 1));
-                            const KeyRange kr = visible(p, sq, tok, tok);
-#pragma unroll
-                            for (int j = 0; j < 4; j++) {
-                                const int key = key0 + 4 * g + j;
-                                in[j][k] = key >= kr.lo && key < min(kr.hi, sq.len);
-                            }
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const float2 f = unpair(y[j][nt]);
-                            y[j][nt] = pair2(in[j][0] ? f.x : -INFINITY, in[j][1] ? f.y : -INFINITY);
-                        }
-                    }
-                }
-            };
-            scores();
-            // raise the maximum where a score passes it by far
-            float top[NT][2];
-            bool raise = false;
+            Warp<D, NT> w;
+            // Queries: lane (g, t) holds row g of each group, dimensions D/4 t .. + D/4 - 1,
+            // paired as the codes of a word come out of it: (0,4) (1,5) (2,6) (3,7).
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-                const float2 f0 = unpair(y[0][nt]), f1 = unpair(y[1][nt]), f2 = unpair(y[2][nt]), f3 = unpair(y[3][nt]);
-                top[nt][0] = fmaxf(fmaxf(f0.x, f1.x), fmaxf(f2.x, f3.x));
-                top[nt][1] = fmaxf(fmaxf(f0.y, f1.y), fmaxf(f2.y, f3.y));
-                raise = raise || fmaxf(top[nt][0], top[nt][1]) > kRaise;
-            }
-            if (__any_sync(0xffffffffu, raise)) {
-                // With no maximum yet the scores are taken again, less nothing.
-                bool none = false;
+                const int rr = nt * 8 + (kDup ? g & 3 : g);
+                uint4 x[D / 32];
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++)
+                for (int k = 0; k < D / 32; k++)
+                    x[k] = make_uint4(0, 0, 0, 0);
+                if (rr < rows - r0 && n_mine > 0) {
+                    const int i = p.by_group.of(r0 + rr);
+                    const int64_t tok = sg.t0 + i, head = sg.head * p.group + (r0 + rr - i * p.group);
+                    const uint16_t *at = p.q.p + tok * p.q.ts + head * p.q.hs + (D / 4) * t;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(at);
 #pragma unroll
-                    for (int k = 0; k < 2; k++)
-                        none = none || w.m[nt][k] == -INFINITY;
-                const bool fresh = __any_sync(0xffffffffu, none);
-                float old[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        old[nt][k] = w.m[nt][k];
-                        if (fresh)
-                            w.m[nt][k] = 0.f;
-                    }
-                if (fresh) {
-                    scores();
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++) {
-                        const float2 f0 = unpair(y[0][nt]), f1 = unpair(y[1][nt]), f2 = unpair(y[2][nt]),
-                                     f3 = unpair(y[3][nt]);
-                        top[nt][0] = fmaxf(fmaxf(f0.x, f1.x), fmaxf(f2.x, f3.x));
-                        top[nt][1] = fmaxf(fmaxf(f0.y, f1.y), fmaxf(f2.y, f3.y));
-                    }
+                    for (int k = 0; k < D / 32; k++)
+                        x[k] = src[k];
                 }
+                float sum = 0.f;
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    float f[2];
+                for (int k = 0; k < D / 32; k++) {
+                    w.q[nt][2 * k][0] = mul2_bf16(__byte_perm(x[k].x, x[k].z, 0x5410), kQUpLow);
+                    w.q[nt][2 * k][1] = mul2_bf16(__byte_perm(x[k].x, x[k].z, 0x7632), kQUpHigh);
+                    w.q[nt][2 * k + 1][0] = mul2_bf16(__byte_perm(x[k].y, x[k].w, 0x5410), kQUpLow);
+                    w.q[nt][2 * k + 1][1] = mul2_bf16(__byte_perm(x[k].y, x[k].w, 0x7632), kQUpHigh);
+                    const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        float x = top[nt][k];
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1)
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                        const float m2 = fmaxf(old[nt][k], x + w.m[nt][k]);
-                        f[k] = m2 == -INFINITY ? 1.f : exp2_fast(old[nt][k] - m2);
-                        w.m[nt][k] = m2;
-#pragma unroll
-                        for (int d = 0; d < D / 16; d++) {
-                            w.o[d][nt][k] *= f[k];
-                            w.o[d][nt][2 + k] *= f[k];
-                        }
-                    }
-                    w.l[nt] = mul2(w.l[nt], pair2(f[0], f[1]));
-                    w.z[nt] = mul2(w.z[nt], pair2(f[0], f[1]));
+                    for (int i = 0; i < 4; i++)
+                        sum += bf16_lo(a[i]) + bf16_hi(a[i]);
                 }
-                scores();
-            }
-            // probabilities, as the B operand of the product with V: p s in two BF16
-            uint32_t hi[2][NT][2], lo[2][NT][2];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                w.qs[nt] = pair2(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
+                w.m[nt][0] = w.m[nt][1] = -INFINITY;
+                w.l[nt] = w.z[nt] = 0;
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++)
+                for (int i = 0; i < D / 16; i++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        w.o[i][nt][k] = 0.f;
+            }
+
+            for (int i = 0; i < n_mine; i++) {
+                for (; calls > 0; calls--) {  // the ring's fill at first, then a tile for a tile
+                    issue(fill);
+                    fill = fill + 1 == ST ? 0 : fill + 1;
+                }
+                calls = 1;
+                asm volatile("cp.async.wait_group %0;" :: "n"(ST - 1) : "memory");
+                __syncwarp();
+                const unsigned char *const st = ring + stage * kStageBytes<D>;
+                const uint32_t st_at = ring_at + stage * kStageBytes<D>;
+                stage = stage + 1 == ST ? 0 : stage + 1;
+                const int key0 = (sg.first + i) * kTile;
+
+                // scores
+                float sc[2][NT][4];
+#pragma unroll
+                for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            sc[mt][nt][k] = 0.f;
+                uint32_t a[4][D / 32];  // [key 4 g + j][words]
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const float s = bf16_lo(vpar[j]) * kPUp, mid = fmaf(8.f / kPUp, s, bf16_hi(vpar[j]));
-                    const float2 f = unpair(y[j][nt]);
-                    const uint64_t pr = pair2(exp2_fast(f.x), exp2_fast(f.y));
-                    uint64_t ps = mul2(pr, pair2(s, s));
-                    w.l[nt] = add2(w.l[nt], pr);
-                    if (open) {  // a masked key's scale may be anything
-                        const float2 a = unpair(ps), b = unpair(mul2(pr, pair2(mid, mid)));
-                        const bool in0 = f.x != -INFINITY, in1 = f.y != -INFINITY;
-                        ps = pair2(in0 ? a.x : 0.f, in1 ? a.y : 0.f);
-                        w.z[nt] = add2(w.z[nt], pair2(in0 ? b.x : 0.f, in1 ? b.y : 0.f));
+                    // row 4 g + j, bytes D / 8 t ..
+                    const uint32_t s0 = D == 128 ? g * 16 + (t ^ turn<D>(g)) : g * 8 + ((t >> 1) ^ turn<D>(g));
+                    const unsigned char *at = st + ((s0 * 16) ^ (D == 128 ? (j & 1) * 64 : j * 32)) +
+                                              (D == 128 ? (j >> 1) * 128 : (t & 1) * 8);
+                    if constexpr (D == 128) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+                        a[j][0] = x.x, a[j][1] = x.y, a[j][2] = x.z, a[j][3] = x.w;
                     } else {
-                        w.z[nt] = fma2(pr, pair2(mid, mid), w.z[nt]);
-                    }
-                    const float2 a = unpair(ps);
-                    const uint32_t h = bf16_pack(a.x, a.y);
-                    const float2 rest = unpair(add2(ps, pair2(-bf16_lo(h), -bf16_hi(h))));
-                    const uint32_t r = bf16_pack(rest.x, rest.y);
-                    if constexpr (kDup) {
-                        hi[j >> 1][nt][j & 1] = transpose8x8(t < 2 ? h : r);
-                    } else {
-                        hi[j >> 1][nt][j & 1] = transpose8x8(h);
-                        lo[j >> 1][nt][j & 1] = transpose8x8(r);
+                        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                        a[j][0] = x.x, a[j][1] = x.y;
                     }
                 }
-            // output
 #pragma unroll
-            for (int mt = 0; mt < 2; mt++)
+                for (int k = 0; k < D / 32; k++)
 #pragma unroll
-                for (int c = 0; c < D / 64; c++) {
-                    // x[2 e + h]: rows 8 h + 2t, + 1, the four codes 4 g .. of chunk 2 c + e
-                    uint32_t x[4];
-                    const uint32_t i = lane & 7, h = (lane >> 3) & 1, e0 = lane >> 4;
-                    const uint32_t s0 = D == 128 ? i * 16 + ((h * 4 + e0) ^ turn<D>(i)) : i * 8 + ((h * 2 + e0) ^ turn<D>(i));
-                    ldmatrix_t(x, st_at + kTile * (D / 2) + ((s0 * 16) ^ (D == 128 ? c * 32 : mt * 64)) +
-                                      (D == 128 ? mt * 128 : 0));
+                    for (int j = 0; j < 2; j++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++)
+                        for (int mt = 0; mt < 2; mt++) {
+                            const uint32_t x = j ? a[2 * mt][k] >> 8 : a[2 * mt][k];
+                            const uint32_t y = j ? a[2 * mt + 1][k] >> 8 : a[2 * mt + 1][k];
+                            const uint32_t a0 = codes.low(x), a1 = codes.low(y), a2 = codes.high(x), a3 = codes.high(y);
 #pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            const uint32_t y = j ? x[2 * e] >> 8 : x[2 * e], z = j ? x[2 * e + 1] >> 8 : x[2 * e + 1];
-                            const uint32_t a0 = codes.low_mid(y), a1 = codes.high_mid(y);
-                            const uint32_t a2 = codes.low_mid(z), a3 = codes.high_mid(z);
+                            for (int nt = 0; nt < NT; nt++)
+                                mma16816(sc[mt][nt], a0, a1, a2, a3, w.q[nt][2 * k + j][0], w.q[nt][2 * k + j][1]);
+                        }
+                // sc[mt][nt][2 h + k]: key 4 g + 2 mt + h, row 8 nt + 2 t + k.
+                // In log2 units and less the maximum: y - m = acc * a + (c * qs - m).
+                const uint4 kp = *reinterpret_cast<const uint4 *>(st + kTile * D + g * 16);
+                const uint4 vp = *reinterpret_cast<const uint4 *>(st + kTile * (D + 4) + g * 16);
+                const uint32_t kpar[4] = {kp.x, kp.y, kp.z, kp.w}, vpar[4] = {vp.x, vp.y, vp.z, vp.w};
+                const bool open = key0 < all_lo || key0 + kTile > all_hi;
+                uint64_t y[4][NT];
+                auto scores = [&]() {
 #pragma unroll
-                            for (int nt = 0; nt < NT; nt++) {
-                                float(&o)[4] = w.o[4 * c + 2 * e + j][nt];
-                                mma16816(o, a0, a1, a2, a3, hi[mt][nt][0], hi[mt][nt][1]);
-                                if constexpr (!kDup)
-                                    mma16816(o, a0, a1, a2, a3, lo[mt][nt][0], lo[mt][nt][1]);
+                    for (int j = 0; j < 4; j++) {
+                        const float a = bf16_lo(kpar[j]) * c1_up, c = bf16_hi(kpar[j]) * p.c1;
+                        const uint64_t aa = pair2(a, a), cc = pair2(c, c);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+                            y[j][nt] = fma2(pair2(sc[j >> 1][nt][2 * (j & 1)], sc[j >> 1][nt][2 * (j & 1) + 1]), aa,
+                                            fma2(cc, w.qs[nt], pair2(-w.m[nt][0], -w.m[nt][1])));
+                    }
+                    if (open) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++) {
+                            bool in[4][2];
+#pragma unroll
+                            for (int k = 0; k < 2; k++) {
+                                const int row = 8 * nt + (kDup ? (2 * t + k) & 3 : 2 * t + k);
+                                const int tok = p.by_group.of(r0 + min(row, rows - r0 - 1));
+                                const KeyRange kr = visible(p, sq, tok, tok);
+#pragma unroll
+                                for (int j = 0; j < 4; j++) {
+                                    const int key = key0 + 4 * g + j;
+                                    in[j][k] = key >= kr.lo && key < min(kr.hi, sq.len);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                const float2 f = unpair(y[j][nt]);
+                                y[j][nt] = pair2(in[j][0] ? f.x : -INFINITY, in[j][1] ? f.y : -INFINITY);
                             }
                         }
+                    }
+                };
+                scores();
+                // raise the maximum where a score passes it by far
+                float top[NT][2];
+                auto highest = [&](int nt) {
+                    const float2 a = unpair(y[0][nt]), b = unpair(y[1][nt]), c = unpair(y[2][nt]), d = unpair(y[3][nt]);
+                    top[nt][0] = fmaxf(fmaxf(a.x, b.x), fmaxf(c.x, d.x));
+                    top[nt][1] = fmaxf(fmaxf(a.y, b.y), fmaxf(c.y, d.y));
+                };
+                bool raise = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    highest(nt);
+                    raise = raise || fmaxf(top[nt][0], top[nt][1]) > kRaise;
                 }
-            __syncwarp();
-        }
-        // A whole item is written out; a part of one goes to the workspace, or
-        // (the warp's last) to its ring.
-        const bool whole = sg.tiles == sg.of;
-        const bool last = u == u_end && sgi == n_segs - 1;
-        float *part = nullptr;
-        if (!whole) {
-            if (last) {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                if (__any_sync(0xffffffffu, raise)) {
+                    // With no maximum yet the scores are taken again, less nothing.
+                    bool none = false;
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int k = 0; k < 2; k++)
+                            none = none || w.m[nt][k] == -INFINITY;
+                    const bool fresh = __any_sync(0xffffffffu, none);
+                    float old[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            old[nt][k] = w.m[nt][k];
+                            if (fresh)
+                                w.m[nt][k] = 0.f;
+                        }
+                    if (fresh) {
+                        scores();
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+                            highest(nt);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        float f[2];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            float x = top[nt][k];
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1)
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                            const float m2 = fmaxf(old[nt][k], x + w.m[nt][k]);
+                            f[k] = m2 == -INFINITY ? 1.f : exp2_fast(old[nt][k] - m2);
+                            w.m[nt][k] = m2;
+#pragma unroll
+                            for (int d = 0; d < D / 16; d++) {
+                                w.o[d][nt][k] *= f[k];
+                                w.o[d][nt][2 + k] *= f[k];
+                            }
+                        }
+                        w.l[nt] = mul2(w.l[nt], pair2(f[0], f[1]));
+                        w.z[nt] = mul2(w.z[nt], pair2(f[0], f[1]));
+                    }
+                    scores();
+                }
+                // probabilities, as the B operand of the product with V: p s in two BF16
+                uint32_t hi[2][NT][2], lo[2][NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const float s = bf16_lo(vpar[j]) * kPUp, mid = fmaf(8.f / kPUp, s, bf16_hi(vpar[j]));
+                        const float2 f = unpair(y[j][nt]);
+                        const uint64_t pr = pair2(exp2_fast(f.x), exp2_fast(f.y));
+                        uint64_t ps = mul2(pr, pair2(s, s));
+                        w.l[nt] = add2(w.l[nt], pr);
+                        if (open) {  // a masked key's scale may be anything
+                            const float2 a = unpair(ps), b = unpair(mul2(pr, pair2(mid, mid)));
+                            const bool in0 = f.x != -INFINITY, in1 = f.y != -INFINITY;
+                            ps = pair2(in0 ? a.x : 0.f, in1 ? a.y : 0.f);
+                            w.z[nt] = add2(w.z[nt], pair2(in0 ? b.x : 0.f, in1 ? b.y : 0.f));
+                        } else {
+                            w.z[nt] = fma2(pr, pair2(mid, mid), w.z[nt]);
+                        }
+                        const float2 a = unpair(ps);
+                        const uint32_t h = bf16_pack(a.x, a.y);
+                        const float2 rest = unpair(add2(ps, pair2(-bf16_lo(h), -bf16_hi(h))));
+                        const uint32_t r = bf16_pack(rest.x, rest.y);
+                        if constexpr (kDup) {
+                            hi[j >> 1][nt][j & 1] = transpose8x8(t < 2 ? h : r);
+                        } else {
+                            hi[j >> 1][nt][j & 1] = transpose8x8(h);
+                            lo[j >> 1][nt][j & 1] = transpose8x8(r);
+                        }
+                    }
+                // output
+#pragma unroll
+                for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+                    for (int c = 0; c < D / 64; c++) {
+                        // x[2 e + h]: rows 8 h + 2t, + 1, the four codes 4 g .. of chunk 2 c + e
+                        uint32_t x[4];
+                        const uint32_t i = lane & 7, h = (lane >> 3) & 1, e0 = lane >> 4;
+                        const uint32_t s0 = i * (D / 8) + ((h * (D / 32) + e0) ^ turn<D>(i));
+                        ldmatrix_t(x, st_at + kTile * (D / 2) + ((s0 * 16) ^ (D == 128 ? c * 32 : mt * 64)) +
+                                          (D == 128 ? mt * 128 : 0));
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+#pragma unroll
+                            for (int j = 0; j < 2; j++) {
+                                const uint32_t y = x[2 * e] >> 8 * j, z = x[2 * e + 1] >> 8 * j;
+                                const uint32_t a0 = codes.low_mid(y), a1 = codes.high_mid(y);
+                                const uint32_t a2 = codes.low_mid(z), a3 = codes.high_mid(z);
+#pragma unroll
+                                for (int nt = 0; nt < NT; nt++) {
+                                    float(&o)[4] = w.o[4 * c + 2 * e + j][nt];
+                                    mma16816(o, a0, a1, a2, a3, hi[mt][nt][0], hi[mt][nt][1]);
+                                    if constexpr (!kDup)
+                                        mma16816(o, a0, a1, a2, a3, lo[mt][nt][0], lo[mt][nt][1]);
+                                }
+                            }
+                    }
                 __syncwarp();
             }
-            part = last ? reinterpret_cast<float *>(ring)
-                        : p.parts + (2 * uint64_t(gridDim.x) + blockIdx.x * kWarps + warp) * PF;
-            if (lane == 0)
-                parts[2 * warp + last] = Part{part, sg.u0, sg.rt, sg.t0, sg.tokens, sg.head, sg.tiles, sg.of};
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-            const float2 l2 = unpair(w.l[nt]), z2 = unpair(w.z[nt]);
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                float l = k ? l2.y : l2.x, z = k ? z2.y : z2.x;
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    l += __shfl_xor_sync(0xffffffffu, l, o);
-                    z += __shfl_xor_sync(0xffffffffu, z, o);
+            // A whole item is written out; a part of one goes to the workspace, or
+            // (the warp's last) to its ring.
+            const bool whole = sg.tiles == sg.of;
+            const bool last = u == u_end && sgi == n_segs - 1;
+            float *part = nullptr;
+            if (!whole) {
+                if (last) {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncwarp();
                 }
-                float o[D / 8];  // o[4 c + i]: dimension 32 c + 4 g + i of row 8 nt + 2 t + k
+                part = last ? reinterpret_cast<float *>(ring)
+                            : p.parts + (2 * uint64_t(gridDim.x) + blockIdx.x * kWarps + warp) * PF;
+                if (lane == 0)
+                    parts[2 * warp + last] = Part{part, sg.u0, sg.rt, sg.t0, sg.tokens, sg.head, sg.tiles, sg.of};
+            }
 #pragma unroll
-                for (int i = 0; i < D / 16; i++) {
-                    o[2 * i] = w.o[i][nt][k] * kPDownLow;
-                    o[2 * i + 1] = w.o[i][nt][2 + k] * kPDownHigh;
-                }
-                if constexpr (kDup) {  // the rests' products are in the columns four on
+            for (int nt = 0; nt < NT; nt++) {
+                const float2 l2 = unpair(w.l[nt]), z2 = unpair(w.z[nt]);
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    float l = k ? l2.y : l2.x, z = k ? z2.y : z2.x;
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        l += __shfl_xor_sync(0xffffffffu, l, o);
+                        z += __shfl_xor_sync(0xffffffffu, z, o);
+                    }
+                    float o[D / 8];  // o[4 c + i]: dimension 32 c + 4 g + i of row 8 nt + 2 t + k
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++) {
+                        o[2 * i] = w.o[i][nt][k] * kPDownLow;
+                        o[2 * i + 1] = w.o[i][nt][2 + k] * kPDownHigh;
+                    }
+                    if constexpr (kDup) {  // the rests' products are in the columns four on
+#pragma unroll
+                        for (int i = 0; i < D / 8; i++)
+                            o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
+                    }
 #pragma unroll
                     for (int i = 0; i < D / 8; i++)
-                        o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
-                }
+                        o[i] += z;
+                    const int row = 8 * nt + 2 * t + k;
+                    if ((!kDup || t < 2) && r0 + row < rows) {
+                        if (whole) {
 #pragma unroll
-                for (int i = 0; i < D / 8; i++)
-                    o[i] += z;
-                const int row = 8 * nt + 2 * t + k;
-                if ((!kDup || t < 2) && r0 + row < rows) {
-                    if (whole) {
+                            for (int i = 0; i < D / 32; i++)
+                                store_row<D>(p, sg.t0, sg.head, r0 + row, 8 * i + g,
+                                             make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]),
+                                             w.m[nt][k], l);
+                        } else {
+                            float4 *const dst = reinterpret_cast<float4 *>(part) + row * (D / 4) + g;
 #pragma unroll
-                        for (int i = 0; i < D / 32; i++)
-                            store_row<D>(p, sg.t0, sg.head, r0 + row, 8 * i + g,
-                                         make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]), w.m[nt][k], l);
-                    } else {
-                        float4 *const dst = reinterpret_cast<float4 *>(part) + row * (D / 4) + g;
-#pragma unroll
-                        for (int i = 0; i < D / 32; i++)
-                            dst[8 * i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                        if (g == 0) {
-                            part[RB * D + row] = w.m[nt][k];
-                            part[RB * D + RB + row] = l;
+                            for (int i = 0; i < D / 32; i++)
+                                dst[8 * i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            if (g == 0) {
+                                part[RB * D + row] = w.m[nt][k];
+                                part[RB * D + RB + row] = l;
+                            }
                         }
                     }
                 }
             }
-        }
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -608,7 +635,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             for (int k = 0; k < 2 * kWarps; k++)
                 if (in >> k & 1) {
                     const float *q = parts[k].at;
-                    join_scaled(l, acc, exp2_fast(w[k] - m0), q[RB * D + RB + row], reinterpret_cast<const float4 *>(q)[x]);
+                    join_scaled(l, acc, exp2_fast(w[k] - m0), q[RB * D + RB + row],
+                                reinterpret_cast<const float4 *>(q)[x]);
                 }
             const int c = x % (D / 4);
             if (tiles == head.of) {
@@ -762,14 +790,18 @@ int kv4_decode_ctas() { return 2 * sm_count(); }
 size_t kv4_decode_part_floats(int head_dim) { return (2 + kWarps) * size_t(kv4_decode_ctas()) * 16 * (head_dim + 2); }
 
 uw_status launch_kv4_decode(const AttnParams &p, int head_dim, int64_t rows, int64_t max_units, cudaStream_t st) {
-    const bool dup = rows > 0 && rows <= 4, wide = rows == 0 || rows > 8;
+    const bool dup = rows > 0 && rows <= 4, wide = rows == 0 || (rows > 8 && (max_units == 0 || max_units > kNarrow));
     int64_t ctas = wide ? kv4_decode_ctas() / 2 : kv4_decode_ctas();
     if (max_units > 0)
         ctas = std::min(ctas, max_units);
     const int n = int(ctas);
-    if (head_dim == 128)
-        return wide ? launch<128, 2, false>(p, n, st) : dup ? launch<128, 1, true>(p, n, st) : launch<128, 1, false>(p, n, st);
-    return wide ? launch<64, 2, false>(p, n, st) : dup ? launch<64, 1, true>(p, n, st) : launch<64, 1, false>(p, n, st);
+    auto of = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        return wide  ? launch<D, 2, false>(p, n, st)
+               : dup ? launch<D, 1, true>(p, n, st)
+                     : launch<D, 1, false>(p, n, st);
+    };
+    return head_dim == 128 ? of(std::integral_constant<int, 128>()) : of(std::integral_constant<int, 64>());
 }
 
 }  // namespace uw
