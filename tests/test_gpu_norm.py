@@ -111,6 +111,46 @@ def test_strided_rows(uw, d, xs, rs, hs, ys, off):
         assert np.all(gaps == 0x1234) and np.all(b[:off] == 0x1234) and np.all(b[off + n * stride:] == 0x1234)
 
 
+@pytest.mark.parametrize("d", [1, 3, 6, 7, 9, 14, 15, 17, 263, 1018, 1025, 2047, 4099, 8201, 16377, 16384])
+@pytest.mark.parametrize("off", [0, 1, 5])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_rows_alike_that_begin_anywhere(uw, d, off, bits):
+    """Rows of all tensors at the same odd distance from 16-byte steps, the weights at another."""
+    n = 9
+    xb, rb, wb = _inputs(n, d, d + off)
+    h_ref, y_ref = _reference(xb, rb, wb, 1e-5)
+    stride = {"x": d, "r": d + 8, "h": d + 16, "y": d}
+
+    def spread(name, values, dtype):
+        st = stride[name]
+        buf = np.full(off + (n - 1) * st + d + 16, 0x34, dtype)
+        rows = np.lib.stride_tricks.as_strided(buf[off:], (n, d), (st * buf.itemsize, buf.itemsize))
+        if values is not None:
+            rows[:] = values
+        t = _dev(buf) if dtype == np.uint16 else torch.from_numpy(buf).cuda()
+        return t, t[off:].as_strided((n, d), (st, 1))
+
+    (_, x), (_, r), (hb, h) = spread("x", xb, np.uint16), spread("r", rb, np.uint16), spread("h", None, np.uint16)
+    yb, y = spread("y", None, np.uint16 if bits == 16 else np.uint8)
+    w = _dev(np.concatenate([np.zeros(2, np.uint16), wb]))[2:]
+    scale = torch.empty(n, dtype=torch.float32, device="cuda")
+    uw.rmsnorm(x, w, y, 1e-5, residual=r, residual_out=h, scale=None if bits == 16 else scale)
+    torch.cuda.synchronize()
+    assert np.array_equal(_bits(h.contiguous()), h_ref)
+    if bits == 16:
+        err = np.abs(f32(_bits(y.contiguous())).reshape(n, d) - y_ref)
+        assert np.all(err <= _rel(d) * np.abs(y_ref))
+    else:
+        s = scale.cpu().numpy().astype(np.float64)[:, None]
+        got = y.contiguous().view(torch.float8_e4m3fn).float().cpu().numpy() * s
+        slack = (d + 16) * 2.0 ** -23
+        assert np.all(np.abs(got - y_ref) <= (2.0 ** -4 + slack) * np.abs(y_ref) + 2.0 ** -10 * s)
+    for buf, name in ((hb, "h"), (yb, "y")):
+        b, st = buf.cpu().numpy(), stride[name]
+        used = (off + st * np.arange(n)[:, None] + np.arange(d)).ravel()
+        assert np.all(np.delete(b, used) == 0x34)
+
+
 @pytest.mark.parametrize("d", [512, 4096, 777])
 def test_in_place(uw, d):
     """The residual stream updated in place, the norm written over x."""
