@@ -420,8 +420,10 @@ uw_status uw_mlp_autotune_workspace_size(const uw_mlp_matrix *m, int32_t n_layer
  *   weight_dev    d BF16 values.
  *   y_dev         BF16 rows (written), y_stride apart; may be x_dev.
  * Any d > 0 (UW_ERR_SHAPE otherwise) up to 2^31 - 1 (UW_ERR_UNSUPPORTED); BF16
- * pointers need 2-byte alignment, and rows of a multiple of 8 values on
- * 16-byte boundaries run on 16-byte loads.  n = 0 does nothing. */
+ * pointers need 2-byte alignment.  Rows of up to 16384 values are read once, in
+ * 16-byte steps, if the rows of x, residual, residual_out and y lie at the same
+ * distance from 16-byte boundaries; fastest where that is none.  n = 0 does
+ * nothing. */
 uw_status uw_rmsnorm(const uint16_t *x_dev, int64_t x_stride, const uint16_t *residual_dev,
                      int64_t residual_stride, uint16_t *residual_out_dev, int64_t residual_out_stride,
                      const uint16_t *weight_dev, int64_t n, int64_t d, float eps, uint16_t *y_dev,
@@ -524,8 +526,9 @@ uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start_dev, const int
  * tokens of every sequence (appended before).  Query head h reads kv head
  * h / (q_heads / kv_heads).  A token at position p sees the keys at
  *     max(0, p - window + 1) .. p   (causal; without: .. len - 1)
- * (window 0: from 0).  One that sees no key gets o = 0 and lse = -inf.  What
- * lies in a page past a sequence's length is never looked at.
+ * (window 0: from 0).  One that sees no key gets o = 0 and lse = -inf.  What a
+ * token does not see, past a sequence's length or masked, takes no part in its
+ * result, whatever its bits.
  *   q, out    q_heads heads (a multiple of kv_heads, UW_ERR_SHAPE otherwise).
  *   lse_dev   fp32 [n_tokens, q_heads]: log(sum exp(scale q.k)) (written), or NULL.
  *   max_new, max_len  upper bounds of the sequences' new tokens and lengths as
@@ -533,15 +536,20 @@ uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start_dev, const int
  *             is split: a wrong one costs time, never the result.
  *   softmax_scale  0 for 1 / sqrt(head_dim).
  *   ws_dev    at least uw_kv4_workspace_size bytes.
- * Softmax statistics and sums are fp32; the same call gives the same bits. */
+ * Softmax statistics and sums are fp32; the same call gives the same bits.
+ * Ranges: |q| below 2^79, scales of K (times softmax_scale) below 2^42 and of V
+ * below 2^39; past them a result may not be finite.  A product q c (c: a code)
+ * below 2^-41 may be taken as 0, and so may p scale of V (p: a probability)
+ * below 2^-57. */
 uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *start_dev, const int32_t *len_dev,
                            int64_t n_tokens, const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *out,
                            float *lse_dev, int64_t max_new, int64_t max_len, float softmax_scale, int32_t causal,
                            int32_t window, void *ws_dev, size_t ws_bytes, void *stream);
 
 /* uw_check_status -- synchronise `stream`, read and clear the error word the
- * kernels record in the workspace.  Returns UW_OK, UW_ERR_CORRUPT or
- * UW_ERR_TIMEOUT (or UW_ERR_CUDA if the stream itself failed). */
+ * kernels record in the workspace.  Returns UW_OK, UW_ERR_CORRUPT (a blob, or a
+ * page table, length, start or position, that does not hold) or UW_ERR_TIMEOUT
+ * (or UW_ERR_CUDA if the stream itself failed). */
 uw_status uw_check_status(void *ws_dev, void *stream);
 
 /* Variant names for diagnostics; NULL for an unknown (strategy, variant). */

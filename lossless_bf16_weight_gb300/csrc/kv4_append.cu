@@ -7,8 +7,12 @@
 // heads of 128): its time is latency.  For prompts instructions and memory are
 // about even.  A vector belongs to D / 8 lanes, 16 bytes each; a warp takes q heads
 // of one token, or k and v heads, 32 / (D / 8) at a time, and finds the token's
-// place and its row of the rotation table once for all of them.  Minimum and
-// maximum are joined by shuffles within the vector's lanes.
+// place and its row of the rotation table once for all of them, while the
+// first vectors are on their way.  Minimum and maximum are joined by shuffles
+// within the vector's lanes.
+//
+// Measured, 32 query and 8 kv heads of 128: append 1 token 2.3 us, 64 tokens 3.3,
+// 8143 tokens 40 us (4.4 TB/s); read 1.7, 2.1 and 12.6 us (3.5 TB/s).
 //
 // The rotation rounds each product and the sum (no fused multiply-add), and the
 // quotient of the quantisation is correctly rounded, so that the same inputs
@@ -34,7 +38,8 @@ struct AppendParams {
     float minus_zero;             // -0, which the compiler does not know (rotate())
 };
 
-constexpr int kAhead = 2;  // vectors a lane has on their way
+// Vectors a lane has on their way (8143 and 64 tokens: 2 41.8 and 3.3 us, 4 41.8 and 4.4, 1 45.8 and 3.3).
+constexpr int kAhead = 2;
 
 // Smaller halves of two pairs of BF16; NaN wherever one is.
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
@@ -298,7 +303,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View v, const Ro
 }
 
 // Vectors a warp takes one after the other (up to `most`) of the `all` of a token:
-// warps for two per scheduler come first, longer ones after that.
+// warps for two per scheduler come first, longer ones after that (8143 tokens
+// appended in 40 us, with one vector a warp 95; read in 12.6 and 19.7).
 int rounds_of(int64_t tokens, int all, int most) {
     int n = 1;
     while (2 * n <= most && n < all && tokens * ((all + 2 * n - 1) / (2 * n)) >= 152 * 4 * 2)

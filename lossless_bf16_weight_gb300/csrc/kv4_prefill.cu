@@ -1,8 +1,13 @@
 // Attention over the 4-bit paged cache for sequences with many rows (new
 // tokens x query heads of a kv head): prompts and their chunks.
 //
-// Bound by the tensor cores and by what stands around them: every key of an
-// item is unpacked once for 256 rows, and every score takes its exponential.
+// The floor is the tensor cores'; what bounds the kernel is the chain of each
+// softmax warp from a score to its probability: a step (256 rows x 128 keys) of
+// 4860 cycles has the tensor cores busy for 38%, the exponential unit for 19%,
+// the fp32 units for 36% and issue slots for 46%, and two softmax warps a
+// scheduler are what registers and tensor memory (256 columns of scores, 256 of
+// outputs) allow.  So every key of an item is unpacked once for 256 rows, and a
+// softmax thread has as many independent scores in flight as its registers hold.
 // One persistent CTA an SM takes an equal share of all (256 rows x 128 keys)
 // steps (kv4_attn.cuh).  Warp roles:
 //   softmax   warps 0-3 and 4-7: the upper and lower 128 rows, 32 a warp.  They
@@ -23,6 +28,14 @@
 // against them.  The running maximum is only raised when the probabilities of
 // 64 keys add up to more than 2^24 (BF16 and fp32 hold that without
 // loss), so that no score is compared and O is rarely rescaled.
+//
+// Measured, 32 query and 8 kv heads of 128, causal:
+//   a prompt of 8192 tokens                 675 us (815 TFLOP/s, 0.43 of cuBLAS's burst)
+//   64 new tokens after 524288              617 us (890 TFLOP/s)
+//   a prompt of 2048 tokens                 81 us (424 TFLOP/s)
+// Tried beside this: 32 keys at a time with the next scores on their way 778 us
+// (less to do at a time for each warp), no branch between scores and P 700,
+// the two halves' exponentials in turns 689, one half started later 677.
 #include <cmath>
 #include <type_traits>
 
@@ -38,7 +51,7 @@ namespace {
 constexpr int kRows = 256, kKeys = 128;
 constexpr int kSoftmax = 256, kUnpack = 128;          // threads
 constexpr int kThreads = kSoftmax + kUnpack + 128;    // and a warpgroup whose first warp issues the products
-constexpr int kItemCost = 3;                          // what an item costs beyond its steps, in steps
+constexpr int kItemCost = 3;  // what an item costs beyond its steps, in steps (a prompt of 8192 tokens: 675 us, with 0 847)
 constexpr int kSegs = 32;
 constexpr int kStages = 2, kParStages = 4;
 constexpr float kRaise = 16777216.f;                  // 2^24: headroom of the probabilities of 64 keys
@@ -581,25 +594,26 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
         }
         if (active) {
 #pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 16) {
-                uint32_t w[16];
+            for (int d0 = 0; d0 < D; d0 += 32) {
+                uint32_t w[2][16];
 #pragma unroll
                 for (int i = 0; i < 16; i++)
-                    w[i] = 0;
+                    w[0][i] = w[1][i] = 0;
                 if (valued) {
-                    tmem_ld16(o_tm + d0, w);
+                    tmem_ld16(o_tm + d0, w[0]);
+                    tmem_ld16(o_tm + d0 + 16, w[1]);
                     tmem_ld_wait();
                 }
-                float o[16];
+                float o[32];
 #pragma unroll
-                for (int i = 0; i < 16; i++)
-                    o[i] = fmaf(__uint_as_float(w[i]), i & 1 ? kPDownHigh : kPDownLow, z);
+                for (int i = 0; i < 32; i++)
+                    o[i] = fmaf(__uint_as_float(w[i / 16][i % 16]), i & 1 ? kPDownHigh : kPDownLow, z);
                 if (r < rows) {
                     if (whole) {
-                        store_dims<16>(p, sg.t0, sg.head, r, d0, o, row_m, l);
+                        store_dims<32>(p, sg.t0, sg.head, r, d0, o, row_m, l);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; i++)
+                        for (int i = 0; i < 8; i++)
                             reinterpret_cast<float4 *>(part)[(d0 / 4 + i) * kRows + threadIdx.x] =
                                 make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
@@ -625,30 +639,37 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                 __threadfence();
                 auto at = [&](uint32_t i) { return p.parts + (2 * uint64_t(i) + (i == f ? 1 : 0)) * PF; };
                 float mt = -INFINITY, lt = 0.f;
+#pragma unroll 4
                 for (uint32_t i = f; i <= e; i++)
                     mt = fmaxf(mt, __ldcg(at(i) + kRows * D + threadIdx.x));
                 const float m0 = mt == -INFINITY ? 0.f : mt;
+#pragma unroll 4
                 for (uint32_t i = f; i <= e; i++)
                     lt = fmaf(exp2_fast(__ldcg(at(i) + kRows * D + threadIdx.x) - m0),
                               __ldcg(at(i) + kRows * D + kRows + threadIdx.x), lt);
 #pragma unroll 1
-                for (int d0 = 0; d0 < D; d0 += 16) {
-                    float o[16];
+                for (int d0 = 0; d0 < D; d0 += 32) {
+                    float o[32];
 #pragma unroll
-                    for (int k = 0; k < 16; k++)
+                    for (int k = 0; k < 32; k++)
                         o[k] = 0.f;
+#pragma unroll 2
                     for (uint32_t i = f; i <= e; i++) {
-                        const float w = exp2_fast(__ldcg(at(i) + kRows * D + threadIdx.x) - m0);
+                        const float *const part = at(i);
+                        float4 x[8];
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(at(i)) + (d0 / 4 + k) * kRows + threadIdx.x);
-                            o[4 * k] = fmaf(w, x.x, o[4 * k]);
-                            o[4 * k + 1] = fmaf(w, x.y, o[4 * k + 1]);
-                            o[4 * k + 2] = fmaf(w, x.z, o[4 * k + 2]);
-                            o[4 * k + 3] = fmaf(w, x.w, o[4 * k + 3]);
+                        for (int k = 0; k < 8; k++)
+                            x[k] = __ldcg(reinterpret_cast<const float4 *>(part) + (d0 / 4 + k) * kRows + threadIdx.x);
+                        const float w = exp2_fast(__ldcg(part + kRows * D + threadIdx.x) - m0);
+#pragma unroll
+                        for (int k = 0; k < 8; k++) {
+                            o[4 * k] = fmaf(w, x[k].x, o[4 * k]);
+                            o[4 * k + 1] = fmaf(w, x[k].y, o[4 * k + 1]);
+                            o[4 * k + 2] = fmaf(w, x[k].z, o[4 * k + 2]);
+                            o[4 * k + 3] = fmaf(w, x[k].w, o[4 * k + 3]);
                         }
                     }
-                    store_dims<16>(p, sg.t0, sg.head, r, d0, o, mt, lt);
+                    store_dims<32>(p, sg.t0, sg.head, r, d0, o, mt, lt);
                 }
             }
             softmax_sync();  // sh.arrived is read

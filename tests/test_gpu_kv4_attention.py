@@ -182,6 +182,17 @@ def test_sharp_and_flat_scores(uw, new):
     _run(uw, 12, 8, 2, 64, 64, [new], [150 + new], scale=2.0)
 
 
+@pytest.mark.parametrize("new", [[1, 3], [5, 2], [200, 77]])
+@pytest.mark.parametrize("k_up,v_up", [(20, 0), (-20, 0), (0, 30), (0, -30), (12, -12)])
+def test_large_and_small_values(uw, new, k_up, v_up):
+    """Keys and values far from 1 (the softmax's scale keeps the scores where they were): exact powers of two."""
+    def change(pages, table, qb):
+        for par, up in zip(pages.pars, (k_up, v_up)):
+            finite = (par & 0x7F80) != 0x7F80
+            par[:] = np.where(finite, ref.bf16(ref.f32(par).reshape(par.shape) * 2.0 ** up).reshape(par.shape), par)
+    _run(uw, 31, 8, 2, 128, 32, new, [600, 333], scale=128 ** -0.5 * 2.0 ** -k_up, change=change)
+
+
 def test_bad_pages_are_reported(uw):
     hk, d, page = 2, 64, 16
     pages = torch.zeros(2, hk, page * (d + 8), dtype=torch.uint8, device="cuda")
