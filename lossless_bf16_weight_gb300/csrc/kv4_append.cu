@@ -12,7 +12,7 @@
 // within the vector's lanes.
 //
 // Measured, 32 query and 8 kv heads of 128: append 1 token 2.3 us, 64 tokens 3.3,
-// 8143 tokens 40 us (4.4 TB/s); read 1.7, 2.1 and 12.6 us (3.5 TB/s).
+// 8143 tokens 40 us (4.4 TB/s); read 1.7, 2.2 and 10.5 us (4.0 TB/s).
 //
 // The rotation rounds each product and the sum (no fused multiply-add), and the
 // quotient of the quantisation is correctly rounded, so that the same inputs
@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
         if (p.interleaved) {
             const float4 cs = *reinterpret_cast<const float4 *>(p.cos + row + 4 * c);
             const float4 sn = *reinterpret_cast<const float4 *>(p.sin + row + 4 * c);
-            r.c[0] = pair2(cs.x, cs.x), r.c[1] = pair2(cs.y, cs.y), r.c[2] = pair2(cs.z, cs.z), r.c[3] = pair2(cs.w, cs.w);
+            r.c[0] = pair2(cs.x, cs.x), r.c[1] = pair2(cs.y, cs.y);
+            r.c[2] = pair2(cs.z, cs.z), r.c[3] = pair2(cs.w, cs.w);
             r.s[0] = pair2(-sn.x, sn.x), r.s[1] = pair2(-sn.y, sn.y);
             r.s[2] = pair2(-sn.z, sn.z), r.s[3] = pair2(-sn.w, sn.w);
         } else {
@@ -215,7 +216,8 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
                 uint32_t a[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
                 rotate(r, zero, a, o[n]);
                 if (n0 + n < rounds && j0 + (n0 + n) * G < all)
-                    *reinterpret_cast<uint4 *>(dst + int64_t(n0 + n) * G * p.qo.hs) = make_uint4(a[0], a[1], a[2], a[3]);
+                    *reinterpret_cast<uint4 *>(dst + int64_t(n0 + n) * G * p.qo.hs) =
+                        make_uint4(a[0], a[1], a[2], a[3]);
             }
             n0 += kAhead;
             if (n0 >= rounds)
@@ -254,7 +256,9 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
     }
 }
 
-template <int D>
+// Ahead: vectors a lane has on their way, as many as it has in all or one (8143 tokens:
+// 8 10.5 us, 4 11.4, 2 13.0; one token with 8 1.94 us, with one 1.75).
+template <int D, int Ahead>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View v, const Rows ko, const Rows vo, const int chunk) {
     constexpr int L = D / 8, G = 32 / L;
     grid_dep_launch();
@@ -277,34 +281,53 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View v, const Ro
         return;
     }
     const int slot = pos & ((1 << v.page_log2) - 1);
-    const int64_t block = int64_t(D + 8) << v.page_log2;
+    const uint32_t block = uint32_t(D + 8) << v.page_log2;  // (all heads of a page: below 2^32)
     const uint8_t *const page = kv4_block<D>(v, s, pos, 0);
+    if (!page)
+        return;
     const int h0 = int(unit - t * per_token) * G * chunk + lane / L;
-#pragma unroll 4
-    for (int ci = 0; ci < chunk; ci++) {
-        const int h = h0 + ci * G;
-        if (h >= total)
-            break;
-        const int is_v = h >= v.heads, hk = is_v ? h - v.heads : h;
-        if (!page)
-            continue;
-        const uint8_t *blk = page + hk * block;
-        const uint32_t codes = *reinterpret_cast<const uint32_t *>(blk + kv4_codes<D>(v.page_log2, slot, is_v) + 4 * c);
-        const uint32_t par = *reinterpret_cast<const uint32_t *>(blk + kv4_params<D>(v.page_log2, slot, is_v));
-        const float scale = bf16_lo(par), lo = bf16_hi(par);
-        uint32_t o[4];
+    uint16_t *const ko_at = ko.p + t * ko.ts + 8 * c, *const vo_at = vo.p + t * vo.ts + 8 * c;
+    const uint64_t minus16 = pair2(-16.f, -16.f);
+    for (int c0 = 0; c0 < chunk; c0 += Ahead) {
+        // all loads before the first store, which could otherwise not pass it
+        uint32_t codes[Ahead], par[Ahead];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            o[k] = bf16_pack(fmaf(float((codes >> (8 * k)) & 15u), scale, lo),
-                             fmaf(float((codes >> (8 * k + 4)) & 15u), scale, lo));
-        const Rows &dst = is_v ? vo : ko;
-        *reinterpret_cast<uint4 *>(dst.p + t * dst.ts + hk * dst.hs + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int n = 0; n < Ahead; n++) {
+            const int h = h0 + (c0 + n) * G;
+            const bool in = c0 + n < chunk && h < total, is_v = h >= v.heads;
+            const uint8_t *const blk = page + (is_v ? h - v.heads : h) * block;
+            const uint8_t *const code_at = blk + kv4_codes<D>(v.page_log2, slot, is_v) + 4 * c;
+            const uint8_t *const par_at = blk + kv4_params<D>(v.page_log2, slot, is_v);
+            codes[n] = in ? *reinterpret_cast<const uint32_t *>(code_at) : 0u;
+            par[n] = in ? *reinterpret_cast<const uint32_t *>(par_at) : 0u;
+        }
+#pragma unroll
+        for (int n = 0; n < Ahead; n++) {
+            const int h = h0 + (c0 + n) * G;
+            if (c0 + n >= chunk || h >= total)
+                return;
+            const uint64_t scale = pair2(bf16_lo(par[n]), bf16_lo(par[n]));
+            const uint64_t lo = pair2(bf16_hi(par[n]), bf16_hi(par[n]));
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                // a code at the top of the mantissa of 16 is 16 + c
+                auto up = [&](int at) {
+                    const uint32_t x = at < 19 ? codes[n] << (19 - at) : codes[n] >> (at - 19);
+                    return __uint_as_float((x & 0x780000u) | 0x41800000u);
+                };
+                const float2 x = unpair(fma2(add2(pair2(up(8 * k), up(8 * k + 4)), minus16), scale, lo));
+                o[k] = bf16_pack(x.x, x.y);
+            }
+            uint16_t *const dst = h >= v.heads ? vo_at + (h - v.heads) * vo.hs : ko_at + h * ko.hs;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
 }
 
 // Vectors a warp takes one after the other (up to `most`) of the `all` of a token:
 // warps for two per scheduler come first, longer ones after that (8143 tokens
-// appended in 40 us, with one vector a warp 95; read in 12.6 and 19.7).
+// appended in 40 us, with one vector a warp 95; read in 10.5, with two 15).
 int rounds_of(int64_t tokens, int all, int most) {
     int n = 1;
     while (2 * n <= most && n < all && tokens * ((all + 2 * n - 1) / (2 * n)) >= 152 * 4 * 2)
@@ -380,9 +403,8 @@ extern "C" uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start, co
         return UW_ERR_UNSUPPORTED;
     const dim3 grid(unsigned((units + 7) / 8));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return (c->head_dim == 128 ? launch_overlapped(kv4_read_kernel<128>, grid, dim3(256), 0, st, view, ko, vo, chunk)
-                               : launch_overlapped(kv4_read_kernel<64>, grid, dim3(256), 0, st, view, ko, vo, chunk)) ==
-                   cudaSuccess
-               ? UW_OK
-               : UW_ERR_CUDA;
+    auto run = [&](auto kernel) { return launch_overlapped(kernel, grid, dim3(256), 0, st, view, ko, vo, chunk); };
+    const cudaError_t e = c->head_dim == 128 ? (chunk > 1 ? run(kv4_read_kernel<128, 8>) : run(kv4_read_kernel<128, 1>))
+                                             : (chunk > 1 ? run(kv4_read_kernel<64, 8>) : run(kv4_read_kernel<64, 1>));
+    return e == cudaSuccess ? UW_OK : UW_ERR_CUDA;
 }

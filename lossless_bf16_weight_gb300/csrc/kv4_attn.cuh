@@ -25,7 +25,7 @@ namespace uw {
 // n * ceil(2^(31 + s) / d) >> (31 + s) with 2^s >= d.
 struct Divisor {
     uint32_t d, mul, shift;
-    explicit Divisor(uint32_t d = 1) : d(d), shift(31) {
+    Divisor(uint32_t d = 1) : d(d), shift(31) {
         while ((1ull << (shift - 31)) < d)
             shift++;
         mul = uint32_t(((1ull << shift) + d - 1) / d);
@@ -371,7 +371,8 @@ __device__ __forceinline__ void store_dims(const AttnParams &p, int t0, int kv_h
     uint4 *const dst = reinterpret_cast<uint4 *>(p.o.p + tok * p.o.ts + head * p.o.hs + d0);
 #pragma unroll
     for (int k = 0; k < N / 8; k++)
-        dst[k] = make_uint4(bf16_pack(o[8 * k] * inv, o[8 * k + 1] * inv), bf16_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+        dst[k] = make_uint4(bf16_pack(o[8 * k] * inv, o[8 * k + 1] * inv),
+                            bf16_pack(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
                             bf16_pack(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
                             bf16_pack(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
     if (p.lse && d0 == 0)

@@ -30,9 +30,10 @@
 // loss), so that no score is compared and O is rarely rescaled.
 //
 // Measured, 32 query and 8 kv heads of 128, causal:
-//   a prompt of 8192 tokens                 675 us (815 TFLOP/s, 0.43 of cuBLAS's burst)
-//   64 new tokens after 524288              617 us (890 TFLOP/s)
-//   a prompt of 2048 tokens                 81 us (424 TFLOP/s)
+//   a prompt of 8192 tokens                 666 us (826 TFLOP/s, 0.43 of cuBLAS's burst)
+//   64 new tokens after 524288              608 us (905 TFLOP/s)
+//   a prompt of 2048 tokens                 79 us (435 TFLOP/s): to the first scores 9 us, an item's
+//                                           output 2.5, a join 3 to 8
 // Tried beside this: 32 keys at a time with the next scores on their way 778 us
 // (less to do at a time for each warp), no branch between scores and P 700,
 // the two halves' exponentials in turns 689, one half started later 677.
@@ -51,7 +52,8 @@ namespace {
 constexpr int kRows = 256, kKeys = 128;
 constexpr int kSoftmax = 256, kUnpack = 128;          // threads
 constexpr int kThreads = kSoftmax + kUnpack + 128;    // and a warpgroup whose first warp issues the products
-constexpr int kItemCost = 3;  // what an item costs beyond its steps, in steps (a prompt of 8192 tokens: 675 us, with 0 847)
+// What an item costs beyond its steps, in steps (a prompt of 8192 tokens: 675 us, with 0 847).
+constexpr int kItemCost = 3;
 constexpr int kSegs = 32;
 constexpr int kStages = 2, kParStages = 4;
 constexpr float kRaise = 16777216.f;                  // 2^24: headroom of the probabilities of 64 keys
@@ -125,7 +127,8 @@ __device__ __forceinline__ void mma_role(const AttnParams &p, Shared &sh, uint32
         if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < kKeys / 32; i++)
-                mma_ts(tm + 256 + half * D, tm + half * kKeys + h * (kKeys / 2) + i * 8, v + 2 * i, kIdO, more || i > 0);
+                mma_ts(tm + 256 + half * D, tm + half * kKeys + h * (kKeys / 2) + i * 8, v + 2 * i, kIdO,
+                       more || i > 0);
             mma_commit(bars + 8 * (kPvDone + 2 * half + h));
         }
         __syncwarp();
@@ -353,7 +356,8 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
                     for (int i = 0; i < 4; i++)
                         e[i] = __byte_perm(rv[n][2 * i], rv[n][2 * i + 1], sel[jj]);
                     const uint32_t to = vt + v_to[jj] + n * (D * 128);
-                    sts128(to, sub2(e[0] & m_a, c_a), sub2(e[1] & m_a, c_a), sub2(e[2] & m_a, c_a), sub2(e[3] & m_a, c_a));
+                    sts128(to, sub2(e[0] & m_a, c_a), sub2(e[1] & m_a, c_a), sub2(e[2] & m_a, c_a),
+                           sub2(e[3] & m_a, c_a));
                     sts128(to ^ v_flip, sub2(e[0] & m_b, c_b), sub2(e[1] & m_b, c_b), sub2(e[2] & m_b, c_b),
                            sub2(e[3] & m_b, c_b));
                 }
@@ -433,7 +437,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                         uint32_t x[64];  // [32 keys][16 rows' half][key group][row g, g + 8][pair]
 #pragma unroll
                         for (int c = 0; c < 4; c++)
-                            tmem_ld_16x256_x4(s_tm + 64 * h + 32 * (c >> 1) + (uint32_t(16 * (c & 1)) << 16), x + 16 * c);
+                            tmem_ld_16x256_x4(s_tm + 64 * h + 32 * (c >> 1) + (uint32_t(16 * (c & 1)) << 16),
+                                              x + 16 * c);
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 8; k++) {

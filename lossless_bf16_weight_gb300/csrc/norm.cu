@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(256) norm_warp_kernel(const NormParams p) {
 // (Rows of up to 16384 that begin anywhere take up to 288 threads, two CTAs an SM: 2000
 // x 16383 to 8 bits 65 us, one CTA 103.)
 template <int V, bool k8, bool kOdd>
-__global__ void __launch_bounds__(kOdd && V == 8 ? 288 : 512, kOdd && V == 8 ? 2 : 0) norm_cta_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kOdd && V == 8 ? 288 : 512, kOdd && V == 8 ? 2 : 0)
+    norm_cta_kernel(const NormParams p) {
     __shared__ float slots[64];
     grid_dep_launch();
     grid_dep_wait();
