@@ -126,6 +126,7 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
     p.q_heads = q_heads;
     p.group = q_heads / c->kv_heads;
     p.by_group = Divisor(uint32_t(p.group));
+    p.out32 = ((reinterpret_cast<uintptr_t>(p.o.p) | uintptr_t(p.o.ts) * 2 | uintptr_t(p.o.hs) * 2) & 31) == 0;
     p.causal = causal != 0;
     p.window = window;
     uint8_t *const wsb = static_cast<uint8_t *>(ws);
