@@ -50,12 +50,14 @@ bool kv4_rows(const uw_kv4_rows *r, Rows *out) {
 namespace {
 
 // Sequences with up to so many rows (new tokens x query heads of a kv head)
-// take the kernel for few rows.  Measured with 8 kv heads of 128, that kernel and
-// the other: 16 sequences of 4096 keys, 16 rows 41 and 82 us, 32 rows 65 and 81,
-// 64 rows 110 and 83; one sequence of 8192 keys, 64 rows 29 and 48: with few steps
-// (256 rows x 128 keys) in all, what the other kernel takes to start decides.
-constexpr int kFewRows = 32, kFewRowsShort = 64;
-constexpr int64_t kShortSteps = 1024;
+// take the kernel for few rows: kFewRows, or what a call of kShort units (32 keys
+// x 8 rows) in all makes, up to kFewRowsShort (whose row tiles a CTA looks through
+// one by one).  That kernel and the other, 8 kv heads of 128: 16 sequences of 4096 keys, 16
+// rows 41 and 82 us, 32 rows 65 and 81, 64 rows 110 and 83; one sequence of 8192 keys, 64
+// rows 29 and 48; of 1000 keys, 256 rows 23 and 32, 512 rows 32 and 34, 1024 rows 44 and 35;
+// prompts of 64 tokens of 4 heads 10.9 and 17.2, of 128 17.0 and 17.9, of 512 43 and 29.
+constexpr int kFewRows = 32, kFewRowsShort = 1024;
+constexpr int64_t kShort = 24576;
 
 // Workspace: [error word | counters and parts of the kernel for few rows | the
 // same of the other].
@@ -134,16 +136,18 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
     // Which sequences take which kernel is decided on the device by their rows;
     // the host's bounds only leave out a launch that has none, and a wrong bound
     // leaves all sequences to the kernel that is launched.
-    const int64_t rows = max_new * p.group;
-    const bool few_steps = max_len > 0 && (max_len + 127) / 128 * c->kv_heads * c->n_seqs <= kShortSteps;
-    const int few_rows = few_steps ? kFewRowsShort : kFewRows;
+    const int64_t rows = std::min<int64_t>(max_new, INT32_MAX) * p.group;
+    // units of eight rows of each sequence (bounds may be any number)
+    const int64_t of_one = (std::min<int64_t>(max_len, INT32_MAX) / 32 + 2) * c->kv_heads;
+    const int64_t eight = std::min<int64_t>(std::min<int64_t>(of_one, INT32_MAX) * c->n_seqs, 1ll << 40);
+    const int few_rows = max_len > 0 ? int(std::clamp<int64_t>(kShort / eight * 8, kFewRows, kFewRowsShort)) : kFewRows;
     const bool few = rows == 0 || rows <= few_rows || c->n_seqs > 1, many = rows == 0 || rows > few_rows;
     if (few) {
         p.rows_min = 0;
         p.rows_max = many ? few_rows : INT32_MAX;
         p.counters = reinterpret_cast<uint32_t *>(wsb + w.few_counters);
         p.parts = reinterpret_cast<float *>(wsb + w.few_parts);
-        const int64_t units = max_len > 0 && !many ? (max_len / 32 + 2) * (rows / 8 + 1) * c->kv_heads * c->n_seqs : 0;
+        const int64_t units = max_len > 0 && !many ? eight * (rows / 8 + 1) : 0;
         // beside prompts most of the other sequences have one new token
         const uw_status r = launch_kv4_decode(p, c->head_dim, many ? std::max(p.group, 5) : rows, units, st);
         if (r != UW_OK)

@@ -54,6 +54,9 @@ constexpr int kSoftmax = 256, kUnpack = 128;          // threads
 constexpr int kThreads = kSoftmax + kUnpack + 128;    // and a warpgroup whose first warp issues the products
 // What an item costs beyond its steps, in steps (a prompt of 8192 tokens: 675 us, with 0 847).
 constexpr int kItemCost = 3;
+// Units of a CTA at least: an item in many parts is joined part after part (128
+// tokens of 8 heads after 8000 keys 55 us, with one unit 84; other short calls alike).
+constexpr int kMinShare = 4;
 constexpr int kSegs = 32;
 constexpr int kStages = 2, kParStages = 4;
 constexpr float kRaise = 16777216.f;                  // 2^24: headroom of the probabilities of 64 keys
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const AttnPara
     grid_dep_launch();
     grid_dep_wait();
     const uint64_t total = build_row<S, kThreads, true>(p, sh.row);
-    const uint32_t workers = uint32_t(min(total, uint64_t(gridDim.x)));
+    const uint32_t workers = uint32_t(min((total + kMinShare - 1) / kMinShare, uint64_t(gridDim.x)));
     if (blockIdx.x >= workers)
         return;
     if (warp == kThreads / 32 - 1)

@@ -121,6 +121,37 @@ def test_many_tokens(uw, hq, hk, d, page, new, lens, causal, window):
     _run(uw, hq + 1, hq, hk, d, page, new, lens, causal, window)
 
 
+@pytest.mark.parametrize("hq,hk,d,page,new,lens", MANY)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 100)])
+def test_many_tokens_of_unknown_bounds(uw, hq, hk, d, page, new, lens, causal, window):
+    """The same without bounds, which leaves them to the kernel for many rows however short they are."""
+    _run(uw, hq + 1, hq, hk, d, page, new, lens, causal, window, hints=False)
+
+
+@pytest.mark.parametrize("hints", [True, False])
+@pytest.mark.parametrize("hq,hk,new,lens", [(8, 1, [128], [128]), (8, 1, [129], [131]), (8, 1, [127, 130, 1], [900] * 3),
+                                            (32, 8, [64, 3], [64, 64]), (4, 4, [90], [5000])])
+def test_rows_about_the_choice_of_kernel(uw, hq, hk, new, lens, hints):
+    _run(uw, hq + len(new), hq, hk, 128, 32, new, lens, hints=hints)
+
+
+@pytest.mark.parametrize("max_new,max_len", [(2 ** 62, 2 ** 62), (2 ** 62, 1), (1, 2 ** 62), (2 ** 31, 2 ** 31)])
+def test_absurd_bounds(uw, max_new, max_len):
+    rng = np.random.default_rng(3)
+    pages, table = _cache(rng, 2, 64, 16, [70, 300])
+    q = _dev(ref.bf16(rng.standard_normal((71, 4, 64))))
+    cache = uw.kv4_cache(_dev(pages.bytes), _dev(table), 2, 64, 16)
+    ws = torch.empty(uw.kv4_workspace_size(cache, 4), dtype=torch.uint8, device="cuda")
+    uw.workspace_init(ws)
+    start, length = _dev(ref.starts([70, 1])), _dev(np.array([70, 300], np.int32))
+    want, got = torch.empty_like(q), torch.empty_like(q)
+    uw.kv4_attention(cache, start, length, q, want, ws, 70, 300)
+    uw.kv4_attention(cache, start, length, q, got, ws, max_new, max_len)
+    assert uw.check_status(ws) == 0
+    diff = ref.f32(want.cpu().numpy().view(np.uint16)) - ref.f32(got.cpu().numpy().view(np.uint16))
+    assert np.abs(diff).max() <= 2.0 ** -5      # values of up to 5, two kernels' roundings
+
+
 @pytest.mark.parametrize("new,lens", [([5], [3]), ([9, 1], [0, 0]), ([200, 2], [150, 1]), ([1, 300], [0, 40])])
 @pytest.mark.parametrize("causal", [True, False])
 def test_rows_that_see_nothing(uw, new, lens, causal):
