@@ -51,7 +51,6 @@ enum StatusFlag : uint32_t {
     kStatusBadTile = 2u,    // tile offsets / sizes out of range
     kStatusBadEscape = 4u,  // escape counts inconsistent
     kStatusTimeout = 8u,    // a bounded wait gave up
-    kStatusBadCache = 16u,  // a page number, length or start that does not fit the cache or the call
 };
 
 constexpr int kPrefixEntries = 1 << kLmax;

@@ -57,7 +57,7 @@
 #include "decode.cuh"
 #include "kernels.h"
 #include "pair_stage.cuh"
-#include "tc.cuh"
+#include "tmem.cuh"
 
 namespace uw {
 

@@ -13,6 +13,10 @@
 
 namespace uw {
 
+// The status word's bit (beside StatusFlag's) for a page number, length or start
+// that does not fit the cache or the call.
+constexpr uint32_t kStatusBadCache = 16u;
+
 struct Kv4View {
     uint8_t *pages;
     const int32_t *table;
@@ -39,7 +43,7 @@ struct Seq {
 __device__ __forceinline__ Seq kv4_seq(const Kv4View &v, int s) {
     const int32_t a = __ldg(v.start + s), b = __ldg(v.start + s + 1), len = __ldg(v.len + s);
     if (a < 0 || b < a || b > v.n_tokens || len < 0 || int64_t(len) > (int64_t(v.width) << v.page_log2)) {
-        atomicOr(v.status, uint32_t(kStatusBadCache));
+        atomicOr(v.status, kStatusBadCache);
         return {0, 0, 0};
     }
     return {a, b - a, len};
@@ -51,7 +55,7 @@ template <int D>
 __device__ __forceinline__ uint8_t *kv4_block(const Kv4View &v, int s, int32_t p, int head) {
     const int32_t page = __ldg(v.table + int64_t(s) * v.table_stride + (p >> v.page_log2));
     if (uint32_t(page) >= uint64_t(v.n_pages)) {
-        atomicOr(v.status, uint32_t(kStatusBadCache));
+        atomicOr(v.status, kStatusBadCache);
         return nullptr;
     }
     return v.pages + (int64_t(page) * v.heads + head) * (int64_t(D + 8) << v.page_log2);

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
     const int32_t pos = q.len - q.n + (int32_t(t) - q.t0);
     if (pos < 0 || (p.rot && pos >= p.rope_len)) {
         if (lane == 0)
-            atomicOr(v.status, uint32_t(kStatusBadCache));
+            atomicOr(v.status, kStatusBadCache);
         return;
     }
     if (r.on) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View v, const Ro
     const int32_t pos = q.len - q.n + (int32_t(t) - q.t0);
     if (pos < 0) {
         if (lane == 0)
-            atomicOr(v.status, uint32_t(kStatusBadCache));
+            atomicOr(v.status, kStatusBadCache);
         return;
     }
     const int slot = pos & ((1 << v.page_log2) - 1);

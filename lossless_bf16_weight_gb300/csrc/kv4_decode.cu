@@ -5,7 +5,7 @@
 // so memory is the floor; what bounds the kernel is what a warp does with 32 keys
 // of 128 (4352 bytes): 555 instructions, 160 of them the logic that takes the
 // codes apart and 64 the subtractions of their middle, at 0.62 instructions a
-// cycle.  A CTA of eight warps takes an equal share of all key
+// cycle, which 0.9 of a copy's rate is not far from.  A CTA of eight warps takes an equal share of all key
 // tiles (kv4_attn.cuh), and each of its warps an equal share of that, which it
 // works through by itself: a ring of tiles in flight (cp.async) runs on from
 // item to item, an item that lies in one warp's share is written out by that
@@ -38,9 +38,10 @@
 // in place of shuffles.
 //
 // Measured, 32 query and 8 kv heads of 128:
-//   one token, 131072 keys        @LONG
-//   64 tokens, 100 to 8192 keys   38 us (2.9 TB/s)
-//   one token, 290 keys           8.6 us
+//   one token, 131071 keys       40.6 us (3.5 TB/s)
+//   one token, 1048576 keys      205 us (5.6 TB/s, of 6.8 for a copy); keys more cost at 6.1 TB/s
+//   64 tokens, 40 to 8192 keys   38 us (2.9 TB/s)
+//   one token, 257 keys          8.8 us
 // A call's first 6 us go to finding the shares and the first loads, its last
 // 6 to the joins, whose steps wait for one another's loads.
 #include <algorithm>
@@ -61,10 +62,10 @@ constexpr int kWarps = 8;
 constexpr int kTile = 32;            // keys of a unit
 constexpr float kRaise = 24.f;       // log2 headroom of a probability
 // What an item costs a warp beyond its tiles (queries, output), in tiles: 64
-// tokens of 100 to 8192 keys 45.8 us with none, 40.5 with 1, 38.4 with 2, 37.8 with 3, 38.0 with 4.
+// tokens of 40 to 8192 keys 45.8 us with none, 40.5 with 1, 38.4 with 2, 37.8 with 3, 38.0 with 4.
 constexpr int kItemCost = 3;
 // Items up to this many tiles are not cut between CTAs while shares are short:
-// one token of 290 keys 11.2 us if they are, 8.6 if not.
+// one token of 257 keys 11.2 us if they are, 8.6 if not.
 constexpr uint32_t kWholeTiles = 32;
 // Sequences of more than eight rows are taken sixteen at a time (each key
 // unpacked once for all, but one CTA an SM) only if there are more units (32 keys
@@ -133,7 +134,7 @@ struct Part {
 };
 
 // NT groups of eight rows; kDup (NT = 1): up to four rows, which rows 4..7 repeat
-// (one token, 131072 keys 40.6 us, with a second product for the rests 44.2).
+// (one token, 131071 keys 40.6 us, with a second product for the rests 44.2).
 template <int D, int NT, bool kDup>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kernel(const AttnParams p) {
     static_assert(!kDup || NT == 1, "rows repeated in one group");
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (bad)
-        atomicOr(v.status, uint32_t(kStatusBadCache));
+        atomicOr(v.status, kStatusBadCache);
     __syncthreads();
 
     // Items that the cuts between the warps go through: consecutive parts of

@@ -43,7 +43,7 @@
 #include "kernels.h"
 #include "kv4_attn.cuh"
 #include "kv4_codes.cuh"
-#include "tc.cuh"
+#include "tmem.cuh"
 
 namespace uw {
 
@@ -241,7 +241,7 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
         auto bad = [&](int page) {
             if (uint32_t(page) < uint32_t(v.n_pages))
                 return false;
-            atomicOr(v.status, uint32_t(kStatusBadCache));
+            atomicOr(v.status, kStatusBadCache);
             return true;
         };
         // A key or eight keys of V that are not there are zeros; pages are
