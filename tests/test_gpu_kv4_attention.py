@@ -237,6 +237,37 @@ def test_bad_pages_are_reported(uw):
         assert uw.check_status(ws) == 4
 
 
+@pytest.mark.parametrize("new", [2, 200])
+def test_pages_past_32_bits(uw, new):
+    """The same tokens in a pool's first pages and in pages whose offset is beyond 4 GB."""
+    hq, hk, d, page, n_pages, length = 8, 8, 128, 256, 16000, 700
+    size = uw.kv4_page_bytes(hk, d, page)
+    assert (n_pages - 4) * size > 2 ** 32
+    pool = torch.empty(n_pages * size, dtype=torch.uint8, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    qkv = torch.randn(length, hq + 2 * hk, d, generator=gen, device="cuda").bfloat16()
+    outs = []
+    for first in (0, n_pages - 3):
+        table = torch.arange(first, first + 3, dtype=torch.int32, device="cuda")[None]
+        cache = uw.kv4_cache(pool, table, hk, d, page)
+        ws = torch.empty(uw.kv4_workspace_size(cache, hq), dtype=torch.uint8, device="cuda")
+        uw.workspace_init(ws)
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+        span = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, length], [length], [0, new])]
+        uw.kv4_append(cache, span[0], span[1], None, k, v, None, None, None, ws)
+        ko, vo, out = torch.empty_like(k), torch.empty_like(v), torch.empty_like(q[:new])
+        uw.kv4_read(cache, span[0], span[1], ko, vo, ws)
+        uw.kv4_attention(cache, span[2], span[1], q[:new], out, ws)  # no bounds: few rows and many by their number
+        assert uw.check_status(ws) == 0
+        outs.append((ko, vo, out))
+    for low, high in zip(*outs):
+        assert torch.equal(low, high)
+    # half a step of the scale, and the rounding of the value read back
+    step = (outs[0][0].float() - qkv[:, hq:hq + hk].float()).abs().amax(-1)
+    span = qkv[:, hq:hq + hk].float().aminmax(dim=-1)
+    assert (step <= (span.max - span.min) / 30 * 1.01 + 2.0 ** -8 * 5).all()
+
+
 def test_on_another_stream(uw):
     """All work is enqueued on the stream that is passed."""
     side = torch.cuda.Stream()
