@@ -172,11 +172,12 @@ def _stream(stream):
 
 def _current_stream() -> int:
     """torch.cuda.current_stream().cuda_stream without building the Stream
-    object (2.9 us a call against 0.4 us, of 3 us for a launch)."""
+    object (2.9 us a call against 0.2 us, of 3 us for a launch)."""
     global _current_stream
     import torch
-    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
-    if raw is not None:
+    raw, device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is not None and device is not None:
+        torch.cuda.current_device()  # (initialises CUDA)
         _current_stream = lambda: raw(device())  # noqa: E731
     else:
         _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
