@@ -528,7 +528,8 @@ uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start_dev, const int
  *     max(0, p - window + 1) .. p   (causal; without: .. len - 1)
  * (window 0: from 0).  One that sees no key gets o = 0 and lse = -inf.  What a
  * token does not see, past a sequence's length or masked, takes no part in its
- * result, whatever its bits.
+ * result, whatever its bits; pages that lie before every new token's window are
+ * not looked at, nor are their numbers in the table.
  *   q, out    q_heads heads (a multiple of kv_heads, UW_ERR_SHAPE otherwise).
  *   lse_dev   fp32 [n_tokens, q_heads]: log(sum exp(scale q.k)) (written), or NULL.
  *   max_new, max_len  upper bounds of the sequences' new tokens and lengths as

@@ -259,6 +259,7 @@ struct Seg {
     uint64_t u0;
     int32_t s, head, rt, t0, tokens, len;
     int32_t first, tiles, of;  // `of`: the item's tiles
+    int32_t lo;                // the first key that some row sees: pages before its page are not looked at
     int32_t all_lo, all_hi;    // keys that every row sees
 };
 // A warp lists the segments of the units from u (in item `it`) up to `end`,
@@ -289,6 +290,7 @@ __device__ __forceinline__ uint64_t list_segments(const AttnParams &p, Item &it,
                 g.first = it.keys.lo / S::kKeys + int(a);
                 g.tiles = max(tiles, 0);
                 g.of = int(it.tiles);
+                g.lo = it.keys.lo;
                 const int r0 = it.rt * S::kRows, r1 = r0 + min(S::kRows, it.q.n * p.group - r0) - 1;
                 const int i0 = p.by_group.of(r0), i1 = p.by_group.of(r1);
                 g.all_lo = visible(p, it.q, i1, i1).lo;

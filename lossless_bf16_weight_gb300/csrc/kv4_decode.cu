@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         nx_last = sg.len - 1;
         nx_base = v.pages + (sg.head * block + (lane & 15) * 16);
         nx_table = v.table + int64_t(sg.s) * v.table_stride;
-        nx_page = __ldg(nx_table + (min(nx_key, nx_last) >> v.page_log2));
+        nx_page = __ldg(nx_table + (min(max(nx_key, sg.lo), nx_last) >> v.page_log2));
     };
     constexpr int RC = D / 32;  // 16-byte chunks of a row
     const uint32_t first_row = (lane & 16) + (lane & 15) / RC;

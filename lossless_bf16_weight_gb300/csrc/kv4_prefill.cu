@@ -231,7 +231,7 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
         uint4 rk[KC];
         uint32_t rv[VT][8], rp[2];
         int pk, pv[VT];
-        auto page_of = [&](int at) { return __ldg(table + (min(at, sg.len - 1) >> v.page_log2)); };
+        auto page_of = [&](int at) { return __ldg(table + (min(max(at, sg.lo), sg.len - 1) >> v.page_log2)); };
         auto pages = [&](int key0) {
             pk = page_of(key0 + key);
 #pragma unroll

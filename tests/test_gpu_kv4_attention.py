@@ -196,6 +196,25 @@ def test_masked_keys_may_hold_anything(uw, new):
     _run(uw, 8, 4, 2, 128, 16, [new], lens, window=40, change=change)
 
 
+@pytest.mark.parametrize("new,window", [(1, 5), (1, 16), (3, 40), (20, 100), (200, 300), (200, 33), (1, 1)])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("hints", [True, False])
+def test_pages_before_the_window_may_be_gone(uw, new, window, page, hints):
+    """The table holds no page numbers for what every row's window has left behind."""
+    lens = [new + 901, new + 75]
+
+    def change(pages, table, qb):
+        for s, m in enumerate(lens):
+            gone = max(m - new - window + 1, 0) // page
+            # the pages hold NaN, and the numbers are none
+            for p in table[s, :gone]:
+                for par in pages.pars:
+                    par[p] = 0x7FC0
+            table[s, :gone] = -1
+
+    _run(uw, 13, 8, 2, 128, page, [new, new], lens, window=window, change=change, hints=hints)
+
+
 @pytest.mark.parametrize("new", [1, 3, 200])
 def test_sharp_and_flat_scores(uw, new):
     """One key far above the others (early, late, in between), and all scores equal."""
