@@ -30,9 +30,9 @@
 // loss), so that no score is compared and O is rarely rescaled.
 //
 // Measured, 32 query and 8 kv heads of 128, causal:
-//   a prompt of 8192 tokens                 653 us (842 TFLOP/s, 0.44 of cuBLAS's burst)
-//   64 new tokens after 524288              606 us (907 TFLOP/s)
-//   a prompt of 2048 tokens                 79 us (438 TFLOP/s): to the first scores 9 us, an item's
+//   a prompt of 8192 tokens                 646 us (851 TFLOP/s, 0.45 of cuBLAS's burst)
+//   64 new tokens after 524288              600 us (916 TFLOP/s)
+//   a prompt of 2048 tokens                 78 us (440 TFLOP/s): to the first scores 9 us, an item's
 //                                           output 2, a join 3 to 8
 // Tried beside this: 32 keys at a time with the next scores on their way 778 us
 // (less to do at a time for each warp), no branch between scores and P 700,
