@@ -51,7 +51,6 @@
 #include "kernels.h"
 #include "kv4_attn.cuh"
 #include "kv4_codes.cuh"
-#include "kv4_host.h"
 #include "tc.cuh"
 
 namespace uw {
