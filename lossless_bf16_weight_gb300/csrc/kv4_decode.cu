@@ -38,10 +38,10 @@
 // in place of shuffles.
 //
 // Measured, 32 query and 8 kv heads of 128:
-//   one token, 131071 keys       40.6 us (3.5 TB/s)
-//   one token, 1048576 keys      205 us (5.6 TB/s, of 6.8 for a copy); keys more cost at 6.1 TB/s
-//   64 tokens, 40 to 8192 keys   38 us (2.9 TB/s)
-//   one token, 257 keys          8.8 us
+//   one token, 131071 keys       39.3 us (3.6 TB/s)
+//   one token, 1048576 keys      203 us (5.6 TB/s, of 6.8 for a copy); keys more cost at 6.1 TB/s
+//   64 tokens, 40 to 8192 keys   37 us (3.0 TB/s)
+//   one token, 257 keys          8.1 us
 // A call's first 6 us go to finding the shares and the first loads, its last
 // 6 to the joins, whose steps wait for one another's loads.
 #include <algorithm>
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
         u = list_segments<S, kSegs>(p, it, u, u_end, segs, &n_segs);
         nx_seg = 0;
         next_seg();
-        int fill = stage, calls = ST;
+        int fill = stage, to_fill = ST;
         for (int sgi = 0; sgi < n_segs; sgi++) {
             const Seg &sg = segs[sgi];
             const int n_mine = sg.tiles;
@@ -277,13 +277,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             Warp<D, NT> w;
             // Queries: lane (g, t) holds row g of each group, dimensions D/4 t .. + D/4 - 1,
             // paired as the codes of a word come out of it: (0,4) (1,5) (2,6) (3,7).
+            uint4 xq[NT][D / 32];
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
                 const int rr = nt * 8 + (kDup ? g & 3 : g);
-                uint4 x[D / 32];
 #pragma unroll
                 for (int k = 0; k < D / 32; k++)
-                    x[k] = make_uint4(0, 0, 0, 0);
+                    xq[nt][k] = make_uint4(0, 0, 0, 0);
                 if (rr < rows - r0 && n_mine > 0) {
                     const int i = p.by_group.of(r0 + rr);
                     const int64_t tok = sg.t0 + i, head = sg.head * p.group + (r0 + rr - i * p.group);
@@ -291,8 +291,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                     const uint4 *src = reinterpret_cast<const uint4 *>(at);
 #pragma unroll
                     for (int k = 0; k < D / 32; k++)
-                        x[k] = src[k];
+                        xq[nt][k] = src[k];
                 }
+            }
+            // the ring's fill, while the first queries are on their way
+#pragma unroll 1
+            for (; to_fill > 0; to_fill--) {
+                issue(fill);
+                fill = fill + 1 == ST ? 0 : fill + 1;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+                const uint4(&x)[D / 32] = xq[nt];
                 float sum = 0.f;
 #pragma unroll
                 for (int k = 0; k < D / 32; k++) {
@@ -318,11 +328,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             }
 
             for (int i = 0; i < n_mine; i++) {
-                for (; calls > 0; calls--) {  // the ring's fill at first, then a tile for a tile
-                    issue(fill);
-                    fill = fill + 1 == ST ? 0 : fill + 1;
-                }
-                calls = 1;
                 asm volatile("cp.async.wait_group %0;" :: "n"(ST - 1) : "memory");
                 __syncwarp();
                 const unsigned char *const st = ring + stage * kStageBytes<D>;
@@ -526,6 +531,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                             }
                     }
                 __syncwarp();
+                issue(fill);  // a tile for a tile
+                fill = fill + 1 == ST ? 0 : fill + 1;
             }
             // A whole item is written out; a part of one goes to the workspace, or
             // (the warp's last) to its ring.
