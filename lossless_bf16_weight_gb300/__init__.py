@@ -484,7 +484,7 @@ def mlp_autotune(mats, x, y, ws, passes: int = 2, stream=None, side_stream=None)
 # ---------------------------------------------------------------- around the matmuls of a decoder layer
 def _row_stride(t, shape, size: int, name: str, what: str) -> int:
     """Row stride in elements of a [n, d] (or, for one row, [d]) tensor of
-    `size`-byte elements whose rows are contiguous."""
+    `size`-byte elements whose rows are contiguous; `shape` is one or the other."""
     if t.shape == shape and t.itemsize == size and t.is_contiguous():
         return shape[-1]
     d, n = shape[-1], shape[0] if len(shape) == 2 else 1
@@ -500,9 +500,11 @@ def _row_stride(t, shape, size: int, name: str, what: str) -> int:
 def rmsnorm(x, weight, y, eps: float = 1e-5, residual=None, residual_out=None, scale=None, stream=None):
     """uw_rmsnorm: h = bf16(x + residual) into residual_out (if given), y = h / rms(h) * weight in BF16.
     With `scale` (fp32, one for each row): uw_rmsnorm_e4m3, y holds e4m3 bytes (torch.float8_e4m3fn or uint8).
-    Rows may be strided."""
+    Tensors are [n, d], whose rows may be strided, or [d]; more dimensions are for the caller to flatten."""
     what = "uw_rmsnorm" if scale is None else "uw_rmsnorm_e4m3"
     shape = x.shape
+    if not 1 <= len(shape) <= 2:
+        raise UwError(UW_ERR_SHAPE, "%s (x is %s, neither [n, d] nor [d])" % (what, tuple(shape)))
     d, n = shape[-1], shape[0] if len(shape) == 2 else 1
     xs = _row_stride(x, shape, 2, "x", what)
     ys = _row_stride(y, shape, 2 if scale is None else 1, "y", what)
