@@ -46,14 +46,16 @@ struct AttnParams {
     uint32_t *counters;       // [gridDim.x], left at zero
 };
 
-// Keys [lo, hi) that some row of tokens [i0, i1] of a sequence sees.
+// Keys [lo, hi) that some row of tokens [i0, i1] of a sequence sees.  (Of more
+// new tokens than the sequence holds the first have negative positions, and
+// a window may be any number: nothing is subtracted from a negative one.)
 struct KeyRange {
     int32_t lo, hi;
 };
 __device__ __forceinline__ KeyRange visible(const AttnParams &p, const Seq &s, int i0, int i1) {
     const int32_t before = s.len - s.n;
     const int32_t hi = p.causal ? before + i1 + 1 : s.len;
-    const int32_t lo = p.window ? before + i0 - p.window + 1 : 0;
+    const int32_t lo = p.window ? max(before + i0 + 1, 0) - p.window : 0;
     return {max(lo, 0), max(hi, 0)};
 }
 
