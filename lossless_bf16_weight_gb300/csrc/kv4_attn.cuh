@@ -268,7 +268,8 @@ struct Seg {
 // at most kMost of them; returns the unit after them and leaves `it` there.
 // An item's last units, which are no tiles, are nobody's; one that sees no
 // key at all is a segment without tiles of the share that has its first unit.
-// The sequences' lengths are read 32 at a time.
+// The sequences' lengths are read 32 at a time.  `segs` may be a list that
+// the warp has just worked through.
 template <class S, int kMost>
 __device__ __forceinline__ uint64_t list_segments(const AttnParams &p, Item &it, uint64_t u, uint64_t end, Seg *segs,
                                                   int *count) {
@@ -276,6 +277,7 @@ __device__ __forceinline__ uint64_t list_segments(const AttnParams &p, Item &it,
     int base = it.s, n = 0;
     Seq next{0, 0, 0};
     bool loaded = false;
+    __syncwarp();  // every lane has read the list before
     while (u < end && n < kMost) {
         const uint32_t a = uint32_t(u - it.u0), b = uint32_t(min(end - it.u0, uint64_t(it.n)));
         const int tiles = int(min(b, it.tiles)) - int(a);

@@ -13,3 +13,10 @@ pytestmark = pytest.mark.gpu
 def test_windows_of_any_size(uw, new, lens, window, causal, hints):
     """A window as good as none, with more new tokens than the sequence holds (their first positions are negative)."""
     _run(uw, 3, 8, 2, 128, 16, new, lens, causal, window, hints=hints)
+
+
+@pytest.mark.parametrize("count,hq,hk,new", [(4000, 8, 8, 1), (3000, 20, 4, 2), (2500, 8, 8, 5)])
+def test_more_items_than_a_warp_lists_at_once(uw, count, hq, hk, new):
+    """Many short sequences: each warp of the kernel for few rows goes through several lists of items."""
+    lens = [new + (7 * i) % 37 for i in range(count)]
+    _run(uw, count, hq, hk, 64, 16, [new] * count, lens)
