@@ -412,7 +412,8 @@ uw_status uw_mlp_autotune_workspace_size(const uw_mlp_matrix *m, int32_t n_layer
  *     h = bf16(x + residual)      (h = x without a residual)
  *     y = bf16(h / sqrt(mean(h^2) + eps) * weight)
  * The mean, the root and the products are in fp32; y is rounded to BF16 once.
- * (Squares or products past fp32's range, |h| above 1.8e19, give 0 or NaN.)
+ * (A sum of squares past fp32's range gives 0 or NaN: values of h of
+ * 1.8e19 / sqrt(d), or single ones of 1.8e19.  So may a product h * weight past it.)
  *   x_dev         BF16 rows, x_stride elements apart (x_stride >= d).
  *   residual_dev  BF16 rows to add, or NULL (then residual_out_dev is NULL too).
  *   residual_out_dev  h (written), or NULL if it is not wanted; may be

@@ -90,12 +90,13 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float a, float b) {
 struct RowScale {
     float scale, a, b;
     __device__ __forceinline__ RowScale(float top, float rstd) {
-        const float own = top * rstd / kE4m3Max;
+        float own = top * rstd / kE4m3Max;
+        own = own < INFINITY ? own : __int_as_float(0x7fffffff);  // NaN stays NaN
         scale = max_nan(own, kMinScale);
         const bool least = own <= kMinScale, small = top < 1e-30f;  // 448 / top beyond fp32
         a = least ? rstd : small ? 1.f / top : kE4m3Max / top;
         b = least ? 1.f / kMinScale : small ? kE4m3Max : 1.f;
-        if (!(own <= INFINITY))
+        if (!(own < INFINITY))
             a = scale;
     }
     __device__ __forceinline__ float of(float u) const { return u * a * b; }
