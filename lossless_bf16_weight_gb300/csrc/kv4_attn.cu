@@ -59,17 +59,18 @@ namespace {
 constexpr int kFewRows = 32, kFewRowsShort = 1024;
 constexpr int64_t kShort = 24576;
 
-// Workspace: [error word | counters and parts of the kernel for few rows | the
-// same of the other].
+// Workspace: [error word | counters of the kernel for few rows | of the other |
+// parts of the one | of the other].  The counters, which a call finds at zero, lie in
+// the same place for every head size, so that one workspace serves both.
 struct Layout {
-    size_t few_counters, few_parts, many_counters, many_parts, total;
+    size_t few_counters, many_counters, few_parts, many_parts, total;
 };
 Layout layout(int head_dim) {
     Layout w;
     w.few_counters = 256;
-    w.few_parts = align_up(w.few_counters + 4 * size_t(kv4_decode_ctas()), 256);
-    w.many_counters = align_up(w.few_parts + 4 * kv4_decode_part_floats(head_dim), 256);
-    w.many_parts = align_up(w.many_counters + 4 * size_t(kv4_prefill_ctas()), 256);
+    w.many_counters = align_up(w.few_counters + 4 * size_t(kv4_decode_ctas()), 256);
+    w.few_parts = align_up(w.many_counters + 4 * size_t(kv4_prefill_ctas()), 256);
+    w.many_parts = align_up(w.few_parts + 4 * kv4_decode_part_floats(head_dim), 256);
     w.total = w.many_parts + 4 * kv4_prefill_part_floats(head_dim);
     return w;
 }
