@@ -35,12 +35,15 @@ struct Step {
 struct Chain {
     int64_t D = 0, Fmax = 0;
     std::vector<Step> steps;
-    size_t control = 256;  // the matmuls' status word, split counters and partials
+    // The matmuls' split counters lie before `partial` whatever their rows, and
+    // nothing else does but the status word: they are to be zero for the next matmul.
+    size_t partial = 256;       // where the matmuls' partials begin
+    size_t partial_bytes = 0;   // their size, the largest matmul's
     size_t slot = 0;       // largest form a hard matrix writes
     int nhard = 0;
 };
 
-// Workspace: [control | x ping | x pong | g | u | h | slot 0 | slot 1 ...].
+// Workspace: [status, counters | partials | x ping | x pong | g | u | h | slot 0 | slot 1 ...].
 struct ChainLayout {
     size_t xa, xb, g, u, h, slots, slot_stride, total;
 };
@@ -49,7 +52,7 @@ ChainLayout chain_layout(const Chain &c, int64_t batch, int slots) {
     ChainLayout L;
     const size_t xbytes = align256(size_t(batch) * size_t(c.D) * 2);
     const size_t fbytes = align256(size_t(batch) * size_t(c.Fmax) * 2);
-    L.xa = align256(c.control);
+    L.xa = align256(c.partial + c.partial_bytes);
     L.xb = L.xa + xbytes;
     L.g = L.xb + xbytes;
     L.u = L.g + fbytes;
@@ -125,7 +128,9 @@ uw_status plan_chain(const uw_mlp_matrix *m, int32_t n_layers, int64_t batch, co
             c.nhard++;
             c.slot = std::max(c.slot, s.form_bytes);
         }
-        c.control = std::max(c.control, run_layout(d.rows, d.cols, batch, s.variant).weights);
+        const WsLayout wl = run_layout(d.rows, d.cols, batch, s.variant);
+        c.partial = std::max(c.partial, wl.partial);
+        c.partial_bytes = std::max(c.partial_bytes, wl.weights - wl.partial);
     }
     return UW_OK;
 }
@@ -235,7 +240,7 @@ uw_status run_chain(const uw_mlp_matrix *m, int32_t n_layers, const uint16_t *x,
         p.y = out;
         p.status = reinterpret_cast<uint32_t *>(ws + wl.status);
         p.counters = reinterpret_cast<uint32_t *>(ws + wl.counters);
-        p.partial = reinterpret_cast<float *>(ws + wl.partial);
+        p.partial = reinterpret_cast<float *>(ws + c.partial);
         p.rows = d.rows;
         p.cols = d.cols;
         p.batch = batch;

@@ -3,12 +3,39 @@ workspace does not reach the results of the next, whatever that one's shape."""
 import pytest
 import torch
 
+import workloads as wl
+
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def g(uw):
+    from tests import _gpu
+    return _gpu
 
 
 def _normal(seed, *shape):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+
+@pytest.mark.parametrize("batch", [2, 3, 8, 15])
+def test_chain_does_not_depend_on_the_call_before(g, uw, batch):
+    """A chain whose wide and narrow matrices are both split along their columns."""
+    dim, inner = 1024, 4096
+    mats = [g.Compressed(wl.normal_weights(r, c, 0.02, i)) for i, (r, c) in
+            enumerate([(inner, dim), (inner, dim), (dim, inner)])]
+    chain = uw.mlp_matrices([(m.desc, m.blob_dev, None, None) for m in mats])
+    ws = g.workspace(uw.mlp_workspace_size(chain, batch))
+    for seed in (1, 2, 1):
+        x = _normal(seed, batch, dim)
+        y = torch.empty_like(x)
+        uw.mlp_forward(chain, x, y, ws)
+        assert uw.check_status(ws) == 0
+        gate, up = (torch.from_numpy(m.matmul(x).view("int16")).cuda() for m in mats[:2])
+        h = torch.empty_like(gate)
+        uw.swiglu(gate, up, h)
+        assert (g.host_bits(y.view(torch.int16)) == mats[2].matmul(h)).all()
 
 
 def test_attention_workspace_serves_both_head_sizes(uw):
