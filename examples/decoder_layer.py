@@ -68,12 +68,14 @@ class DecoderLayer:
         self.mlp = uw.mlp_matrices([(self.m[n].desc, self.m[n].blob, None, None) for n in ("gate", "up", "down")])
         empty = uw.kv4_cache(self.pages, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), kv_heads, head_dim,
                              page_size)
-        need = max([uw.workspace_size(self.m[n].desc, b) for n in ("qkv", "o") for b in (1, 8, max_tokens)]
-                   + [uw.mlp_workspace_size(self.mlp, b) for b in (1, 8, max_tokens)])
-        self.ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-        self.kv_ws = torch.empty(uw.kv4_workspace_size(empty, q_heads), dtype=torch.uint8, device="cuda")
-        uw.workspace_init(self.ws)
-        uw.workspace_init(self.kv_ws)
+        # A call finds its counters in its workspace as its last one left them, so every matrix
+        # shape, the chain and the cache have workspaces of their own.
+        need = {n: max(uw.workspace_size(self.m[n].desc, b) for b in (1, 8, max_tokens)) for n in ("qkv", "o")}
+        need["mlp"] = max(uw.mlp_workspace_size(self.mlp, b) for b in (1, 8, max_tokens))
+        need["kv"] = uw.kv4_workspace_size(empty, q_heads)
+        self.ws = {n: torch.empty(size, dtype=torch.uint8, device="cuda") for n, size in need.items()}
+        for ws in self.ws.values():
+            uw.workspace_init(ws)
 
     def forward(self, x, residual, cache, start, length, max_new, max_len):
         """x, residual [tokens, hidden] BF16 (residual None in the first layer).  Returns (MLP's output, h')."""
@@ -86,23 +88,23 @@ class DecoderLayer:
             h = torch.empty_like(x)
             uw.rmsnorm(x, self.norms[0], y, self.eps, residual=residual, residual_out=h)
         qkv = torch.empty(t, hq + 2 * hk, d, dtype=x.dtype, device=x.device)
-        uw.matmul(self.m["qkv"].desc, self.m["qkv"].blob, y, qkv, self.ws)
+        uw.matmul(self.m["qkv"].desc, self.m["qkv"].blob, y, qkv, self.ws["qkv"])
         q = torch.empty(t, hq, d, dtype=x.dtype, device=x.device)
         uw.kv4_append(cache, start, length, qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], q, self.cos, self.sin,
-                      self.kv_ws)
+                      self.ws["kv"])
         a = torch.empty_like(q)
-        uw.kv4_attention(cache, start, length, q, a, self.kv_ws, max_new, max_len)
+        uw.kv4_attention(cache, start, length, q, a, self.ws["kv"], max_new, max_len)
         o = torch.empty_like(x)
-        uw.matmul(self.m["o"].desc, self.m["o"].blob, a.view(t, hq * d), o, self.ws)
+        uw.matmul(self.m["o"].desc, self.m["o"].blob, a.view(t, hq * d), o, self.ws["o"])
         h2 = torch.empty_like(x)
         uw.rmsnorm(o, self.norms[1], y, self.eps, residual=h, residual_out=h2)
         out = torch.empty_like(x)
-        uw.mlp_forward(self.mlp, y, out, self.ws)
+        uw.mlp_forward(self.mlp, y, out, self.ws["mlp"])
         return out, h2
 
     def check(self):
         """Synchronises; errors that a kernel recorded raise."""
-        for ws in (self.ws, self.kv_ws):
+        for ws in self.ws.values():
             status = uw.check_status(ws)
             if status != uw.UW_OK:
                 raise uw.UwError(status, "decoder layer")

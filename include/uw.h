@@ -42,7 +42,10 @@
  *     Scratch space ("workspace") is passed in by the caller; its size comes
  *     from uw_workspace_size and it must be cleared once with
  *     uw_workspace_init before first use.  Kernels leave it ready for the
- *     next call.  One workspace must not be used by two calls that may run
+ *     next call of the same kind: matmuls of a matrix of as many rows, the same
+ *     chain, or the calls of a cache (any batch, plan and head size); their
+ *     counters lie elsewhere for others, so clear it again before it serves
+ *     those.  One workspace must not be used by two calls that may run
  *     at the same time.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Device work is enqueued on it and the call returns without

@@ -1,11 +1,16 @@
 """Workspaces that serve one call after another: what a call leaves in its
 workspace does not reach the results of the next, whatever that one's shape."""
+import os
+import sys
+
 import pytest
 import torch
 
 import workloads as wl
 
 pytestmark = pytest.mark.gpu
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 
 @pytest.fixture(scope="module")
@@ -66,3 +71,17 @@ def test_attention_workspace_serves_both_head_sizes(uw):
             own = torch.empty(need, dtype=torch.uint8, device="cuda")
             uw.workspace_init(own)
             assert torch.equal(run(d, shared, tokens), run(d, own, tokens))
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 15, 40])
+def test_layer_steps_do_not_depend_on_the_ones_before(uw, tokens):
+    """Projections of 4096 and 1024 rows, which small batches split along their columns."""
+    from decoder_layer import DecoderLayer, Sequences
+    layer = DecoderLayer(1024, 1024, 16, 8, 128, pages=8, page_size=16, max_tokens=64, max_positions=64, seed=5)
+    outs = []
+    for seed in (1, 2, 1):
+        out, h = layer.forward(_normal(seed, tokens, 1024), None, *Sequences(layer, 1, 64).extend([tokens]))
+        layer.check()
+        outs.append((out.clone(), h.clone()))
+    assert not torch.equal(outs[0][0], outs[1][0])
+    assert torch.equal(outs[0][0], outs[2][0]) and torch.equal(outs[0][1], outs[2][1])
