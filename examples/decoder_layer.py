@@ -70,8 +70,10 @@ class DecoderLayer:
                              page_size)
         # A call finds its counters in its workspace as its last one left them, so every matrix
         # shape, the chain and the cache have workspaces of their own.
-        need = {n: max(uw.workspace_size(self.m[n].desc, b) for b in (1, 8, max_tokens)) for n in ("qkv", "o")}
-        need["mlp"] = max(uw.mlp_workspace_size(self.mlp, b) for b in (1, 8, max_tokens))
+        # (A smaller batch may need more than a larger one, which is cut up less.)
+        batches = range(1, max_tokens + 1)
+        need = {n: max(uw.workspace_size(self.m[n].desc, b) for b in batches) for n in ("qkv", "o")}
+        need["mlp"] = max(uw.mlp_workspace_size(self.mlp, b) for b in batches)
         need["kv"] = uw.kv4_workspace_size(empty, q_heads)
         self.ws = {n: torch.empty(size, dtype=torch.uint8, device="cuda") for n, size in need.items()}
         for ws in self.ws.values():

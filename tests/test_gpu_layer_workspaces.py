@@ -85,3 +85,12 @@ def test_layer_steps_do_not_depend_on_the_ones_before(uw, tokens):
         outs.append((out.clone(), h.clone()))
     assert not torch.equal(outs[0][0], outs[1][0])
     assert torch.equal(outs[0][0], outs[2][0]) and torch.equal(outs[0][1], outs[2][1])
+
+
+@pytest.mark.parametrize("tokens", [129, 161, 299])
+def test_layer_takes_every_batch_up_to_its_limit(uw, tokens):
+    from decoder_layer import DecoderLayer, Sequences
+    layer = DecoderLayer(1024, 1024, 8, 2, 128, pages=24, page_size=16, max_tokens=300, max_positions=300, seed=5)
+    out, h = layer.forward(_normal(1, tokens, 1024), None, *Sequences(layer, 1, 300).extend([tokens]))
+    layer.check()
+    assert torch.isfinite(out.float()).all() and torch.isfinite(h.float()).all()
