@@ -250,11 +250,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
             }
             if ((lane & 8) == 0)
                 cp_async16_zfill(dst + par_to, page + (slot * 4 + par_off), bytes);
-            nx_key += kTile;
-            if (--nx_tiles == 0)
+            if (--nx_tiles == 0) {
                 next_seg();
-            else
+            } else {
+                nx_key += kTile;
                 nx_page = __ldg(nx_table + (min(nx_key, nx_last) >> v.page_log2));
+            }
         }
         cp_async_commit();
     };
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) kv4_decode_kerne
                 const uint4 kp = *reinterpret_cast<const uint4 *>(st + kTile * D + g * 16);
                 const uint4 vp = *reinterpret_cast<const uint4 *>(st + kTile * (D + 4) + g * 16);
                 const uint32_t kpar[4] = {kp.x, kp.y, kp.z, kp.w}, vpar[4] = {vp.x, vp.y, vp.z, vp.w};
-                const bool open = key0 < all_lo || key0 + kTile > all_hi;
+                const bool open = key0 < all_lo || all_hi - key0 < kTile;  // (key0 + kTile may be 2^31)
                 uint64_t y[4][NT];
                 auto scores = [&]() {
 #pragma unroll

@@ -268,7 +268,7 @@ __device__ __forceinline__ void unpack_role(const AttnParams &p, Shared &sh, uin
             for (int n = 0; n < VT; n++) {
                 const int at = key0 + 8 * (kg + n * KG);
                 const uint8_t *b = base + pv[n] * page_bytes + kv4_codes<D>(v.page_log2, at & mask, 1) + vw * 4;
-                if (!bad(pv[n]) && at + 8 <= sg.len) {
+                if (!bad(pv[n]) && sg.len - at >= 8) {
 #pragma unroll
                     for (int i = 0; i < 8; i++)
                         rv[n][i] = __ldg(reinterpret_cast<const uint32_t *>(b + i * (D / 2)));
@@ -416,7 +416,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
                     qs[i] = pair2(q, q);
                 }
             }
-            const bool open = key0 < sg.all_lo || key0 + kKeys > sg.all_hi;
+            const bool open = key0 < sg.all_lo || sg.all_hi - key0 < kKeys;  // (key0 + kKeys may be 2^31)
             auto tile = [&](auto masked) {
                 constexpr bool kOpen = decltype(masked)::value;
                 int lo[4], hi[4];  // the rows' keys in this tile, less the thread's first
