@@ -539,7 +539,8 @@ uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start_dev, const int
  *   max_new, max_len  upper bounds of the sequences' new tokens and lengths as
  *             the host knows them (0: not known).  They only choose how the work
  *             is split: a wrong one costs time, never the result.
- *   softmax_scale  0 for 1 / sqrt(head_dim).
+ *   softmax_scale  0 for 1 / sqrt(head_dim); else from 2^-126 to 2^42
+ *             (UW_ERR_UNSUPPORTED otherwise).
  *   ws_dev    at least uw_kv4_workspace_size bytes.
  * Softmax statistics and sums are fp32; the same call gives the same bits.
  * Ranges: |q| below 2^79, scales of K (times softmax_scale) below 2^42 and of V

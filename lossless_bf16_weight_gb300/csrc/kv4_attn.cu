@@ -1,10 +1,12 @@
 // Entry points of the 4-bit paged cache's attention, and the checks of what the
 // cache's calls are given.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "kernels.h"
 #include "kv4_attn.cuh"
+#include "kv4_codes.cuh"
 #include "kv4_host.h"
 
 namespace uw {
@@ -117,7 +119,11 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
         return UW_ERR_INVALID_ARG;
     if (q_heads <= 0 || q_heads % c->kv_heads)
         return UW_ERR_SHAPE;
+    p.c1 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(float(c->head_dim))) * 1.44269504089f;
     if (q_heads > kKv4MaxHeads || n_tokens * (q_heads / c->kv_heads) > 0x7fffffff)
+        return UW_ERR_UNSUPPORTED;
+    // the kernels take codes in units of 2^-133 and so multiply by c1 * kQDown
+    if (!(p.c1 >= FLT_MIN) || !std::isfinite(p.c1 * kQDown))
         return UW_ERR_UNSUPPORTED;
     if (none)
         return UW_OK;
@@ -125,7 +131,6 @@ extern "C" uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *star
     if (ws_bytes < w.total)
         return UW_ERR_BUFFER_TOO_SMALL;
     p.lse = lse;
-    p.c1 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(float(c->head_dim))) * 1.44269504089f;
     p.q_heads = q_heads;
     p.group = q_heads / c->kv_heads;
     p.by_group = Divisor(uint32_t(p.group));

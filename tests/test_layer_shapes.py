@@ -1,6 +1,9 @@
-"""What the binding of the layer operators refuses beyond wrong sizes: tensors of
-another rank, of which a call would take the first row only.  On the CPU,
-against a stand-in for the library that records which entry points were reached."""
+"""What the layer operators refuse beyond wrong sizes, on the CPU: tensors of
+another rank, of which a call would take the first row only (against a stand-in for the
+library that records which entry points were reached), and a softmax scale that
+the kernels could not take (the C ABI itself, with addresses that are never read)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -59,3 +62,14 @@ def test_rmsnorm_of_a_single_number_is_refused(uw, fake):
     x = torch.zeros((), dtype=torch.bfloat16)
     _refused(uw, SHAPE, uw.rmsnorm, x, _bits(1), x, stream=0)
     assert fake.calls == []
+
+
+@pytest.mark.parametrize("scale,want", [(2.0 ** 43, UNSUPPORTED), (1e30, UNSUPPORTED), (2.0 ** -127, UNSUPPORTED),
+                                        (2.0 ** 42, OK), (2.0 ** -126, OK), (0.0, OK), (1.0, OK), (-0.0, OK)])
+def test_softmax_scales(uw, scale, want):
+    """No tokens: a scale that is taken needs no device."""
+    p = 1 << 20
+    cache, rows = uw.Kv4CacheDesc(p, p, 10, 4, 4, 2, 2, 128, 16), uw.Kv4Rows(p, 1024, 128)
+    got = uw.load().uw_kv4_attention(ctypes.byref(cache), p, p, 0, rows, 4, rows, None, 1, 100, scale, 1, 0, p, 1 << 40,
+                                     None)
+    assert got == want
