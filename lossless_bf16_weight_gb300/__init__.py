@@ -584,9 +584,11 @@ def kv4_append(cache: Kv4Cache, start, length, q, k, v, q_out, cos, sin, ws, int
     _kv4_seqs(cache, start, length, what)
     kr = _kv4_rows(k, n, d.kv_heads, d.head_dim, "k", what)
     vr = _kv4_rows(v, n, d.kv_heads, d.head_dim, "v", what)
+    if (q is None) != (q_out is None) or (cos is None) != (sin is None):
+        raise UwError(UW_ERR_INVALID_ARG, "%s (q and q_out, cos and sin: both or neither)" % what)
     heads = 0 if q is None else q.shape[1] if q.dim() == 3 else -1
     qr = orow = None
-    if q is not None or q_out is not None:
+    if q is not None:
         qr = _kv4_rows(q, n, heads, d.head_dim, "q", what)
         orow = _kv4_rows(q_out, n, heads, d.head_dim, "q_out", what)
     rope_len = rot = 0

@@ -73,3 +73,25 @@ def test_softmax_scales(uw, scale, want):
     got = uw.load().uw_kv4_attention(ctypes.byref(cache), p, p, 0, rows, 4, rows, None, 1, 100, scale, 1, 0, p, 1 << 40,
                                      None)
     assert got == want
+
+
+@pytest.fixture
+def call(uw):
+    """A right call of kv4_append: its arguments by name."""
+    d = 64
+    cache = uw.kv4_cache(torch.zeros(3, uw.kv4_page_bytes(2, d, 16), dtype=torch.uint8),
+                         torch.zeros(2, 4, dtype=torch.int32), 2, d, 16)
+    qkv, cos = _bits(5, 8, d), torch.zeros(9, 32)
+    return dict(cache=cache, start=torch.zeros(3, dtype=torch.int32), length=torch.zeros(2, dtype=torch.int32),
+                q=qkv[:, :4], k=qkv[:, 4:6], v=qkv[:, 6:], q_out=_bits(5, 4, d), cos=cos, sin=cos, ws=torch.zeros(256),
+                stream=0)
+
+
+@pytest.mark.parametrize("left_out", ["q", "q_out", "cos", "sin"])
+def test_append_takes_pairs_of_arguments_only_together(uw, fake, call, left_out):
+    """q without q_out or cosines without sines: refused, not taken as if neither had been given."""
+    uw.kv4_append(**call)
+    assert len(fake.calls) == 1
+    call[left_out] = None
+    _refused(uw, INVALID, uw.kv4_append, **call)
+    assert len(fake.calls) == 1
