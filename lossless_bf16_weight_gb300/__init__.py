@@ -482,13 +482,23 @@ def mlp_autotune(mats, x, y, ws, passes: int = 2, stream=None, side_stream=None)
 
 
 # ---------------------------------------------------------------- around the matmuls of a decoder layer
-def _row_stride(t, shape, size: int, name: str, what: str) -> int:
-    """Row stride in elements of a [n, d] (or, for one row, [d]) tensor of
-    `size`-byte elements whose rows are contiguous; `shape` is one or the other."""
-    if t.shape == shape and t.itemsize == size and t.is_contiguous():
+def _types():
+    """The tensor types that hold BF16 values, e4m3 values, int32 and fp32 (the first two also as plain bits)."""
+    global _types
+    import torch
+    found = (frozenset((torch.bfloat16, torch.int16, torch.uint16)),
+             frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8)), torch.int32, torch.float32)
+    _types = lambda: found  # noqa: E731
+    return found
+
+
+def _row_stride(t, shape, kinds, name: str, what: str) -> int:
+    """Row stride in elements of a [n, d] (or, for one row, [d]) tensor of one
+    of the types `kinds` whose rows are contiguous; `shape` is one or the other."""
+    if t.shape == shape and t.dtype in kinds and t.is_contiguous():
         return shape[-1]
     d, n = shape[-1], shape[0] if len(shape) == 2 else 1
-    if t.itemsize != size or t.shape[-1] != d or t.numel() != n * d or t.dim() > 2:
+    if t.dtype not in kinds or t.shape[-1] != d or t.numel() != n * d or t.dim() > 2:
         raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s)" % (what, name, tuple(t.shape), t.dtype))
     if t.is_contiguous():
         return d
@@ -506,14 +516,17 @@ def rmsnorm(x, weight, y, eps: float = 1e-5, residual=None, residual_out=None, s
     if not 1 <= len(shape) <= 2:
         raise UwError(UW_ERR_SHAPE, "%s (x is %s, neither [n, d] nor [d])" % (what, tuple(shape)))
     d, n = shape[-1], shape[0] if len(shape) == 2 else 1
-    xs = _row_stride(x, shape, 2, "x", what)
-    ys = _row_stride(y, shape, 2 if scale is None else 1, "y", what)
+    bf16, e4m3, _, fp32 = _types()
+    xs = _row_stride(x, shape, bf16, "x", what)
+    ys = _row_stride(y, shape, bf16 if scale is None else e4m3, "y", what)
     rp = hp = None
     rs = hs = 0
     if residual is not None:
-        rp, rs = residual.data_ptr(), _row_stride(residual, shape, 2, "residual", what)
+        rp, rs = residual.data_ptr(), _row_stride(residual, shape, bf16, "residual", what)
     if residual_out is not None:
-        hp, hs = residual_out.data_ptr(), _row_stride(residual_out, shape, 2, "residual_out", what)
+        hp, hs = residual_out.data_ptr(), _row_stride(residual_out, shape, bf16, "residual_out", what)
+    if weight.dtype not in bf16 or (scale is not None and scale.dtype is not fp32):
+        raise UwError(UW_ERR_SHAPE, "%s (weight is not BF16, or scale not fp32)" % what)
     _refuse(_short((weight, 2 * d, "weight")), what)
     if scale is None:
         _check(load().uw_rmsnorm(x.data_ptr(), xs, rp, rs, hp, hs, weight.data_ptr(), n, d, eps, y.data_ptr(), ys,
@@ -544,7 +557,7 @@ def kv4_cache(pages, table, kv_heads: int, head_dim: int, page_size: int) -> Kv4
     size = kv4_page_bytes(kv_heads, head_dim, page_size)
     if not pages.is_contiguous() or _nbytes(pages) % size:
         raise UwError(UW_ERR_SHAPE, "uw_kv4_cache (pages are not whole pages of %d bytes)" % size)
-    if table.dim() != 2 or table.element_size() != 4 or (table.shape[1] > 1 and table.stride(1) != 1):
+    if table.dim() != 2 or table.dtype is not _types()[2] or (table.shape[1] > 1 and table.stride(1) != 1):
         raise UwError(UW_ERR_SHAPE, "uw_kv4_cache (table is not int32 [sequences, pages])")
     stride = table.stride(0) if table.shape[0] > 1 else table.shape[1]
     d = Kv4CacheDesc(pages.data_ptr(), table.data_ptr(), _nbytes(pages) // size, stride, table.shape[1],
@@ -559,7 +572,7 @@ def kv4_workspace_size(cache: Kv4Cache, q_heads: int) -> int:
 
 
 def _kv4_rows(t, n: int, heads: int, dim: int, name: str, what: str) -> Kv4Rows:
-    if t.shape != (n, heads, dim) or t.itemsize != 2:
+    if t.shape != (n, heads, dim) or t.dtype not in _types()[0]:
         raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s, not BF16 [%d, %d, %d])" % (what, name, tuple(t.shape),
                                                                                   t.dtype, n, heads, dim))
     ts, hs, ds = t.stride()
@@ -570,9 +583,9 @@ def _kv4_rows(t, n: int, heads: int, dim: int, name: str, what: str) -> Kv4Rows:
 
 def _kv4_seqs(cache, start, length, what):
     """start and length are int32 [sequences + 1] and [sequences] at least."""
-    n = cache.n_seqs
-    if not (start.is_contiguous() and length.is_contiguous() and start.itemsize == 4 == length.itemsize and start.numel() > n
-            and length.numel() >= n):
+    n, int32 = cache.n_seqs, _types()[2]
+    if not (start.is_contiguous() and length.is_contiguous() and start.dtype is int32 and length.dtype is int32
+            and start.numel() > n and length.numel() >= n):
         _refuse("start and length are not int32 of %d and %d values" % (n + 1, n), what)
 
 
@@ -594,7 +607,8 @@ def kv4_append(cache: Kv4Cache, start, length, q, k, v, q_out, cos, sin, ws, int
     rope_len = rot = 0
     if cos is not None:
         rope = cos.shape
-        if len(rope) != 2 or rope != sin.shape or cos.itemsize != 4 or sin.itemsize != 4:
+        fp32 = _types()[3]
+        if len(rope) != 2 or rope != sin.shape or cos.dtype is not fp32 or sin.dtype is not fp32:
             raise UwError(UW_ERR_SHAPE, "%s (cos and sin are not fp32 [positions, pairs])" % what)
         if not (cos.is_contiguous() and sin.is_contiguous()):
             raise UwError(UW_ERR_INVALID_ARG, "%s (cos and sin are not contiguous)" % what)
@@ -624,6 +638,8 @@ def kv4_attention(cache: Kv4Cache, start, length, q, out, ws, max_new: int = 0, 
     qr = _kv4_rows(q, n, heads, d.head_dim, "q", what)
     orow = _kv4_rows(out, n, heads, d.head_dim, "out", what)
     if lse is not None:
+        if lse.dtype is not _types()[3]:
+            raise UwError(UW_ERR_SHAPE, "%s (lse is not fp32)" % what)
         _refuse(_short((lse, 4 * n * heads, "lse")), what)
     _check(load().uw_kv4_attention(cache.ref, start.data_ptr(), length.data_ptr(), n, qr, heads, orow,
                                    None if lse is None else lse.data_ptr(), max_new, max_len, scale, causal, window,

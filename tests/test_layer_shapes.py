@@ -95,3 +95,48 @@ def test_append_takes_pairs_of_arguments_only_together(uw, fake, call, left_out)
     call[left_out] = None
     _refused(uw, INVALID, uw.kv4_append, **call)
     assert len(fake.calls) == 1
+
+
+def test_rmsnorm_refuses_other_types_of_the_same_size(uw, fake):
+    """16-bit floats that are not BF16, fp32 weights, 8-bit floats that are not e4m3, scales that are not fp32."""
+    x, w, y = _bits(4, 64), _bits(64), _bits(4, 64)
+    q, s = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.zeros(4)
+    uw.rmsnorm(x, w, y, residual=x, residual_out=y, stream=0)
+    uw.rmsnorm(x.view(torch.int16), w.view(torch.int16), y.view(torch.int16), stream=0)  # bits
+    for out in (q, q.view(torch.uint8), q.view(torch.int8)):
+        uw.rmsnorm(x, w, out, scale=s, stream=0)
+    assert len(fake.calls) == 5
+    _refused(uw, SHAPE, uw.rmsnorm, x.half(), w, y, stream=0)
+    _refused(uw, SHAPE, uw.rmsnorm, x, w, y.half(), stream=0)
+    _refused(uw, SHAPE, uw.rmsnorm, x, w, y, residual=x.half(), stream=0)
+    _refused(uw, SHAPE, uw.rmsnorm, x, w, y, residual=x, residual_out=x.half(), stream=0)
+    _refused(uw, SHAPE, uw.rmsnorm, x, w.float(), y, stream=0)
+    _refused(uw, SHAPE, uw.rmsnorm, x, w.half(), y, stream=0)
+    _refused(uw, SHAPE, uw.rmsnorm, x, w, q.view(torch.uint8).view(torch.float8_e5m2), scale=s, stream=0)
+    _refused(uw, SHAPE, uw.rmsnorm, x, w, q, scale=s.double(), stream=0)
+    _refused(uw, SHAPE, uw.rmsnorm, x, w, q, scale=s.int(), stream=0)
+    assert len(fake.calls) == 5
+
+
+def test_cache_calls_refuse_other_types_of_the_same_size(uw, fake, call):
+    def changed(name, f):
+        return dict(call, **{name: f(call[name])})
+
+    for name, f in (("q", torch.Tensor.half), ("k", torch.Tensor.half), ("v", torch.Tensor.half),
+                    ("q_out", torch.Tensor.half), ("cos", torch.Tensor.int), ("sin", torch.Tensor.int),
+                    ("start", torch.Tensor.float), ("length", torch.Tensor.float)):
+        with pytest.raises(uw.UwError):
+            uw.kv4_append(**changed(name, f))
+    with pytest.raises(uw.UwError):
+        uw.kv4_cache(call["cache"].pages, call["cache"].table.float(), 2, 64, 16)
+    c, start, length, ws = (call[n] for n in ("cache", "start", "length", "ws"))
+    q, kv = _bits(5, 4, 64), _bits(5, 2, 64)
+    _refused(uw, SHAPE, uw.kv4_read, c, start, length, kv.half(), kv, ws, stream=0)
+    _refused(uw, SHAPE, uw.kv4_read, c, start, length, kv, kv.half(), ws, stream=0)
+    _refused(uw, SHAPE, uw.kv4_attention, c, start, length, q.half(), q, ws, stream=0)
+    _refused(uw, SHAPE, uw.kv4_attention, c, start, length, q, q.half(), ws, stream=0)
+    _refused(uw, SHAPE, uw.kv4_attention, c, start, length, q, q, ws, lse=torch.zeros(20, dtype=torch.float64), stream=0)
+    _refused(uw, SHAPE, uw.kv4_attention, c, start, length, q, q, ws, lse=torch.zeros(40, dtype=torch.bfloat16), stream=0)
+    assert fake.calls == []
+    uw.kv4_attention(c, start, length, q.view(torch.int16), q, ws, lse=torch.zeros(20), stream=0)
+    assert len(fake.calls) == 1
