@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View v, const Ro
 // appended in 40 us, with one vector a warp 95; read in 10.5, with two 15).
 int rounds_of(int64_t tokens, int all, int most) {
     int n = 1;
-    while (2 * n <= most && n < all && tokens * ((all + 2 * n - 1) / (2 * n)) >= 152 * 4 * 2)
+    const int64_t two = 2 * 4 * int64_t(sm_count());  // warps, of four schedulers an SM
+    while (2 * n <= most && n < all && tokens * ((all + 2 * n - 1) / (2 * n)) >= two)
         n *= 2;
     return n;
 }
