@@ -59,3 +59,14 @@ def test_positions_up_to_31_bits(uw, new, page, short, causal):
         for h in range(hk):
             want = ref.bf16(ref.value(*pages.get(which, few[0], held - short, h)))[-new:]
             assert np.array_equal(got[:, h].cpu().numpy().view(np.uint16), want)
+
+
+@pytest.mark.parametrize("new,count,hq,hk,d", [([20, 40], 260, 32, 8, 128), ([9, 9, 9, 17], 400, 64, 4, 64),
+                                               ([33, 20, 128, 65, 25], 150, 12, 4, 128), ([8, 8, 30], 360, 128, 8, 64)])
+@pytest.mark.parametrize("window", [0, 1])
+def test_short_items_beside_full_ones(uw, new, count, hq, hk, d, window):
+    """Items of up to 128 rows, which the lower half of the kernel for many rows passes over, then ones of more,
+    many of both a CTA."""
+    new = [new[i % len(new)] for i in range(count)]
+    lens = [n + (11 * i) % 50 for i, n in enumerate(new)]
+    _run(uw, count + window, hq, hk, d, 16, new, lens, False, window, hints=False)
