@@ -575,7 +575,7 @@ def _kv4_rows(t, n: int, heads: int, dim: int, name: str, what: str) -> Kv4Rows:
     if t.shape != (n, heads, dim) or t.dtype not in _types()[0]:
         raise UwError(UW_ERR_SHAPE, "%s (%s is %s of %s, not BF16 [%d, %d, %d])" % (what, name, tuple(t.shape),
                                                                                   t.dtype, n, heads, dim))
-    ts, hs, ds = t.stride()
+    ts, hs, ds = t.stride() if n else (0, 0, 1)
     if ds != 1:
         raise UwError(UW_ERR_INVALID_ARG, "%s (%s: a head's values are not contiguous)" % (what, name))
     return Kv4Rows(t.data_ptr(), ts if n > 1 else 0, hs if heads > 1 else 0)

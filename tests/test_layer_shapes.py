@@ -140,3 +140,14 @@ def test_cache_calls_refuse_other_types_of_the_same_size(uw, fake, call):
     assert fake.calls == []
     uw.kv4_attention(c, start, length, q.view(torch.int16), q, ws, lse=torch.zeros(20), stream=0)
     assert len(fake.calls) == 1
+
+
+def test_no_tokens_have_no_strides(uw, fake, call):
+    """Views of no tokens, whatever their strides, are nothing to do; for tokens they have to be rows."""
+    c, start, length, ws = (call[n] for n in ("cache", "start", "length", "ws"))
+    odd = lambda n, h: torch.zeros(n, 64, h, dtype=torch.bfloat16).transpose(1, 2)  # noqa: E731
+    uw.kv4_append(c, start, length, odd(0, 4), odd(0, 2), odd(0, 2), odd(0, 4), None, None, ws, stream=0)
+    uw.kv4_read(c, start, length, odd(0, 2), odd(0, 2), ws, stream=0)
+    uw.kv4_attention(c, start, length, odd(0, 4), odd(0, 4), ws, stream=0)
+    assert len(fake.calls) == 3
+    _refused(uw, INVALID, uw.kv4_read, c, start, length, odd(1, 2), odd(1, 2), ws, stream=0)
