@@ -472,8 +472,9 @@ uw_status uw_rmsnorm_e4m3(const uint16_t *x_dev, int64_t x_stride, const uint16_
  * start, len and the table are device memory, so that a step can be captured
  * in a CUDA graph; the kernels check what they read there: a page outside the
  * pool, a length beyond table_width pages, a start outside the call's tokens
- * or a negative position to append to touches nothing and is reported by
- * uw_check_status as UW_ERR_CORRUPT.  Tokens of no sequence are left alone. */
+ * or a negative position to append to touches nothing of the cache and is
+ * reported by uw_check_status as UW_ERR_CORRUPT (the keys and values of a page
+ * outside the pool count as zeros).  Tokens of no sequence are left alone. */
 typedef struct {
     void *pages_dev;          /* n_pages pages, 16-byte aligned                   */
     const int32_t *table_dev; /* [n_seqs] rows of page numbers                    */
@@ -537,12 +538,20 @@ uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start_dev, const int
  *   q, out    q_heads heads (a multiple of kv_heads, UW_ERR_SHAPE otherwise).
  *   lse_dev   fp32 [n_tokens, q_heads]: log(sum exp(scale q.k)) (written), or NULL.
  *   max_new, max_len  upper bounds of the sequences' new tokens and lengths as
- *             the host knows them (0: not known).  They only choose how the work
- *             is split: a wrong one costs time, never the result.
+ *             the host knows them (0: not known).  They choose how the work is
+ *             split and, with the sequences' rows, which of two kernels takes
+ *             them: a wrong one costs time, and other bounds may give other bits
+ *             within the errors below.
  *   softmax_scale  0 for 1 / sqrt(head_dim); else from 2^-126 to 2^42
  *             (UW_ERR_UNSUPPORTED otherwise).
  *   ws_dev    at least uw_kv4_workspace_size bytes.
  * Softmax statistics and sums are fp32; the same call gives the same bits.
+ * In the product with V a probability times its value's scale is the sum of
+ * two BF16 values in the kernel for few rows (2^-16 of it) and one BF16 value in
+ * the kernel for many, as of prompts (2^-8 of it), so that o before its rounding
+ * is off by up to that much of sum p |v - z|, z = lo + 8 scale; the sum of p z is
+ * fp32.  A sequence of up to 32 rows (new tokens x query heads of a kv head) takes
+ * the former, unless it is the only one of its call and max_new says more.
  * Ranges: |q| below 2^79, scales of K (times softmax_scale) below 2^42 and of V
  * below 2^39; past them a result may not be finite.  A product q c (c: a code)
  * below 2^-41 may be taken as 0, and so may p scale of V (p: a probability)

@@ -41,7 +41,7 @@
 //   one token, 131071 keys       39.3 us (3.6 TB/s)
 //   one token, 1048576 keys      203 us (5.6 TB/s, of 6.8 for a copy); keys more cost at 6.1 TB/s
 //   64 tokens, 40 to 8192 keys   37 us (3.0 TB/s)
-//   one token, 257 keys          8.1 us
+//   one token, 257 keys          8.2 us
 // A call's first 6 us go to finding the shares and the first loads, its last
 // 6 to the joins, whose steps wait for one another's loads.
 #include <algorithm>

@@ -25,14 +25,19 @@
 //             works on one half of the keys, the products of the other half run.
 // Both products take the codes as they are (Codes in kv4_codes.cuh: integers in units
 // of 2^-133, no rounded K or V), the queries and probabilities scaled up
-// against them.  The running maximum is only raised when the probabilities of
-// 64 keys add up to more than 2^24 (BF16 and fp32 hold that without
-// loss), so that no score is compared and O is rarely rescaled.
+// against them.  The running maximum is only raised when some thread's sixteen
+// probabilities of a row and 64 keys add up to more than 2^24 (BF16 and fp32 hold
+// that without loss), so that no score is compared and O is rarely rescaled.
+// P s is rounded to one BF16 (the sum of the values' middles is fp32): its rest
+// as a second operand, as the kernel for few rows has it, would cost the softmax
+// warps, which bound this one, a difference, a packing and a store for each score.
+// Prompts are 0.0022 off from 64 bits in the 2-norm, with 0.0017 the output's
+// own rounding.
 //
 // Measured, 32 query and 8 kv heads of 128, causal:
-//   a prompt of 8192 tokens                 646 us (851 TFLOP/s, 0.45 of cuBLAS's burst)
-//   64 new tokens after 524288              600 us (916 TFLOP/s)
-//   a prompt of 2048 tokens                 78 us (440 TFLOP/s): to the first scores 9 us, an item's
+//   a prompt of 8192 tokens                 654 us (841 TFLOP/s, 0.44 of cuBLAS's burst)
+//   64 new tokens after 524288              605 us (908 TFLOP/s)
+//   a prompt of 2048 tokens                 81 us (427 TFLOP/s): to the first scores 9 us, an item's
 //                                           output 2, a join 3 to 8
 // Tried beside this: 32 keys at a time with the next scores on their way 778 us
 // (less to do at a time for each warp), no branch between scores and P 700,
@@ -59,7 +64,7 @@ constexpr int kItemCost = 3;
 constexpr int kMinShare = 4;
 constexpr int kSegs = 32;
 constexpr int kStages = 2, kParStages = 4;
-constexpr float kRaise = 16777216.f;                  // 2^24: headroom of the probabilities of 64 keys
+constexpr float kRaise = 16777216.f;                  // 2^24: headroom of a thread's 16 probabilities of 64 keys
 constexpr uint32_t kTmemCols = 512;
 
 enum Bar {
@@ -399,7 +404,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams &p, Shared &sh, ui
         // The warp's 32 rows lie like the rows of a matrix product's fragment: a
         // thread has rows g + 8 i (i < 4) and of them the key pairs 8 k + 2 t, so that a
         // pair's scales and offsets are read once for four rows.
-        float m[4], lim[4];      // maximum; the sum of 64 keys' probabilities from which it is raised
+        float m[4], lim[4];      // maximum; the sum of 16 probabilities from which it is raised
         uint64_t mm[4], qs[4];   // less the maximum, and the sum of q, in pairs
         uint64_t l2[4], z2[4];
 #pragma unroll
