@@ -4,8 +4,9 @@
 //   read    the new tokens' entries as BF16
 //
 // A decode step moves little (48 vectors of 256 bytes a token for 32 + 2 x 8
-// heads of 128): its time is latency.  For prompts instructions and memory are
-// about even.  A vector belongs to D / 8 lanes, 16 bytes each; a warp takes q heads
+// heads of 128): its time is latency.  For prompts it is loads in flight: issue
+// slots are 64% used, memory runs at 0.67 of a copy, and four CTAs of 64 registers a
+// thread are what an SM holds.  A vector belongs to D / 8 lanes, 16 bytes each; a warp takes q heads
 // of one token, or k and v heads, 32 / (D / 8) at a time, and finds the token's
 // place and its row of the rotation table once for all of them, while the
 // first vectors are on their way.  Minimum and maximum are joined by shuffles
