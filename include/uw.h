@@ -445,6 +445,42 @@ uw_status uw_rmsnorm_e4m3(const uint16_t *x_dev, int64_t x_stride, const uint16_
                           const uint16_t *weight_dev, int64_t n, int64_t d, float eps, uint8_t *q_dev,
                           int64_t q_stride, float *scale_dev, void *stream);
 
+/* uw_block_norm -- the norms around a block, its gate and scales, and the residual
+ * addition, of n rows of d, x being the block's output:
+ *     z = x, or with a post_weight x / sqrt(mean(x^2) + eps) * (post_weight + weight_offset)
+ *     h = bf16(residual_scale * residual + block_scale * gate * z)
+ *     y = bf16(h / sqrt(mean(h^2) + eps) * (weight + weight_offset))
+ * Means, roots and products are in fp32; h and y are rounded to BF16 once.
+ * (Sums of squares, of x and of h, past fp32's range give 0 or NaN, as in uw_rmsnorm; so
+ * may a product x * gate * (post_weight + weight_offset) past it.)
+ *   x_dev, residual_dev  BF16 rows, their strides apart.
+ *   residual_out_dev  h (written), or NULL; may be residual_dev or x_dev itself (in
+ *                 place), with that stride.
+ *   weight_dev, y_dev  d BF16 values, and BF16 rows (written); y_dev may be x_dev or
+ *                 residual_dev, but not residual_out_dev.  Both NULL if only h is wanted.
+ * Types, alignment, sizes and speed as for uw_rmsnorm (a gate of every row counts among the
+ * rows that lie alike).  n = 0 does nothing. */
+typedef struct {
+    const uint16_t *post_weight_dev; /* d BF16 values, or NULL: no norm after the block */
+    const uint16_t *gate_dev;        /* BF16, or NULL: none                             */
+    int64_t gate_stride;             /* 0: d values for all rows; else a gate of every
+                                        row, so far apart                               */
+    float weight_offset;             /* 0, or 1 for weights held as their distance from 1 */
+    float residual_scale, block_scale, eps;
+} uw_block;
+
+uw_status uw_block_norm(const uw_block *b, const uint16_t *x_dev, int64_t x_stride, const uint16_t *residual_dev,
+                        int64_t residual_stride, uint16_t *residual_out_dev, int64_t residual_out_stride,
+                        const uint16_t *weight_dev, int64_t n, int64_t d, uint16_t *y_dev, int64_t y_stride,
+                        void *stream);
+
+/* uw_block_norm_e4m3 -- the same with y in 8 bits and a scale for each row, as
+ * uw_rmsnorm_e4m3 (q_dev and weight_dev not NULL). */
+uw_status uw_block_norm_e4m3(const uw_block *b, const uint16_t *x_dev, int64_t x_stride, const uint16_t *residual_dev,
+                             int64_t residual_stride, uint16_t *residual_out_dev, int64_t residual_out_stride,
+                             const uint16_t *weight_dev, int64_t n, int64_t d, uint8_t *q_dev, int64_t q_stride,
+                             float *scale_dev, void *stream);
+
 /* The cache of keys and values of one layer, 4 bits a value, in pages.
  *
  * A page holds page_size tokens of every kv head.  The block of one (page,
@@ -520,6 +556,45 @@ uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start_dev, const i
                         const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *q_out, const uw_kv4_rows *k,
                         const uw_kv4_rows *v, const float *cos_dev, const float *sin_dev, int64_t rope_len,
                         int32_t rot_dim, int32_t interleaved, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* Positions on several axes (time, height and width of images and video, say):
+ * token t has the position pos[a * axis_stride + t] on axis a, and pair i of a vector's
+ * values turns by the position p on axis pair_axis[i], as
+ *     (a, b) -> bf16(a*cos[p][i] - b*sin[p][i]), bf16(b*cos[p][i] + a*sin[p][i])
+ * with pairs and roundings as in uw_kv4_append.  Positions are device memory;
+ * a token of which one (on any axis) is negative or at or past rope_len touches nothing and is reported
+ * by uw_check_status as UW_ERR_CORRUPT. */
+typedef struct {
+    const int32_t *pos_dev;
+    int64_t axis_stride;       /* int32 elements, at least the call's tokens        */
+    int32_t n_axes;            /* 1 .. 4                                            */
+    int32_t rot_dim;           /* a multiple of 16, at most head_dim                */
+    const uint8_t *pair_axis;  /* host memory: rot_dim / 2 numbers below n_axes, read by the call */
+    const float *cos_dev, *sin_dev;  /* fp32 [rope_len, rot_dim / 2], 16-byte aligned */
+    int64_t rope_len;
+    int32_t interleaved;       /* pairs (x[2i], x[2i + 1]) instead of (x[i], x[i + rot_dim / 2]) */
+} uw_rope;
+
+/* uw_rope_axes -- rotate q and k, without a cache.
+ *   q, k      q_heads and k_heads heads, read; q_out, k_out the rotated ones (written); may be q
+ *             and k themselves, and must not overlap them otherwise.  q and q_out NULL with
+ *             q_heads = 0, likewise k; one of the two is there (UW_ERR_SHAPE otherwise).
+ *   head_dim  any multiple of 8 (UW_ERR_UNSUPPORTED otherwise); values past rot_dim
+ *             (16 to 256 here) are copied.
+ *   ws_dev    a workspace of at least 256 bytes (the error word). */
+uw_status uw_rope_axes(const uw_rope *r, int64_t n_tokens, const uw_kv4_rows *q, int32_t q_heads,
+                       const uw_kv4_rows *q_out, const uw_kv4_rows *k, int32_t k_heads, const uw_kv4_rows *k_out,
+                       int32_t head_dim, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* uw_kv4_append_axes -- uw_kv4_append with the rotation of uw_rope.  A token's place in
+ * the cache still goes by start and len.
+ *   r         as above; rot_dim 0: no rotation, and positions are not looked at.
+ *   k_out     the rotated k (written; may be k), or NULL.
+ * Others as for uw_kv4_append. */
+uw_status uw_kv4_append_axes(const uw_kv4_cache *c, const int32_t *start_dev, const int32_t *len_dev, int64_t n_tokens,
+                             const uw_rope *r, const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *q_out,
+                             const uw_kv4_rows *k, const uw_kv4_rows *v, const uw_kv4_rows *k_out, void *ws_dev,
+                             size_t ws_bytes, void *stream);
 
 /* uw_kv4_read -- the new tokens' entries as the cache holds them: k and v
  * [n_tokens, kv_heads, head_dim] (written) = bf16(lo + c * scale).  With

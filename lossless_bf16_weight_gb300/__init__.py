@@ -80,11 +80,26 @@ class Kv4Rows(ctypes.Structure):
     _fields_ = [("dev", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class Block(ctypes.Structure):
+    """The norm after a block, its gate and scales (uw_block)."""
+    _fields_ = [("post_weight_dev", ctypes.c_void_p), ("gate_dev", ctypes.c_void_p), ("gate_stride", ctypes.c_int64),
+                ("weight_offset", ctypes.c_float), ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
+class Rope(ctypes.Structure):
+    """Positions on several axes and the tables they turn by (uw_rope)."""
+    _fields_ = [("pos_dev", ctypes.c_void_p), ("axis_stride", ctypes.c_int64), ("n_axes", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("pair_axis", ctypes.c_char_p), ("cos_dev", ctypes.c_void_p),
+                ("sin_dev", ctypes.c_void_p), ("rope_len", ctypes.c_int64), ("interleaved", ctypes.c_int32)]
+
+
 _lib = None
 
 # (name, restype, argtypes) of every symbol in include/uw.h
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _F32, _CACHE, _ROWS = ctypes.c_float, ctypes.POINTER(Kv4CacheDesc), ctypes.POINTER(Kv4Rows)
+_BLOCK, _ROPE = ctypes.POINTER(Block), ctypes.POINTER(Rope)
 SIGNATURES = [
     ("uw_compress", ctypes.c_int, [_P, _I64, _I64, _P, ctypes.POINTER(_SZ)]),
     ("uw_blob_info", ctypes.c_int, [_P, _SZ, ctypes.POINTER(Desc)]),
@@ -116,6 +131,11 @@ SIGNATURES = [
                                                       ctypes.POINTER(_SZ)]),
     ("uw_rmsnorm", ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _F32, _P, _I64, _P]),
     ("uw_rmsnorm_e4m3", ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _F32, _P, _I64, _P, _P]),
+    ("uw_block_norm", ctypes.c_int, [_BLOCK, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _P]),
+    ("uw_block_norm_e4m3", ctypes.c_int, [_BLOCK, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _P]),
+    ("uw_rope_axes", ctypes.c_int, [_ROPE, _I64, _ROWS, _I32, _ROWS, _ROWS, _I32, _ROWS, _I32, _P, _SZ, _P]),
+    ("uw_kv4_append_axes", ctypes.c_int, [_CACHE, _P, _P, _I64, _ROPE, _ROWS, _I32, _ROWS, _ROWS, _ROWS, _ROWS, _P,
+                                          _SZ, _P]),
     ("uw_kv4_page_bytes", ctypes.c_int, [_I32, _I32, _I32, ctypes.POINTER(_SZ)]),
     ("uw_kv4_workspace_size", ctypes.c_int, [_CACHE, _I32, ctypes.POINTER(_SZ)]),
     ("uw_kv4_append", ctypes.c_int, [_CACHE, _P, _P, _I64, _ROWS, _I32, _ROWS, _ROWS, _ROWS, _P, _P, _I64, _I32,
@@ -537,6 +557,74 @@ def rmsnorm(x, weight, y, eps: float = 1e-5, residual=None, residual_out=None, s
                                       ys, scale.data_ptr(), _stream(stream)), what)
 
 
+def _here(what: str, *tensors):
+    """Refuses tensors that are not on the current CUDA device, whose stream the call would be made on."""
+    for t in tensors:
+        if t is not None and (t.get_device() < 0 or t.get_device() != _current_device()):
+            raise UwError(UW_ERR_INVALID_ARG, "%s (a tensor is on %s, not on the current CUDA device)" % (what, t.device))
+
+
+def _current_device() -> int:
+    """torch.cuda.current_device() without the check that CUDA is initialised (it is, once there are tensors)."""
+    global _current_device
+    import torch
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device()
+
+
+def block_norm(x, residual, weight, residual_out, y, eps: float = 1e-5, post_weight=None, gate=None,
+               residual_scale: float = 1.0, block_scale: float = 1.0, weight_offset: float = 0.0, scale=None,
+               stream=None):
+    """uw_block_norm: z = x, with post_weight its norm times post_weight + weight_offset; h = bf16(residual_scale *
+    residual + block_scale * gate * z) into residual_out (or None); y = the norm of h times weight + weight_offset in BF16
+    (weight and y None: only h).  With `scale` (fp32, one for each row): uw_block_norm_e4m3, y holds e4m3 bytes.
+    Tensors are [n, d], whose rows may be strided, or [d]; gate is [d] for all rows, or like x."""
+    what = "uw_block_norm" if scale is None else "uw_block_norm_e4m3"
+    shape = x.shape
+    if not 1 <= len(shape) <= 2:
+        raise UwError(UW_ERR_SHAPE, "%s (x is %s, neither [n, d] nor [d])" % (what, tuple(shape)))
+    d, n = shape[-1], shape[0] if len(shape) == 2 else 1
+    bf16, e4m3, _, fp32 = _types()
+    xs, rs = _row_stride(x, shape, bf16, "x", what), _row_stride(residual, shape, bf16, "residual", what)
+    hp = yp = wp = gp = pp = None
+    hs = ys = gs = 0
+    if residual_out is not None:
+        hp, hs = residual_out.data_ptr(), _row_stride(residual_out, shape, bf16, "residual_out", what)
+    if (weight is None) != (y is None):
+        raise UwError(UW_ERR_INVALID_ARG, "%s (weight and y: both or neither)" % what)
+    if y is not None:
+        yp, ys = y.data_ptr(), _row_stride(y, shape, bf16 if scale is None else e4m3, "y", what)
+    if gate is not None:
+        gp = gate.data_ptr()
+        if gate.dim() == 2:
+            gs = _row_stride(gate, shape, bf16, "gate", what)
+        elif gate.dim() != 1 or gate.dtype not in bf16:
+            raise UwError(UW_ERR_SHAPE, "%s (gate is %s of %s)" % (what, tuple(gate.shape), gate.dtype))
+        else:
+            _refuse(_short((gate, 2 * d, "gate")), what)
+    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
+        if t is not None:
+            if t.dtype not in bf16:
+                raise UwError(UW_ERR_SHAPE, "%s (%s is not BF16)" % (what, name))
+            _refuse(_short((t, 2 * d, name)), what)
+    if weight is not None:
+        wp = weight.data_ptr()
+    if post_weight is not None:
+        pp = post_weight.data_ptr()
+    b = Block(pp, gp, gs, weight_offset, residual_scale, block_scale, eps)
+    if scale is not None:
+        if scale.dtype is not fp32:
+            raise UwError(UW_ERR_SHAPE, "%s (scale is not fp32)" % what)
+        _refuse(_short((scale, 4 * n, "scale")), what)
+    _here(what, x, residual, weight, residual_out, y, post_weight, gate, scale)
+    if scale is None:
+        _check(load().uw_block_norm(b, x.data_ptr(), xs, residual.data_ptr(), rs, hp, hs, wp, n, d, yp, ys,
+                                    _stream(stream)), what)
+    else:
+        _check(load().uw_block_norm_e4m3(b, x.data_ptr(), xs, residual.data_ptr(), rs, hp, hs, wp, n, d, yp, ys,
+                                         scale.data_ptr(), _stream(stream)), what)
+
+
 class Kv4Cache:
     """A layer's cache: its descriptor with the tensors behind it (made by kv4_cache)."""
 
@@ -616,6 +704,66 @@ def kv4_append(cache: Kv4Cache, start, length, q, k, v, q_out, cos, sin, ws, int
     _check(load().uw_kv4_append(cache.ref, start.data_ptr(), length.data_ptr(), n, qr, heads, orow, kr, vr,
                                 cos.data_ptr() if rot else None, sin.data_ptr() if rot else None, rope_len, rot,
                                 interleaved, ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
+
+
+def _rope(pos, pair_axis, cos, sin, n: int, interleaved: bool, what: str) -> Rope:
+    _, _, int32, fp32 = _types()
+    if pos.dim() != 2 or pos.shape[1] != n or pos.dtype is not int32 or (n > 1 and pos.stride(1) != 1):
+        raise UwError(UW_ERR_SHAPE, "%s (pos is not int32 [axes, %d])" % (what, n))
+    rope = cos.shape
+    if len(rope) != 2 or rope != sin.shape or cos.dtype is not fp32 or sin.dtype is not fp32 or rope[1] != len(pair_axis):
+        raise UwError(UW_ERR_SHAPE, "%s (cos and sin are not fp32 [positions, pairs])" % what)
+    if not (cos.is_contiguous() and sin.is_contiguous()):
+        raise UwError(UW_ERR_INVALID_ARG, "%s (cos and sin are not contiguous)" % what)
+    return Rope(pos.data_ptr(), pos.stride(0) if pos.shape[0] > 1 else n, pos.shape[0], 2 * rope[1], pair_axis,
+                cos.data_ptr(), sin.data_ptr(), rope[0], interleaved)
+
+
+def _head_rows(t, n: int, dim: int, name: str, what: str):
+    """Heads and rows of [n, heads, dim]; (0, None) for None."""
+    if t is None:
+        return 0, None
+    heads = t.shape[1] if t.dim() == 3 else -1
+    return heads, _kv4_rows(t, n, heads, dim, name, what)
+
+
+def rope_axes(q, k, pos, pair_axis: bytes, q_out, k_out, cos, sin, ws, interleaved: bool = False, stream=None):
+    """uw_rope_axes: rotate q and k [tokens, heads, head_dim] (either may be None) into q_out and k_out by the positions
+    pos, int32 [axes, tokens]; pair i turns by axis pair_axis[i].  cos and sin fp32 [positions, pairs]."""
+    what = "uw_rope_axes"
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise UwError(UW_ERR_INVALID_ARG, "%s (q and q_out, k and k_out: both or neither)" % what)
+    some = k if q is None else q
+    if some is None or some.dim() != 3:
+        raise UwError(UW_ERR_SHAPE, "%s (q and k are not [tokens, heads, head_dim])" % what)
+    n, d = some.shape[0], some.shape[2]
+    hq, qr = _head_rows(q, n, d, "q", what)
+    hk, kr = _head_rows(k, n, d, "k", what)
+    qo = None if q is None else _kv4_rows(q_out, n, hq, d, "q_out", what)
+    ko = None if k is None else _kv4_rows(k_out, n, hk, d, "k_out", what)
+    r = _rope(pos, pair_axis, cos, sin, n, interleaved, what)
+    _here(what, q, k, q_out, k_out, pos, cos, sin, ws)
+    _check(load().uw_rope_axes(r, n, qr, hq, qo, kr, hk, ko, d, ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
+
+
+def kv4_append_axes(cache: Kv4Cache, start, length, pos, pair_axis: bytes, q, k, v, q_out, cos, sin, ws, k_out=None,
+                    interleaved: bool = False, stream=None):
+    """uw_kv4_append_axes: kv4_append with positions on several axes (pos and pair_axis as for rope_axes); k_out, if
+    given, takes the rotated k."""
+    what, d = "uw_kv4_append_axes", cache
+    n = k.shape[0]
+    _kv4_seqs(cache, start, length, what)
+    kr = _kv4_rows(k, n, d.kv_heads, d.head_dim, "k", what)
+    vr = _kv4_rows(v, n, d.kv_heads, d.head_dim, "v", what)
+    if (q is None) != (q_out is None):
+        raise UwError(UW_ERR_INVALID_ARG, "%s (q and q_out: both or neither)" % what)
+    hq, qr = _head_rows(q, n, d.head_dim, "q", what)
+    qo = None if q is None else _kv4_rows(q_out, n, hq, d.head_dim, "q_out", what)
+    ko = None if k_out is None else _kv4_rows(k_out, n, d.kv_heads, d.head_dim, "k_out", what)
+    r = _rope(pos, pair_axis, cos, sin, n, interleaved, what)
+    _here(what, cache.pages, cache.table, start, length, pos, q, k, v, q_out, k_out, cos, sin, ws)
+    _check(load().uw_kv4_append_axes(cache.ref, start.data_ptr(), length.data_ptr(), n, r, qr, hq, qo, kr, vr, ko,
+                                     ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
 
 
 def kv4_read(cache: Kv4Cache, start, length, k, v, ws, stream=None):

@@ -1,0 +1,320 @@
+// The norms around a block of a layer, with its gate, scales and residual sum:
+//     z = x, or x (mean(x^2) + eps)^(-1/2) (wp + off)
+//     h = bf16(rs r + bs g z)
+//     y = h (mean(h^2) + eps)^(-1/2) (w + off)
+// with y in BF16, or in e4m3 with a scale for each row, or left out.
+//
+// Memory bound: x, r (and a gate of every row) are read once, h and y written
+// once, in 16-byte steps; a row stays in registers through its two sums, x in fp32 and r as it
+// came.  One warp a row up to 1024 values, one CTA a row above, rows that may begin
+// anywhere as in norm.cu; rows that are not alike or have more than 16384 values are
+// taken value by value, with h read back (or made again) for the second norm.
+#include <cmath>
+
+#include "norm.cuh"
+
+namespace uw {
+
+namespace {
+
+struct BlockParams {
+    const uint16_t *x, *r, *g, *wp, *w;
+    uint16_t *h;
+    void *y;
+    float *scale;
+    int64_t xs, rs, gs, hs, ys, n, d;  // gs 0: one gate for all rows
+    float eps, off, r_scale, b_scale;
+};
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        f[2 * k] = bf16_lo(a[k]);
+        f[2 * k + 1] = bf16_hi(a[k]);
+    }
+}
+
+// A row kept in registers by T threads (a warp or a CTA), V vectors of 8 each.
+// kOdd: the row begins anywhere (norm.cuh).
+template <int V, bool k8, bool kWarp, bool kOdd>
+__device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int t, int T, float *slots) {
+    const int before = kOdd ? int(reinterpret_cast<uintptr_t>(p.x + row * p.xs) >> 1) & 7 : 0;
+    auto first = [&](int v) { return 8 * (int64_t(v) * T + t) - before; };
+    auto weights = [&](const uint16_t *w, int v) { return load8_weights<kOdd, kWarp>(w, first(v), p.d); };
+    auto gates = [&](int v) {
+        return p.gs ? load8<kOdd>(p.g, p.gs, p.n, p.d, row, first(v)) : weights(p.g, v);
+    };
+    float f[V][8];
+    // all loads before the first store, which could otherwise not pass it (short rows of their
+    // own weights too; where a row begins anywhere, those are loaded where they are used)
+    uint4 r[V], a[V], g[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        unpack8(load8<kOdd>(p.x, p.xs, p.n, p.d, row, first(v)), f[v]);
+        r[v] = load8<kOdd>(p.r, p.rs, p.n, p.d, row, first(v));
+    }
+    if constexpr (!kOdd) {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            if (p.g)
+                g[v] = gates(v);
+            if (p.wp)
+                a[v] = weights(p.wp, v);
+        }
+    }
+    float c = p.b_scale;  // of x
+    if (p.wp) {
+        float ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; v++)
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                ss = fmaf(f[v][k], f[v][k], ss);
+        ss = kWarp ? warp_sum(ss) : cta_reduce<false>(ss, slots);
+        c *= rsqrtf(ss / float(p.d) + p.eps);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        if (p.g) {
+            float gf[8];
+            unpack8(kOdd ? gates(v) : g[v], gf);
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                f[v][k] *= gf[k];
+        }
+        if (p.wp) {
+            float wf[8];
+            unpack8(kOdd ? weights(p.wp, v) : a[v], wf);
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                f[v][k] *= wf[k] + p.off;
+        }
+        float rf[8];
+        unpack8(r[v], rf);
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            h[k] = bf16_pack(fmaf(f[v][2 * k], c, p.r_scale * rf[2 * k]),
+                             fmaf(f[v][2 * k + 1], c, p.r_scale * rf[2 * k + 1]));
+        if constexpr (kOdd) {  // what is not the row's counts for nothing, whatever the scales make of it
+            const int64_t i = first(v);
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                h[k] &= (i + 2 * k >= 0 && i + 2 * k < p.d ? 0xffffu : 0u) |
+                        (i + 2 * k + 1 >= 0 && i + 2 * k + 1 < p.d ? 0xffff0000u : 0u);
+        }
+        if (p.h)
+            store8<kOdd>(p.h + row * p.hs, first(v), p.d, h);
+        unpack8(make_uint4(h[0], h[1], h[2], h[3]), f[v]);
+        if (!kOdd && first(v) >= p.d) {
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                f[v][k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            ss = fmaf(f[v][k], f[v][k], ss);
+    }
+    if (!p.y)
+        return;
+    if constexpr (!kOdd) {
+#pragma unroll
+        for (int v = 0; v < V; v++)
+            a[v] = weights(p.w, v);
+    }
+    ss = kWarp ? warp_sum(ss) : cta_reduce<false>(ss, slots + 32);
+    const float rstd = rsqrtf(ss / float(p.d) + p.eps);
+    float top = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        float wf[8];
+        unpack8(kOdd ? weights(p.w, v) : a[v], wf);
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            f[v][k] *= wf[k] + p.off;
+        if constexpr (k8) {
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                top = max_nan(top, fabsf(f[v][k]));
+        } else {
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                y[k] = bf16_pack(f[v][2 * k] * rstd, f[v][2 * k + 1] * rstd);
+            store8<kOdd>(static_cast<uint16_t *>(p.y) + row * p.ys, first(v), p.d, y);
+        }
+    }
+    if constexpr (k8) {
+        const RowScale s(kWarp ? warp_max(top) : cta_reduce<true>(top, slots + 64), rstd);
+        if (t == 0)
+            p.scale[row] = s.scale;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            uint32_t q[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+                q[k] = to_e4m3x2(s.of(f[v][4 * k]), s.of(f[v][4 * k + 1])) |
+                       uint32_t(to_e4m3x2(s.of(f[v][4 * k + 2]), s.of(f[v][4 * k + 3]))) << 16;
+            store8<kOdd>(static_cast<uint8_t *>(p.y) + row * p.ys, first(v), p.d, q);
+        }
+    }
+}
+
+template <int V, bool k8, bool kOdd>
+__global__ void __launch_bounds__(256) block_warp_kernel(const BlockParams p) {
+    grid_dep_launch();
+    grid_dep_wait();
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row < p.n)
+        block_row<V, k8, true, kOdd>(p, row, threadIdx.x & 31, 32, nullptr);
+}
+
+// (Rows of 16384 that begin anywhere lie on up to 2049 steps: 513 threads.)
+template <int V, bool k8, bool kOdd>
+__global__ void __launch_bounds__(V == 2 ? 256 : 544) block_cta_kernel(const BlockParams p) {
+    __shared__ float slots[96];
+    grid_dep_launch();
+    grid_dep_wait();
+    block_row<V, k8, false, kOdd>(p, blockIdx.x, threadIdx.x, blockDim.x, slots);
+}
+
+// Rows of any kind, value by value.
+template <bool k8>
+__global__ void __launch_bounds__(512) block_any_kernel(const BlockParams p) {
+    __shared__ float slots[96];
+    grid_dep_launch();
+    grid_dep_wait();
+    const int64_t row = blockIdx.x;
+    const uint16_t *const x = p.x + row * p.xs, *const r = p.r + row * p.rs;
+    const uint16_t *const g = p.g ? p.g + row * p.gs : nullptr;
+    uint16_t *const h = p.h ? p.h + row * p.hs : nullptr;
+    float c = p.b_scale;
+    if (p.wp) {
+        float ss = 0.f;
+        for (int64_t i = threadIdx.x; i < p.d; i += blockDim.x) {
+            const float f = bf16_lo(x[i]);
+            ss = fmaf(f, f, ss);
+        }
+        c *= rsqrtf(cta_reduce<false>(ss, slots) / float(p.d) + p.eps);
+    }
+    auto made = [&](int64_t i) {
+        float f = bf16_lo(x[i]);
+        if (g)
+            f *= bf16_lo(g[i]);
+        if (p.wp)
+            f *= bf16_lo(p.wp[i]) + p.off;
+        return __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(f, c, p.r_scale * bf16_lo(r[i]))));
+    };
+    float ss = 0.f;
+    for (int64_t i = threadIdx.x; i < p.d; i += blockDim.x) {
+        const uint16_t b = made(i);
+        if (h)
+            h[i] = b;
+        const float f = bf16_lo(b);
+        ss = fmaf(f, f, ss);
+    }
+    if (!p.y)
+        return;
+    // from here on x or r may lie under h: what was written is read back
+    auto value = [&](int64_t i) { return bf16_lo(h ? h[i] : made(i)); };
+    const float rstd = rsqrtf(cta_reduce<false>(ss, slots + 32) / float(p.d) + p.eps);
+    float top = 0.f;
+    if constexpr (k8) {
+        for (int64_t i = threadIdx.x; i < p.d; i += blockDim.x)
+            top = max_nan(top, fabsf(value(i) * (bf16_lo(p.w[i]) + p.off)));
+        top = cta_reduce<true>(top, slots + 64);
+    }
+    const RowScale s(top, rstd);
+    if (k8 && threadIdx.x == 0)
+        p.scale[row] = s.scale;
+    for (int64_t i = threadIdx.x; i < p.d; i += blockDim.x) {
+        const float u = value(i) * (bf16_lo(p.w[i]) + p.off);
+        if constexpr (k8)
+            static_cast<uint8_t *>(p.y)[row * p.ys + i] = to_e4m3(s.of(u));
+        else
+            static_cast<uint16_t *>(p.y)[row * p.ys + i] = __bfloat16_as_ushort(__float2bfloat16_rn(u * rstd));
+    }
+}
+
+template <bool k8, bool kOdd>
+cudaError_t launch_rows(const BlockParams &p, cudaStream_t st) {
+    const int vecs = int((p.d + (kOdd ? 14 : 7)) / 8);  // vectors of a row, wherever it begins
+    if (vecs <= kWarpDim / 8) {
+        const dim3 grid(unsigned((p.n + 7) / 8)), block(256);
+        if (vecs <= 32)
+            return launch_overlapped(block_warp_kernel<1, k8, kOdd>, grid, block, 0, st, p);
+        if (vecs <= 64)
+            return launch_overlapped(block_warp_kernel<2, k8, kOdd>, grid, block, 0, st, p);
+        return launch_overlapped(block_warp_kernel<4, k8, kOdd>, grid, block, 0, st, p);
+    }
+    const dim3 grid(static_cast<unsigned>(p.n));
+    if (vecs <= 512)
+        return launch_overlapped(block_cta_kernel<2, k8, kOdd>, grid, dim3((vecs + 63) / 64 * 32), 0, st, p);
+    return launch_overlapped(block_cta_kernel<4, k8, kOdd>, grid, dim3((vecs + 127) / 128 * 32), 0, st, p);
+}
+
+template <bool k8>
+cudaError_t launch_block(const BlockParams &p, bool vec, bool alike, cudaStream_t st) {
+    if (p.d > kMaxVecDim || !alike)
+        return launch_overlapped(block_any_kernel<k8>, dim3(unsigned(p.n)), dim3(512), 0, st, p);
+    return vec ? launch_rows<k8, false>(p, st) : launch_rows<k8, true>(p, st);
+}
+
+uintptr_t bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+uw_status run_block(const uw_block *b, const uint16_t *x, int64_t xs, const uint16_t *r, int64_t rs, uint16_t *h,
+                    int64_t hs, const uint16_t *w, int64_t n, int64_t d, void *y, int64_t ys, float *scale, bool k8,
+                    void *stream) {
+    if (!b || n < 0 || !(b->eps >= 0.f) || !std::isfinite(b->weight_offset) || !std::isfinite(b->residual_scale) ||
+        !std::isfinite(b->block_scale))
+        return UW_ERR_INVALID_ARG;
+    // no rows need no buffers (those of empty tensors are null)
+    if (n != 0 && (!x || !r || !w != !y || (!y && (!h || k8)) || (k8 && !scale)))
+        return UW_ERR_INVALID_ARG;
+    if (d <= 0)
+        return UW_ERR_SHAPE;
+    if (n > 0x7fffffff || d > 0x7fffffff)
+        return UW_ERR_UNSUPPORTED;
+    const uint16_t *const g = b->gate_dev;
+    const int64_t gs = g && b->gate_stride ? b->gate_stride : 0;
+    if ((n > 1 && (xs < d || rs < d || (y && ys < d) || (h && hs < d))) || gs < 0 || (gs && n > 1 && gs < d))
+        return UW_ERR_INVALID_ARG;
+    if (n == 0)
+        return UW_OK;
+    if (((bits(x) | bits(r) | bits(h) | bits(w) | bits(g) | bits(b->post_weight_dev)) & 1) || (!k8 && (bits(y) & 1)) ||
+        (k8 && (bits(scale) & 3)))
+        return UW_ERR_INVALID_ARG;
+    // where a tensor's rows begin, in values: eight of them are 16 bytes (8 of e4m3)
+    const uint64_t x0 = bits(x) / 2;
+    auto as_x = [&](uint64_t first, int64_t stride) {
+        return (first - x0) % 8 == 0 && (n == 1 || (stride - xs) % 8 == 0);
+    };
+    const bool alike = as_x(bits(r) / 2, rs) && (!y || as_x(bits(y) / (k8 ? 1 : 2), ys)) &&
+                       (!h || as_x(bits(h) / 2, hs)) && (!gs || as_x(bits(g) / 2, gs));
+    // (what is not given is null and on every step)
+    const bool vec = d % 8 == 0 && x0 % 8 == 0 && (n == 1 || xs % 8 == 0) &&
+                     ((bits(w) | bits(b->post_weight_dev) | (gs ? 0 : bits(g))) & 15) == 0;
+    const BlockParams p{x,  r,  g,  b->post_weight_dev, w, h, y, scale, xs, rs, gs, hs, ys, n, d, b->eps,
+                        b->weight_offset, b->residual_scale, b->block_scale};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return (k8 ? launch_block<true>(p, vec, alike, st) : launch_block<false>(p, vec, alike, st)) == cudaSuccess
+               ? UW_OK
+               : UW_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace uw
+
+extern "C" uw_status uw_block_norm(const uw_block *b, const uint16_t *x, int64_t xs, const uint16_t *r, int64_t rs,
+                                   uint16_t *h, int64_t hs, const uint16_t *w, int64_t n, int64_t d, uint16_t *y,
+                                   int64_t ys, void *stream) {
+    return uw::run_block(b, x, xs, r, rs, h, hs, w, n, d, y, ys, nullptr, false, stream);
+}
+
+extern "C" uw_status uw_block_norm_e4m3(const uw_block *b, const uint16_t *x, int64_t xs, const uint16_t *r,
+                                        int64_t rs, uint16_t *h, int64_t hs, const uint16_t *w, int64_t n, int64_t d,
+                                        uint8_t *q, int64_t qs, float *scale, void *stream) {
+    return uw::run_block(b, x, xs, r, rs, h, hs, w, n, d, q, qs, scale, true, stream);
+}

@@ -23,6 +23,7 @@
 #include "kernels.h"
 #include "kv4.cuh"
 #include "kv4_host.h"
+#include "rope.cuh"
 
 namespace uw {
 
@@ -37,6 +38,9 @@ struct AppendParams {
     int32_t q_units, kv_units;    // warps a token: of q heads, and of k and v heads
     int32_t q_rounds, kv_rounds;  // heads such a warp takes one after the other (times 32 / (D / 8))
     float minus_zero;             // -0, which the compiler does not know (rotate())
+    // positions on several axes (kAxes): each token's, and the rotated k in BF16, if wanted
+    Axes axes;
+    Rows ko;
 };
 
 // Vectors a lane has on their way (8143 and 64 tokens: 2 41.8 and 3.3 us, 4 41.8 and 4.4, 1 45.8 and 3.3).
@@ -109,32 +113,9 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[4], uint32_t *p
     return codes;
 }
 
-// A lane's share of a token's rotation: its eight values are one side of
-// eight pairs (half split: the other side lies rot / 2 values on or back), or four
-// whole pairs (interleaved).
-struct Rotation {
-    uint64_t c[4], s[4];  // cosines and sines of two values each, the sines with the sign of the side
-    bool on, interleaved;
-};
-
-// Rotated values of a lane, own c + other s: own ones in a, the other side's in
-// b (half split).  Each product is rounded and then the sum: a product is a
-// fused multiply-add to a -0 that comes with the call, as the assembler joins
-// a plain product, and one with a -0 that it sees, with the sum.
-__device__ __forceinline__ void rotate(const Rotation &r, uint64_t zero, uint32_t (&a)[4], const uint4 &other) {
-    if (!r.on)
-        return;
-    const uint32_t b[4] = {other.x, other.y, other.z, other.w};
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const float u = bf16_lo(a[k]), w = bf16_hi(a[k]);
-        const uint64_t o = r.interleaved ? pair2(w, u) : pair2(bf16_lo(b[k]), bf16_hi(b[k]));
-        const float2 y = unpair(add2(fma2(pair2(u, w), r.c[k], zero), fma2(o, r.s[k], zero)));
-        a[k] = bf16_pack(y.x, y.y);
-    }
-}
-
-template <int D>
+// kAxes: a pair turns by its token's position on the pair's axis, not by the
+// place in the sequence, and k_out, if there is one, takes the rotated k.
+template <int D, bool kAxes>
 __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p) {
     constexpr int L = D / 8;       // lanes of a vector
     constexpr int G = 32 / L;      // vectors a warp takes at once
@@ -180,30 +161,32 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
     if (t < q.t0 || t >= int64_t(q.t0) + q.n)
         return;  // a token of no sequence
     const int32_t pos = q.len - q.n + (int32_t(t) - q.t0);
-    if (pos < 0 || (p.rot && pos >= p.rope_len)) {
+    AxesAt turn;
+    if (pos < 0 || (p.rot && (kAxes ? !turn.find(p.axes, t, p.rope_len) : pos >= p.rope_len))) {
         if (lane == 0)
             atomicOr(v.status, kStatusBadCache);
         return;
     }
-    if (r.on) {
+    if (kAxes && r.on) {
+        const int j = p.interleaved ? 4 * c : second ? i0 - half : i0;
+        const float4 c0 = turn.four(p.axes, p.cos, half, j), s0 = turn.four(p.axes, p.sin, half, j);
+        if (p.interleaved) {
+            r.of_pairs(c0, s0);
+        } else {
+            r.of_side(c0, s0, 0, second);
+            r.of_side(turn.four(p.axes, p.cos, half, j + 4), turn.four(p.axes, p.sin, half, j + 4), 1, second);
+        }
+    } else if (r.on) {
         const int64_t row = int64_t(pos) * half;
         if (p.interleaved) {
-            const float4 cs = *reinterpret_cast<const float4 *>(p.cos + row + 4 * c);
-            const float4 sn = *reinterpret_cast<const float4 *>(p.sin + row + 4 * c);
-            r.c[0] = pair2(cs.x, cs.x), r.c[1] = pair2(cs.y, cs.y);
-            r.c[2] = pair2(cs.z, cs.z), r.c[3] = pair2(cs.w, cs.w);
-            r.s[0] = pair2(-sn.x, sn.x), r.s[1] = pair2(-sn.y, sn.y);
-            r.s[2] = pair2(-sn.z, sn.z), r.s[3] = pair2(-sn.w, sn.w);
+            r.of_pairs(*reinterpret_cast<const float4 *>(p.cos + row + 4 * c),
+                       *reinterpret_cast<const float4 *>(p.sin + row + 4 * c));
         } else {
-            const float sign = second ? 1.f : -1.f;
             const int j = second ? i0 - half : i0;
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const float4 cs = *reinterpret_cast<const float4 *>(p.cos + row + j + 4 * k);
-                const float4 sn = *reinterpret_cast<const float4 *>(p.sin + row + j + 4 * k);
-                r.c[2 * k] = pair2(cs.x, cs.y), r.c[2 * k + 1] = pair2(cs.z, cs.w);
-                r.s[2 * k] = pair2(sign * sn.x, sign * sn.y), r.s[2 * k + 1] = pair2(sign * sn.z, sign * sn.w);
-            }
+            for (int k = 0; k < 2; k++)
+                r.of_side(*reinterpret_cast<const float4 *>(p.cos + row + j + 4 * k),
+                          *reinterpret_cast<const float4 *>(p.sin + row + j + 4 * k), k, second);
         }
     }
 
@@ -232,6 +215,8 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
     const int slot = pos & ((1 << v.page_log2) - 1);
     const int64_t block = int64_t(D + 8) << v.page_log2;
     for (int n0 = 0;;) {
+        if constexpr (kAxes)
+            __syncwarp();  // k_out may be k
 #pragma unroll
         for (int n = 0; n < kAhead; n++) {
             const int j = j0 + (n0 + n) * G;
@@ -241,6 +226,9 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
             uint32_t a[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
             if (!is_v)
                 rotate(r, zero, a, o[n]);
+            if (kAxes && p.ko.p && !is_v)
+                *reinterpret_cast<uint4 *>(p.ko.p + t * p.ko.ts + j * p.ko.hs + i0) =
+                    make_uint4(a[0], a[1], a[2], a[3]);
             uint32_t params;
             const uint32_t codes = quantise<D>(a, &params);
             if (j < all) {
@@ -342,11 +330,12 @@ int rounds_of(int64_t tokens, int all, int most) {
 
 using namespace uw;
 
-extern "C" uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start, const int32_t *len, int64_t n_tokens,
-                                   const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *q_out,
-                                   const uw_kv4_rows *k, const uw_kv4_rows *v, const float *cos, const float *sin,
-                                   int64_t rope_len, int32_t rot_dim, int32_t interleaved, void *ws, size_t ws_bytes,
-                                   void *stream) {
+// Both entry points: axes NULL turns every pair by the token's place.
+static uw_status run_append(const uw_kv4_cache *c, const int32_t *start, const int32_t *len, int64_t n_tokens,
+                            const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *q_out, const uw_kv4_rows *k,
+                            const uw_kv4_rows *v, const float *cos, const float *sin, int64_t rope_len,
+                            int32_t rot_dim, int32_t interleaved, const uw_rope *axes, const uw_kv4_rows *k_out,
+                            void *ws, size_t ws_bytes, void *stream) {
     AppendParams p{};
     uw_status s = kv4_view(c, start, len, n_tokens, ws, ws_bytes, &p.v);
     if (s != UW_OK)
@@ -358,9 +347,12 @@ extern "C" uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start, 
         return UW_ERR_UNSUPPORTED;
     if ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) & 15)
         return UW_ERR_INVALID_ARG;
+    if (axes && (s = rope_axes_map(*axes, p.v.n_tokens, &p.axes)) != UW_OK)
+        return s;
     if (p.v.n_tokens == 0)
         return UW_OK;
-    if (!kv4_rows(k, &p.k) || !kv4_rows(v, &p.vv) || (q && (!kv4_rows(q, &p.q) || !kv4_rows(q_out, &p.qo))))
+    if (!kv4_rows(k, &p.k) || !kv4_rows(v, &p.vv) || (q && (!kv4_rows(q, &p.q) || !kv4_rows(q_out, &p.qo))) ||
+        (k_out && !kv4_rows(k_out, &p.ko)))
         return UW_ERR_INVALID_ARG;
     p.cos = cos;
     p.sin = sin;
@@ -379,10 +371,29 @@ extern "C" uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start, 
         return UW_ERR_UNSUPPORTED;
     const dim3 grid(unsigned((units + 7) / 8));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return (c->head_dim == 128 ? launch_overlapped(kv4_append_kernel<128>, grid, dim3(256), 0, st, p)
-                               : launch_overlapped(kv4_append_kernel<64>, grid, dim3(256), 0, st, p)) == cudaSuccess
-               ? UW_OK
-               : UW_ERR_CUDA;
+    auto run = [&](auto kernel) { return launch_overlapped(kernel, grid, dim3(256), 0, st, p); };
+    const cudaError_t e = c->head_dim == 128 ? (axes ? run(kv4_append_kernel<128, true>) : run(kv4_append_kernel<128, false>))
+                                             : (axes ? run(kv4_append_kernel<64, true>) : run(kv4_append_kernel<64, false>));
+    return e == cudaSuccess ? UW_OK : UW_ERR_CUDA;
+}
+
+extern "C" uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start, const int32_t *len, int64_t n_tokens,
+                                   const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *q_out,
+                                   const uw_kv4_rows *k, const uw_kv4_rows *v, const float *cos, const float *sin,
+                                   int64_t rope_len, int32_t rot_dim, int32_t interleaved, void *ws, size_t ws_bytes,
+                                   void *stream) {
+    return run_append(c, start, len, n_tokens, q, q_heads, q_out, k, v, cos, sin, rope_len, rot_dim, interleaved,
+                      nullptr, nullptr, ws, ws_bytes, stream);
+}
+
+extern "C" uw_status uw_kv4_append_axes(const uw_kv4_cache *c, const int32_t *start, const int32_t *len,
+                                        int64_t n_tokens, const uw_rope *r, const uw_kv4_rows *q, int32_t q_heads,
+                                        const uw_kv4_rows *q_out, const uw_kv4_rows *k, const uw_kv4_rows *v,
+                                        const uw_kv4_rows *k_out, void *ws, size_t ws_bytes, void *stream) {
+    if (!r)
+        return UW_ERR_INVALID_ARG;
+    return run_append(c, start, len, n_tokens, q, q_heads, q_out, k, v, r->cos_dev, r->sin_dev, r->rope_len,
+                      r->rot_dim, r->interleaved, r, k_out, ws, ws_bytes, stream);
 }
 
 extern "C" uw_status uw_kv4_read(const uw_kv4_cache *c, const int32_t *start, const int32_t *len, int64_t n_tokens,
