@@ -636,6 +636,35 @@ uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *start_dev, cons
                            float *lse_dev, int64_t max_new, int64_t max_len, float softmax_scale, int32_t causal,
                            int32_t window, void *ws_dev, size_t ws_bytes, void *stream);
 
+/* uw_attention -- o = softmax(scale * q K^T) V over keys and values as they were projected
+ * (BF16, no cache): whole prompts, or images in a vision tower, of different lengths
+ * packed behind each other.
+ * Sequence s has the tokens start[s] .. start[s + 1] - 1 of q and out and the keys
+ * kv_start[s] .. kv_start[s + 1] - 1 of k and v; with kv_start NULL the tokens are the
+ * keys too.  Of n tokens and m keys token i has the position p = m - n + i; which keys it sees, and what
+ * one that sees none gets, is as for uw_kv4_attention (causal, window).  So is what
+ * heads read which (q_heads a multiple of kv_heads, UW_ERR_SHAPE otherwise), and that what a
+ * token does not see takes no part in its result, whatever its bits.
+ *   start_dev, kv_start_dev  int32 [n_seqs + 1] in device memory, checked there: a
+ *             sequence outside the call's tokens or keys is left alone and reported by
+ *             uw_check_status as UW_ERR_CORRUPT.  Tokens of no sequence are left alone.
+ *   n_tokens, n_keys  rows of q and out, and of k and v (equal without kv_start,
+ *             UW_ERR_SHAPE otherwise).
+ *   q, k, v, out  head_dim 64 or 128; strides of any order.  (k and v of more than
+ *             one key with token stride 0: UW_ERR_UNSUPPORTED.)
+ *   lse_dev   fp32 [n_tokens, q_heads]: log(sum exp(scale q.k)) (written), or NULL.
+ *   softmax_scale  0 for 1 / sqrt(head_dim).
+ *   ws_dev    at least uw_attention_workspace_size bytes, cleared once by
+ *             uw_workspace_init; it serves calls of any sequences and heads.
+ * Scores, softmax statistics and sums are fp32; a probability is rounded to one BF16 for the product with
+ * V (2^-8 of it).  The same call gives the same bits.  Scores q.k times scale beyond fp32 give NaN. */
+uw_status uw_attention_workspace_size(int32_t head_dim, size_t *bytes);
+uw_status uw_attention(const int32_t *start_dev, const int32_t *kv_start_dev, int32_t n_seqs, int64_t n_tokens,
+                       int64_t n_keys, const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *k,
+                       const uw_kv4_rows *v, int32_t kv_heads, int32_t head_dim, const uw_kv4_rows *out,
+                       float *lse_dev, float softmax_scale, int32_t causal, int32_t window, void *ws_dev,
+                       size_t ws_bytes, void *stream);
+
 /* uw_check_status -- synchronise `stream`, read and clear the error word the
  * kernels record in the workspace.  Returns UW_OK, UW_ERR_CORRUPT (a blob, or a
  * page table, length, start or position, that does not hold) or UW_ERR_TIMEOUT

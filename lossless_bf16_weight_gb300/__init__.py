@@ -143,6 +143,9 @@ SIGNATURES = [
     ("uw_kv4_read", ctypes.c_int, [_CACHE, _P, _P, _I64, _ROWS, _ROWS, _P, _SZ, _P]),
     ("uw_kv4_attention", ctypes.c_int, [_CACHE, _P, _P, _I64, _ROWS, _I32, _ROWS, _P, _I64, _I64, _F32, _I32, _I32,
                                         _P, _SZ, _P]),
+    ("uw_attention_workspace_size", ctypes.c_int, [_I32, ctypes.POINTER(_SZ)]),
+    ("uw_attention", ctypes.c_int, [_P, _P, _I32, _I64, _I64, _ROWS, _I32, _ROWS, _ROWS, _I32, _I32, _ROWS, _P, _F32,
+                                    _I32, _I32, _P, _SZ, _P]),
     ("uw_check_status", ctypes.c_int, [_P, _P]),
     ("uw_selftest_bounded_wait", ctypes.c_int, [_P, _SZ, ctypes.c_uint32, _P]),
     ("uw_variant_name", ctypes.c_char_p, [_I32, _I32]),
@@ -792,6 +795,36 @@ def kv4_attention(cache: Kv4Cache, start, length, q, out, ws, max_new: int = 0, 
     _check(load().uw_kv4_attention(cache.ref, start.data_ptr(), length.data_ptr(), n, qr, heads, orow,
                                    None if lse is None else lse.data_ptr(), max_new, max_len, scale, causal, window,
                                    ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
+
+
+def attention_workspace_size(head_dim: int) -> int:
+    n = _SZ(0)
+    _check(load().uw_attention_workspace_size(head_dim, ctypes.byref(n)), "uw_attention_workspace_size")
+    return int(n.value)
+
+
+def attention(q, k, v, out, start, ws, kv_start=None, scale: float = 0.0, causal: bool = True, window: int = 0, lse=None,
+              stream=None):
+    """uw_attention: attention of q [tokens, q heads, head_dim] over k and v [keys, kv heads, head_dim] into out;
+    sequence s has the tokens start[s] .. start[s + 1] - 1 (int32) and the same keys, or those of kv_start."""
+    what, int32 = "uw_attention", _types()[2]
+    if q.dim() != 3 or k.dim() != 3:
+        raise UwError(UW_ERR_SHAPE, "%s (q and k are not [tokens, heads, head_dim])" % what)
+    (n, hq, d), (m, hk, _) = q.shape, k.shape
+    qr, orow = _kv4_rows(q, n, hq, d, "q", what), _kv4_rows(out, n, hq, d, "out", what)
+    kr, vr = _kv4_rows(k, m, hk, d, "k", what), _kv4_rows(v, m, hk, d, "v", what)
+    seqs = start.numel() - 1
+    for t in (start, start if kv_start is None else kv_start):
+        if t.dtype is not int32 or t.dim() != 1 or t.numel() != seqs + 1 or seqs < 0 or not t.is_contiguous():
+            raise UwError(UW_ERR_SHAPE, "%s (start and kv_start are not int32 [sequences + 1])" % what)
+    if lse is not None:
+        if lse.dtype is not _types()[3]:
+            raise UwError(UW_ERR_SHAPE, "%s (lse is not fp32)" % what)
+        _refuse(_short((lse, 4 * n * hq, "lse")), what)
+    _here(what, q, k, v, out, start, kv_start, lse, ws)
+    _check(load().uw_attention(start.data_ptr(), None if kv_start is None else kv_start.data_ptr(), seqs, n, m, qr, hq, kr,
+                               vr, hk, d, orow, None if lse is None else lse.data_ptr(), scale, causal, window,
+                               ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
 
 
 def selftest_bounded_wait(ws, tries: int, stream=None) -> None:

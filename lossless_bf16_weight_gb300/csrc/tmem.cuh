@@ -12,6 +12,37 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
+// One box of a 3-D tensor map into shared memory, as tma_load_2d (tc.cuh).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x0, int x1, int x2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x0), "r"(x1), "r"(x2), "r"(bar) : "memory");
+}
+
+// Shared-memory matrix descriptor of a B operand whose rows are its K side (a tile
+// [K][N] with N contiguous, in blocks of 64 values of N, 128-byte swizzle): 8 rows
+// of K lie 1024 bytes apart (stride byte offset), the blocks `block` bytes (leading byte
+// offset).  Goes with kTransposeB in the instruction descriptor.
+__device__ __forceinline__ uint64_t sdesc_sw128_n(uint32_t addr, uint32_t block) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(block >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+constexpr uint32_t kTransposeB = 1u << 16;
+
+// 32 lanes x 32 fp32 columns: thread t of the warp gets lane (taddr >> 16) + t.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
 // 16 lanes x 32 fp32 columns spread like an mma.sync accumulator: with g, t =
 // thread / 4, thread % 4 of the warp, v[4 i + 2 r + k] is lane g + 8 r, column 8 i + 2 t + k.
 __device__ __forceinline__ void tmem_ld_16x256_x4(uint32_t taddr, uint32_t *v) {
