@@ -7,25 +7,21 @@
 //   softmax   warps 0-3 and 4-7: the upper and lower 128 rows, a row a thread.  They read
 //             S from tensor memory, take the exponentials and write P (BF16) over S, where
 //             the second product reads it; at the end of an item they write the rows' output.
-//   helper    warps 8-11: the queries of an item into shared memory, in a ring of three
-//             halves, so that those of the next item come in beside this one; V of tiles that
-//             some row does not see in full (see below).
-//   MMA       warps 12 and 13, for the upper and lower rows, one elected thread each (a
-//             thread takes some 50 cycles for each product that it issues and 140 for a wait, 3500 a
-//             step for both halves): S = Q K^T and O += P V with tcgen05.mma, 128 rows and 128 keys
-//             each; while the softmax works on one half of the rows, the products of the other
-//             half run.
+//   check     warps 8-11: V of tiles that some row does not see in full (see below);
+//             queries where they do not come by a tensor map.
+//   MMA       warps 12 and 13, for the upper and lower rows, one elected thread each: S = Q K^T and
+//             O += P V with tcgen05.mma, 128 rows and 128 keys each.
 //   copies    warp 14, one elected thread: tiles of K and V by tensor-map copies, two
 //             stages of each.  V lies as it comes, [keys][dims], and is the second product's
 //             operand with its rows along the product.
 // The running maximum is only raised when some row's probabilities of a tile add up to
-// more than 2^24 (BF16 and fp32 hold that without loss), so that after the first keys no score
+// more than 2^40 (BF16 and fp32 hold that without loss), so that after the first keys no score
 // is compared and O is rarely rescaled.  P is rounded to one BF16 (2^-8, the one rounding beside
 // the output's); its sum is fp32 of the unrounded values.
 //
 // What a row does not see takes no part in it, whatever its bits: a masked score is
 // replaced before its exponential, and since 0 times a V that is not finite is not 0, the
-// helper looks through V's tiles that are not seen by all rows, zeroes keys past the sequence's
+// check warps look through V's tiles that are not seen by all rows, zero keys past the sequence's
 // end and values that are not finite, and an item with such a value adds them at its end to the rows
 // that see their keys.
 #include <cudaTypedefs.h>
@@ -46,13 +42,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // gemm_tc.cu
 namespace {
 
 constexpr int kRows = 256, kKeys = 128;
-constexpr int kSoftmax = 256, kHelper = 128;          // threads
-constexpr int kThreads = kSoftmax + kHelper + 128;    // and a warpgroup of the MMA and copying warps
-constexpr int kItemCost = 3;                          // what an item costs beyond its steps, in steps
+constexpr int kSoftmax = 256, kCheck = 128;         // threads
+constexpr int kThreads = kSoftmax + kCheck + 128;   // and a warpgroup of the MMA, copying and listing warps
+constexpr int kItemCost = 4;                          // what an item costs beyond its steps, in steps
 constexpr int kMinShare = 4;                          // units of a CTA at least
 constexpr int kSegs = 16;
-constexpr int kStages = 2, kQSlots = 3;
-constexpr float kRaise = 16777216.f;                  // 2^24: headroom of the sum of a tile's probabilities
+constexpr int kStages = 2;
+constexpr float kRaise = 1099511627776.f;             // 2^40: headroom of the sum of a tile's probabilities
 constexpr uint32_t kTmemCols = 512;
 
 // The call's sequences: tokens start[s] .. and keys kstart[s] ..
@@ -81,45 +77,92 @@ struct PackedParams {
     Divisor by_group;
     bool out32;                  // rows of o begin on 32-byte steps
     bool heads_outer[2], one_head[2];  // of K, V: the tensor map's outermost dimension is the head; all heads are one
+    bool q_map;                  // queries come by qmap
     int32_t rows_min, rows_max;  // any
     float *parts;                // parts of kRows * (D + 2) floats: output, maximum, sum
     uint32_t *counters;          // [gridDim.x], left at zero
     CUtensorMap kmap, vmap;      // 64 dimensions x 128 keys of one head
+    CUtensorMap qmap;            // 64 dimensions x 128 rows: a kv head's query heads x tokens
 };
 
 enum Bar {
-    kQFull, kQEmpty = kQFull + kQSlots, kKFull = kQEmpty + kQSlots, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVOk = kVFull + kStages,
-    kVEmpty = kVOk + kStages, kTurn = kVEmpty + kStages, kSFull = kTurn + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2,
-    kBars = kPvDone + 2
+    kQFull, kQEmpty = kQFull + 2, kKFull = kQEmpty + 2, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVOk = kVFull + kStages,
+    kVEmpty = kVOk + kStages, kTurn = kVEmpty + kStages, kSegFull = kTurn + 2, kSegFree = kSegFull + kSegs,
+    kSFull = kSegFree + kSegs, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+    kDrain = kPvDone + 2, kJoin = kDrain + 2, kBars
 };
 
 struct Shared {
     uint64_t bars[kBars];
-    uint64_t listed_to;
-    Seg segs[kSegs];
+    Seg segs[kSegs];       // a ring: s < 0 after the last
     int32_t key0[kSegs];   // the sequence's first key
     uint32_t hurt[kSegs];  // V of a tile that not all rows see holds a value that is not finite
     uint32_t tmem, dead, arrived;
-    int n_segs;
 };
 
 template <int D>
 constexpr uint32_t kTileBytes = kKeys * D * 2;  // 128 rows of Q, 128 keys of K or V
+// With heads of 64 one warp issues all products (mma_role).
 template <int D>
-constexpr size_t kSmem = 1024 + (kQSlots + 2 * kStages) * size_t(kTileBytes<D>);
+constexpr bool kOneMma = D == 64;
+constexpr uint32_t kOutBytes = kSoftmax / 32 * 32 * 128;  // 64 dimensions of a softmax warp's rows
+template <int D>
+constexpr size_t kSmem = 1024 + kOutBytes + (2 + 2 * kStages) * size_t(kTileBytes<D>);
 
 // A wait that every thread of a role makes at the same place.  One that runs
 // out marks the kernel dead: all later waits return at once, every role
 // walks through its remaining steps without waiting, and the status word tells.
 __device__ __forceinline__ bool is_dead(Shared &sh) { return *reinterpret_cast<volatile uint32_t *>(&sh.dead) != 0; }
+// What is ready, or soon, is found by a few looks; then a thread is suspended for up to a microsecond at a time
+// (a prompt of 8192 tokens 374 us, without the looks 394).
+constexpr uint32_t kHintNs = 1000, kTries = kWaitTries / 8;
+__device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "n"(kHintNs) : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void wait(Shared &sh, uint32_t bar, uint32_t parity, uint32_t *status) {
-    if (mbar_try_wait(bar, parity) || is_dead(sh))
-        return;
-    if (!mbar_wait(bar, parity, status, kStatusTimeout))
-        *reinterpret_cast<volatile uint32_t *>(&sh.dead) = 1;
+    for (int i = 0; i < 4; i++)
+        if (look(bar, parity))
+            return;
+    for (uint32_t i = 0; i < kTries; i++)
+        if (try_wait(bar, parity) || is_dead(sh))
+            return;
+    atomicOr(status, kStatusTimeout);
+    *reinterpret_cast<volatile uint32_t *>(&sh.dead) = 1;
 }
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Segment n of the CTA's share, once it is listed; null after the last.
+__device__ __forceinline__ const Seg *segment(Shared &sh, uint32_t bars, uint32_t n, uint32_t *status) {
+    wait(sh, bars + 8 * (kSegFull + n % kSegs), (n / kSegs) & 1, status);
+    const Seg *const sg = sh.segs + n % kSegs;
+    return is_dead(sh) || sg->s < 0 ? nullptr : sg;
+}
+// A warp (or the one thread of a role) is done with it.
+template <int D>
+constexpr uint32_t kSegUsers = (kSoftmax + kCheck) / 32 + (kOneMma<D> ? 2 : 3);
+__device__ __forceinline__ void segment_done(uint32_t bars, uint32_t n) { mbar_arrive(bars + 8 * (kSegFree + n % kSegs)); }
+
+// All softmax warps are here: a wait with a limit, as the halves may part where one has run out.
+__device__ __forceinline__ void softmax_sync(Shared &sh, uint32_t bars, uint32_t &turns, uint32_t *status) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bars + 8 * kJoin);
+    wait(sh, bars + 8 * kJoin, turns++ & 1, status);
+}
 
 // Byte offset of 16-byte chunk c (8 values) of row r in a tile of 128 rows:
 // blocks of 64 values, 128-byte swizzle.
@@ -132,104 +175,134 @@ __device__ __forceinline__ bool is_open(const Seg &sg, int key0) {
     return key0 < sg.all_lo || sg.all_hi - key0 < kKeys;  // (key0 + kKeys may be 2^31)
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // All of the thread's groups of copies but the last are done.
 __device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4]) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 
 // A value that is the same in all lanes, so that what follows from it stays in uniform
 // registers, which the products' descriptors and addresses are taken from.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-template <int D>
+// The products of the upper rows (half 0) and the lower ones, or with kBoth of all.
+//
+// A step is a half's outputs of the last tile and, behind them, as S lies over P, its
+// scores of the next; the halves in turns, so that one half's products run while the other's
+// softmax does.  With heads of 128 a warp for each half takes turns with the other: an elected thread
+// takes 60 cycles for each of 16 products and 140 for each wait, which for both halves is more than the
+// tensor cores' 2048 (8192 tokens, not causal, 613 us; by one warp 673; by two without turns, which
+// interleave their products, 948).  With heads of 64 there are half as many products and one warp does
+// (496 us, two 556).
+template <int D, bool kBoth>
 __device__ __forceinline__ void mma_role(const PackedParams &p, Shared &sh, uint32_t bars, uint32_t q_at,
-                                         uint32_t k_at, uint32_t v_at, int half, uint32_t &steps, uint32_t &cnt,
-                                         uint32_t &halves, uint32_t &turns) {
+                                         uint32_t k_at, uint32_t v_at, int part) {
     constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys), kIdO = idesc_bf16_f32(128, D) | kTransposeB;
-    const uint32_t tm = uint32_t(uniform(int(sh.tmem))), s_tm = tm + half * kKeys, o_tm = tm + 256 + half * D;
+    constexpr int kHalves = kBoth ? 2 : 1;
+    const uint32_t tm = uint32_t(uniform(int(sh.tmem)));
+    uint32_t steps = 0, turns = 0, cnt[kHalves] = {}, items[kHalves] = {};
     // Descriptors of the tiles; a step of 16 values along the first product adds 32
     // bytes, the next block of 64 values 128 * 128, a step of 16 keys along the second 16 * 128.
     const uint64_t q_desc = sdesc_sw128(q_at), k_desc = sdesc_sw128(k_at), v_desc = sdesc_sw128_n(v_at, 128 * 128);
     auto at = [](int i) { return uint64_t((i / 4) * (128 * 8) + (i % 4) * 2); };
-    const int n_segs = uniform(sh.n_segs);
-    for (int s = 0; s < n_segs; s++) {
-        const Seg &sg = sh.segs[s];
+    for (uint32_t n = 0;; n++) {
+        const Seg *const sgp = segment(sh, bars, n, p.v.status);
+        if (!uniform(sgp != nullptr))
+            break;
+        const Seg &sg = *sgp;
         const int tiles = uniform(sg.tiles), rows = uniform(sg.tokens * p.group - sg.rt * kRows);
+        if (elect_one())
+            segment_done(bars, n);
+        __syncwarp();
         if (tiles == 0)
             continue;
-        const bool two = rows > 128, active = half == 0 || two;
-        const uint32_t slot = (halves + half) % kQSlots;
-        // The halves take turns, each with its outputs and next scores, so that one half's products
-        // run while the other's softmax does (without turns both end up at the same place).
-        auto my_turn = [&]() {
-            if (two)
-                wait(sh, bars + 8 * (kTurn + half), (turns & 1) ^ (half ^ 1), p.v.status);
-        };
-        auto pass = [&]() {  // by the elected thread
-            if (two)
-                mbar_arrive(bars + 8 * (kTurn + (half ^ 1)));
-        };
-        // Step j's scores behind step j - 1's outputs: S lies over P.
+        const bool two = rows > 128;
         for (int j = 0; j <= tiles; j++) {
             const uint32_t step = steps + j, before = step - 1, k_stage = step % kStages, v_stage = before % kStages;
-            if (j > 0)
-                wait(sh, bars + 8 * (kVOk + v_stage), (before / kStages) & 1, p.v.status);
-            if (!active) {
-                if (j > 0 && elect_one())
-                    mbar_arrive(bars + 8 * (kVEmpty + v_stage));
-                if (j < tiles) {
-                    wait(sh, bars + 8 * (kKFull + k_stage), (step / kStages) & 1, p.v.status);
-                    if (elect_one())
-                        mbar_arrive(bars + 8 * (kKEmpty + k_stage));
-                }
-                continue;
-            }
-            // (a wait takes 140 cycles, done or not: the probabilities', which all else waits for, comes last)
+            const uint64_t v = v_desc + v_stage * (kTileBytes<D> >> 4), k = k_desc + k_stage * (kTileBytes<D> >> 4);
+            // (a wait takes 140 cycles, done or not: the one that all else waits for comes last)
             if (j < tiles)
                 wait(sh, bars + 8 * (kKFull + k_stage), (step / kStages) & 1, p.v.status);
-            if (j == 0)
-                wait(sh, bars + 8 * (kQFull + slot), ((halves + half) / kQSlots) & 1, p.v.status);
-            my_turn();
-            turns += two;
             if (j > 0)
-                wait(sh, bars + 8 * (kPFull + half), cnt++ & 1, p.v.status);
-            tc_fence_after();
-            if (elect_one()) {
-                if (j > 0) {
-                    const uint64_t v = v_desc + v_stage * (kTileBytes<D> >> 4);
+                wait(sh, bars + 8 * (kVOk + v_stage), (before / kStages) & 1, p.v.status);
 #pragma unroll
-                    for (int i = 0; i < kKeys / 16; i++)
-                        mma_ts(o_tm, s_tm + 8 * i, v + i * (16 * 8), kIdO, j > 1 || i > 0);
-                    mma_commit(bars + 8 * (kPvDone + half));
-                    mma_commit(bars + 8 * (kVEmpty + v_stage));
+            for (int h = 0; h < kHalves; h++) {
+                const int half = kBoth ? h : part;
+                if (half && !two) {
+                    if (!kBoth && elect_one()) {  // nothing to do with these tiles
+                        if (j > 0)
+                            mbar_arrive(bars + 8 * (kVEmpty + v_stage));
+                        if (j < tiles)
+                            mbar_arrive(bars + 8 * (kKEmpty + k_stage));
+                    }
+                    continue;
                 }
-                if (j < tiles) {
-                    const uint64_t q = q_desc + slot * (kTileBytes<D> >> 4), k = k_desc + k_stage * (kTileBytes<D> >> 4);
+                const uint32_t s_tm = tm + half * kKeys, o_tm = tm + 256 + half * D;
+                if (j == 0)
+                    wait(sh, bars + 8 * (kQFull + half), items[h]++ & 1, p.v.status);
+                if (!kBoth && two)
+                    wait(sh, bars + 8 * (kTurn + half), (turns++ & 1) ^ (half ^ 1), p.v.status);
+                if (j > 0)
+                    wait(sh, bars + 8 * (kPFull + half), cnt[h]++ & 1, p.v.status);
+                tc_fence_after();
+                if (elect_one()) {
+                    if (j > 0) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; i++)
-                        mma_bf16(s_tm, q + at(i), k + at(i), kIdS, i > 0);
-                    mma_commit(bars + 8 * (kSFull + half));
-                    mma_commit(bars + 8 * (kKEmpty + k_stage));
-                    if (j == tiles - 1)
-                        mma_commit(bars + 8 * (kQEmpty + slot));
+                        for (int i = 0; i < kKeys / 16; i++)
+                            mma_ts(o_tm, s_tm + 8 * i, v + i * (16 * 8), kIdO, j > 1 || i > 0);
+                        mma_commit(bars + 8 * (kPvDone + half));
+                    }
+                    if (j < tiles) {
+                        const uint64_t q = q_desc + half * (kTileBytes<D> >> 4);
+#pragma unroll
+                        for (int i = 0; i < D / 16; i++)
+                            mma_bf16(s_tm, q + at(i), k + at(i), kIdS, i > 0);
+                        mma_commit(bars + 8 * (kSFull + half));
+                        if (j == tiles - 1)
+                            mma_commit(bars + 8 * (kQEmpty + half));
+                    }
+                    if (!kBoth || half == int(two)) {
+                        if (j > 0)
+                            mma_commit(bars + 8 * (kVEmpty + v_stage));
+                        if (j < tiles)
+                            mma_commit(bars + 8 * (kKEmpty + k_stage));
+                    }
+                    if (!kBoth && two)
+                        mbar_arrive(bars + 8 * (kTurn + (half ^ 1)));
                 }
-                pass();
+                __syncwarp();
             }
-            __syncwarp();
         }
         steps += tiles;
-        halves += two ? 2 : 1;
     }
-    // every commit has arrived before the barriers go
-    if (steps > 0)
-        wait(sh, bars + 8 * (kVEmpty + (steps - 1) % kStages), ((steps - 1) / kStages) & 1, p.v.status);
+    // whatever became of the rest, all products are done before the barriers and the tensor memory go
+    if (elect_one())
+        mma_commit(bars + 8 * (kDrain + part));
+    __syncwarp();
+    mbar_wait(bars + 8 * (kDrain + part), 0, p.v.status, kStatusTimeout);
 }
 
 template <int D>
-__device__ __forceinline__ void copy_role(const PackedParams &p, Shared &sh, uint32_t bars, uint32_t k_at,
-                                          uint32_t v_at, uint32_t &steps) {
+__device__ __forceinline__ void copy_role(const PackedParams &p, Shared &sh, uint32_t bars, uint32_t q_at,
+                                          uint32_t k_at, uint32_t v_at) {
+    uint32_t steps = 0, items[2] = {0, 0};
+    auto copy_q = [&](int half, int kv_head, int token) {
+        wait(sh, bars + 8 * (kQEmpty + half), (items[half] & 1) ^ 1, p.v.status);
+        if (is_dead(sh))
+            return;
+        mbar_expect_tx(bars + 8 * (kQFull + half), kTileBytes<D>);
+#pragma unroll
+        for (int b = 0; b < D / 64; b++)
+            tma_load_3d(q_at + half * kTileBytes<D> + b * (128 * 128), &p.qmap, 64 * b, kv_head * p.group, token,
+                        bars + 8 * (kQFull + half));
+        items[half]++;
+    };
     auto copy = [&](const CUtensorMap &map, int which, uint32_t to, int head, int key, uint32_t bar) {
         head = p.one_head[which] ? 0 : head;
         mbar_expect_tx(bar, kTileBytes<D>);
@@ -240,65 +313,93 @@ __device__ __forceinline__ void copy_role(const PackedParams &p, Shared &sh, uin
     };
     // What is on its way ends before the CTA does, whatever became of the rest: n tiles of K, n - less of V.
     auto drain = [&](uint32_t n, uint32_t less) {
+        for (int half = 0; half < 2; half++)
+            if (items[half] > 0)
+                mbar_wait(bars + 8 * (kQFull + half), (items[half] - 1) & 1, p.v.status, kStatusTimeout);
         for (uint32_t i = n - min(n, uint32_t(kStages)); i < n; i++) {
             mbar_wait(bars + 8 * (kKFull + i % kStages), (i / kStages) & 1, p.v.status, kStatusTimeout);
             if (i + less < n)
                 mbar_wait(bars + 8 * (kVFull + i % kStages), (i / kStages) & 1, p.v.status, kStatusTimeout);
         }
     };
-    for (int s = 0; s < sh.n_segs; s++) {
-        const Seg &sg = sh.segs[s];
-        for (int j = 0; j < sg.tiles; j++, steps++) {
+    for (uint32_t n = 0;; n++) {
+        const Seg *const sgp = segment(sh, bars, n, p.v.status);
+        if (!sgp)
+            break;
+        const int tiles = sgp->tiles, head = sgp->head, first = sh.key0[n % kSegs] + sgp->first * kKeys;
+        // (with a map a half tile's 128 rows are whole tokens)
+        const int rows = sgp->tokens * p.group - sgp->rt * kRows, token = sgp->t0 + p.by_group.of(sgp->rt * kRows);
+        segment_done(bars, n);
+        if (p.q_map && tiles > 0)
+            copy_q(0, head, token);
+        for (int j = 0; j < tiles; j++, steps++) {
             const uint32_t stage = steps % kStages, free = ((steps / kStages) & 1) ^ 1;
-            const int key = sh.key0[s] + (sg.first + j) * kKeys;
+            const int key = first + j * kKeys;
             wait(sh, bars + 8 * (kKEmpty + stage), free, p.v.status);
             if (is_dead(sh))
                 return drain(steps, 0);
-            copy(p.kmap, 0, k_at + stage * kTileBytes<D>, sg.head, key, bars + 8 * (kKFull + stage));
+            copy(p.kmap, 0, k_at + stage * kTileBytes<D>, head, key, bars + 8 * (kKFull + stage));
+            if (p.q_map && j == 0 && rows > 128)
+                copy_q(1, head, token + p.by_group.of(128));
             wait(sh, bars + 8 * (kVEmpty + stage), free, p.v.status);
             if (is_dead(sh))
                 return drain(steps + 1, 1);
-            copy(p.vmap, 1, v_at + stage * kTileBytes<D>, sg.head, key, bars + 8 * (kVFull + stage));
+            copy(p.vmap, 1, v_at + stage * kTileBytes<D>, head, key, bars + 8 * (kVFull + stage));
         }
     }
+    if (is_dead(sh))
+        drain(steps, 0);
 }
 
+// Where row rr of a half of an item lies, chunk c.
+__device__ __forceinline__ uint16_t *row_at(const PackedParams &p, const Rows &rows, const Seg &sg, int half, int rr,
+                                            int c) {
+    const int r = sg.rt * kRows + 128 * half + rr, i = p.by_group.of(r);
+    return rows.p + (sg.t0 + int64_t(i)) * rows.ts + (sg.head * p.group + (r - i * p.group)) * rows.hs + 8 * c;
+}
+__device__ __forceinline__ int rows_of(const PackedParams &p, const Seg &sg, int half) {
+    return min(sg.tokens * p.group - sg.rt * kRows - 128 * half, 128);
+}
+
+// V of tiles that some row does not see in full, and queries that do not come by a map.
 template <int D>
-__device__ __forceinline__ void helper_role(const PackedParams &p, Shared &sh, uint32_t bars, uint32_t q_at,
-                                            uint32_t v_at, uint32_t &steps, uint32_t &halves) {
+__device__ __forceinline__ void check_role(const PackedParams &p, Shared &sh, uint32_t bars, uint32_t q_at,
+                                           uint32_t v_at) {
     constexpr int C = D / 8;  // 16-byte chunks of a row
     const int t = threadIdx.x - kSoftmax, lane = t & 31;
-    for (int s = 0; s < sh.n_segs; s++) {
-        const Seg &sg = sh.segs[s];
-        if (sg.tiles == 0)
-            continue;
-        const int r0 = sg.rt * kRows, rows = min(sg.tokens * p.group - r0, kRows), two = rows > 128;
-        for (int half = 0; half <= two; half++) {
-            const uint32_t slot = (halves + half) % kQSlots;
-            wait(sh, bars + 8 * (kQEmpty + slot), (((halves + half) / kQSlots) & 1) ^ 1, p.v.status);
+    uint32_t steps = 0, items[2] = {0, 0};
+    auto load_q = [&](const Seg *sgp) {
+        if (p.q_map || !sgp || sgp->tiles == 0)
+            return;
+        const Seg &sg = *sgp;
+        const int halves = rows_of(p, sg, 1) > 0 ? 2 : 1;
+        for (int half = 0; half < halves; half++) {
+            const int rows = rows_of(p, sg, half);
+            wait(sh, bars + 8 * (kQEmpty + half), (items[half]++ & 1) ^ 1, p.v.status);
 #pragma unroll 4
-            for (int x = t; x < 128 * C; x += kHelper) {
+            for (int x = t; x < 128 * C; x += kCheck) {
                 const int rr = x / C, c = x % C;
-                const bool in = 128 * half + rr < rows;
-                const int r = r0 + (in ? 128 * half + rr : 0), i = p.by_group.of(r);
-                cp_async16_zfill(q_at + slot * kTileBytes<D> + tile_at(rr, c),
-                                 p.q.p + (sg.t0 + int64_t(i)) * p.q.ts +
-                                     (sg.head * p.group + (r - i * p.group)) * p.q.hs + 8 * c,
+                const bool in = rr < rows;
+                cp_async16_zfill(q_at + half * kTileBytes<D> + tile_at(rr, c), row_at(p, p.q, sg, half, in ? rr : 0, c),
                                  in ? 16 : 0);
             }
             cp_async_commit();
         }
-        for (int half = 0; half <= two; half++) {
-            if (half < two)
+        for (int half = 0; half < halves; half++) {
+            if (half + 1 < halves)
                 cp_async_wait_but_one();
             else
                 cp_async_wait_all();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(bars + 8 * (kQFull + (halves + half) % kQSlots));
+                mbar_arrive(bars + 8 * (kQFull + half));
         }
-        halves += 1 + two;
+    };
+    const Seg *sgp = segment(sh, bars, 0, p.v.status);
+    load_q(sgp);
+    for (uint32_t n = 0; sgp; n++) {
+        const Seg &sg = *sgp;
         for (int j = 0; j < sg.tiles; j++, steps++) {
             const uint32_t stage = steps % kStages;
             const int key0 = (sg.first + j) * kKeys;
@@ -307,48 +408,174 @@ __device__ __forceinline__ void helper_role(const PackedParams &p, Shared &sh, u
                 // a key a thread
                 const uint32_t tile = v_at + stage * kTileBytes<D>;
                 const bool there = t < sg.len - key0;
-                bool hurt = false;
+                uint32_t any = 0;  // a sign bit for a value that is not finite
+                if (there) {
 #pragma unroll
-                for (int c = 0; c < C; c++) {
-                    const uint32_t at = tile + tile_at(t, c);
-                    uint32_t w[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
-                    bool bad = false;
+                    for (int c = 0; c < C; c++) {
+                        uint32_t w[4];
+                        lds128(tile + tile_at(t, c), w);
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        bad = bad || not_finite(w[k]);
-                    if (bad || !there) {
+                        for (int k = 0; k < 4; k++)
+                            any |= (w[k] & 0x7f807f80u) + 0x00800080u;
+                    }
+                }
+                const bool hurt = (any & 0x80008000u) != 0;
+                if (hurt || !there) {
+#pragma unroll 1
+                    for (int c = 0; c < C; c++) {
+                        const uint32_t at = tile + tile_at(t, c);
+                        uint32_t w[4];
+                        lds128(at, w);
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             const bool low = (w[k] & 0x7f80u) == 0x7f80u, high = (w[k] & 0x7f800000u) == 0x7f800000u;
                             w[k] = there ? w[k] & ((low ? 0u : 0xffffu) | (high ? 0u : 0xffff0000u)) : 0u;
                         }
                         sts128(at, w[0], w[1], w[2], w[3]);
-                        hurt = hurt || (bad && there);
                     }
                 }
                 if (hurt)
-                    *reinterpret_cast<volatile uint32_t *>(&sh.hurt[s]) = 1;
+                    *reinterpret_cast<volatile uint32_t *>(&sh.hurt[n % kSegs]) = 1;
                 fence_proxy_async_smem();
             }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bars + 8 * (kVOk + stage));
         }
+        const Seg *const next = segment(sh, bars, n + 1, p.v.status);
+        load_q(next);
+        __syncwarp();
+        if (lane == 0)
+            segment_done(bars, n);
+        sgp = next;
     }
+}
+
+// Where the CTA's share begins, found by all threads at once, of up to kThreads / 2 sequences: a thread stands for
+// some row tiles of one sequence, their units (of one head) summed up over the threads.
+struct Plan {
+    uint64_t sums[kThreads / 32];
+    uint64_t first[kThreads / 2 + 1];  // units of one head before each sequence
+    uint64_t base, at;                 // the share's sequence and head: their first unit; its unit among one head's
+    int32_t seq, head;
+    Item item;
+};
+template <class S>
+__device__ __forceinline__ uint64_t plan_units(const PackedParams &p, Plan &plan, uint64_t *before, uint64_t *mine) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int each_seq = kThreads / p.v.n_seqs, s = t / each_seq;  // threads of a sequence
+    uint64_t n = 0;
+    if (s < p.v.n_seqs) {
+        const Seq q = seq_of(p.v, s);
+        const int rts = S::mine(p, q) ? S::row_tiles(p, q) : 0, each = (rts + each_seq - 1) / each_seq;
+        const int rt0 = (t - s * each_seq) * each, rt1 = min(rt0 + each, rts);
+        for (int rt = rt0; rt < rt1; rt++)
+            n += S::units(p, q, rt);
+    }
+    uint64_t upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o)
+            upto += x;
+    }
+    if (lane == 31)
+        plan.sums[warp] = upto;
+    __syncthreads();
+    uint64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; w++) {
+        const uint64_t x = plan.sums[w];
+        upto += w < warp ? x : 0;
+        all += x;
+    }
+    if (s < p.v.n_seqs && t == s * each_seq)
+        plan.first[s] = upto - n;
+    if (t == 0)
+        plan.first[p.v.n_seqs] = all;
+    __syncthreads();
+    *before = upto - n;
+    *mine = n;
+    return all * p.v.heads;
+}
+// The item that holds unit u (of fewer than all) into plan.item; all threads call.
+template <class S>
+__device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uint64_t u, uint64_t before, uint64_t mine) {
+    const int t = threadIdx.x, each_seq = kThreads / p.v.n_seqs, s = t / each_seq;
+    if (s < p.v.n_seqs && t == s * each_seq) {
+        const uint64_t lo = plan.first[s] * p.v.heads, per_head = plan.first[s + 1] - plan.first[s];
+        if (u >= lo && u < lo + per_head * p.v.heads) {
+            const uint64_t head = divide(u - lo, per_head);
+            plan.seq = s;
+            plan.head = int(head);
+            plan.base = lo + head * per_head;
+            plan.at = plan.first[s] + (u - plan.base);
+        }
+    }
+    __syncthreads();
+    if (s == plan.seq && plan.at >= before && plan.at - before < mine) {
+        Item it;
+        it.s = s;
+        it.head = plan.head;
+        it.q = seq_of(p.v, s);
+        const int each = (S::row_tiles(p, it.q) + each_seq - 1) / each_seq;
+        uint64_t to = before;
+        for (int rt = (t - s * each_seq) * each;; rt++) {
+            S::set_tile(p, it, rt);
+            if (plan.at < to + it.n)
+                break;
+            to += it.n;
+        }
+        it.u0 = plan.base + (to - plan.first[s]);
+        plan.item = it;
+    }
+}
+
+// The segments of the CTA's share from unit u (in item `it`) on, one after the other into the ring;
+// a warp.  `most`: how many; returns where it stopped.
+template <class S>
+__device__ __forceinline__ uint64_t list_role(const PackedParams &p, Shared &sh, uint32_t bars, Item &it, uint64_t u,
+                                              uint64_t end, uint32_t first, uint32_t most) {
+    for (uint32_t n = first; n < most;) {
+        const uint32_t slot = n % kSegs;
+        wait(sh, bars + 8 * (kSegFree + slot), ((n / kSegs) & 1) ^ 1, p.v.status);
+        if (is_dead(sh))
+            break;
+        int found = 0;
+        if (u < end)
+            u = list_segments<S, 1>(p, it, u, end, sh.segs + slot, &found);
+        if (found == 0 && u < end)
+            continue;
+        if ((threadIdx.x & 31) == 0) {
+            if (found) {
+                sh.key0[slot] = __ldg(p.v.kstart + sh.segs[slot].s);
+                sh.hurt[slot] = 0;
+            } else {
+                sh.segs[slot].s = -1;
+            }
+            mbar_arrive(bars + 8 * (kSegFull + slot));
+        }
+        if (!found)
+            break;
+        n++;
+    }
+    return u;
 }
 
 template <int D>
 __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, uint32_t bars, uint64_t total,
-                                             uint32_t workers, uint64_t cut0, uint32_t &cnt) {
+                                             uint32_t workers, uint64_t cut0, uint32_t out_at) {
     constexpr int PF = kRows * (D + 2);
     const int half = threadIdx.x >> 7, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t s_tm = sh.tmem + lanes + half * kKeys, o_tm = sh.tmem + lanes + 256 + half * D;
     const uint64_t c1 = pair2(p.c1, p.c1);
-    for (int sgi = 0; sgi < sh.n_segs; sgi++) {
-        const Seg &sg = sh.segs[sgi];
+    uint32_t cnt = 0, turns = 0;
+    for (uint32_t n = 0;; n++) {
+        const Seg *const sgp = segment(sh, bars, n, p.v.status);
+        if (!sgp)
+            break;
+        const Seg &sg = *sgp;
         const int r0 = sg.rt * kRows, rows = sg.tokens * p.group;
         const int r = r0 + int(threadIdx.x);
         const bool active = r0 + 128 * half < rows;  // this half has rows
@@ -368,94 +595,100 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             const int key0 = (sg.first + j) * kKeys;
             wait(sh, bars + 8 * (kSFull + half), cnt & 1, p.v.status);
             tc_fence_after();
-            auto tile = [&](auto masked) {
-                constexpr bool kOpen = decltype(masked)::value;
-                const int lo = mine.lo - key0, hi = mine.hi - key0;  // the row's keys of the tile
-                auto seen = [&](int k) { return !kOpen || (k >= lo && k < hi); };
-                // Raise the maximum to that of these keys, in rows that need it (not in others,
-                // whose bits then depend on no other row): what the row has so far is scaled down.
-                auto raise = [&](bool need) {
+            const int lo = mine.lo - key0, hi = mine.hi - key0;  // the row's keys of the tile
+            const bool open = is_open(sg, key0);
+            // (Code that runs once an item is kept short: instructions that are not at hand come eight in 60 cycles.)
+            for (int look = open ? kKeys : j == 0 ? 32 : 0;; look = kKeys) {
+                if (look > 0) {
+                    // Raise the maximum to that of the first 32 keys (of an item's first tile: most often that will
+                    // do) or of all, in rows where it is more than 30 higher (not in others, whose bits then
+                    // depend on no other row): what the row has so far is scaled down.
                     float top = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < kKeys; c += 32) {
+                    for (int c = 0; c < look; c += 32) {
                         uint32_t x[32];
                         tmem_ld32(s_tm + c, x);
                         tmem_ld_wait();
+                        const int from = lo - c, to = hi - c;
 #pragma unroll
                         for (int k = 0; k < 32; k++)
-                            if (seen(c + k))
-                                top = fmaxf(top, __uint_as_float(x[k]));
+                            top = k >= from && k < to ? fmaxf(top, __uint_as_float(x[k])) : top;
                     }
+                    const bool need = !(top * p.c1 - m <= 30.f);
                     const float m2 = need ? fmaxf(m, top * p.c1) : m, m20 = m2 == -INFINITY ? 0.f : m2;
                     const float f = !need ? 1.f : m == -INFINITY ? 0.f : exp2_fast(m - m20);
                     l2 = mul2(l2, pair2(f, f));
                     m = m2;
                     mm = pair2(-m20, -m20);
                     lim = m2 == -INFINITY ? unset : kRaise;
-                    if (j > 0) {
+                    if (j > 0 && __any_sync(0xffffffffu, need)) {
                         wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int d0 = 0; d0 < D; d0 += 32) {
-                            uint32_t w[32];
-                            tmem_ld32(o_tm + d0, w);
+                        for (int d0 = 0; d0 < D; d0 += 16) {
+                            uint32_t w[16];
+                            tmem_ld16(o_tm + d0, w);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; i++)
+                            for (int i = 0; i < 16; i++)
                                 w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-                            tmem_st32(o_tm + d0, w);
+                            tmem_st16(o_tm + d0, w);
                         }
                     }
-                };
-                // Scores are loaded 32 ahead of those whose exponentials are taken; returns the
-                // sum of the probabilities, whose pairs come into pk.
-                uint32_t pk[2][32];
-                auto exps = [&]() {
-                    uint32_t x[2][32];
-                    uint64_t sum[2] = {0, 0};
-                    tmem_ld32(s_tm, x[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; c++) {
+                }
+                if (open) {
+                    // 32 keys at a time; their P lies over S of those before
+#pragma unroll 1
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t x[32], pk[16];
+                        tmem_ld32(s_tm + c, x);
                         tmem_ld_wait();
-                        if (c < 3)
-                            tmem_ld32(s_tm + 32 * (c + 1), x[(c + 1) & 1]);
+                        const int from = lo - c, to = hi - c;
 #pragma unroll
                         for (int k = 0; k < 16; k++) {
-                            const uint32_t *const w = x[c & 1] + 2 * k;
-                            float2 y = unpair(fma2(pair2(__uint_as_float(w[0]), __uint_as_float(w[1])), c1, mm));
-                            if constexpr (kOpen) {
-                                y.x = seen(32 * c + 2 * k) ? y.x : -INFINITY;
-                                y.y = seen(32 * c + 2 * k + 1) ? y.y : -INFINITY;
-                            }
-                            const float a = exp2_fast(y.x), b = exp2_fast(y.y);
-                            sum[k & 1] = add2(sum[k & 1], pair2(a, b));
-                            pk[c >> 1][16 * (c & 1) + k] = bf16_pack(a, b);
+                            const float2 y = unpair(fma2(pair2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
+                                                         c1, mm));
+                            const float a = exp2_fast(2 * k >= from && 2 * k < to ? y.x : -INFINITY);
+                            const float b = exp2_fast(2 * k + 1 >= from && 2 * k + 1 < to ? y.y : -INFINITY);
+                            l2 = add2(l2, pair2(a, b));
+                            pk[k] = bf16_pack(a, b);
                         }
+                        tmem_st16(s_tm + c / 2, pk);
                     }
-                    return add2(sum[0], sum[1]);
-                };
-                if (j == 0)
-                    raise(true);
-                uint64_t sum = exps();
-                const float2 f = unpair(sum);
-                const bool need = j > 0 && f.x + f.y > lim;
-                if (__any_sync(0xffffffffu, need)) {
-                    raise(need);
-                    sum = exps();
+                    break;
                 }
-                l2 = add2(l2, sum);
+                // Scores are loaded 32 ahead of those whose exponentials are taken.
+                uint32_t x[2][32], pk[2][32];
+                uint64_t sum[2] = {0, 0};
+                tmem_ld32(s_tm, x[0]);
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    tmem_ld_wait();
+                    if (c < 3)
+                        tmem_ld32(s_tm + 32 * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+                    for (int k = 0; k < 16; k++) {
+                        const uint32_t *const w = x[c & 1] + 2 * k;
+                        const float2 y = unpair(fma2(pair2(__uint_as_float(w[0]), __uint_as_float(w[1])), c1, mm));
+                        const float a = exp2_fast(y.x), b = exp2_fast(y.y);
+                        sum[k & 1] = add2(sum[k & 1], pair2(a, b));
+                        pk[c >> 1][16 * (c & 1) + k] = bf16_pack(a, b);
+                    }
+                }
+                sum[0] = add2(sum[0], sum[1]);
+                const float2 f = unpair(sum[0]);
+                if (look < kKeys && __any_sync(0xffffffffu, f.x + f.y > lim))
+                    continue;
+                l2 = add2(l2, sum[0]);
                 tmem_st32(s_tm, pk[0]);
                 tmem_st32(s_tm + 32, pk[1]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bars + 8 * (kPFull + half));
-            };
-            if (is_open(sg, key0))
-                tile(std::true_type());
-            else
-                tile(std::false_type());
+                break;
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bars + 8 * (kPFull + half));
             cnt++;
         }
 
@@ -468,80 +701,108 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
             tc_fence_after();
         }
-        const bool hurt = valued && *reinterpret_cast<volatile uint32_t *>(&sh.hurt[sgi]) != 0;
-        if (active) {
+        const bool hurt = valued && *reinterpret_cast<volatile uint32_t *>(&sh.hurt[n % kSegs]) != 0;
+        if (hurt) {
+            // values of V that are not finite, of the keys that the row sees in tiles that not all do
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 32) {
                 uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 32; i++)
-                    w[i] = 0;
-                if (valued) {
-                    tmem_ld32(o_tm + d0, w);
-                    tmem_ld_wait();
-                }
-                float o[32];
-#pragma unroll
-                for (int i = 0; i < 32; i++)
-                    o[i] = __uint_as_float(w[i]);
-                if (hurt) {
-                    // values of V that are not finite, of the keys that the row sees in tiles that not all do
+                tmem_ld32(o_tm + d0, w);
+                tmem_ld_wait();
 #pragma unroll 1
-                    for (int j = 0; j < sg.tiles; j++) {
-                        const int key0 = (sg.first + j) * kKeys;
-                        if (!is_open(sg, key0))
-                            continue;
-#pragma unroll 1
-                        for (int k = 0; k < kKeys; k++) {
-                            const int key = key0 + k;
-                            if (!(key >= mine.lo && key < mine.hi))
-                                continue;
-                            const uint4 *src = reinterpret_cast<const uint4 *>(
-                                p.val.p + (sh.key0[sgi] + int64_t(key)) * p.val.ts + sg.head * p.val.hs + d0);
+                for (int key = max(mine.lo, sg.first * kKeys); key < min(mine.hi, (sg.first + sg.tiles) * kKeys); key++) {
+                    if (!is_open(sg, key & ~(kKeys - 1)))
+                        continue;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        p.val.p + (sh.key0[n % kSegs] + int64_t(key)) * p.val.ts + sg.head * p.val.hs + d0);
 #pragma unroll
-                            for (int c = 0; c < 4; c++) {
-                                const uint4 v = __ldg(src + c);
-                                const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+                    for (int c = 0; c < 4; c++) {
+                        const uint4 v = __ldg(src + c);
+                        const uint32_t a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                                for (int i = 0; i < 4; i++) {
-                                    if ((a[i] & 0x7f80u) == 0x7f80u)
-                                        o[8 * c + 2 * i] += bf16_lo(a[i]);
-                                    if ((a[i] & 0x7f800000u) == 0x7f800000u)
-                                        o[8 * c + 2 * i + 1] += bf16_hi(a[i]);
-                                }
-                            }
+                        for (int i = 0; i < 4; i++) {
+                            uint32_t &low = w[8 * c + 2 * i], &high = w[8 * c + 2 * i + 1];
+                            if ((a[i] & 0x7f80u) == 0x7f80u)
+                                low = __float_as_uint(__uint_as_float(low) + bf16_lo(a[i]));
+                            if ((a[i] & 0x7f800000u) == 0x7f800000u)
+                                high = __float_as_uint(__uint_as_float(high) + bf16_hi(a[i]));
                         }
                     }
                 }
-                if (r < rows) {
-                    if (whole) {
-                        store_dims<32>(p, sg.t0, sg.head, r, d0, o, m, l);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            reinterpret_cast<float4 *>(part)[(d0 / 4 + i) * kRows + threadIdx.x] =
-                                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
-                }
+                __syncwarp();
+                tmem_st32(o_tm + d0, w);
             }
+            tmem_st_wait();
+        }
+        if (active) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: o is 0 and stays 0
+            // A warp's rows lie in shared memory for a moment, 64 dimensions at a time, so that they go out by whole
+            // lines (an item's output by rows of their threads takes 2.3 us).
+            const uint32_t mine_at = out_at + warp * (32 * 128);
+            const uint64_t row_of = reinterpret_cast<uint64_t>(row_at(p, p.o, sg, half, min(threadIdx.x & 127, rows - r0 - 128 * half - 1), 0));
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 16) {
+                uint32_t w[16];
+                if (valued) {
+                    tmem_ld16(o_tm + d0, w);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        w[i] = 0;
+                }
+                auto o = [&](int i) { return __uint_as_float(w[i]); };
+                if (!whole) {
+                    if (r < rows) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            reinterpret_cast<float4 *>(part)[(d0 / 4 + i) * kRows + threadIdx.x] =
+                                make_float4(o(4 * i), o(4 * i + 1), o(4 * i + 2), o(4 * i + 3));
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+                    sts128(mine_at + sw128_offset(lane, (d0 & 63) / 8 + c), bf16_pack(o(8 * c) * inv, o(8 * c + 1) * inv),
+                           bf16_pack(o(8 * c + 2) * inv, o(8 * c + 3) * inv),
+                           bf16_pack(o(8 * c + 4) * inv, o(8 * c + 5) * inv),
+                           bf16_pack(o(8 * c + 6) * inv, o(8 * c + 7) * inv));
+                if ((d0 & 63) != 48)
+                    continue;
+                __syncwarp();
+#pragma unroll 2
+                for (int k = 0; k < 8; k++) {
+                    const int row = 4 * k + (lane >> 3), c = lane & 7;
+                    const uint64_t to = __shfl_sync(0xffffffffu, row_of, row) + 2 * (d0 - 48) + 16 * c;
+                    uint32_t v[4];
+                    lds128(mine_at + sw128_offset(row, c), v);
+                    if (r0 + 32 * warp + row < rows)
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
             if (!whole) {
                 part[kRows * D + threadIdx.x] = m;
                 part[kRows * D + kRows + threadIdx.x] = l;
+            } else if (p.lse && r < rows) {
+                const int i = p.by_group.of(r);
+                p.lse[(sg.t0 + int64_t(i)) * p.q_heads + sg.head * p.group + (r - i * p.group)] =
+                    l == 0.f ? -INFINITY : 0.69314718056f * (m + log2f(l));
             }
-            tc_fence_before();
         }
         if (!whole) {
             // An item that goes on in other CTAs: whoever arrives last joins the parts.
             const uint32_t f = share_of(sg.u0, total, workers), e = share_of(sg.u0 + sg.of - 1, total, workers);
             __threadfence();
-            softmax_sync();
+            softmax_sync(sh, bars, turns, p.v.status);
             if (threadIdx.x == 0) {
                 sh.arrived = atomicAdd(p.counters + f, 1u) == e - f;
                 if (sh.arrived)
                     p.counters[f] = 0;  // ready for the next call
             }
-            softmax_sync();
-            if (sh.arrived && r < rows) {
+            softmax_sync(sh, bars, turns, p.v.status);
+            if (sh.arrived && active) {
                 __threadfence();
                 auto at = [&](uint32_t i) { return p.parts + (2 * uint64_t(i) + (i == f ? 1 : 0)) * PF; };
                 float mt = -INFINITY, lt = 0.f;
@@ -554,32 +815,36 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                     lt = fmaf(exp2_fast(__ldcg(at(i) + kRows * D + threadIdx.x) - m0),
                               __ldcg(at(i) + kRows * D + kRows + threadIdx.x), lt);
 #pragma unroll 1
-                for (int d0 = 0; d0 < D; d0 += 32) {
-                    float o[32];
+                for (int d0 = 0; d0 < D; d0 += 64) {
+                    float o[64];
 #pragma unroll
-                    for (int k = 0; k < 32; k++)
+                    for (int k = 0; k < 64; k++)
                         o[k] = 0.f;
-#pragma unroll 2
+#pragma unroll 1
                     for (uint32_t i = f; i <= e; i++) {
                         const float *const part = at(i);
-                        float4 x[8];
+                        float4 x[16];
 #pragma unroll
-                        for (int k = 0; k < 8; k++)
+                        for (int k = 0; k < 16; k++)
                             x[k] = __ldcg(reinterpret_cast<const float4 *>(part) + (d0 / 4 + k) * kRows + threadIdx.x);
                         const float w = exp2_fast(__ldcg(part + kRows * D + threadIdx.x) - m0);
 #pragma unroll
-                        for (int k = 0; k < 8; k++) {
+                        for (int k = 0; k < 16; k++) {
                             o[4 * k] = fmaf(w, x[k].x, o[4 * k]);
                             o[4 * k + 1] = fmaf(w, x[k].y, o[4 * k + 1]);
                             o[4 * k + 2] = fmaf(w, x[k].z, o[4 * k + 2]);
                             o[4 * k + 3] = fmaf(w, x[k].w, o[4 * k + 3]);
                         }
                     }
-                    store_dims<32>(p, sg.t0, sg.head, r, d0, o, mt, lt);
+                    if (r < rows)
+                        store_dims<64>(p, sg.t0, sg.head, r, d0, o, mt, lt);
                 }
             }
-            softmax_sync();  // sh.arrived is read
+            softmax_sync(sh, bars, turns, p.v.status);  // sh.arrived is read
         }
+        __syncwarp();
+        if (lane == 0)
+            segment_done(bars, n);
     }
 }
 
@@ -588,86 +853,78 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     using S = Sched<kRows, kKeys, kItemCost>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ Shared sh;
-    // The row of units lies where the tiles will: it is not looked at after the first list is made.
+    // What the share's begin is found with lies where the tiles will: it is not looked at after the first segment is
+    // listed.
     Row<kThreads> &row = *reinterpret_cast<Row<kThreads> *>(smem_raw);
-    static_assert(sizeof(row) <= kSmem<D>, "");
-    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    Plan &plan = *reinterpret_cast<Plan *>(smem_raw);
+    static_assert(sizeof(row) <= kSmem<D> && sizeof(plan) <= kSmem<D>, "");
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
     const uint32_t raw = smem_addr(smem_raw), q_at = (raw + 1023u) & ~1023u;
-    const uint32_t k_at = q_at + kQSlots * kTileBytes<D>, v_at = k_at + kStages * kTileBytes<D>;
+    const uint32_t out_at = q_at + 2 * kTileBytes<D>, k_at = out_at + kOutBytes;
+    const uint32_t v_at = k_at + kStages * kTileBytes<D>;
     const uint32_t bars = smem_addr(sh.bars);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; i++) {
-            const bool helpers = i < kQEmpty || (i >= kVOk && i < kVEmpty), rows = i >= kPFull && i < kPvDone,
+            const bool check = (i < kQEmpty && !p.q_map) || (i >= kVOk && i < kVEmpty), rows = i >= kPFull && i < kPvDone,
                        both = (i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kTurn);
-            mbar_init(bars + 8 * i, helpers ? kHelper / 32 : rows ? 4 : both ? 2 : 1);
+            const bool free = i >= kSegFree && i < kSFull;
+            mbar_init(bars + 8 * i, check ? kCheck / 32 : rows ? 4 : both ? (kOneMma<D> ? 1 : 2) : free ? kSegUsers<D> : i == kJoin ? kSoftmax / 32 : 1);
         }
         mbar_init_fence();
         sh.dead = 0;
+        prefetch_map(&p.kmap);
+        prefetch_map(&p.vmap);
+        prefetch_map(&p.qmap);
     }
     grid_dep_launch();
     grid_dep_wait();
-    const uint64_t total = build_row<S, kThreads, true>(p, row);
+    const bool few = p.v.n_seqs <= kThreads / 2;
+    uint64_t before = 0, mine = 0;
+    const uint64_t total = few ? plan_units<S>(p, plan, &before, &mine) : build_row<S, kThreads, true>(p, row);
     const uint32_t workers = uint32_t(min((total + kMinShare - 1) / kMinShare, uint64_t(gridDim.x)));
     if (blockIdx.x >= workers)
         return;
     if (warp == kThreads / 32 - 1)
         tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
     const uint64_t cut0 = mul_div(total, blockIdx.x, workers), cut1 = mul_div(total, blockIdx.x + 1, workers);
-    // From here on every role walks through the lists of segments by itself;
-    // barrier 0 stands before and after a list's work.  Registers a thread by
-    // warpgroup: 2 x 184 + 88 + 56 = 4 x 128, the launch's.
-    tc_fence_before();
-    fence_proxy_async_smem();  // the row's memory is the copies' from then on
-    if (warp < kSoftmax / 32) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        Item it{};
-        if (warp == 0)
-            it = locate<S>(p, row, cut0);
-        uint32_t cnt = 0;
-        for (uint64_t u = cut0; u < cut1;) {
-            if (warp == 0) {
-                int n;
-                const uint64_t to = list_segments<S, kSegs>(p, it, u, cut1, sh.segs, &n);
-                if (lane < n) {
-                    sh.key0[lane] = __ldg(p.v.kstart + sh.segs[lane].s);
-                    sh.hurt[lane] = 0;
-                }
-                if (lane == 0) {
-                    sh.listed_to = to;
-                    sh.n_segs = n;
-                }
-            }
-            __syncthreads();
-            tc_fence_after();
-            u = sh.listed_to;
-            softmax_role<D>(p, sh, bars, total, workers, cut0, cnt);
-            __syncthreads();
-        }
-    } else if (warp < (kSoftmax + kHelper) / 32) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        uint32_t steps = 0, halves = 0;
-        for (uint64_t u = cut0; u < cut1;) {
-            __syncthreads();
-            u = sh.listed_to;
-            helper_role<D>(p, sh, bars, q_at, v_at, steps, halves);
-            __syncthreads();
-        }
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        uint32_t steps = 0, halves = 0, cnt = 0, turns = 0;
-        const int part = warp - (kSoftmax + kHelper) / 32;
-        for (uint64_t u = cut0; u < cut1;) {
-            __syncthreads();
-            tc_fence_after();
-            u = sh.listed_to;
-            if (part < 2)
-                mma_role<D>(p, sh, bars, q_at, k_at, v_at, part, steps, cnt, halves, turns);
-            else if (part == 2 && elect_one())
-                copy_role<D>(p, sh, bars, k_at, v_at, steps);
-            __syncwarp();
-            __syncthreads();
-        }
+    if (few) {
+        plan_item<S>(p, plan, cut0, before, mine);
+        __syncthreads();
     }
+    Item it{};
+    uint64_t listed = cut0;
+    if (warp == kThreads / 32 - 1) {  // (no other warp waits for the first segment in a loop)
+        it = few ? plan.item : locate<S>(p, row, cut0);
+        listed = list_role<S>(p, sh, bars, it, cut0, cut1, 0, 1);
+    }
+    tc_fence_before();
+    fence_proxy_async_smem();  // the row's memory is the copies' from here on
+    __syncthreads();
+    tc_fence_after();
+    // From here on every role walks through the segments by itself.  Registers a thread by
+    // warpgroup: 2 x 176 + 88 + 72 = 4 x 128, the launch's.
+    if (warp < kSoftmax / 32) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        softmax_role<D>(p, sh, bars, total, workers, cut0, out_at);
+    } else if (warp < (kSoftmax + kCheck) / 32) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        check_role<D>(p, sh, bars, q_at, v_at);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int part = warp - (kSoftmax + kCheck) / 32;
+        if (part == 0 || (part == 1 && !kOneMma<D>)) {
+            mma_role<D, kOneMma<D>>(p, sh, bars, q_at, k_at, v_at, part);
+        } else if (part == 2) {
+            if (elect_one())
+                copy_role<D>(p, sh, bars, q_at, k_at, v_at);
+        } else if (part == 3) {
+            list_role<S>(p, sh, bars, it, listed, cut1, 1, UINT32_MAX);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     if (warp == kThreads / 32 - 1)
         tmem_dealloc(sh.tmem, kTmemCols);
 }
@@ -688,6 +945,21 @@ bool encode_keys_map(CUtensorMap *m, const Rows &r, int64_t n, int heads, int di
     const cuuint64_t strides[2] = {cuuint64_t(std::min(hs, ts)) * 2, cuuint64_t(std::max(hs, ts)) * 2};
     const cuuint32_t box[3] = {64, *heads_outer ? cuuint32_t(kKeys) : 1u, *heads_outer ? 1u : cuuint32_t(kKeys)};
     const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// Q as boxes of 64 dimensions x a kv head's query heads x the tokens of 128 rows, where that comes out even and
+// rows lie in that order; otherwise the kernel does without.
+bool encode_q_map(CUtensorMap *m, const Rows &r, int64_t n, int heads, int dim, int group) {
+    const auto enc = tensor_map_encoder();
+    const int64_t hs = heads > 1 ? r.hs : dim, ts = n > 1 ? r.ts : std::max<int64_t>(hs * heads, dim);
+    if (!enc || group > 128 || 128 % group || hs == 0 || ts < hs)
+        return false;
+    const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(n)};
+    const cuuint64_t strides[2] = {cuuint64_t(hs) * 2, cuuint64_t(ts) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(group), cuuint32_t(128 / group)}, estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, r.p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
@@ -778,6 +1050,7 @@ extern "C" uw_status uw_attention(const int32_t *start, const int32_t *kv_start,
     if (n_keys > 0 && (!encode_keys_map(&p.kmap, keys, n_keys, kv_heads, head_dim, &p.heads_outer[0], &p.one_head[0]) ||
                        !encode_keys_map(&p.vmap, p.val, n_keys, kv_heads, head_dim, &p.heads_outer[1], &p.one_head[1])))
         return UW_ERR_CUDA;
+    p.q_map = encode_q_map(&p.qmap, p.q, n_tokens, q_heads, head_dim, p.group);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return (head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st)) == cudaSuccess ? UW_OK : UW_ERR_CUDA;
 }

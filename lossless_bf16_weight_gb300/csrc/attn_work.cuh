@@ -78,6 +78,10 @@ struct Sched {
     static __device__ __forceinline__ uint32_t tiles(const KeyRange &k) {
         return k.hi > k.lo ? uint32_t((k.hi - 1) / T - k.lo / T + 1) : 0u;
     }
+    template <class P>
+    static __device__ __forceinline__ uint32_t units(const P &p, const Seq &s, int rt) {
+        return kCost + tiles(tile_keys(p, s, rt));
+    }
     // Units of one head of a sequence: by one thread, and by a warp that
     // shares its row tiles.
     template <class P>
