@@ -806,14 +806,15 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                 __threadfence();
                 auto at = [&](uint32_t i) { return p.parts + (2 * uint64_t(i) + (i == f ? 1 : 0)) * PF; };
                 float mt = -INFINITY, lt = 0.f;
-#pragma unroll 4
-                for (uint32_t i = f; i <= e; i++)
-                    mt = fmaxf(mt, __ldcg(at(i) + kRows * D + threadIdx.x));
+#pragma unroll 2
+                for (uint32_t i = f; i <= e; i++) {
+                    const float mi = __ldcg(at(i) + kRows * D + threadIdx.x);
+                    const float li = __ldcg(at(i) + kRows * D + kRows + threadIdx.x);
+                    const float m2 = fmaxf(mt, mi), m20 = m2 == -INFINITY ? 0.f : m2;
+                    lt = fmaf(exp2_fast(mi - m20), li, lt * exp2_fast(mt - m20));
+                    mt = m2;
+                }
                 const float m0 = mt == -INFINITY ? 0.f : mt;
-#pragma unroll 4
-                for (uint32_t i = f; i <= e; i++)
-                    lt = fmaf(exp2_fast(__ldcg(at(i) + kRows * D + threadIdx.x) - m0),
-                              __ldcg(at(i) + kRows * D + kRows + threadIdx.x), lt);
 #pragma unroll 1
                 for (int d0 = 0; d0 < D; d0 += 64) {
                     float o[64];
@@ -822,23 +823,31 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                         o[k] = 0.f;
 #pragma unroll 1
                     for (uint32_t i = f; i <= e; i++) {
-                        const float *const part = at(i);
-                        float4 x[16];
+                        const float *const from = at(i);
+                        float x[64];
+                        if (i == blockIdx.x && valued) {  // its own is still there
+                            uint32_t w[2][32];
+                            tmem_ld32(o_tm + d0, w[0]);
+                            tmem_ld32(o_tm + d0 + 32, w[1]);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 16; k++)
-                            x[k] = __ldcg(reinterpret_cast<const float4 *>(part) + (d0 / 4 + k) * kRows + threadIdx.x);
-                        const float w = exp2_fast(__ldcg(part + kRows * D + threadIdx.x) - m0);
+                            for (int k = 0; k < 64; k++)
+                                x[k] = __uint_as_float(w[k / 32][k % 32]);
+                        } else {
 #pragma unroll
-                        for (int k = 0; k < 16; k++) {
-                            o[4 * k] = fmaf(w, x[k].x, o[4 * k]);
-                            o[4 * k + 1] = fmaf(w, x[k].y, o[4 * k + 1]);
-                            o[4 * k + 2] = fmaf(w, x[k].z, o[4 * k + 2]);
-                            o[4 * k + 3] = fmaf(w, x[k].w, o[4 * k + 3]);
+                            for (int k = 0; k < 16; k++)
+                                *reinterpret_cast<float4 *>(x + 4 * k) = __ldcg(
+                                    reinterpret_cast<const float4 *>(from) + (d0 / 4 + k) * kRows + threadIdx.x);
                         }
+                        const float w = exp2_fast(__ldcg(from + kRows * D + threadIdx.x) - m0);
+#pragma unroll
+                        for (int k = 0; k < 64; k++)
+                            o[k] = fmaf(w, x[k], o[k]);
                     }
                     if (r < rows)
                         store_dims<64>(p, sg.t0, sg.head, r, d0, o, mt, lt);
                 }
+                tc_fence_before();
             }
             softmax_sync(sh, bars, turns, p.v.status);  // sh.arrived is read
         }
