@@ -562,9 +562,12 @@ def rmsnorm(x, weight, y, eps: float = 1e-5, residual=None, residual_out=None, s
 
 def _here(what: str, *tensors):
     """Refuses tensors that are not on the current CUDA device, whose stream the call would be made on."""
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() < 0 or t.get_device() != _current_device()):
-            raise UwError(UW_ERR_INVALID_ARG, "%s (a tensor is on %s, not on the current CUDA device)" % (what, t.device))
+        if t is not None and t.get_device() != device:
+            device = -1
+    if device < 0 or device != _current_device():
+        raise UwError(UW_ERR_INVALID_ARG, "%s (tensors are not all on the current CUDA device)" % what)
 
 
 def _current_device() -> int:
@@ -745,7 +748,7 @@ def rope_axes(q, k, pos, pair_axis: bytes, q_out, k_out, cos, sin, ws, interleav
     qo = None if q is None else _kv4_rows(q_out, n, hq, d, "q_out", what)
     ko = None if k is None else _kv4_rows(k_out, n, hk, d, "k_out", what)
     r = _rope(pos, pair_axis, cos, sin, n, interleaved, what)
-    _here(what, q, k, q_out, k_out, pos, cos, sin, ws)
+    _here(what, some, q, k, q_out, k_out, pos, cos, sin, ws)
     _check(load().uw_rope_axes(r, n, qr, hq, qo, kr, hk, ko, d, ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
 
 

@@ -36,8 +36,8 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
 }
 
 // A row kept in registers by T threads (a warp or a CTA), V vectors of 8 each.
-// kOdd: the row begins anywhere (norm.cuh).
-template <int V, bool k8, bool kWarp, bool kOdd>
+// kOdd: the row begins anywhere (norm.cuh).  kLate: weights and gate are loaded where they are used.
+template <int V, bool k8, bool kWarp, bool kOdd, bool kLate = kOdd>
 __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int t, int T, float *slots) {
     const int before = kOdd ? int(reinterpret_cast<uintptr_t>(p.x + row * p.xs) >> 1) & 7 : 0;
     auto first = [&](int v) { return 8 * (int64_t(v) * T + t) - before; };
@@ -46,15 +46,14 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
         return p.gs ? load8<kOdd>(p.g, p.gs, p.n, p.d, row, first(v)) : weights(p.g, v);
     };
     float f[V][8];
-    // all loads before the first store, which could otherwise not pass it (short rows of their
-    // own weights too; where a row begins anywhere, those are loaded where they are used)
+    // the row's loads before the first store, which could otherwise not pass it
     uint4 r[V], a[V], g[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
         unpack8(load8<kOdd>(p.x, p.xs, p.n, p.d, row, first(v)), f[v]);
         r[v] = load8<kOdd>(p.r, p.rs, p.n, p.d, row, first(v));
     }
-    if constexpr (!kOdd) {
+    if constexpr (!kLate) {
 #pragma unroll
         for (int v = 0; v < V; v++) {
             if (p.g)
@@ -79,14 +78,14 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
     for (int v = 0; v < V; v++) {
         if (p.g) {
             float gf[8];
-            unpack8(kOdd ? gates(v) : g[v], gf);
+            unpack8(kLate ? gates(v) : g[v], gf);
 #pragma unroll
             for (int k = 0; k < 8; k++)
                 f[v][k] *= gf[k];
         }
         if (p.wp) {
             float wf[8];
-            unpack8(kOdd ? weights(p.wp, v) : a[v], wf);
+            unpack8(kLate ? weights(p.wp, v) : a[v], wf);
 #pragma unroll
             for (int k = 0; k < 8; k++)
                 f[v][k] *= wf[k] + p.off;
@@ -119,7 +118,7 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
     }
     if (!p.y)
         return;
-    if constexpr (!kOdd) {
+    if constexpr (!kLate) {
 #pragma unroll
         for (int v = 0; v < V; v++)
             a[v] = weights(p.w, v);
@@ -130,7 +129,7 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
 #pragma unroll
     for (int v = 0; v < V; v++) {
         float wf[8];
-        unpack8(kOdd ? weights(p.w, v) : a[v], wf);
+        unpack8(kLate ? weights(p.w, v) : a[v], wf);
 #pragma unroll
         for (int k = 0; k < 8; k++)
             f[v][k] *= wf[k] + p.off;
@@ -171,13 +170,14 @@ __global__ void __launch_bounds__(256) block_warp_kernel(const BlockParams p) {
         block_row<V, k8, true, kOdd>(p, row, threadIdx.x & 31, 32, nullptr);
 }
 
-// (Rows of 16384 that begin anywhere lie on up to 2049 steps: 513 threads.)
-template <int V, bool k8, bool kOdd>
-__global__ void __launch_bounds__(V == 2 ? 256 : 544) block_cta_kernel(const BlockParams p) {
+// kLate: weights and gate are loaded where they are used.  (Rows of 16384 that begin anywhere lie on up to
+// 2049 steps: 513 threads.)
+template <int V, bool k8, bool kOdd, bool kLate, int kMost, int kCtas>
+__global__ void __launch_bounds__(kMost, kCtas) block_cta_kernel(const BlockParams p) {
     __shared__ float slots[96];
     grid_dep_launch();
     grid_dep_wait();
-    block_row<V, k8, false, kOdd>(p, blockIdx.x, threadIdx.x, blockDim.x, slots);
+    block_row<V, k8, false, kOdd, kLate>(p, blockIdx.x, threadIdx.x, blockDim.x, slots);
 }
 
 // Rows of any kind, value by value.
@@ -250,9 +250,25 @@ cudaError_t launch_rows(const BlockParams &p, cudaStream_t st) {
         return launch_overlapped(block_warp_kernel<4, k8, kOdd>, grid, block, 0, st, p);
     }
     const dim3 grid(static_cast<unsigned>(p.n));
-    if (vecs <= 512)
-        return launch_overlapped(block_cta_kernel<2, k8, kOdd>, grid, dim3((vecs + 63) / 64 * 32), 0, st, p);
-    return launch_overlapped(block_cta_kernel<4, k8, kOdd>, grid, dim3((vecs + 127) / 128 * 32), 0, st, p);
+    auto run = [&](auto kernel, int V) {
+        return launch_overlapped(kernel, grid, dim3((vecs + 32 * V - 1) / (32 * V) * 32), 0, st, p);
+    };
+    if constexpr (kOdd) {
+        return vecs <= 512 ? run(block_cta_kernel<2, k8, true, true, 256, 1>, 2)
+                           : run(block_cta_kernel<4, k8, true, true, 544, 1>, 4);
+    } else {
+        // Up to two rows an SM: as many threads as a row has steps (257 x 5120 to 8 bits 4.1 us, half as many
+        // 4.5, a quarter 5.5).  More: what keeps the most loads on their way, by CTAs of an SM and registers
+        // (8191 x 4096 45.2 us with 5 CTAs of 256 threads, 47.5 with 4; 4000 x 8192 46.7 with 3 of 512, 56.8 with
+        // twice the steps a thread; 2000 x 16384 54.8 with 2, with one and early weights 67).
+        if (vecs <= 1024 && p.n <= 2 * sm_count())
+            return run(block_cta_kernel<1, k8, false, false, 1024, 1>, 1);
+        if (vecs <= 512)
+            return run(block_cta_kernel<2, k8, false, false, 256, 5>, 2);
+        if (vecs <= 1024)
+            return run(block_cta_kernel<2, k8, false, true, 512, 3>, 2);
+        return run(block_cta_kernel<4, k8, false, true, 512, 2>, 4);
+    }
 }
 
 template <bool k8>
