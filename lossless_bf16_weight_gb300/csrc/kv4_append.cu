@@ -20,6 +20,8 @@
 // give the same codes as the formula computed step by step in fp32; a code is a
 // step function, and a last-bit difference before it could show as a whole step
 // after it.
+#include <type_traits>
+
 #include "kernels.h"
 #include "kv4.cuh"
 #include "kv4_host.h"
@@ -40,6 +42,7 @@ struct AppendParams {
     float minus_zero;             // -0, which the compiler does not know (rotate())
     // positions on several axes (kAxes): each token's, and the rotated k in BF16, if wanted
     Axes axes;
+    RopePlan plan;  // of q
     Rows ko;
 };
 
@@ -134,6 +137,29 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
     // other sides of their pairs (the same cache lines), before anything is
     // written: q_out may be q.
     const bool of_q = part < p.q_units;
+    if (kAxes && p.rot && of_q) {  // both sides of a pair by one lane
+        const int first = part * p.plan.rounds * p.plan.per;
+        auto rotated = [&](auto interleaved) {
+            rope_heads<decltype(interleaved)::value>(
+                p.plan, p.axes, p.cos, p.sin, pair2(p.minus_zero, p.minus_zero), first, p.q_heads,
+                [&](int j) { return p.q.p + t * p.q.ts + j * p.q.hs; },
+                [&](int j) { return p.qo.p + t * p.qo.ts + j * p.qo.hs; }, [&](AxesAt &turn) {
+                    const Seq q = kv4_seq(v, kv4_find_seq(v, int(t)));
+                    if (t < q.t0 || t >= int64_t(q.t0) + q.n)
+                        return false;  // a token of no sequence
+                    if (q.len - q.n + (int32_t(t) - q.t0) >= 0 && turn.find(p.axes, t, p.rope_len))
+                        return true;
+                    if (lane == 0)
+                        atomicOr(v.status, kStatusBadCache);
+                    return false;
+                });
+        };
+        if (p.interleaved)
+            rotated(std::true_type());
+        else
+            rotated(std::false_type());
+        return;
+    }
     const int rounds = of_q ? p.q_rounds : p.kv_rounds, all = of_q ? p.q_heads : 2 * v.heads;
     const int j0 = (of_q ? part : part - p.q_units) * rounds * G + lane / L;
     const int half = p.rot / 2, i0 = 8 * c;
@@ -366,6 +392,10 @@ static uw_status run_append(const uw_kv4_cache *c, const int32_t *start, const i
     p.kv_rounds = rounds_of(n_tokens, kv_all, 8);
     p.q_units = (q_all + p.q_rounds - 1) / p.q_rounds;
     p.kv_units = (kv_all + p.kv_rounds - 1) / p.kv_rounds;
+    if (axes && rot_dim && q_heads) {
+        p.plan = RopePlan(n_tokens, q_heads, rot_dim, c->head_dim, 2 * 4 * int64_t(sm_count()));
+        p.q_units = p.plan.units;
+    }
     const int64_t units = n_tokens * (p.q_units + p.kv_units);
     if (units > int64_t(8) * 0x7fffffff)
         return UW_ERR_UNSUPPORTED;

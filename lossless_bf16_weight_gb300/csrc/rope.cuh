@@ -82,6 +82,99 @@ __device__ __forceinline__ void rotate(const Rotation &r, uint64_t zero, uint32_
     }
 }
 
+// How a warp takes the heads of one token: `lanes` lanes for a head, eight pairs each, both sides; `per` heads at
+// once, `rounds` times, `units` warps a token; what is not rotated has `tail` 16-byte steps a head.
+struct RopePlan {
+    int32_t half, lanes, per, rounds, units, tail;
+    RopePlan() = default;
+    RopePlan(int64_t tokens, int heads, int rot, int head_dim, int64_t warps) {
+        half = rot / 2;
+        lanes = rot / 16;
+        per = 32 / lanes;
+        tail = (head_dim - rot) / 8;
+        const int all = (heads + per - 1) / per;
+        // `warps` (two a scheduler) come first, longer ones after that
+        rounds = 1;
+        while (2 * rounds <= 16 && rounds < all && tokens * ((all + 2 * rounds - 1) / (2 * rounds)) >= warps)
+            rounds *= 2;
+        units = (all + rounds - 1) / rounds;
+        rounds = (all + units - 1) / units;
+    }
+};
+
+constexpr int kRopeAhead = 2;  // heads a lane has on their way
+
+// Heads from `first` on (below `heads`) of a warp's token rotated: src(j) and dst(j) are where head j lies.  find()
+// looks the token up, while the first heads are on their way; false: nothing is to be touched.  A lane reads
+// what it writes, so dst may be src.
+template <bool kInterleaved, class Src, class Dst, class Find>
+__device__ __forceinline__ void rope_heads(const RopePlan &p, const Axes &axes, const float *cos, const float *sin,
+                                           uint64_t zero, int first, int heads, Src src, Dst dst, Find find) {
+    const int lane = threadIdx.x & 31;
+    const int mine = lane / p.lanes, pc = lane - mine * p.lanes;
+    const bool busy = mine < p.per;
+    const int at0 = kInterleaved ? 16 * pc : 8 * pc, at1 = kInterleaved ? at0 + 8 : p.half + at0;
+    uint4 x[kRopeAhead][2];
+    auto fetch = [&](int n0) {
+#pragma unroll
+        for (int n = 0; n < kRopeAhead; n++) {
+            const int j = first + (n0 + n) * p.per + mine;
+            const bool in = busy && n0 + n < p.rounds && j < heads;
+            const uint16_t *const at = src(in ? j : first);
+            x[n][0] = in ? *reinterpret_cast<const uint4 *>(at + at0) : make_uint4(0, 0, 0, 0);
+            x[n][1] = in ? *reinterpret_cast<const uint4 *>(at + at1) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    fetch(0);
+    AxesAt turn;
+    if (!find(turn))
+        return;
+    Rotation r[2];
+    r[0].on = r[1].on = true;
+    r[0].interleaved = r[1].interleaved = kInterleaved;
+    if (busy) {
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const float4 cs = turn.four(axes, cos, p.half, 8 * pc + 4 * k);
+            const float4 sn = turn.four(axes, sin, p.half, 8 * pc + 4 * k);
+            if (kInterleaved) {
+                r[k].of_pairs(cs, sn);
+            } else {
+                r[0].of_side(cs, sn, k, false);
+                r[1].of_side(cs, sn, k, true);
+            }
+        }
+    }
+    for (int n0 = 0; n0 < p.rounds;) {
+#pragma unroll
+        for (int n = 0; n < kRopeAhead; n++) {
+            const int j = first + (n0 + n) * p.per + mine;
+            uint32_t a[4] = {x[n][0].x, x[n][0].y, x[n][0].z, x[n][0].w};
+            uint32_t b[4] = {x[n][1].x, x[n][1].y, x[n][1].z, x[n][1].w};
+            rotate(r[0], zero, a, x[n][1]);
+            rotate(r[1], zero, b, x[n][0]);
+            if (busy && n0 + n < p.rounds && j < heads) {
+                uint16_t *const at = dst(j);
+                *reinterpret_cast<uint4 *>(at + at0) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4 *>(at + at1) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+        }
+        n0 += kRopeAhead;
+        if (n0 < p.rounds)
+            fetch(n0);
+    }
+    if (!p.tail)
+        return;
+    const int last = min(first + p.rounds * p.per, heads);
+    for (int i = lane; i < (last - first) * p.tail; i += 32) {
+        const int j = first + i / p.tail, at = 2 * p.half + 8 * (i % p.tail);
+        const uint16_t *const from = src(j) + at;
+        uint16_t *const to = dst(j) + at;
+        if (from != to)
+            *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+    }
+}
+
 // rope.cu: the caller's axes, checked, as the kernels take them.
 uw_status rope_axes_map(const uw_rope &r, int64_t n_tokens, Axes *a);
 
