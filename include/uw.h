@@ -651,13 +651,16 @@ uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *start_dev, cons
  *   n_tokens, n_keys  rows of q and out, and of k and v (equal without kv_start,
  *             UW_ERR_SHAPE otherwise).
  *   q, k, v, out  head_dim 64 or 128; strides of any order.  (k and v of more than
- *             one key with token stride 0: UW_ERR_UNSUPPORTED.)
+ *             one key with token stride 0: UW_ERR_UNSUPPORTED; head stride 0: one head for
+ *             all.)  out may be q itself.
  *   lse_dev   fp32 [n_tokens, q_heads]: log(sum exp(scale q.k)) (written), or NULL.
  *   softmax_scale  0 for 1 / sqrt(head_dim).
  *   ws_dev    at least uw_attention_workspace_size bytes, cleared once by
  *             uw_workspace_init; it serves calls of any sequences and heads.
  * Scores, softmax statistics and sums are fp32; a probability is rounded to one BF16 for the product with
- * V (2^-8 of it).  The same call gives the same bits.  Scores q.k times scale beyond fp32 give NaN. */
+ * V (2^-8 of it).  The same call gives the same bits.
+ * Ranges: scores q.k, times scale too, within fp32 and |v| below 2^80; past them a result may not be
+ * finite. */
 uw_status uw_attention_workspace_size(int32_t head_dim, size_t *bytes);
 uw_status uw_attention(const int32_t *start_dev, const int32_t *kv_start_dev, int32_t n_seqs, int64_t n_tokens,
                        int64_t n_keys, const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *k,

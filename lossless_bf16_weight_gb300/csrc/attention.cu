@@ -14,9 +14,10 @@
 //   copies    warp 14, one elected thread: tiles of K and V by tensor-map copies, two
 //             stages of each.  V lies as it comes, [keys][dims], and is the second product's
 //             operand with its rows along the product.
-// The running maximum is only raised when some row's probabilities of a tile add up to
-// more than 2^40 (BF16 and fp32 hold that without loss), so that after the first keys no score
-// is compared and O is rarely rescaled.  P is rounded to one BF16 (2^-8, the one rounding beside
+// A row's running maximum is only raised when its probabilities of a tile add up to
+// more than 2^40 (BF16 and fp32 hold that without loss; with 2^24, rows of which one or the other
+// goes past it in every other tile, 8192 tokens take 774 us instead of 673), so that after the first keys no
+// score is compared and O is rarely rescaled.  P is rounded to one BF16 (2^-8, the one rounding beside
 // the output's); its sum is fp32 of the unrounded values.
 //
 // What a row does not see takes no part in it, whatever its bits: a masked score is
@@ -76,7 +77,8 @@ struct PackedParams {
     int32_t q_heads, group, causal, window;
     Divisor by_group;
     bool out32;                  // rows of o begin on 32-byte steps
-    bool heads_outer[2], one_head[2];  // of K, V: the tensor map's outermost dimension is the head; all heads are one
+    // of K and V: the tensor map's outermost dimension is the head; all heads are one
+    bool heads_outer[2], one_head[2];
     bool q_map;                  // queries come by qmap
     int32_t rows_min, rows_max;  // any
     float *parts;                // parts of kRows * (D + 2) floats: output, maximum, sum
@@ -86,8 +88,8 @@ struct PackedParams {
 };
 
 enum Bar {
-    kQFull, kQEmpty = kQFull + 2, kKFull = kQEmpty + 2, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVOk = kVFull + kStages,
-    kVEmpty = kVOk + kStages, kTurn = kVEmpty + kStages, kSegFull = kTurn + 2, kSegFree = kSegFull + kSegs,
+    kQFull, kQEmpty = kQFull + 2, kKFull = kQEmpty + 2, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages,
+    kVOk = kVFull + kStages, kVEmpty = kVOk + kStages, kTurn = kVEmpty + kStages, kSegFull = kTurn + 2, kSegFree = kSegFull + kSegs,
     kSFull = kSegFree + kSegs, kPFull = kSFull + 2, kPvDone = kPFull + 2,
     kDrain = kPvDone + 2, kJoin = kDrain + 2, kBars
 };
@@ -115,7 +117,7 @@ constexpr size_t kSmem = 1024 + kOutBytes + (2 + 2 * kStages) * size_t(kTileByte
 __device__ __forceinline__ bool is_dead(Shared &sh) { return *reinterpret_cast<volatile uint32_t *>(&sh.dead) != 0; }
 // What is ready, or soon, is found by a few looks; then a thread is suspended for up to a microsecond at a time
 // (a prompt of 8192 tokens 374 us, without the looks 394).
-constexpr uint32_t kHintNs = 1000, kTries = kWaitTries / 8;
+constexpr uint32_t kHintNs = 1000;
 __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -138,7 +140,7 @@ __device__ __forceinline__ void wait(Shared &sh, uint32_t bar, uint32_t parity, 
     for (int i = 0; i < 4; i++)
         if (look(bar, parity))
             return;
-    for (uint32_t i = 0; i < kTries; i++)
+    for (uint32_t i = 0; i < kWaitTries; i++)
         if (try_wait(bar, parity) || is_dead(sh))
             return;
     atomicOr(status, kStatusTimeout);
@@ -597,12 +599,15 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             tc_fence_after();
             const int lo = mine.lo - key0, hi = mine.hi - key0;  // the row's keys of the tile
             const bool open = is_open(sg, key0);
-            // (Code that runs once an item is kept short: instructions that are not at hand come eight in 60 cycles.)
+            // (What runs once an item is kept in short loops: unrolled, twelve packed prompts take 88 us instead
+            // of 78.)
+            bool over = true;  // the row's maximum is to be raised
             for (int look = open ? kKeys : j == 0 ? 32 : 0;; look = kKeys) {
                 if (look > 0) {
                     // Raise the maximum to that of the first 32 keys (of an item's first tile: most often that will
-                    // do) or of all, in rows where it is more than 30 higher (not in others, whose bits then
-                    // depend on no other row): what the row has so far is scaled down.
+                    // do) or of all, in rows that need it by their own sum or, where that is not looked at, a maximum
+                    // more than 2^30 higher (not in others, so that a row's bits depend on no other row): what the
+                    // row has so far is scaled down.
                     float top = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < look; c += 32) {
@@ -614,7 +619,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                         for (int k = 0; k < 32; k++)
                             top = k >= from && k < to ? fmaxf(top, __uint_as_float(x[k])) : top;
                     }
-                    const bool need = !(top * p.c1 - m <= 30.f);
+                    const bool need = open ? !(top * p.c1 - m <= 30.f) : over;
                     const float m2 = need ? fmaxf(m, top * p.c1) : m, m20 = m2 == -INFINITY ? 0.f : m2;
                     const float f = !need ? 1.f : m == -INFINITY ? 0.f : exp2_fast(m - m20);
                     l2 = mul2(l2, pair2(f, f));
@@ -677,7 +682,8 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 const float2 f = unpair(sum[0]);
-                if (look < kKeys && __any_sync(0xffffffffu, f.x + f.y > lim))
+                over = f.x + f.y > lim;
+                if (look < kKeys && __any_sync(0xffffffffu, over))
                     continue;
                 l2 = add2(l2, sum[0]);
                 tmem_st32(s_tm, pk[0]);
@@ -704,13 +710,14 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
         const bool hurt = valued && *reinterpret_cast<volatile uint32_t *>(&sh.hurt[n % kSegs]) != 0;
         if (hurt) {
             // values of V that are not finite, of the keys that the row sees in tiles that not all do
+            const int last = min(mine.hi - 1, (sg.first + sg.tiles - 1) * kKeys + (kKeys - 1));
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 32) {
                 uint32_t w[32];
                 tmem_ld32(o_tm + d0, w);
                 tmem_ld_wait();
 #pragma unroll 1
-                for (int key = max(mine.lo, sg.first * kKeys); key < min(mine.hi, (sg.first + sg.tiles) * kKeys); key++) {
+                for (int key = max(mine.lo, sg.first * kKeys); key <= last; key++) {
                     if (!is_open(sg, key & ~(kKeys - 1)))
                         continue;
                     const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -739,7 +746,8 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             // A warp's rows lie in shared memory for a moment, 64 dimensions at a time, so that they go out by whole
             // lines (an item's output by rows of their threads takes 2.3 us).
             const uint32_t mine_at = out_at + warp * (32 * 128);
-            const uint64_t row_of = reinterpret_cast<uint64_t>(row_at(p, p.o, sg, half, min(threadIdx.x & 127, rows - r0 - 128 * half - 1), 0));
+            const int in_half = min(int(threadIdx.x & 127), rows - r0 - 128 * half - 1);
+            const uint64_t row_of = reinterpret_cast<uint64_t>(row_at(p, p.o, sg, half, in_half, 0));
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 16) {
                 uint32_t w[16];
@@ -874,10 +882,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t bars = smem_addr(sh.bars);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; i++) {
-            const bool check = (i < kQEmpty && !p.q_map) || (i >= kVOk && i < kVEmpty), rows = i >= kPFull && i < kPvDone,
-                       both = (i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kTurn);
-            const bool free = i >= kSegFree && i < kSFull;
-            mbar_init(bars + 8 * i, check ? kCheck / 32 : rows ? 4 : both ? (kOneMma<D> ? 1 : 2) : free ? kSegUsers<D> : i == kJoin ? kSoftmax / 32 : 1);
+            uint32_t n = 1;  // a commit, a copy's announcement
+            if ((i < kQEmpty && !p.q_map) || (i >= kVOk && i < kVEmpty))
+                n = kCheck / 32;
+            else if (i >= kPFull && i < kPvDone)
+                n = 4;
+            else if ((i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kTurn))
+                n = kOneMma<D> ? 1 : 2;
+            else if (i >= kSegFree && i < kSFull)
+                n = kSegUsers<D>;
+            else if (i == kJoin)
+                n = kSoftmax / 32;
+            mbar_init(bars + 8 * i, n);
         }
         mbar_init_fence();
         sh.dead = 0;
