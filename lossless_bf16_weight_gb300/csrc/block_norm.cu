@@ -4,11 +4,22 @@
 //     y = h (mean(h^2) + eps)^(-1/2) (w + off)
 // with y in BF16, or in e4m3 with a scale for each row, or left out.
 //
-// Memory bound: x, r (and a gate of every row) are read once, h and y written
-// once, in 16-byte steps; a row stays in registers through its two sums, x in fp32 and r as it
-// came.  One warp a row up to 1024 values, one CTA a row above, rows that may begin
-// anywhere as in norm.cu; rows that are not alike or have more than 16384 values are
+// Memory bound, and with 13 instructions a value not far from bound by issue slots (75% of them with 16): x, r
+// (and a gate of every row) are read once, h and y written once, in 16-byte steps; a row stays in
+// registers through its two sums, x and r as they came.  One warp a row up to 1024 values, one CTA a row above,
+// rows that may begin anywhere as in norm.cu; rows that are not alike or have more than 16384 values are
 // taken value by value, with h read back (or made again) for the second norm.
+//
+// Measured, with a norm after the block and a gate for all rows unless stated (of 6.8 TB/s for a copy):
+//   1 x 4096, no gate      2.5 us
+//   257 x 5120 to 8 bits   4.1 us
+//   8191 x 4096            43.8 us (6.1 TB/s); to 8 bits 47.1 (5.0); a gate of every row 50.8 (6.6)
+//   16000 x 2048           41.2 us (6.4 TB/s)
+//   4000 x 8192            45.4 us (5.8 TB/s); 2000 x 16384 49.2 (5.3)
+//   8000 x 1000            11.8 us (in L2); 8000 x 1001 25.5
+//   8000 x 4097            83.6 us (3.1 TB/s: three weights a value shifted into place)
+// One CTA for many rows, weights and gate kept in registers and the next row's x and r on their way: 55 us
+// for 8191 x 4096 (its registers leave too few warps).
 #include <cmath>
 
 #include "norm.cuh"
@@ -26,14 +37,29 @@ struct BlockParams {
     float eps, off, r_scale, b_scale;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        f[2 * k] = bf16_lo(a[k]);
-        f[2 * k + 1] = bf16_hi(a[k]);
-    }
+// Two values each: a b + c with the products of BF16 pairs exact, and a + c, by the instructions that take BF16 as
+// it is (a conversion for each value otherwise, which with three reads and two sums of a value is what issue slots
+// go to: 8191 x 4096 45.1 us without).
+__device__ __forceinline__ void fma_pair(uint32_t a, uint32_t b, float &c0, float &c1) {
+    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\t"
+        "mov.b32 {al, ah}, %2;\n\t"
+        "mov.b32 {bl, bh}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, al, bl, %0;\n\t"
+        "fma.rn.f32.bf16 %1, ah, bh, %1;\n\t}"
+        : "+f"(c0), "+f"(c1)
+        : "r"(a), "r"(b));
 }
+__device__ __forceinline__ float2 add_pair(uint32_t a, float c) {
+    float2 r;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "add.rn.f32.bf16 %0, l, %3;\n\t"
+        "add.rn.f32.bf16 %1, h, %3;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(a), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t word(const uint4 &v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
 
 // A row kept in registers by T threads (a warp or a CTA), V vectors of 8 each.
 // kOdd: the row begins anywhere (norm.cuh).  kLate: weights and gate are loaded where they are used.
@@ -45,12 +71,11 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
     auto gates = [&](int v) {
         return p.gs ? load8<kOdd>(p.g, p.gs, p.n, p.d, row, first(v)) : weights(p.g, v);
     };
-    float f[V][8];
     // the row's loads before the first store, which could otherwise not pass it
-    uint4 r[V], a[V], g[V];
+    uint4 x[V], r[V], a[V], g[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
-        unpack8(load8<kOdd>(p.x, p.xs, p.n, p.d, row, first(v)), f[v]);
+        x[v] = load8<kOdd>(p.x, p.xs, p.n, p.d, row, first(v));
         r[v] = load8<kOdd>(p.r, p.rs, p.n, p.d, row, first(v));
     }
     if constexpr (!kLate) {
@@ -64,57 +89,53 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
     }
     float c = p.b_scale;  // of x
     if (p.wp) {
-        float ss = 0.f;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int v = 0; v < V; v++)
 #pragma unroll
-            for (int k = 0; k < 8; k++)
-                ss = fmaf(f[v][k], f[v][k], ss);
-        ss = kWarp ? warp_sum(ss) : cta_reduce<false>(ss, slots);
+            for (int k = 0; k < 4; k++)
+                fma_pair(word(x[v], k), word(x[v], k), s0, s1);
+        const float ss = kWarp ? warp_sum(s0 + s1) : cta_reduce<false>(s0 + s1, slots);
         c *= rsqrtf(ss / float(p.d) + p.eps);
     }
-    float ss = 0.f;
+    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-        if (p.g) {
-            float gf[8];
-            unpack8(kLate ? gates(v) : g[v], gf);
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-                f[v][k] *= gf[k];
-        }
-        if (p.wp) {
-            float wf[8];
-            unpack8(kLate ? weights(p.wp, v) : a[v], wf);
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-                f[v][k] *= wf[k] + p.off;
-        }
-        float rf[8];
-        unpack8(r[v], rf);
+        const uint4 gv = !p.g ? make_uint4(0, 0, 0, 0) : kLate ? gates(v) : g[v];
+        const uint4 wv = !p.wp ? make_uint4(0, 0, 0, 0) : kLate ? weights(p.wp, v) : a[v];
         uint32_t h[4];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            h[k] = bf16_pack(fmaf(f[v][2 * k], c, p.r_scale * rf[2 * k]),
-                             fmaf(f[v][2 * k + 1], c, p.r_scale * rf[2 * k + 1]));
+        for (int k = 0; k < 4; k++) {
+            const uint32_t xw = word(x[v], k), rw = word(r[v], k);
+            float f0 = 0.f, f1 = 0.f;
+            if (p.g) {
+                fma_pair(xw, word(gv, k), f0, f1);
+            } else {
+                f0 = bf16_lo(xw);
+                f1 = bf16_hi(xw);
+            }
+            if (p.wp) {
+                const float2 w = add_pair(word(wv, k), p.off);
+                f0 *= w.x;
+                f1 *= w.y;
+            }
+            h[k] = bf16_pack(fmaf(f0, c, p.r_scale * bf16_lo(rw)), fmaf(f1, c, p.r_scale * bf16_hi(rw)));
+        }
+        const int64_t i = first(v);
         if constexpr (kOdd) {  // what is not the row's counts for nothing, whatever the scales make of it
-            const int64_t i = first(v);
 #pragma unroll
             for (int k = 0; k < 4; k++)
                 h[k] &= (i + 2 * k >= 0 && i + 2 * k < p.d ? 0xffffu : 0u) |
                         (i + 2 * k + 1 >= 0 && i + 2 * k + 1 < p.d ? 0xffff0000u : 0u);
+        } else if (i >= p.d) {
+            h[0] = h[1] = h[2] = h[3] = 0;
         }
         if (p.h)
-            store8<kOdd>(p.h + row * p.hs, first(v), p.d, h);
-        unpack8(make_uint4(h[0], h[1], h[2], h[3]), f[v]);
-        if (!kOdd && first(v) >= p.d) {
+            store8<kOdd>(p.h + row * p.hs, i, p.d, h);
 #pragma unroll
-            for (int k = 0; k < 8; k++)
-                f[v][k] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-            ss = fmaf(f[v][k], f[v][k], ss);
+        for (int k = 0; k < 4; k++)
+            fma_pair(h[k], h[k], s0, s1);
+        x[v] = make_uint4(h[0], h[1], h[2], h[3]);
     }
     if (!p.y)
         return;
@@ -123,27 +144,28 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
         for (int v = 0; v < V; v++)
             a[v] = weights(p.w, v);
     }
-    ss = kWarp ? warp_sum(ss) : cta_reduce<false>(ss, slots + 32);
+    const float ss = kWarp ? warp_sum(s0 + s1) : cta_reduce<false>(s0 + s1, slots + 32);
     const float rstd = rsqrtf(ss / float(p.d) + p.eps);
-    float top = 0.f;
+    float top = 0.f, f[k8 ? V : 1][8];
 #pragma unroll
     for (int v = 0; v < V; v++) {
-        float wf[8];
-        unpack8(kLate ? weights(p.w, v) : a[v], wf);
+        const uint4 wv = kLate ? weights(p.w, v) : a[v];
+        uint32_t y[4];
 #pragma unroll
-        for (int k = 0; k < 8; k++)
-            f[v][k] *= wf[k] + p.off;
-        if constexpr (k8) {
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-                top = max_nan(top, fabsf(f[v][k]));
-        } else {
-            uint32_t y[4];
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                y[k] = bf16_pack(f[v][2 * k] * rstd, f[v][2 * k + 1] * rstd);
-            store8<kOdd>(static_cast<uint16_t *>(p.y) + row * p.ys, first(v), p.d, y);
+        for (int k = 0; k < 4; k++) {
+            const uint32_t hw = word(x[v], k);
+            const float2 w = add_pair(word(wv, k), p.off);
+            const float u0 = bf16_lo(hw) * w.x, u1 = bf16_hi(hw) * w.y;
+            if constexpr (k8) {
+                f[v][2 * k] = u0;
+                f[v][2 * k + 1] = u1;
+                top = max_nan(top, max_nan(fabsf(u0), fabsf(u1)));
+            } else {
+                y[k] = bf16_pack(u0 * rstd, u1 * rstd);
+            }
         }
+        if constexpr (!k8)
+            store8<kOdd>(static_cast<uint16_t *>(p.y) + row * p.ys, first(v), p.d, y);
     }
     if constexpr (k8) {
         const RowScale s(kWarp ? warp_max(top) : cta_reduce<true>(top, slots + 64), rstd);
@@ -254,13 +276,13 @@ cudaError_t launch_rows(const BlockParams &p, cudaStream_t st) {
         return launch_overlapped(kernel, grid, dim3((vecs + 32 * V - 1) / (32 * V) * 32), 0, st, p);
     };
     if constexpr (kOdd) {
-        return vecs <= 512 ? run(block_cta_kernel<2, k8, true, true, 256, 1>, 2)
-                           : run(block_cta_kernel<4, k8, true, true, 544, 1>, 4);
+        return vecs <= 1088 ? run(block_cta_kernel<2, k8, true, true, 544, 2>, 2)
+                            : run(block_cta_kernel<4, k8, true, true, 544, 1>, 4);
     } else {
         // Up to two rows an SM: as many threads as a row has steps (257 x 5120 to 8 bits 4.1 us, half as many
         // 4.5, a quarter 5.5).  More: what keeps the most loads on their way, by CTAs of an SM and registers
-        // (8191 x 4096 45.2 us with 5 CTAs of 256 threads, 47.5 with 4; 4000 x 8192 46.7 with 3 of 512, 56.8 with
-        // twice the steps a thread; 2000 x 16384 54.8 with 2, with one and early weights 67).
+        // (measured before fma_pair: 8191 x 4096 45.2 us with 5 CTAs of 256 threads, 47.5 with 4; 4000 x 8192 46.7
+        // with 3 of 512, 56.8 with twice the steps a thread; 2000 x 16384 54.8 with 2, with one and early weights 67).
         if (vecs <= 1024 && p.n <= 2 * sm_count())
             return run(block_cta_kernel<1, k8, false, false, 1024, 1>, 1);
         if (vecs <= 512)
