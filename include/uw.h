@@ -589,7 +589,8 @@ uw_status uw_rope_axes(const uw_rope *r, int64_t n_tokens, const uw_kv4_rows *q,
 /* uw_kv4_append_axes -- uw_kv4_append with the rotation of uw_rope.  A token's place in
  * the cache still goes by start and len.
  *   r         as above; rot_dim 0: no rotation, and positions are not looked at.
- *   k_out     the rotated k (written; may be k), or NULL.
+ *   k_out     the rotated k (written, whether or not the token's page is in the pool; may be
+ *             k), or NULL.
  * Others as for uw_kv4_append. */
 uw_status uw_kv4_append_axes(const uw_kv4_cache *c, const int32_t *start_dev, const int32_t *len_dev, int64_t n_tokens,
                              const uw_rope *r, const uw_kv4_rows *q, int32_t q_heads, const uw_kv4_rows *q_out,

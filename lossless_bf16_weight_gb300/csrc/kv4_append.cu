@@ -144,10 +144,11 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
                 p.plan, p.axes, p.cos, p.sin, pair2(p.minus_zero, p.minus_zero), first, p.q_heads,
                 [&](int j) { return p.q.p + t * p.q.ts + j * p.q.hs; },
                 [&](int j) { return p.qo.p + t * p.qo.ts + j * p.qo.hs; }, [&](AxesAt &turn) {
+                    const bool found = turn.find(p.axes, t, p.rope_len);
                     const Seq q = kv4_seq(v, kv4_find_seq(v, int(t)));
                     if (t < q.t0 || t >= int64_t(q.t0) + q.n)
                         return false;  // a token of no sequence
-                    if (q.len - q.n + (int32_t(t) - q.t0) >= 0 && turn.find(p.axes, t, p.rope_len))
+                    if (found && q.len - q.n + (int32_t(t) - q.t0) >= 0)
                         return true;
                     if (lane == 0)
                         atomicOr(v.status, kStatusBadCache);
@@ -182,27 +183,33 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
         }
     };
     fetch(0);
+    // positions on axes and their rows of the tables do not wait for the token's place
+    bool found = true;
+    if (kAxes && p.rot) {
+        AxesAt turn;
+        found = turn.find(p.axes, t, p.rope_len);
+        if (found && r.on) {
+            const int j = p.interleaved ? 4 * c : second ? i0 - half : i0;
+            const float4 c0 = turn.four(p.axes, p.cos, half, j), s0 = turn.four(p.axes, p.sin, half, j);
+            if (p.interleaved) {
+                r.of_pairs(c0, s0);
+            } else {
+                r.of_side(c0, s0, 0, second);
+                r.of_side(turn.four(p.axes, p.cos, half, j + 4), turn.four(p.axes, p.sin, half, j + 4), 1, second);
+            }
+        }
+    }
     const int s = kv4_find_seq(v, int(t));
     const Seq q = kv4_seq(v, s);
     if (t < q.t0 || t >= int64_t(q.t0) + q.n)
         return;  // a token of no sequence
     const int32_t pos = q.len - q.n + (int32_t(t) - q.t0);
-    AxesAt turn;
-    if (pos < 0 || (p.rot && (kAxes ? !turn.find(p.axes, t, p.rope_len) : pos >= p.rope_len))) {
+    if (pos < 0 || !found || (!kAxes && p.rot && pos >= p.rope_len)) {
         if (lane == 0)
             atomicOr(v.status, kStatusBadCache);
         return;
     }
-    if (kAxes && r.on) {
-        const int j = p.interleaved ? 4 * c : second ? i0 - half : i0;
-        const float4 c0 = turn.four(p.axes, p.cos, half, j), s0 = turn.four(p.axes, p.sin, half, j);
-        if (p.interleaved) {
-            r.of_pairs(c0, s0);
-        } else {
-            r.of_side(c0, s0, 0, second);
-            r.of_side(turn.four(p.axes, p.cos, half, j + 4), turn.four(p.axes, p.sin, half, j + 4), 1, second);
-        }
-    } else if (r.on) {
+    if (!kAxes && r.on) {
         const int64_t row = int64_t(pos) * half;
         if (p.interleaved) {
             r.of_pairs(*reinterpret_cast<const float4 *>(p.cos + row + 4 * c),
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
         }
     }
     uint8_t *const page = kv4_block<D>(v, s, pos, 0);  // the token's page, block of head 0
-    if (!page)
+    if (!page && !(kAxes && p.ko.p))
         return;
     const int slot = pos & ((1 << v.page_log2) - 1);
     const int64_t block = int64_t(D + 8) << v.page_log2;
@@ -257,7 +264,7 @@ __global__ void __launch_bounds__(256, 4) kv4_append_kernel(const AppendParams p
                     make_uint4(a[0], a[1], a[2], a[3]);
             uint32_t params;
             const uint32_t codes = quantise<D>(a, &params);
-            if (j < all) {
+            if (j < all && (!kAxes || page)) {
                 uint8_t *const blk = page + (is_v ? j - v.heads : j) * block;
                 *reinterpret_cast<uint32_t *>(blk + kv4_codes<D>(v.page_log2, slot, is_v) + 4 * c) = codes;
                 if (c == 0)

@@ -212,6 +212,25 @@ def test_tokens_of_no_sequence_and_bad_positions(uw):
     assert np.all(codes[2] == 0x77) and np.all(codes[5:] == 0x77) and np.all(pages.cpu().numpy()[1] == 0x77)
 
 
+def test_a_page_outside_the_pool(uw):
+    """Nothing of the cache is touched and the call says so; q and k come out rotated all the same."""
+    rng = np.random.default_rng(7)
+    hq, hk, d, page, t = 3, 2, 128, 16, 20
+    cos, sin = _tables(rng, 40, 64)
+    axis, pos = _axis(rng, 64, 3, "sections"), rng.integers(0, 40, (3, t)).astype(np.int32)
+    qkv = ref.bf16(rng.standard_normal((t, hq + 2 * hk, d)))
+    pages = torch.full((2, hk, page * (d + 8)), 0x77, dtype=torch.uint8, device="cuda")
+    cache = uw.kv4_cache(pages, _dev(np.array([[1, 2]], np.int32)), hk, d, page)     # page 2 is none of the pool's
+    x, ws = _dev(qkv), _ws(uw)
+    q, k = torch.zeros(t, hq, d, dtype=torch.int16, device="cuda"), torch.zeros(t, hk, d, dtype=torch.int16, device="cuda")
+    uw.kv4_append_axes(cache, _dev(np.array([0, t], np.int32)), _dev(np.array([t], np.int32)), _dev(pos), bytes(axis.tolist()),
+                       x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], q, _dev(cos), _dev(sin), ws, k_out=k)
+    assert uw.check_status(ws) == 4
+    want = _turned(qkv[:, :hq + hk], pos, axis, cos, sin, False)
+    assert np.array_equal(_bits(q), want[:, :hq]) and np.array_equal(_bits(k), want[:, hq:])
+    assert (pages[0] == 0x77).all() and not (pages[1] == 0x77).all()
+
+
 def test_captured_and_replayed(uw):
     rng = np.random.default_rng(5)
     t, h, d = 50, 4, 128
