@@ -45,7 +45,7 @@ namespace {
 constexpr int kRows = 256, kKeys = 128;
 constexpr int kSoftmax = 256, kCheck = 128;         // threads
 constexpr int kThreads = kSoftmax + kCheck + 128;   // and a warpgroup of the MMA, copying and listing warps
-constexpr int kItemCost = 4;                          // what an item costs beyond its steps, in steps
+constexpr int kItemCost = 3;                          // what an item costs beyond its steps, in steps
 constexpr int kMinShare = 4;                          // units of a CTA at least
 constexpr int kSegs = 16;
 constexpr int kStages = 2;
@@ -171,6 +171,9 @@ __device__ __forceinline__ void softmax_sync(Shared &sh, uint32_t bars, uint32_t
 __device__ __forceinline__ uint32_t tile_at(int r, int c) {
     return uint32_t(c >> 3) * (128u * 128u) + sw128_offset(uint32_t(r), uint32_t(c & 7));
 }
+
+// The lowest n bits; none of n below 0, all of n past 32.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
 // Whether some row of the segment does not see some key of the tile at key0.
 __device__ __forceinline__ bool is_open(const Seg &sg, int key0) {
@@ -601,71 +604,64 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             const bool open = is_open(sg, key0);
             // (What runs once an item is kept in short loops: unrolled, twelve packed prompts take 88 us instead
             // of 78.)
-            bool over = true;  // the row's maximum is to be raised
-            for (int look = open ? kKeys : j == 0 ? 32 : 0;; look = kKeys) {
+            uint32_t x[2][32];
+            tmem_ld32(s_tm, x[0]);
+            bool over = j == 0;  // the row's maximum is to be raised
+            int look = open ? kKeys : j == 0 ? 32 : 0;
+            for (bool last = open && j == 0;; last = true, look = kKeys) {
                 if (look > 0) {
-                    // Raise the maximum to that of the first 32 keys (of an item's first tile: most often that will
-                    // do) or of all, in rows that need it by their own sum or, where that is not looked at, a maximum
-                    // more than 2^30 higher (not in others, so that a row's bits depend on no other row): what the
-                    // row has so far is scaled down.
+                    // What the row does not see becomes -inf, whose exponential is 0; from there on an open tile is
+                    // like others.  And the highest score of the first 32 keys (of an item's first tile, where all
+                    // see it: most often that will do) or of all.
                     float top = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < look; c += 32) {
                         uint32_t x[32];
+                        tmem_ld_wait();
                         tmem_ld32(s_tm + c, x);
                         tmem_ld_wait();
-                        const int from = lo - c, to = hi - c;
+                        const uint32_t seen = bits_below(hi - c) & ~bits_below(lo - c);
+                        if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
+#pragma unroll
+                            for (int k = 0; k < 32; k++)
+                                x[k] = seen >> k & 1 ? x[k] : 0xff800000u;
+                            tmem_st32(s_tm + c, x);
+                        }
 #pragma unroll
                         for (int k = 0; k < 32; k++)
-                            top = k >= from && k < to ? fmaxf(top, __uint_as_float(x[k])) : top;
+                            top = fmaxf(top, __uint_as_float(x[k]));
                     }
-                    const bool need = open ? !(top * p.c1 - m <= 30.f) : over;
-                    const float m2 = need ? fmaxf(m, top * p.c1) : m, m20 = m2 == -INFINITY ? 0.f : m2;
-                    const float f = !need ? 1.f : m == -INFINITY ? 0.f : exp2_fast(m - m20);
-                    l2 = mul2(l2, pair2(f, f));
-                    m = m2;
-                    mm = pair2(-m20, -m20);
-                    lim = m2 == -INFINITY ? unset : kRaise;
-                    if (j > 0 && __any_sync(0xffffffffu, need)) {
-                        wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
-                        tc_fence_after();
+                    tmem_st_wait();
+                    if (__any_sync(0xffffffffu, over)) {
+                        // Raised in rows that need it by their own sum (not in others, so that a row's bits depend on
+                        // no other row): what the row has so far is scaled down.
+                        const float m2 = over ? fmaxf(m, top * p.c1) : m, m20 = m2 == -INFINITY ? 0.f : m2;
+                        const float f = !over ? 1.f : m == -INFINITY ? 0.f : exp2_fast(m - m20);
+                        l2 = mul2(l2, pair2(f, f));
+                        m = m2;
+                        mm = pair2(-m20, -m20);
+                        lim = m2 == -INFINITY ? unset : kRaise;
+                        if (j > 0) {
+                            wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int d0 = 0; d0 < D; d0 += 16) {
-                            uint32_t w[16];
-                            tmem_ld16(o_tm + d0, w);
-                            tmem_ld_wait();
+                            for (int d0 = 0; d0 < D; d0 += 16) {
+                                uint32_t w[16];
+                                tmem_ld16(o_tm + d0, w);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; i++)
-                                w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-                            tmem_st16(o_tm + d0, w);
+                                for (int i = 0; i < 16; i++)
+                                    w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                                tmem_st16(o_tm + d0, w);
+                            }
                         }
                     }
-                }
-                if (open) {
-                    // 32 keys at a time; their P lies over S of those before
-#pragma unroll 1
-                    for (int c = 0; c < kKeys; c += 32) {
-                        uint32_t x[32], pk[16];
-                        tmem_ld32(s_tm + c, x);
-                        tmem_ld_wait();
-                        const int from = lo - c, to = hi - c;
-#pragma unroll
-                        for (int k = 0; k < 16; k++) {
-                            const float2 y = unpair(fma2(pair2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])),
-                                                         c1, mm));
-                            const float a = exp2_fast(2 * k >= from && 2 * k < to ? y.x : -INFINITY);
-                            const float b = exp2_fast(2 * k + 1 >= from && 2 * k + 1 < to ? y.y : -INFINITY);
-                            l2 = add2(l2, pair2(a, b));
-                            pk[k] = bf16_pack(a, b);
-                        }
-                        tmem_st16(s_tm + c / 2, pk);
-                    }
-                    break;
                 }
                 // Scores are loaded 32 ahead of those whose exponentials are taken.
-                uint32_t x[2][32], pk[2][32];
+                uint32_t pk[2][32];
                 uint64_t sum[2] = {0, 0};
-                tmem_ld32(s_tm, x[0]);
+                if (look > 0)
+                    tmem_ld32(s_tm, x[0]);
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                     tmem_ld_wait();
@@ -683,7 +679,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                 sum[0] = add2(sum[0], sum[1]);
                 const float2 f = unpair(sum[0]);
                 over = f.x + f.y > lim;
-                if (look < kKeys && __any_sync(0xffffffffu, over))
+                if (!last && __any_sync(0xffffffffu, over))
                     continue;
                 l2 = add2(l2, sum[0]);
                 tmem_st32(s_tm, pk[0]);
@@ -749,39 +745,39 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             const int in_half = min(int(threadIdx.x & 127), rows - r0 - 128 * half - 1);
             const uint64_t row_of = reinterpret_cast<uint64_t>(row_at(p, p.o, sg, half, in_half, 0));
 #pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += 16) {
-                uint32_t w[16];
+            for (int d0 = 0; d0 < D; d0 += 32) {
+                uint32_t w[32];
                 if (valued) {
-                    tmem_ld16(o_tm + d0, w);
+                    tmem_ld32(o_tm + d0, w);
                     tmem_ld_wait();
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; i++)
+                    for (int i = 0; i < 32; i++)
                         w[i] = 0;
                 }
                 auto o = [&](int i) { return __uint_as_float(w[i]); };
                 if (!whole) {
                     if (r < rows) {
 #pragma unroll
-                        for (int i = 0; i < 4; i++)
+                        for (int i = 0; i < 8; i++)
                             reinterpret_cast<float4 *>(part)[(d0 / 4 + i) * kRows + threadIdx.x] =
                                 make_float4(o(4 * i), o(4 * i + 1), o(4 * i + 2), o(4 * i + 3));
                     }
                     continue;
                 }
 #pragma unroll
-                for (int c = 0; c < 2; c++)
+                for (int c = 0; c < 4; c++)
                     sts128(mine_at + sw128_offset(lane, (d0 & 63) / 8 + c), bf16_pack(o(8 * c) * inv, o(8 * c + 1) * inv),
                            bf16_pack(o(8 * c + 2) * inv, o(8 * c + 3) * inv),
                            bf16_pack(o(8 * c + 4) * inv, o(8 * c + 5) * inv),
                            bf16_pack(o(8 * c + 6) * inv, o(8 * c + 7) * inv));
-                if ((d0 & 63) != 48)
+                if ((d0 & 63) != 32)
                     continue;
                 __syncwarp();
 #pragma unroll 2
                 for (int k = 0; k < 8; k++) {
                     const int row = 4 * k + (lane >> 3), c = lane & 7;
-                    const uint64_t to = __shfl_sync(0xffffffffu, row_of, row) + 2 * (d0 - 48) + 16 * c;
+                    const uint64_t to = __shfl_sync(0xffffffffu, row_of, row) + 2 * (d0 - 32) + 16 * c;
                     uint32_t v[4];
                     lds128(mine_at + sw128_offset(row, c), v);
                     if (r0 + 32 * warp + row < rows)
