@@ -140,11 +140,21 @@ __device__ __forceinline__ void wait(Shared &sh, uint32_t bar, uint32_t parity, 
     for (int i = 0; i < 4; i++)
         if (look(bar, parity))
             return;
+#pragma unroll 1
     for (uint32_t i = 0; i < kWaitTries; i++)
         if (try_wait(bar, parity) || is_dead(sh))
             return;
     atomicOr(status, kStatusTimeout);
     *reinterpret_cast<volatile uint32_t *>(&sh.dead) = 1;
+}
+
+// The same at a role's end, whatever became of the rest.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32_t *status) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitTries; i++)
+        if (try_wait(bar, parity))
+            return;
+    atomicOr(status, kStatusTimeout);
 }
 
 // Segment n of the CTA's share, once it is listed; null after the last.
@@ -216,6 +226,7 @@ __device__ __forceinline__ void mma_role(const PackedParams &p, Shared &sh, uint
     // bytes, the next block of 64 values 128 * 128, a step of 16 keys along the second 16 * 128.
     const uint64_t q_desc = sdesc_sw128(q_at), k_desc = sdesc_sw128(k_at), v_desc = sdesc_sw128_n(v_at, 128 * 128);
     auto at = [](int i) { return uint64_t((i / 4) * (128 * 8) + (i % 4) * 2); };
+#pragma unroll 1
     for (uint32_t n = 0;; n++) {
         const Seg *const sgp = segment(sh, bars, n, p.v.status);
         if (!uniform(sgp != nullptr))
@@ -228,6 +239,7 @@ __device__ __forceinline__ void mma_role(const PackedParams &p, Shared &sh, uint
         if (tiles == 0)
             continue;
         const bool two = rows > 128;
+#pragma unroll 1
         for (int j = 0; j <= tiles; j++) {
             const uint32_t step = steps + j, before = step - 1, k_stage = step % kStages, v_stage = before % kStages;
             const uint64_t v = v_desc + v_stage * (kTileBytes<D> >> 4), k = k_desc + k_stage * (kTileBytes<D> >> 4);
@@ -290,7 +302,7 @@ __device__ __forceinline__ void mma_role(const PackedParams &p, Shared &sh, uint
     if (elect_one())
         mma_commit(bars + 8 * (kDrain + part));
     __syncwarp();
-    mbar_wait(bars + 8 * (kDrain + part), 0, p.v.status, kStatusTimeout);
+    drain_wait(bars + 8 * (kDrain + part), 0, p.v.status);
 }
 
 template <int D>
@@ -318,15 +330,18 @@ __device__ __forceinline__ void copy_role(const PackedParams &p, Shared &sh, uin
     };
     // What is on its way ends before the CTA does, whatever became of the rest: n tiles of K, n - less of V.
     auto drain = [&](uint32_t n, uint32_t less) {
+#pragma unroll 1
         for (int half = 0; half < 2; half++)
             if (items[half] > 0)
-                mbar_wait(bars + 8 * (kQFull + half), (items[half] - 1) & 1, p.v.status, kStatusTimeout);
+                drain_wait(bars + 8 * (kQFull + half), (items[half] - 1) & 1, p.v.status);
+#pragma unroll 1
         for (uint32_t i = n - min(n, uint32_t(kStages)); i < n; i++) {
-            mbar_wait(bars + 8 * (kKFull + i % kStages), (i / kStages) & 1, p.v.status, kStatusTimeout);
+            drain_wait(bars + 8 * (kKFull + i % kStages), (i / kStages) & 1, p.v.status);
             if (i + less < n)
-                mbar_wait(bars + 8 * (kVFull + i % kStages), (i / kStages) & 1, p.v.status, kStatusTimeout);
+                drain_wait(bars + 8 * (kVFull + i % kStages), (i / kStages) & 1, p.v.status);
         }
     };
+#pragma unroll 1
     for (uint32_t n = 0;; n++) {
         const Seg *const sgp = segment(sh, bars, n, p.v.status);
         if (!sgp)
@@ -337,6 +352,7 @@ __device__ __forceinline__ void copy_role(const PackedParams &p, Shared &sh, uin
         segment_done(bars, n);
         if (p.q_map && tiles > 0)
             copy_q(0, head, token);
+#pragma unroll 1
         for (int j = 0; j < tiles; j++, steps++) {
             const uint32_t stage = steps % kStages, free = ((steps / kStages) & 1) ^ 1;
             const int key = first + j * kKeys;
@@ -378,6 +394,7 @@ __device__ __forceinline__ void check_role(const PackedParams &p, Shared &sh, ui
             return;
         const Seg &sg = *sgp;
         const int halves = rows_of(p, sg, 1) > 0 ? 2 : 1;
+#pragma unroll 1
         for (int half = 0; half < halves; half++) {
             const int rows = rows_of(p, sg, half);
             wait(sh, bars + 8 * (kQEmpty + half), (items[half]++ & 1) ^ 1, p.v.status);
@@ -390,6 +407,7 @@ __device__ __forceinline__ void check_role(const PackedParams &p, Shared &sh, ui
             }
             cp_async_commit();
         }
+#pragma unroll 1
         for (int half = 0; half < halves; half++) {
             if (half + 1 < halves)
                 cp_async_wait_but_one();
@@ -403,8 +421,10 @@ __device__ __forceinline__ void check_role(const PackedParams &p, Shared &sh, ui
     };
     const Seg *sgp = segment(sh, bars, 0, p.v.status);
     load_q(sgp);
+#pragma unroll 1
     for (uint32_t n = 0; sgp; n++) {
         const Seg &sg = *sgp;
+#pragma unroll 1
         for (int j = 0; j < sg.tiles; j++, steps++) {
             const uint32_t stage = steps % kStages;
             const int key0 = (sg.first + j) * kKeys;
@@ -474,6 +494,7 @@ __device__ __forceinline__ uint64_t plan_units(const PackedParams &p, Plan &plan
         const Seq q = seq_of(p.v, s);
         const int rts = S::mine(p, q) ? S::row_tiles(p, q) : 0, each = (rts + each_seq - 1) / each_seq;
         const int rt0 = (t - s * each_seq) * each, rt1 = min(rt0 + each, rts);
+#pragma unroll 1
         for (int rt = rt0; rt < rt1; rt++)
             n += S::units(p, q, rt);
     }
@@ -525,6 +546,7 @@ __device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uin
         it.q = seq_of(p.v, s);
         const int each = (S::row_tiles(p, it.q) + each_seq - 1) / each_seq;
         uint64_t to = before;
+#pragma unroll 1
         for (int rt = (t - s * each_seq) * each;; rt++) {
             S::set_tile(p, it, rt);
             if (plan.at < to + it.n)
@@ -541,6 +563,7 @@ __device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uin
 template <class S>
 __device__ __forceinline__ uint64_t list_role(const PackedParams &p, Shared &sh, uint32_t bars, Item &it, uint64_t u,
                                               uint64_t end, uint32_t first, uint32_t most) {
+#pragma unroll 1
     for (uint32_t n = first; n < most;) {
         const uint32_t slot = n % kSegs;
         wait(sh, bars + 8 * (kSegFree + slot), ((n / kSegs) & 1) ^ 1, p.v.status);
@@ -576,6 +599,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
     const uint32_t s_tm = sh.tmem + lanes + half * kKeys, o_tm = sh.tmem + lanes + 256 + half * D;
     const uint64_t c1 = pair2(p.c1, p.c1);
     uint32_t cnt = 0, turns = 0;
+#pragma unroll 1
     for (uint32_t n = 0;; n++) {
         const Seg *const sgp = segment(sh, bars, n, p.v.status);
         if (!sgp)
@@ -596,6 +620,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
         const float unset = mine.hi > mine.lo ? -1.f : INFINITY;
         float m = -INFINITY, lim = unset;
         uint64_t mm = 0, l2 = 0;          // less the maximum, and the sum, in pairs
+#pragma unroll 1
         for (int j = 0; active && j < sg.tiles; j++) {
             const int key0 = (sg.first + j) * kKeys;
             wait(sh, bars + 8 * (kSFull + half), cnt & 1, p.v.status);
@@ -608,6 +633,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             tmem_ld32(s_tm, x[0]);
             bool over = j == 0;  // the row's maximum is to be raised
             int look = open ? kKeys : j == 0 ? 32 : 0;
+#pragma unroll 1
             for (bool last = open && j == 0;; last = true, look = kKeys) {
                 if (look > 0) {
                     // What the row does not see becomes -inf, whose exponential is 0; from there on an open tile is
@@ -774,7 +800,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                 if ((d0 & 63) != 32)
                     continue;
                 __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
                 for (int k = 0; k < 8; k++) {
                     const int row = 4 * k + (lane >> 3), c = lane & 7;
                     const uint64_t to = __shfl_sync(0xffffffffu, row_of, row) + 2 * (d0 - 32) + 16 * c;
