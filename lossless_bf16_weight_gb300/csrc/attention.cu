@@ -15,16 +15,30 @@
 //             stages of each.  V lies as it comes, [keys][dims], and is the second product's
 //             operand with its rows along the product.
 // A row's running maximum is only raised when its probabilities of a tile add up to
-// more than 2^40 (BF16 and fp32 hold that without loss; with 2^24, rows of which one or the other
-// goes past it in every other tile, 8192 tokens take 774 us instead of 673), so that after the first keys no
-// score is compared and O is rarely rescaled.  P is rounded to one BF16 (2^-8, the one rounding beside
+// more than 2^40 (BF16 and fp32 hold that without loss; with 2^24, which one row or another of a warp
+// passes in every other tile, 8192 tokens, not causal, take 670 us instead of 593), so that after the first keys
+// no score is compared and O is rarely rescaled.  P is rounded to one BF16 (2^-8, the one rounding beside
 // the output's); its sum is fp32 of the unrounded values.
 //
-// What a row does not see takes no part in it, whatever its bits: a masked score is
-// replaced before its exponential, and since 0 times a V that is not finite is not 0, the
+// What a row does not see takes no part in it, whatever its bits: a masked score becomes -inf where it
+// lies (an "open" tile, which not all rows see in full, takes 2200 cycles with that, 6000 with the mask in the
+// loops of all else), and since 0 times a V that is not finite is not 0, the
 // check warps look through V's tiles that are not seen by all rows, zero keys past the sequence's
 // end and values that are not finite, and an item with such a value adds them at its end to the rows
 // that see their keys.
+//
+// Measured, 32 query and 8 kv heads of 128, causal (cuBLAS's burst rate is 1919 TFLOP/s): 37 tokens 10.4 us, 2048
+// 43.8 (785 TFLOP/s), 8192 324 (1695), 16384 1206 (1823); 8192 not causal 593 to 660 by the
+// clock (1667 to 1855); twelve packed prompts of 1
+// to 2000 tokens 65 (740); heads of 64, 8192 tokens 260 (1060), not causal 470 (1170).  Long prompts are bound
+// by the tensor cores (active in 80% of the cycles, at the clock that the power leaves).  Short and packed ones pay for
+// the share's begin (3.5 us until its first segment is listed, 4 until Q, K and V of all CTAs are there), 2.8
+// us an item between its last products and the next one's first (output 1.9, its first tile 0.9) and a join of
+// parts (7).  With heads of 64 the products are half as long, and what bounds is the way from scores to
+// probabilities and back through both halves (2085 cycles a step; tensor cores 39%, exponentials 39%).
+// Outputs of items by the check warps instead, beside the next item's first tile: 21 prompts of 16 to 3001 tokens
+// 173 us instead of 164 (what runs seldom runs slowly: its instructions have to be fetched first).
+// Exponentials by multiply-adds, one in eight: 7 sequences with heads of 64 124 us instead of 110.
 #include <cudaTypedefs.h>
 
 #include <cfloat>
@@ -45,7 +59,8 @@ namespace {
 constexpr int kRows = 256, kKeys = 128;
 constexpr int kSoftmax = 256, kCheck = 128;         // threads
 constexpr int kThreads = kSoftmax + kCheck + 128;   // and a warpgroup of the MMA, copying and listing warps
-constexpr int kItemCost = 3;                          // what an item costs beyond its steps, in steps
+// What an item costs beyond its steps, in steps (21 packed prompts 171 us, with 2 176, with 4 178).
+constexpr int kItemCost = 3;
 constexpr int kMinShare = 4;                          // units of a CTA at least
 constexpr int kSegs = 16;
 constexpr int kStages = 2;
@@ -89,8 +104,8 @@ struct PackedParams {
 
 enum Bar {
     kQFull, kQEmpty = kQFull + 2, kKFull = kQEmpty + 2, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages,
-    kVOk = kVFull + kStages, kVEmpty = kVOk + kStages, kTurn = kVEmpty + kStages, kSegFull = kTurn + 2, kSegFree = kSegFull + kSegs,
-    kSFull = kSegFree + kSegs, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+    kVOk = kVFull + kStages, kVEmpty = kVOk + kStages, kTurn = kVEmpty + kStages, kSegFull = kTurn + 2,
+    kSegFree = kSegFull + kSegs, kSFull = kSegFree + kSegs, kPFull = kSFull + 2, kPvDone = kPFull + 2,
     kDrain = kPvDone + 2, kJoin = kDrain + 2, kBars
 };
 
@@ -111,12 +126,16 @@ constexpr uint32_t kOutBytes = kSoftmax / 32 * 32 * 128;  // 64 dimensions of a 
 template <int D>
 constexpr size_t kSmem = 1024 + kOutBytes + (2 + 2 * kStages) * size_t(kTileBytes<D>);
 
+// Loops of what runs once an item or a tile are not unrolled: left to the compiler, this kernel has 310 KB of
+// instructions instead of 139, more than their caches hold (21 packed prompts 171 us instead of 164, a batch of
+// five times 1000 tokens with heads of 64 73 instead of 62).
+//
 // A wait that every thread of a role makes at the same place.  One that runs
 // out marks the kernel dead: all later waits return at once, every role
 // walks through its remaining steps without waiting, and the status word tells.
 __device__ __forceinline__ bool is_dead(Shared &sh) { return *reinterpret_cast<volatile uint32_t *>(&sh.dead) != 0; }
 // What is ready, or soon, is found by a few looks; then a thread is suspended for up to a microsecond at a time
-// (a prompt of 8192 tokens 374 us, without the looks 394).
+// (37 tokens 10.4 us, without the looks 11.4; long prompts the same).
 constexpr uint32_t kHintNs = 1000;
 __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -166,7 +185,9 @@ __device__ __forceinline__ const Seg *segment(Shared &sh, uint32_t bars, uint32_
 // A warp (or the one thread of a role) is done with it.
 template <int D>
 constexpr uint32_t kSegUsers = (kSoftmax + kCheck) / 32 + (kOneMma<D> ? 2 : 3);
-__device__ __forceinline__ void segment_done(uint32_t bars, uint32_t n) { mbar_arrive(bars + 8 * (kSegFree + n % kSegs)); }
+__device__ __forceinline__ void segment_done(uint32_t bars, uint32_t n) {
+    mbar_arrive(bars + 8 * (kSegFree + n % kSegs));
+}
 
 // All softmax warps are here: a wait with a limit, as the halves may part where one has run out.
 __device__ __forceinline__ void softmax_sync(Shared &sh, uint32_t bars, uint32_t &turns, uint32_t *status) {
@@ -212,9 +233,9 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 // scores of the next; the halves in turns, so that one half's products run while the other's
 // softmax does.  With heads of 128 a warp for each half takes turns with the other: an elected thread
 // takes 60 cycles for each of 16 products and 140 for each wait, which for both halves is more than the
-// tensor cores' 2048 (8192 tokens, not causal, 613 us; by one warp 673; by two without turns, which
-// interleave their products, 948).  With heads of 64 there are half as many products and one warp does
-// (496 us, two 556).
+// tensor cores' 2048 (8192 tokens 324 us, by one warp 335; by two without turns, which interleave their
+// products, 345, and twelve packed prompts 76 instead of 65).  With heads of 64 there are half as many products and
+// one warp does (8192 tokens, not causal, 468 us, two 486).
 template <int D, bool kBoth>
 __device__ __forceinline__ void mma_role(const PackedParams &p, Shared &sh, uint32_t bars, uint32_t q_at,
                                          uint32_t k_at, uint32_t v_at, int part) {
@@ -625,16 +646,17 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             const int key0 = (sg.first + j) * kKeys;
             wait(sh, bars + 8 * (kSFull + half), cnt & 1, p.v.status);
             tc_fence_after();
-            const int lo = mine.lo - key0, hi = mine.hi - key0;  // the row's keys of the tile
-            const bool open = is_open(sg, key0);
-            // (What runs once an item is kept in short loops: unrolled, twelve packed prompts take 88 us instead
-            // of 78.)
+            // The first scores, before it is known what the tile needs (16 heads of 64, 8192 tokens, not
+            // causal, 253 us, loaded after that 260).
             uint32_t x[2][32];
             tmem_ld32(s_tm, x[0]);
-            bool over = j == 0;  // the row's maximum is to be raised
-            int look = open ? kKeys : j == 0 ? 32 : 0;
+            const int lo = mine.lo - key0, hi = mine.hi - key0;  // the row's keys of the tile
+            const bool open = is_open(sg, key0);
+            bool over = j == 0, last = open && j == 0;  // the row's maximum is to be raised; it is that of all keys
+            int look = open ? kKeys : j == 0 ? 32 : 0;  // the scores to be looked at first
+            tmem_ld_wait();
 #pragma unroll 1
-            for (bool last = open && j == 0;; last = true, look = kKeys) {
+            for (;; last = true, look = kKeys) {
                 if (look > 0) {
                     // What the row does not see becomes -inf, whose exponential is 0; from there on an open tile is
                     // like others.  And the highest score of the first 32 keys (of an item's first tile, where all
@@ -643,7 +665,6 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
 #pragma unroll 1
                     for (int c = 0; c < look; c += 32) {
                         uint32_t x[32];
-                        tmem_ld_wait();
                         tmem_ld32(s_tm + c, x);
                         tmem_ld_wait();
                         const uint32_t seen = bits_below(hi - c) & ~bits_below(lo - c);
@@ -682,15 +703,16 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                             }
                         }
                     }
+                    tmem_ld32(s_tm, x[0]);
+                    tmem_ld_wait();
                 }
                 // Scores are loaded 32 ahead of those whose exponentials are taken.
                 uint32_t pk[2][32];
                 uint64_t sum[2] = {0, 0};
-                if (look > 0)
-                    tmem_ld32(s_tm, x[0]);
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
-                    tmem_ld_wait();
+                    if (c > 0)
+                        tmem_ld_wait();
                     if (c < 3)
                         tmem_ld32(s_tm + 32 * (c + 1), x[(c + 1) & 1]);
 #pragma unroll
@@ -766,7 +788,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
         if (active) {
             const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: o is 0 and stays 0
             // A warp's rows lie in shared memory for a moment, 64 dimensions at a time, so that they go out by whole
-            // lines (an item's output by rows of their threads takes 2.3 us).
+            // lines (8192 tokens 324 us, stored by rows of their threads 340).
             const uint32_t mine_at = out_at + warp * (32 * 128);
             const int in_half = min(int(threadIdx.x & 127), rows - r0 - 128 * half - 1);
             const uint64_t row_of = reinterpret_cast<uint64_t>(row_at(p, p.o, sg, half, in_half, 0));
