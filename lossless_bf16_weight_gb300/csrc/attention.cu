@@ -38,7 +38,7 @@
 // probabilities and back through both halves (2085 cycles a step; tensor cores 39%, exponentials 39%).
 // Outputs of items by the check warps instead, beside the next item's first tile: 21 prompts of 16 to 3001 tokens
 // 173 us instead of 164 (what runs seldom runs slowly: its instructions have to be fetched first).
-// Exponentials by multiply-adds, one in eight: 7 sequences with heads of 64 124 us instead of 110.
+// Exponentials by multiply-adds, one in eight: four sequences with heads of 64 124 us instead of 110.
 #include <cudaTypedefs.h>
 
 #include <cfloat>

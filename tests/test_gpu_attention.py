@@ -294,3 +294,39 @@ def test_nothing_to_do(uw):
     lse = torch.empty(5, 4, device="cuda")
     uw.attention(q, none, none, out, _starts([5]), ws, kv_start=_starts([0]), lse=lse)
     assert (out == 0).all() and lse.isneginf().all() and uw.check_status(ws) == 0
+
+
+@pytest.mark.parametrize("hq,hk,d", [(320, 1, 64), (129, 1, 128), (600, 2, 128)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 9)])
+def test_more_heads_than_a_tile_has_rows(uw, hq, hk, d, causal, window):
+    c = Case(uw, [5, 0, 33], [5, 7, 140], hq, hk, d, causal, window, seed=hq)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("hq,hk,d", [(8, 1, 128), (7, 1, 64)])
+def test_over_the_queries_with_items_in_parts(uw, hq, hk, d):
+    """out may be q: items that several CTAs share, and tiles that end inside the next sequence."""
+    c = Case(uw, [1999, 301, 77], [1999, 301, 77], hq, hk, d, seed=3)
+    want, l = c.run()
+    c.check(want, l)
+    start, n = _starts(c.new), sum(c.new)
+    for _ in range(3):
+        q = c.q.clone()
+        uw.attention(q, c.k, c.v, q, start, c.ws, kv_start=start)
+        assert torch.equal(q[:n], want[:n]) and torch.equal(q[n:], c.q[n:])
+
+
+def test_two_streams_at_once(uw):
+    cases = [Case(uw, [700, 64, 1], [700, 64, 1], 8, 2, 128, seed=5), Case(uw, [513, 900], [513, 900], 4, 4, 64, False, seed=6)]
+    want = [c.run()[0] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.full_like(c.q, 7.0) for _ in range(8)] for c in cases]
+    starts = [_starts(c.new) for c in cases]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for c, s, out, start in zip(cases, streams, outs, starts):
+            with torch.cuda.stream(s):
+                uw.attention(c.q, c.k, c.v, out[i], start, c.ws, kv_start=start, **c.opts)
+    torch.cuda.synchronize()
+    for c, out, w in zip(cases, outs, want):
+        assert uw.check_status(c.ws) == 0 and all(torch.equal(o, w) for o in out)
