@@ -747,6 +747,18 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
         const bool whole = sg.tiles == sg.of, valued = active && sg.tiles > 0;
         const int slot = cut0 > sg.u0 ? 0 : 1;
         float *const part = p.parts + (2 * uint64_t(blockIdx.x) + slot) * PF;
+        // An item that goes on in other CTAs: whoever comes last joins the parts.  If all others are there already (as
+        // they are where the item begins at the end of a share), this part needs not go through memory.
+        uint32_t f = 0, e = 0;
+        bool last = false;
+        if (!whole) {
+            f = share_of(sg.u0, total, workers);
+            e = share_of(sg.u0 + sg.of - 1, total, workers);
+            if (threadIdx.x == 0)
+                sh.arrived = *reinterpret_cast<volatile uint32_t *>(p.counters + f) == e - f;
+            softmax_sync(sh, bars, turns, p.v.status);
+            last = sh.arrived;
+        }
         if (valued) {
             wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
             tc_fence_after();
@@ -785,7 +797,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             }
             tmem_st_wait();
         }
-        if (active) {
+        if (active && !last) {
             const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: o is 0 and stays 0
             // A warp's rows lie in shared memory for a moment, 64 dimensions at a time, so that they go out by whole
             // lines (8192 tokens 324 us, stored by rows of their threads 340).
@@ -844,24 +856,25 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             }
         }
         if (!whole) {
-            // An item that goes on in other CTAs: whoever arrives last joins the parts.
-            const uint32_t f = share_of(sg.u0, total, workers), e = share_of(sg.u0 + sg.of - 1, total, workers);
-            __threadfence();
-            softmax_sync(sh, bars, turns, p.v.status);
-            if (threadIdx.x == 0) {
-                sh.arrived = atomicAdd(p.counters + f, 1u) == e - f;
-                if (sh.arrived)
-                    p.counters[f] = 0;  // ready for the next call
+            if (!last) {
+                __threadfence();
+                softmax_sync(sh, bars, turns, p.v.status);
+                if (threadIdx.x == 0)
+                    sh.arrived = atomicAdd(p.counters + f, 1u) == e - f;
+                softmax_sync(sh, bars, turns, p.v.status);
+                last = sh.arrived;
             }
-            softmax_sync(sh, bars, turns, p.v.status);
-            if (sh.arrived && active) {
+            if (last && threadIdx.x == 0)
+                p.counters[f] = 0;  // ready for the next call
+            if (last && active) {
                 __threadfence();
                 auto at = [&](uint32_t i) { return p.parts + (2 * uint64_t(i) + (i == f ? 1 : 0)) * PF; };
                 float mt = -INFINITY, lt = 0.f;
 #pragma unroll 2
                 for (uint32_t i = f; i <= e; i++) {
-                    const float mi = __ldcg(at(i) + kRows * D + threadIdx.x);
-                    const float li = __ldcg(at(i) + kRows * D + kRows + threadIdx.x);
+                    const bool own = i == blockIdx.x;
+                    const float mi = own ? m : __ldcg(at(i) + kRows * D + threadIdx.x);
+                    const float li = own ? l : __ldcg(at(i) + kRows * D + kRows + threadIdx.x);
                     const float m2 = fmaxf(mt, mi), m20 = m2 == -INFINITY ? 0.f : m2;
                     lt = fmaf(exp2_fast(mi - m20), li, lt * exp2_fast(mt - m20));
                     mt = m2;
@@ -877,7 +890,8 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                     for (uint32_t i = f; i <= e; i++) {
                         const float *const from = at(i);
                         float x[64];
-                        if (i == blockIdx.x && valued) {  // its own is still there
+                        const bool own = i == blockIdx.x;
+                        if (own) {  // still there
                             uint32_t w[2][32];
                             tmem_ld32(o_tm + d0, w[0]);
                             tmem_ld32(o_tm + d0 + 32, w[1]);
@@ -891,7 +905,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                                 *reinterpret_cast<float4 *>(x + 4 * k) = __ldcg(
                                     reinterpret_cast<const float4 *>(from) + (d0 / 4 + k) * kRows + threadIdx.x);
                         }
-                        const float w = exp2_fast(__ldcg(from + kRows * D + threadIdx.x) - m0);
+                        const float w = exp2_fast((own ? m : __ldcg(from + kRows * D + threadIdx.x)) - m0);
 #pragma unroll
                         for (int k = 0; k < 64; k++)
                             o[k] = fmaf(w, x[k], o[k]);
