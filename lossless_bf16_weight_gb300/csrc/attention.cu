@@ -27,14 +27,13 @@
 // end and values that are not finite, and an item with such a value adds them at its end to the rows
 // that see their keys.
 //
-// Measured, 32 query and 8 kv heads of 128, causal (cuBLAS's burst rate is 1919 TFLOP/s): 37 tokens 10.4 us, 2048
-// 43.8 (785 TFLOP/s), 8192 324 (1695), 16384 1206 (1823); 8192 not causal 593 to 660 by the
-// clock (1667 to 1855); twelve packed prompts of 1
-// to 2000 tokens 65 (740); heads of 64, 8192 tokens 260 (1060), not causal 470 (1170).  Long prompts are bound
-// by the tensor cores (active in 80% of the cycles, at the clock that the power leaves).  Short and packed ones pay for
-// the share's begin (3.5 us until its first segment is listed, 4 until Q, K and V of all CTAs are there), 2.8
-// us an item between its last products and the next one's first (output 1.9, its first tile 0.9) and a join of
-// parts (7).  With heads of 64 the products are half as long, and what bounds is the way from scores to
+// Measured, 32 query and 8 kv heads of 128, causal (cuBLAS's burst rate is 1919 TFLOP/s): 37 tokens 10.5 us, 2048
+// 41.0 (840 TFLOP/s), 8192 324 (1700), 16384 1206 (1823); 8192 not causal 593 to 660 by the
+// clock (1667 to 1855); twelve packed prompts of 1 to 2000 tokens 61.6 (780); heads of 64, 8192 tokens 260
+// (1056), not causal 471 (1166).  Long prompts are bound by the tensor cores (active in 80% of the cycles, at
+// the clock that the power leaves).  Short and packed ones pay for the share's begin (3.5 us until its first
+// segment is listed, 4 until Q, K and V of all CTAs are there), 2.8 us an item between its last products and
+// the next one's first (output 1.9, its first tile 0.9) and a join of parts (5.5).  With heads of 64 the products are half as long, and what bounds is the way from scores to
 // probabilities and back through both halves (2085 cycles a step; tensor cores 39%, exponentials 39%).
 // Outputs of items by the check warps instead, beside the next item's first tile: 21 prompts of 16 to 3001 tokens
 // 173 us instead of 164 (what runs seldom runs slowly: its instructions have to be fetched first).
@@ -748,7 +747,8 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
         const int slot = cut0 > sg.u0 ? 0 : 1;
         float *const part = p.parts + (2 * uint64_t(blockIdx.x) + slot) * PF;
         // An item that goes on in other CTAs: whoever comes last joins the parts.  If all others are there already (as
-        // they are where the item begins at the end of a share), this part needs not go through memory.
+        // they are where the item begins at the end of a share), this part needs not go through memory (2048 tokens
+        // 41 us, otherwise 43.7).
         uint32_t f = 0, e = 0;
         bool last = false;
         if (!whole) {
