@@ -33,10 +33,11 @@
 // (1056), not causal 471 (1166).  Long prompts are bound by the tensor cores (active in 80% of the cycles, at
 // the clock that the power leaves).  Short and packed ones pay for the share's begin (3.5 us until its first
 // segment is listed, 4 until Q, K and V of all CTAs are there), 2.8 us an item between its last products and
-// the next one's first (output 1.9, its first tile 0.9) and a join of parts (5.5).  With heads of 64 the products are half as long, and what bounds is the way from scores to
-// probabilities and back through both halves (2085 cycles a step; tensor cores 39%, exponentials 39%).
-// Outputs of items by the check warps instead, beside the next item's first tile: 21 prompts of 16 to 3001 tokens
-// 173 us instead of 164 (what runs seldom runs slowly: its instructions have to be fetched first).
+// the next one's first (output 1.9, its first tile 0.9) and a join of parts (5.5).  With heads of 64 the
+// products are half as long, and what bounds is the way from scores to probabilities and back through both
+// halves (2085 cycles a step; tensor cores 39%, exponentials 39%).
+// Outputs of items by the check warps instead, beside the next item's first tile: 21 prompts of 16 to 3001
+// tokens 173 us instead of 164 (what runs seldom runs slowly: its instructions have to be fetched first).
 // Exponentials by multiply-adds, one in eight: four sequences with heads of 64 124 us instead of 110.
 #include <cudaTypedefs.h>
 
@@ -422,8 +423,8 @@ __device__ __forceinline__ void check_role(const PackedParams &p, Shared &sh, ui
             for (int x = t; x < 128 * C; x += kCheck) {
                 const int rr = x / C, c = x % C;
                 const bool in = rr < rows;
-                cp_async16_zfill(q_at + half * kTileBytes<D> + tile_at(rr, c), row_at(p, p.q, sg, half, in ? rr : 0, c),
-                                 in ? 16 : 0);
+                cp_async16_zfill(q_at + half * kTileBytes<D> + tile_at(rr, c),
+                                 row_at(p, p.q, sg, half, in ? rr : 0, c), in ? 16 : 0);
             }
             cp_async_commit();
         }
@@ -546,7 +547,8 @@ __device__ __forceinline__ uint64_t plan_units(const PackedParams &p, Plan &plan
 }
 // The item that holds unit u (of fewer than all) into plan.item; all threads call.
 template <class S>
-__device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uint64_t u, uint64_t before, uint64_t mine) {
+__device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uint64_t u, uint64_t before,
+                                          uint64_t mine) {
     const int t = threadIdx.x, each_seq = kThreads / p.v.n_seqs, s = t / each_seq;
     if (s < p.v.n_seqs && t == s * each_seq) {
         const uint64_t lo = plan.first[s] * p.v.heads, per_head = plan.first[s + 1] - plan.first[s];
@@ -827,7 +829,8 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                 }
 #pragma unroll
                 for (int c = 0; c < 4; c++)
-                    sts128(mine_at + sw128_offset(lane, (d0 & 63) / 8 + c), bf16_pack(o(8 * c) * inv, o(8 * c + 1) * inv),
+                    sts128(mine_at + sw128_offset(lane, (d0 & 63) / 8 + c),
+                           bf16_pack(o(8 * c) * inv, o(8 * c + 1) * inv),
                            bf16_pack(o(8 * c + 2) * inv, o(8 * c + 3) * inv),
                            bf16_pack(o(8 * c + 4) * inv, o(8 * c + 5) * inv),
                            bf16_pack(o(8 * c + 6) * inv, o(8 * c + 7) * inv));
