@@ -90,7 +90,7 @@ struct PackedParams {
     float *lse;
     float c1;                    // softmax scale * log2(e)
     int32_t q_heads, group, causal, window;
-    Divisor by_group;
+    Divisor by_group, by_each;   // by_each.d: threads that look for the share's begin in one sequence (Plan)
     bool out32;                  // rows of o begin on 32-byte steps
     // of K and V: the tensor map's outermost dimension is the head; all heads are one
     bool heads_outer[2], one_head[2];
@@ -506,15 +506,23 @@ struct Plan {
     int32_t seq, head;
     Item item;
 };
+struct PlanThread {
+    int32_t s, rt0;         // its sequence and first row tile
+    Seq q;
+    uint64_t before, mine;  // units of one head before its row tiles, and theirs
+};
 template <class S>
-__device__ __forceinline__ uint64_t plan_units(const PackedParams &p, Plan &plan, uint64_t *before, uint64_t *mine) {
+__device__ __forceinline__ uint64_t plan_units(const PackedParams &p, Plan &plan, PlanThread &me) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int each_seq = kThreads / p.v.n_seqs, s = t / each_seq;  // threads of a sequence
+    const int each_seq = int(p.by_each.d), s = p.by_each.of(t), nth = t - s * each_seq;
     uint64_t n = 0;
+    me.s = s;
     if (s < p.v.n_seqs) {
         const Seq q = seq_of(p.v, s);
-        const int rts = S::mine(p, q) ? S::row_tiles(p, q) : 0, each = (rts + each_seq - 1) / each_seq;
-        const int rt0 = (t - s * each_seq) * each, rt1 = min(rt0 + each, rts);
+        const int rts = S::mine(p, q) ? S::row_tiles(p, q) : 0, each = p.by_each.of(rts + each_seq - 1);
+        const int rt0 = nth * each, rt1 = min(rt0 + each, rts);
+        me.q = q;
+        me.rt0 = rt0;
 #pragma unroll 1
         for (int rt = rt0; rt < rt1; rt++)
             n += S::units(p, q, rt);
@@ -536,21 +544,20 @@ __device__ __forceinline__ uint64_t plan_units(const PackedParams &p, Plan &plan
         upto += w < warp ? x : 0;
         all += x;
     }
-    if (s < p.v.n_seqs && t == s * each_seq)
+    if (s < p.v.n_seqs && nth == 0)
         plan.first[s] = upto - n;
     if (t == 0)
         plan.first[p.v.n_seqs] = all;
     __syncthreads();
-    *before = upto - n;
-    *mine = n;
+    me.before = upto - n;
+    me.mine = n;
     return all * p.v.heads;
 }
 // The item that holds unit u (of fewer than all) into plan.item; all threads call.
 template <class S>
-__device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uint64_t u, uint64_t before,
-                                          uint64_t mine) {
-    const int t = threadIdx.x, each_seq = kThreads / p.v.n_seqs, s = t / each_seq;
-    if (s < p.v.n_seqs && t == s * each_seq) {
+__device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uint64_t u, const PlanThread &me) {
+    const int s = me.s;
+    if (s < p.v.n_seqs && int(threadIdx.x) == s * int(p.by_each.d)) {
         const uint64_t lo = plan.first[s] * p.v.heads, per_head = plan.first[s + 1] - plan.first[s];
         if (u >= lo && u < lo + per_head * p.v.heads) {
             const uint64_t head = divide(u - lo, per_head);
@@ -561,15 +568,14 @@ __device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uin
         }
     }
     __syncthreads();
-    if (s == plan.seq && plan.at >= before && plan.at - before < mine) {
+    if (s == plan.seq && plan.at >= me.before && plan.at - me.before < me.mine) {
         Item it;
         it.s = s;
         it.head = plan.head;
-        it.q = seq_of(p.v, s);
-        const int each = (S::row_tiles(p, it.q) + each_seq - 1) / each_seq;
-        uint64_t to = before;
+        it.q = me.q;
+        uint64_t to = me.before;
 #pragma unroll 1
-        for (int rt = (t - s * each_seq) * each;; rt++) {
+        for (int rt = me.rt0;; rt++) {
             S::set_tile(p, it, rt);
             if (plan.at < to + it.n)
                 break;
@@ -965,8 +971,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     grid_dep_launch();
     grid_dep_wait();
     const bool few = p.v.n_seqs <= kThreads / 2;
-    uint64_t before = 0, mine = 0;
-    const uint64_t total = few ? plan_units<S>(p, plan, &before, &mine) : build_row<S, kThreads, true>(p, row);
+    PlanThread me{};
+    const uint64_t total = few ? plan_units<S>(p, plan, me) : build_row<S, kThreads, true>(p, row);
     const uint32_t workers = uint32_t(min((total + kMinShare - 1) / kMinShare, uint64_t(gridDim.x)));
     if (blockIdx.x >= workers)
         return;
@@ -974,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
     const uint64_t cut0 = mul_div(total, blockIdx.x, workers), cut1 = mul_div(total, blockIdx.x + 1, workers);
     if (few) {
-        plan_item<S>(p, plan, cut0, before, mine);
+        plan_item<S>(p, plan, cut0, me);
         __syncthreads();
     }
     Item it{};
@@ -1125,6 +1131,7 @@ extern "C" uw_status uw_attention(const int32_t *start, const int32_t *kv_start,
     p.q_heads = q_heads;
     p.group = q_heads / kv_heads;
     p.by_group = Divisor(uint32_t(p.group));
+    p.by_each = Divisor(uint32_t(std::max(kThreads / n_seqs, 1)));
     p.out32 = ((reinterpret_cast<uintptr_t>(p.o.p) | uintptr_t(p.o.ts) * 2 | uintptr_t(p.o.hs) * 2) & 31) == 0;
     p.causal = causal != 0;
     p.window = window;
