@@ -27,11 +27,11 @@
 // end and values that are not finite, and an item with such a value adds them at its end to the rows
 // that see their keys.
 //
-// Measured, 32 query and 8 kv heads of 128, causal (cuBLAS's burst rate is 1919 TFLOP/s): 37 tokens 10.5 us, 2048
-// 41.0 (840 TFLOP/s), 8192 324 (1700), 16384 1206 (1823); 8192 not causal 593 to 660 by the
+// Measured, 32 query and 8 kv heads of 128, causal (cuBLAS's burst rate is 1919 TFLOP/s): 37 tokens 10.0 us, 2048
+// 40.3 (853 TFLOP/s), 8192 321 to 326 (1690 to 1713), 16384 1206 (1823); 8192 not causal 593 to 660 by the
 // clock (1667 to 1855); twelve packed prompts of 1 to 2000 tokens 61.6 (780); heads of 64, 8192 tokens 260
 // (1056), not causal 471 (1166).  Long prompts are bound by the tensor cores (active in 80% of the cycles, at
-// the clock that the power leaves).  Short and packed ones pay for the share's begin (3.5 us until its first
+// the clock that the power leaves).  Short and packed ones pay for the share's begin (3 us until its first
 // segment is listed, 4 until Q, K and V of all CTAs are there), 2.8 us an item between its last products and
 // the next one's first (output 1.9, its first tile 0.9) and a join of parts (5.5).  With heads of 64 the
 // products are half as long, and what bounds is the way from scores to probabilities and back through both
@@ -126,8 +126,8 @@ constexpr uint32_t kOutBytes = kSoftmax / 32 * 32 * 128;  // 64 dimensions of a 
 template <int D>
 constexpr size_t kSmem = 1024 + kOutBytes + (2 + 2 * kStages) * size_t(kTileBytes<D>);
 
-// Loops of what runs once an item or a tile are not unrolled: left to the compiler, this kernel has 310 KB of
-// instructions instead of 139, more than their caches hold (21 packed prompts 171 us instead of 164, a batch of
+// Loops of what runs once an item or a tile are not unrolled: left to the compiler, this kernel had 310 KB of
+// instructions instead of 139 (132 now), more than their caches hold (21 packed prompts 171 us instead of 164, a batch of
 // five times 1000 tokens with heads of 64 73 instead of 62).
 //
 // A wait that every thread of a role makes at the same place.  One that runs
@@ -586,13 +586,12 @@ __device__ __forceinline__ void plan_item(const PackedParams &p, Plan &plan, uin
     }
 }
 
-// The segments of the CTA's share from unit u (in item `it`) on, one after the other into the ring;
-// a warp.  `most`: how many; returns where it stopped.
+// The segments of the CTA's share from unit u (in item `it`) on, one after the other into the ring; a warp.
 template <class S>
-__device__ __forceinline__ uint64_t list_role(const PackedParams &p, Shared &sh, uint32_t bars, Item &it, uint64_t u,
-                                              uint64_t end, uint32_t first, uint32_t most) {
+__device__ __forceinline__ void list_role(const PackedParams &p, Shared &sh, uint32_t bars, Item &it, uint64_t u,
+                                          uint64_t end) {
 #pragma unroll 1
-    for (uint32_t n = first; n < most;) {
+    for (uint32_t n = 0;;) {
         const uint32_t slot = n % kSegs;
         wait(sh, bars + 8 * (kSegFree + slot), ((n / kSegs) & 1) ^ 1, p.v.status);
         if (is_dead(sh))
@@ -615,7 +614,6 @@ __device__ __forceinline__ uint64_t list_role(const PackedParams &p, Shared &sh,
             break;
         n++;
     }
-    return u;
 }
 
 template <int D>
@@ -756,7 +754,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
         float *const part = p.parts + (2 * uint64_t(blockIdx.x) + slot) * PF;
         // An item that goes on in other CTAs: whoever comes last joins the parts.  If all others are there already (as
         // they are where the item begins at the end of a share), this part needs not go through memory (2048 tokens
-        // 41 us, otherwise 43.7).
+        // 41.0 us, otherwise 43.7).
         uint32_t f = 0, e = 0;
         bool last = false;
         if (!whole) {
@@ -984,11 +982,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         __syncthreads();
     }
     Item it{};
-    uint64_t listed = cut0;
-    if (warp == kThreads / 32 - 1) {  // (no other warp waits for the first segment in a loop)
+    if (warp == kThreads / 32 - 1)
         it = few ? plan.item : locate<S>(p, row, cut0);
-        listed = list_role<S>(p, sh, bars, it, cut0, cut1, 0, 1);
-    }
     tc_fence_before();
     fence_proxy_async_smem();  // the row's memory is the copies' from here on
     __syncthreads();
@@ -1010,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             if (elect_one())
                 copy_role<D>(p, sh, bars, q_at, k_at, v_at);
         } else if (part == 3) {
-            list_role<S>(p, sh, bars, it, listed, cut1, 1, UINT32_MAX);
+            list_role<S>(p, sh, bars, it, cut0, cut1);
         }
         __syncwarp();
     }
