@@ -45,8 +45,9 @@
  *     next call of the same kind: matmuls of a matrix of as many rows, the same
  *     chain, or the calls of a cache (any batch, plan and head size); their
  *     counters lie elsewhere for others, so clear it again before it serves
- *     those.  One workspace must not be used by two calls that may run
- *     at the same time.
+ *     those, and after UW_ERR_TIMEOUT (parts of a result that never came may
+ *     still be counted).  One workspace must not be used by two calls that may
+ *     run at the same time.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Device work is enqueued on it and the call returns without
  *     waiting, except where a function says it synchronises.
@@ -657,7 +658,7 @@ uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *start_dev, cons
  *   lse_dev   fp32 [n_tokens, q_heads]: log(sum exp(scale q.k)) (written), or NULL.
  *   softmax_scale  0 for 1 / sqrt(head_dim).
  *   ws_dev    at least uw_attention_workspace_size bytes, cleared once by
- *             uw_workspace_init; it serves calls of any sequences and heads.
+ *             uw_workspace_init; it serves calls of any sequences and heads, after UW_ERR_TIMEOUT too.
  * Scores, softmax statistics and sums are fp32; a probability is rounded to one BF16 for the product with
  * V (2^-8 of it).  The same call gives the same bits.
  * Ranges: scores q.k, times scale too, within fp32 and |v| below 2^80; past them a result may not be
@@ -668,6 +669,11 @@ uw_status uw_attention(const int32_t *start_dev, const int32_t *kv_start_dev, in
                        const uw_kv4_rows *v, int32_t kv_heads, int32_t head_dim, const uw_kv4_rows *out,
                        float *lse_dev, float softmax_scale, int32_t causal, int32_t window, void *ws_dev,
                        size_t ws_bytes, void *stream);
+
+/* uw_selftest_attention_wait -- uw_selftest_bounded_wait for the waits of uw_attention, which are its own: one that runs
+ * out reports a timeout, later ones of the kernel return at once, and those that its end makes have a limit too.
+ * Arguments and results as there. */
+uw_status uw_selftest_attention_wait(void *ws_dev, size_t ws_bytes, uint32_t tries, void *stream);
 
 /* uw_check_status -- synchronise `stream`, read and clear the error word the
  * kernels record in the workspace.  Returns UW_OK, UW_ERR_CORRUPT (a blob, or a

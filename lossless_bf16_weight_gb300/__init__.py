@@ -146,6 +146,7 @@ SIGNATURES = [
     ("uw_attention_workspace_size", ctypes.c_int, [_I32, ctypes.POINTER(_SZ)]),
     ("uw_attention", ctypes.c_int, [_P, _P, _I32, _I64, _I64, _ROWS, _I32, _ROWS, _ROWS, _I32, _I32, _ROWS, _P, _F32,
                                     _I32, _I32, _P, _SZ, _P]),
+    ("uw_selftest_attention_wait", ctypes.c_int, [_P, _SZ, ctypes.c_uint32, _P]),
     ("uw_check_status", ctypes.c_int, [_P, _P]),
     ("uw_selftest_bounded_wait", ctypes.c_int, [_P, _SZ, ctypes.c_uint32, _P]),
     ("uw_variant_name", ctypes.c_char_p, [_I32, _I32]),
@@ -828,6 +829,12 @@ def attention(q, k, v, out, start, ws, kv_start=None, scale: float = 0.0, causal
     _check(load().uw_attention(start.data_ptr(), None if kv_start is None else kv_start.data_ptr(), seqs, n, m, qr, hq, kr,
                                vr, hk, d, orow, None if lse is None else lse.data_ptr(), scale, causal, window,
                                ws.data_ptr(), _nbytes(ws), _stream(stream)), what)
+
+
+def selftest_attention_wait(ws, tries: int, stream=None) -> None:
+    """uw_selftest_attention_wait: the waits of uw_attention run out; read the result with check_status."""
+    _check(load().uw_selftest_attention_wait(_ptr(ws), ws.numel() * ws.element_size(), int(tries), _stream(stream)),
+           "uw_selftest_attention_wait")
 
 
 def selftest_bounded_wait(ws, tries: int, stream=None) -> None:

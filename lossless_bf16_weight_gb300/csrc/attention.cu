@@ -66,6 +66,8 @@ constexpr int kSegs = 16;
 constexpr int kStages = 2;
 constexpr float kRaise = 1099511627776.f;             // 2^40: headroom of the sum of a tile's probabilities
 constexpr uint32_t kTmemCols = 512;
+// A call's number and a count of parts in one word: number * kCall + count.
+constexpr uint64_t kCall = 1024;
 
 // The call's sequences: tokens start[s] .. and keys kstart[s] ..
 struct PackedView {
@@ -97,7 +99,8 @@ struct PackedParams {
     bool q_map;                  // queries come by qmap
     int32_t rows_min, rows_max;  // any
     float *parts;                // parts of kRows * (D + 2) floats: output, maximum, sum
-    uint32_t *counters;          // [gridDim.x], left at zero
+    unsigned long long *calls;     // kCall for each call there was
+    unsigned long long *counters;  // [gridDim.x]: parts that are there of the item that begins in a CTA's share
     CUtensorMap kmap, vmap;      // 64 dimensions x 128 keys of one head
     CUtensorMap qmap;            // 64 dimensions x 128 rows: a kv head's query heads x tokens
 };
@@ -114,6 +117,7 @@ struct Shared {
     Seg segs[kSegs];       // a ring: s < 0 after the last
     int32_t key0[kSegs];   // the sequence's first key
     uint32_t hurt[kSegs];  // V of a tile that not all rows see holds a value that is not finite
+    uint64_t call;         // the call's number * kCall
     uint32_t tmem, dead, arrived;
 };
 
@@ -155,12 +159,13 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
         : "=r"(ok) : "r"(bar), "r"(parity), "n"(kHintNs) : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ void wait(Shared &sh, uint32_t bar, uint32_t parity, uint32_t *status) {
+__device__ __forceinline__ void wait(Shared &sh, uint32_t bar, uint32_t parity, uint32_t *status,
+                                     uint32_t tries = kWaitTries) {
     for (int i = 0; i < 4; i++)
         if (look(bar, parity))
             return;
 #pragma unroll 1
-    for (uint32_t i = 0; i < kWaitTries; i++)
+    for (uint32_t i = 0; i < tries; i++)
         if (try_wait(bar, parity) || is_dead(sh))
             return;
     atomicOr(status, kStatusTimeout);
@@ -168,9 +173,10 @@ __device__ __forceinline__ void wait(Shared &sh, uint32_t bar, uint32_t parity, 
 }
 
 // The same at a role's end, whatever became of the rest.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32_t *status) {
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32_t *status,
+                                           uint32_t tries = kWaitTries) {
 #pragma unroll 1
-    for (uint32_t i = 0; i < kWaitTries; i++)
+    for (uint32_t i = 0; i < tries; i++)
         if (try_wait(bar, parity))
             return;
     atomicOr(status, kStatusTimeout);
@@ -761,7 +767,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             f = share_of(sg.u0, total, workers);
             e = share_of(sg.u0 + sg.of - 1, total, workers);
             if (threadIdx.x == 0)
-                sh.arrived = *reinterpret_cast<volatile uint32_t *>(p.counters + f) == e - f;
+                sh.arrived = *reinterpret_cast<volatile unsigned long long *>(p.counters + f) == sh.call + (e - f);
             softmax_sync(sh, bars, turns, p.v.status);
             last = sh.arrived;
         }
@@ -866,13 +872,13 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             if (!last) {
                 __threadfence();
                 softmax_sync(sh, bars, turns, p.v.status);
-                if (threadIdx.x == 0)
-                    sh.arrived = atomicAdd(p.counters + f, 1u) == e - f;
+                if (threadIdx.x == 0) {
+                    atomicMax(p.counters + f, sh.call);  // what an earlier call left is less
+                    sh.arrived = atomicAdd(p.counters + f, 1ull) == sh.call + (e - f);
+                }
                 softmax_sync(sh, bars, turns, p.v.status);
                 last = sh.arrived;
             }
-            if (last && threadIdx.x == 0)
-                p.counters[f] = 0;  // ready for the next call
             if (last && active) {
                 __threadfence();
                 auto at = [&](uint32_t i) { return p.parts + (2 * uint64_t(i) + (i == f ? 1 : 0)) * PF; };
@@ -968,6 +974,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     grid_dep_launch();
     grid_dep_wait();
+    // The call's number.  All CTAs' additions are kCall, and each makes its own as it reads, so that the first digits
+    // are the same for all of them.
+    unsigned long long call = 0;
+    if (threadIdx.x == 0)
+        call = atomicAdd(p.calls, blockIdx.x == 0 ? kCall + 1 - gridDim.x : 1ull);
     const bool few = p.v.n_seqs <= kThreads / 2;
     PlanThread me{};
     const uint64_t total = few ? plan_units<S>(p, plan, me) : build_row<S, kThreads, true>(p, row);
@@ -984,6 +995,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     Item it{};
     if (warp == kThreads / 32 - 1)
         it = few ? plan.item : locate<S>(p, row, cut0);
+    if (threadIdx.x == 0)
+        sh.call = call / kCall * kCall;
     tc_fence_before();
     fence_proxy_async_smem();  // the row's memory is the copies' from here on
     __syncthreads();
@@ -1014,6 +1027,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     tc_fence_after();
     if (warp == kThreads / 32 - 1)
         tmem_dealloc(sh.tmem, kTmemCols);
+}
+
+// Waits that nothing ends, by one thread: the first gives up, says so and marks the kernel dead; one after it returns
+// at once and says nothing; a drain gives up and says so.  The status word holds a timeout only if all three did.
+__global__ void withheld_arrival_kernel(uint32_t *status, uint32_t tries) {
+    __shared__ Shared sh;
+    const uint32_t bar = smem_addr(sh.bars);
+    mbar_init(bar, 1);
+    mbar_init_fence();
+    sh.dead = 0;
+    wait(sh, bar, 0, status, tries);
+    if (!(atomicExch(status, 0u) & kStatusTimeout) || !is_dead(sh))
+        return;
+    wait(sh, bar, 0, status);
+    if (atomicExch(status, 0u) == 0)
+        drain_wait(bar, 0, status, tries);
 }
 
 // K or V [n, heads, D] as boxes of 64 dimensions x 128 keys of one head; the dimensions in the order of
@@ -1052,23 +1081,25 @@ bool encode_q_map(CUtensorMap *m, const Rows &r, int64_t n, int heads, int dim, 
            CUDA_SUCCESS;
 }
 
-// Workspace: [error word | counters | parts].  The counters, which a call finds at zero, lie in
-// the same place for every head size, so that one workspace serves all.
+// Workspace: [error word | calls there were | counters | parts].  Calls and counters lie in the same place for every head
+// size, so that one workspace serves all.  A counter's word holds its call's number too: parts of an item that never came to
+// their end, as the call ran out of time, count for no later one.
 struct Layout {
-    size_t counters, parts, total;
+    size_t calls, counters, parts, total;
 };
 Layout layout(int head_dim) {
     const size_t ctas = size_t(sm_count());
     Layout w;
-    w.counters = 256;
-    w.parts = align_up(w.counters + 4 * ctas, 256);
+    w.calls = 256;
+    w.counters = w.calls + 8;
+    w.parts = align_up(w.counters + 8 * ctas, 256);
     w.total = w.parts + 4 * 2 * ctas * kRows * (head_dim + 2);
     return w;
 }
 
 template <int D>
 cudaError_t launch(const PackedParams &p, cudaStream_t st) {
-    if (!ensure_smem(attention_kernel<D>, kSmem<D>))
+    if (sm_count() >= int(kCall) || !ensure_smem(attention_kernel<D>, kSmem<D>))
         return cudaErrorUnknown;
     return launch_overlapped(attention_kernel<D>, dim3(unsigned(sm_count())), dim3(kThreads), kSmem<D>, st, p);
 }
@@ -1132,7 +1163,8 @@ extern "C" uw_status uw_attention(const int32_t *start, const int32_t *kv_start,
     p.window = window;
     p.rows_min = 0;
     p.rows_max = INT32_MAX;
-    p.counters = reinterpret_cast<uint32_t *>(wsb + w.counters);
+    p.calls = reinterpret_cast<unsigned long long *>(wsb + w.calls);
+    p.counters = reinterpret_cast<unsigned long long *>(wsb + w.counters);
     p.parts = reinterpret_cast<float *>(wsb + w.parts);
     // (without keys no tile is copied)
     if (n_keys > 0 && (!encode_keys_map(&p.kmap, keys, n_keys, kv_heads, head_dim, &p.heads_outer[0], &p.one_head[0]) ||
@@ -1141,4 +1173,13 @@ extern "C" uw_status uw_attention(const int32_t *start, const int32_t *kv_start,
     p.q_map = encode_q_map(&p.qmap, p.q, n_tokens, q_heads, head_dim, p.group);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return (head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st)) == cudaSuccess ? UW_OK : UW_ERR_CUDA;
+}
+
+extern "C" uw_status uw_selftest_attention_wait(void *ws, size_t ws_bytes, uint32_t tries, void *stream) {
+    if (!ws || tries == 0 || tries > kWaitTries)
+        return UW_ERR_INVALID_ARG;
+    if (ws_bytes < 256)
+        return UW_ERR_BUFFER_TOO_SMALL;
+    withheld_arrival_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint32_t *>(ws), tries);
+    return cudaGetLastError() == cudaSuccess ? UW_OK : UW_ERR_CUDA;
 }
