@@ -14,8 +14,8 @@
 //   copies    warp 14, one elected thread: tiles of K and V by tensor-map copies, two
 //             stages of each.  V lies as it comes, [keys][dims], and is the second product's
 //             operand with its rows along the product.
-// A row's running maximum is only raised when its probabilities of a tile add up to
-// more than 2^40 (BF16 and fp32 hold that without loss; with 2^24, which one row or another of a warp
+// A row's running maximum is only raised when its probabilities so far add up to
+// more than 2^38 (BF16 and fp32 hold that without loss; with 2^24 a tile, which one row or another of a warp
 // passes in every other tile, 8192 tokens, not causal, take 670 us instead of 593), so that after the first keys
 // no score is compared and O is rarely rescaled.  P is rounded to one BF16 (2^-8, the one rounding beside
 // the output's); its sum is fp32 of the unrounded values.
@@ -64,7 +64,9 @@ constexpr int kItemCost = 3;
 constexpr int kMinShare = 4;                          // units of a CTA at least
 constexpr int kSegs = 16;
 constexpr int kStages = 2;
-constexpr float kRaise = 1099511627776.f;             // 2^40: headroom of the sum of a tile's probabilities
+// 2^38: headroom of the sum of a row's probabilities.  A part's output stays below 2^38 |v|, the join of up to 152 of them
+// below 2^46 |v|.
+constexpr float kRaise = 274877906944.f;
 constexpr uint32_t kTmemCols = 512;
 // A call's number and a count of parts in one word: number * kCall + count.
 constexpr uint64_t kCall = 1024;
@@ -647,10 +649,10 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             mine = visible(p, sq, i, i);
             mine.hi = min(mine.hi, sg.len);
         }
-        // The maximum; the sum of a tile's probabilities from which it is raised (any, as long as there is
+        // The maximum; the sum of probabilities from which it is raised (any, as long as there is
         // none; never where there will be none).
         const float unset = mine.hi > mine.lo ? -1.f : INFINITY;
-        float m = -INFINITY, lim = unset;
+        float m = -INFINITY, lim = unset, room = unset;  // room: what of lim is left for a tile
         uint64_t mm = 0, l2 = 0;          // less the maximum, and the sum, in pairs
 #pragma unroll 1
         for (int j = 0; active && j < sg.tiles; j++) {
@@ -693,12 +695,15 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                     if (__any_sync(0xffffffffu, over)) {
                         // Raised in rows that need it by their own sum (not in others, so that a row's bits depend on
                         // no other row): what the row has so far is scaled down.
-                        const float m2 = over ? fmaxf(m, top * p.c1) : m, m20 = m2 == -INFINITY ? 0.f : m2;
+                        // By the sum's logarithm at least, so that it is 1 at most whatever this tile's scores are.
+                        const float2 lf = unpair(l2);
+                        const float m2 = over ? fmaxf(fmaxf(m, m + __log2f(lf.x + lf.y)), top * p.c1) : m;
+                        const float m20 = m2 == -INFINITY ? 0.f : m2;
                         const float f = !over ? 1.f : m == -INFINITY ? 0.f : exp2_fast(m - m20);
                         l2 = mul2(l2, pair2(f, f));
                         m = m2;
                         mm = pair2(-m20, -m20);
-                        lim = m2 == -INFINITY ? unset : kRaise;
+                        lim = room = m2 == -INFINITY ? unset : kRaise;
                         if (j > 0) {
                             wait(sh, bars + 8 * (kPvDone + half), (cnt - 1) & 1, p.v.status);
                             tc_fence_after();
@@ -737,7 +742,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 const float2 f = unpair(sum[0]);
-                over = f.x + f.y > lim;
+                over = f.x + f.y > room;
                 if (!last && __any_sync(0xffffffffu, over))
                     continue;
                 l2 = add2(l2, sum[0]);
@@ -751,6 +756,9 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
             if (lane == 0)
                 mbar_arrive(bars + 8 * (kPFull + half));
             cnt++;
+            // (here, where nothing waits for it: before the comparison 163 us for 21 packed prompts instead of 160)
+            const float2 lf = unpair(l2);
+            room = lim - (lf.x + lf.y);
         }
 
         const float2 lf = unpair(l2);
