@@ -651,7 +651,8 @@ uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *start_dev, cons
  *             sequence outside the call's tokens or keys is left alone and reported by
  *             uw_check_status as UW_ERR_CORRUPT.  Tokens of no sequence are left alone.
  *   n_tokens, n_keys  rows of q and out, and of k and v (equal without kv_start,
- *             UW_ERR_SHAPE otherwise).
+ *             UW_ERR_SHAPE otherwise).  Up to 2^31 - 1, and n_tokens times the query heads of a kv head
+ *             up to 2^31 - 257 (UW_ERR_UNSUPPORTED otherwise).
  *   q, k, v, out  head_dim 64 or 128; strides of any order.  (k and v of more than
  *             one key with token stride 0: UW_ERR_UNSUPPORTED; head stride 0: one head for
  *             all.)  out may be q itself.

@@ -57,6 +57,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // gemm_tc.cu
 namespace {
 
 constexpr int kRows = 256, kKeys = 128;
+// Of a kv head.  Rows are counted in 32 bits, past a sequence's last one up to the end of its tile.
+constexpr int64_t kMostRows = 0x7fffffff - kRows;
 constexpr int kSoftmax = 256, kCheck = 128;         // threads
 constexpr int kThreads = kSoftmax + kCheck + 128;   // and a warpgroup of the MMA, copying and listing warps
 // What an item costs beyond its steps, in steps (21 packed prompts 171 us, with 2 176, with 4 178).
@@ -1145,7 +1147,7 @@ extern "C" uw_status uw_attention(const int32_t *start, const int32_t *kv_start,
     PackedParams p{};
     p.c1 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(float(head_dim))) * 1.44269504089f;
     if ((head_dim != 64 && head_dim != 128) || q_heads > kKv4MaxHeads || n_tokens > 0x7fffffff || n_keys > 0x7fffffff ||
-        n_tokens * (q_heads / kv_heads) > 0x7fffffff || !(p.c1 >= FLT_MIN) || !std::isfinite(p.c1))
+        n_tokens * (q_heads / kv_heads) > kMostRows || !(p.c1 >= FLT_MIN) || !std::isfinite(p.c1))
         return UW_ERR_UNSUPPORTED;
     if (n_tokens == 0 || n_seqs == 0)
         return UW_OK;  // nothing to do needs no buffers (those of empty tensors are null)
