@@ -567,7 +567,8 @@ uw_status uw_kv4_append(const uw_kv4_cache *c, const int32_t *start_dev, const i
  * by uw_check_status as UW_ERR_CORRUPT. */
 typedef struct {
     const int32_t *pos_dev;
-    int64_t axis_stride;       /* int32 elements, at least the call's tokens        */
+    int64_t axis_stride;       /* int32 elements, at least the call's tokens; 0: the same
+                                  positions on all axes (text)                      */
     int32_t n_axes;            /* 1 .. 4                                            */
     int32_t rot_dim;           /* a multiple of 16, at most head_dim                */
     const uint8_t *pair_axis;  /* host memory: rot_dim / 2 numbers below n_axes, read by the call */
