@@ -590,7 +590,8 @@ uw_status uw_rope_axes(const uw_rope *r, int64_t n_tokens, const uw_kv4_rows *q,
 
 /* uw_kv4_append_axes -- uw_kv4_append with the rotation of uw_rope.  A token's place in
  * the cache still goes by start and len.
- *   r         as above; rot_dim 0: no rotation, and positions are not looked at.
+ *   r         as above; rot_dim 0: no rotation, and positions, axes and tables are not looked at (any may be
+ *             NULL or 0).
  *   k_out     the rotated k (written, whether or not the token's page is in the pool; may be
  *             k), or NULL.
  * Others as for uw_kv4_append. */

@@ -715,6 +715,10 @@ def kv4_append(cache: Kv4Cache, start, length, q, k, v, q_out, cos, sin, ws, int
 
 def _rope(pos, pair_axis, cos, sin, n: int, interleaved: bool, what: str) -> Rope:
     _, _, int32, fp32 = _types()
+    if not pair_axis and (cos is None or cos.dim() == 2 and cos.shape[1] == 0) and (cos is None) == (sin is None):
+        return Rope(None, 0, 0, 0, None, None, None, 0, interleaved)    # nothing turns
+    if pos is None or cos is None or sin is None:
+        raise UwError(UW_ERR_SHAPE, "%s (pos, cos and sin: all of them where pairs turn)" % what)
     if pos.dim() != 2 or pos.shape[1] != n or pos.dtype is not int32 or (n > 1 and pos.stride(1) != 1):
         raise UwError(UW_ERR_SHAPE, "%s (pos is not int32 [axes, %d])" % (what, n))
     rope = cos.shape
@@ -756,7 +760,7 @@ def rope_axes(q, k, pos, pair_axis: bytes, q_out, k_out, cos, sin, ws, interleav
 def kv4_append_axes(cache: Kv4Cache, start, length, pos, pair_axis: bytes, q, k, v, q_out, cos, sin, ws, k_out=None,
                     interleaved: bool = False, stream=None):
     """uw_kv4_append_axes: kv4_append with positions on several axes (pos and pair_axis as for rope_axes); k_out, if
-    given, takes the rotated k."""
+    given, takes the rotated k.  With no pairs (pair_axis b"") nothing turns; pos, cos and sin may be None."""
     what, d = "uw_kv4_append_axes", cache
     n = k.shape[0]
     _kv4_seqs(cache, start, length, what)

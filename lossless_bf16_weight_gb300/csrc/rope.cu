@@ -61,7 +61,11 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const RopeParams p) {
 }  // namespace
 
 uw_status rope_axes_map(const uw_rope &r, int64_t n_tokens, Axes *a) {
-    if (r.n_axes < 1 || r.axis_stride < 0 || (n_tokens > 0 && !r.pos_dev) || (r.rot_dim > 0 && !r.pair_axis) ||
+    if (r.rot_dim == 0) {  // nothing turns: positions and axes are not looked at
+        *a = Axes{};
+        return UW_OK;
+    }
+    if (r.n_axes < 1 || r.axis_stride < 0 || (n_tokens > 0 && !r.pos_dev) || !r.pair_axis ||
         (reinterpret_cast<uintptr_t>(r.pos_dev) & 3) || (r.n_axes > 1 && r.axis_stride != 0 && r.axis_stride < n_tokens))
         return UW_ERR_INVALID_ARG;
     if (r.n_axes > kMaxAxes || r.rot_dim > 2 * kMaxPairs)
