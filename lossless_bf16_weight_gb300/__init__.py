@@ -814,7 +814,8 @@ def attention_workspace_size(head_dim: int) -> int:
 def attention(q, k, v, out, start, ws, kv_start=None, scale: float = 0.0, causal: bool = True, window: int = 0, lse=None,
               stream=None):
     """uw_attention: attention of q [tokens, q heads, head_dim] over k and v [keys, kv heads, head_dim] into out;
-    sequence s has the tokens start[s] .. start[s + 1] - 1 (int32) and the same keys, or those of kv_start."""
+    sequence s has the tokens start[s] .. start[s + 1] - 1 (int32) and the same keys, or those of kv_start.  lse: fp32
+    [tokens, q heads], or None."""
     what, int32 = "uw_attention", _types()[2]
     if q.dim() != 3 or k.dim() != 3:
         raise UwError(UW_ERR_SHAPE, "%s (q and k are not [tokens, heads, head_dim])" % what)
@@ -829,6 +830,8 @@ def attention(q, k, v, out, start, ws, kv_start=None, scale: float = 0.0, causal
         if lse.dtype is not _types()[3]:
             raise UwError(UW_ERR_SHAPE, "%s (lse is not fp32)" % what)
         _refuse(_short((lse, 4 * n * hq, "lse")), what)
+        if lse.dim() > 1 and lse.shape[-1] != hq:
+            raise UwError(UW_ERR_SHAPE, "%s (lse is %s, its rows are not of %d heads)" % (what, tuple(lse.shape), hq))
     _here(what, q, k, v, out, start, kv_start, lse, ws)
     _check(load().uw_attention(start.data_ptr(), None if kv_start is None else kv_start.data_ptr(), seqs, n, m, qr, hq, kr,
                                vr, hk, d, orow, None if lse is None else lse.data_ptr(), scale, causal, window,
