@@ -43,9 +43,10 @@
  *     from uw_workspace_size and it must be cleared once with
  *     uw_workspace_init before first use.  Kernels leave it ready for the
  *     next call of the same kind: matmuls of a matrix of as many rows, the same
- *     chain, or the calls of a cache (any batch, plan and head size); their
- *     counters lie elsewhere for others, so clear it again before it serves
- *     those, and after UW_ERR_TIMEOUT (parts of a result that never came may
+ *     chain, the calls of a cache, or uw_attention (any batch, plan and head
+ *     size); uw_rope_axes takes any workspace.  The counters of the kinds lie in
+ *     each other's places, so clear it again before it serves another kind,
+ *     and after UW_ERR_TIMEOUT (parts of a result that never came may
  *     still be counted).  One workspace must not be used by two calls that may
  *     run at the same time.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
