@@ -477,7 +477,7 @@ uw_status uw_block_norm(const uw_block *b, const uint16_t *x_dev, int64_t x_stri
                         void *stream);
 
 /* uw_block_norm_e4m3 -- the same with y in 8 bits and a scale for each row, as
- * uw_rmsnorm_e4m3 (q_dev and weight_dev not NULL). */
+ * uw_rmsnorm_e4m3 (q_dev and weight_dev not NULL; q_dev apart from all other rows). */
 uw_status uw_block_norm_e4m3(const uw_block *b, const uint16_t *x_dev, int64_t x_stride, const uint16_t *residual_dev,
                              int64_t residual_stride, uint16_t *residual_out_dev, int64_t residual_out_stride,
                              const uint16_t *weight_dev, int64_t n, int64_t d, uint8_t *q_dev, int64_t q_stride,
