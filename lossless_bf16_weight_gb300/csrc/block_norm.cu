@@ -10,14 +10,14 @@
 // rows that may begin anywhere as in norm.cu; rows that are not alike or have more than 16384 values are
 // taken value by value, with h read back (or made again) for the second norm.
 //
-// Measured, with a norm after the block and a gate for all rows unless stated (of 6.8 TB/s for a copy):
-//   1 x 4096, no gate      2.5 us
-//   257 x 5120 to 8 bits   4.1 us
-//   8191 x 4096            43.8 us (6.1 TB/s); to 8 bits 47.1 (5.0); a gate of every row 50.8 (6.6)
-//   16000 x 2048           41.2 us (6.4 TB/s)
-//   4000 x 8192            45.4 us (5.8 TB/s); 2000 x 16384 49.2 (5.3)
-//   8000 x 1000            11.8 us (in L2); 8000 x 1001 25.5
-//   8000 x 4097            83.6 us (3.1 TB/s: three weights a value shifted into place)
+// Measured in a graph, with a norm after the block and a gate for all rows unless stated (of 6.8 TB/s for a copy):
+//   1 x 4096, no gate      2.2 us
+//   257 x 5120 to 8 bits   3.9 us
+//   8191 x 4096            42.3 us (6.35 TB/s); to 8 bits 44.9 (5.2); a gate of every row 49.9 (6.7)
+//   16000 x 2048           39.7 us (6.6 TB/s)
+//   4000 x 8192            43.4 us (6.0 TB/s); 2000 x 16384 45.1 (5.8)
+//   8000 x 1000            9.5 us (in L2); 8000 x 1001 21.7
+//   8000 x 4097            82.7 us (3.2 TB/s: three weights a value shifted into place)
 // One CTA for many rows, weights and gate kept in registers and the next row's x and r on their way: 55 us
 // for 8191 x 4096 (its registers leave too few warps).
 #include <cmath>
@@ -35,11 +35,12 @@ struct BlockParams {
     float *scale;
     int64_t xs, rs, gs, hs, ys, n, d;  // gs 0: one gate for all rows
     float eps, off, r_scale, b_scale;
+    float minus_zero;                 // -0, which the compiler does not know
 };
 
 // Two values each: a b + c with the products of BF16 pairs exact, and a + c, by the instructions that take BF16 as
 // it is (a conversion for each value otherwise, which with three reads and two sums of a value is what issue slots
-// go to: 8191 x 4096 45.1 us without).
+// go to: 8191 x 4096 3% more without).
 __device__ __forceinline__ void fma_pair(uint32_t a, uint32_t b, float &c0, float &c1) {
     asm("{\n\t.reg .b16 al, ah, bl, bh;\n\t"
         "mov.b32 {al, ah}, %2;\n\t"
@@ -98,6 +99,7 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
         const float ss = kWarp ? warp_sum(s0 + s1) : cta_reduce<false>(s0 + s1, slots);
         c *= rsqrtf(ss / float(p.d) + p.eps);
     }
+    const uint64_t zero = pair2(p.minus_zero, p.minus_zero), rs = pair2(p.r_scale, p.r_scale);
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int v = 0; v < V; v++) {
@@ -119,7 +121,13 @@ __device__ __forceinline__ void block_row(const BlockParams &p, int64_t row, int
                 f0 *= w.x;
                 f1 *= w.y;
             }
-            h[k] = bf16_pack(fmaf(f0, c, p.r_scale * bf16_lo(rw)), fmaf(f1, c, p.r_scale * bf16_hi(rw)));
+            // Each product is rounded and then the sum (a product is a multiply-add to a -0 that comes with the call, or
+            // the assembler would join one with the sum): a scale like 0.22 is off by up to 2^-25 in fp32, which its
+            // rounded product with a value of few bits is not, and where the exact sum lies between two BF16 values, or
+            // is 0, that decides.
+            const float2 v2 = unpair(add2(fma2(pair2(f0, f1), pair2(c, c), zero),
+                                          fma2(pair2(bf16_lo(rw), bf16_hi(rw)), rs, zero)));
+            h[k] = bf16_pack(v2.x, v2.y);
         }
         const int64_t i = first(v);
         if constexpr (kOdd) {  // what is not the row's counts for nothing, whatever the scales make of it
@@ -227,7 +235,8 @@ __global__ void __launch_bounds__(512) block_any_kernel(const BlockParams p) {
             f *= bf16_lo(g[i]);
         if (p.wp)
             f *= bf16_lo(p.wp[i]) + p.off;
-        return __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(f, c, p.r_scale * bf16_lo(r[i]))));
+        return __bfloat16_as_ushort(
+            __float2bfloat16_rn(__fadd_rn(__fmul_rn(f, c), __fmul_rn(p.r_scale, bf16_lo(r[i])))));
     };
     float ss = 0.f;
     for (int64_t i = threadIdx.x; i < p.d; i += blockDim.x) {
@@ -279,10 +288,10 @@ cudaError_t launch_rows(const BlockParams &p, cudaStream_t st) {
         return vecs <= 1088 ? run(block_cta_kernel<2, k8, true, true, 544, 2>, 2)
                             : run(block_cta_kernel<4, k8, true, true, 544, 1>, 4);
     } else {
-        // Up to two rows an SM: as many threads as a row has steps (257 x 5120 to 8 bits 4.1 us, half as many
-        // 4.5, a quarter 5.5).  More: what keeps the most loads on their way, by CTAs of an SM and registers
-        // (measured before fma_pair: 8191 x 4096 45.2 us with 5 CTAs of 256 threads, 47.5 with 4; 4000 x 8192 46.7
-        // with 3 of 512, 56.8 with twice the steps a thread; 2000 x 16384 54.8 with 2, with one and early weights 67).
+        // Up to two rows an SM: as many threads as a row has steps (257 x 5120 to 8 bits 3.9 us, half as many
+        // 4.4, a quarter 6.5).  More: what keeps the most loads on their way, by CTAs of an SM and registers
+        // (8191 x 4096 42.4 us with 5 CTAs of 256 threads, 45.4 with 4; 4000 x 8192 43.5 with 3 of 512, 42.4 with 4 of 256
+        // and twice the steps a thread, 56.8 when values were converted one by one; 2000 x 16384 45.3 with 2, with one and early weights 59.8).
         if (vecs <= 1024 && p.n <= 2 * sm_count())
             return run(block_cta_kernel<1, k8, false, false, 1024, 1>, 1);
         if (vecs <= 512)
@@ -335,7 +344,7 @@ uw_status run_block(const uw_block *b, const uint16_t *x, int64_t xs, const uint
     const bool vec = d % 8 == 0 && x0 % 8 == 0 && (n == 1 || xs % 8 == 0) &&
                      ((bits(w) | bits(b->post_weight_dev) | (gs ? 0 : bits(g))) & 15) == 0;
     const BlockParams p{x,  r,  g,  b->post_weight_dev, w, h, y, scale, xs, rs, gs, hs, ys, n, d, b->eps,
-                        b->weight_offset, b->residual_scale, b->block_scale};
+                        b->weight_offset, b->residual_scale, b->block_scale, -0.f};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return (k8 ? launch_block<true>(p, vec, alike, st) : launch_block<false>(p, vec, alike, st)) == cudaSuccess
                ? UW_OK
