@@ -583,7 +583,7 @@ typedef struct {
  *             and k themselves, and must not overlap them otherwise.  q and q_out NULL with
  *             q_heads = 0, likewise k; one of the two is there (UW_ERR_SHAPE otherwise).
  *   head_dim  any multiple of 8 (UW_ERR_UNSUPPORTED otherwise); values past rot_dim
- *             (16 to 256 here) are copied.
+ *             (16 to 256 here, so a head of 72 turns by 64 of its values at most) are copied.
  *   ws_dev    a workspace of at least 256 bytes (the error word). */
 uw_status uw_rope_axes(const uw_rope *r, int64_t n_tokens, const uw_kv4_rows *q, int32_t q_heads,
                        const uw_kv4_rows *q_out, const uw_kv4_rows *k, int32_t k_heads, const uw_kv4_rows *k_out,
@@ -664,7 +664,8 @@ uw_status uw_kv4_attention(const uw_kv4_cache *c, const int32_t *start_dev, cons
  *   ws_dev    at least uw_attention_workspace_size bytes, cleared once by
  *             uw_workspace_init; it serves calls of any sequences and heads, after UW_ERR_TIMEOUT too.
  * Scores, softmax statistics and sums are fp32; a probability is rounded to one BF16 for the product with
- * V (2^-8 of it).  The same call gives the same bits.
+ * V (2^-8 of it).  The same call gives the same bits; other sequences or heads beside a row's may change its
+ * last ones, as they move the places where the work is cut.
  * Ranges: scores q.k, times scale too, within fp32 and |v| below 2^80; past them a result may not be
  * finite. */
 uw_status uw_attention_workspace_size(int32_t head_dim, size_t *bytes);

@@ -18,7 +18,8 @@
 // more than 2^38 (BF16 and fp32 hold that without loss; with 2^24 a tile, which one row or another of a warp
 // passes in every other tile, 8192 tokens, not causal, take 670 us instead of 593), so that after the first keys
 // no score is compared and O is rarely rescaled.  P is rounded to one BF16 (2^-8, the one rounding beside
-// the output's); its sum is fp32 of the unrounded values.
+// the output's), as the product's operands have one type and V is BF16; what the rounding leaves, as a second operand, would be
+// half as many products again.  Its sum is fp32 of the unrounded values, whose exponentials are off by about 2^-22.
 //
 // What a row does not see takes no part in it, whatever its bits: a masked score becomes -inf where it
 // lies (an "open" tile, which not all rows see in full, takes 2200 cycles with that, 6000 with the mask in the
@@ -27,13 +28,15 @@
 // end and values that are not finite, and an item with such a value adds them at its end to the rows
 // that see their keys.
 //
-// Measured, 32 query and 8 kv heads of 128, causal (cuBLAS's burst rate is 1919 TFLOP/s): 37 tokens 10.0 us, 2048
-// 40.3 (853 TFLOP/s), 8192 321 to 326 (1690 to 1713), 16384 1206 (1823); 8192 not causal 593 to 660 by the
-// clock (1667 to 1855); twelve packed prompts of 1 to 2000 tokens 61.6 (780); heads of 64, 8192 tokens 260
-// (1056), not causal 471 (1166).  Long prompts are bound by the tensor cores (active in 80% of the cycles, at
-// the clock that the power leaves).  Short and packed ones pay for the share's begin (3 us until its first
-// segment is listed, 4 until Q, K and V of all CTAs are there), 2.8 us an item between its last products and
-// the next one's first (output 1.9, its first tile 0.9) and a join of parts (5.5).  With heads of 64 the
+// Measured, 32 query and 8 kv heads of 128, causal (cuBLAS's burst rate is 1919 TFLOP/s), from the best to the worst of
+// several GPUs and clocks: 37 tokens 9.8 to 10.2 us, 2048 40.3 to 40.8 (843 to 853 TFLOP/s), 8192 318 to 326 (1690 to
+// 1729), 16384 1206 to 1396 (1575 to 1823); 8192 not causal 593 to 660 (1667 to 1855); twelve packed prompts of 1 to
+// 2000 tokens 62 to 64 (700); heads of 64, 8192 tokens 258 (1067), not causal 467 (1177); one token of each of 64 sequences over
+// 4000 keys 171 (6.13 TB/s), 64 tokens over 16384 keys 53 (one row tile a head, cut into 19 shares).
+// Long prompts are bound by the tensor cores (active in 75% of the cycles, not causal 81%, at
+// the clock that the power leaves).  Short and packed ones pay for the share's begin (4 us until its first
+// segment is listed, 3 more until Q, K and V of all CTAs are there), 3 us an item between its last products and
+// the next one's first scores (output 2) and a join of parts (5.5).  With heads of 64 the
 // products are half as long, and what bounds is the way from scores to probabilities and back through both
 // halves (2085 cycles a step; tensor cores 39%, exponentials 39%).
 // Outputs of items by the check warps instead, beside the next item's first tile: 21 prompts of 16 to 3001
@@ -63,7 +66,7 @@ constexpr int kSoftmax = 256, kCheck = 128;         // threads
 constexpr int kThreads = kSoftmax + kCheck + 128;   // and a warpgroup of the MMA, copying and listing warps
 // What an item costs beyond its steps, in steps (21 packed prompts 171 us, with 2 176, with 4 178).
 constexpr int kItemCost = 3;
-constexpr int kMinShare = 4;                          // units of a CTA at least
+constexpr int kMinShare = 4;                          // units of a CTA at most, before more of them are used
 constexpr int kSegs = 16;
 constexpr int kStages = 2;
 // 2^38: headroom of the sum of a row's probabilities.  A part's output stays below 2^38 |v|, the join of up to 152 of them
@@ -695,8 +698,7 @@ __device__ __forceinline__ void softmax_role(const PackedParams &p, Shared &sh, 
                     }
                     tmem_st_wait();
                     if (__any_sync(0xffffffffu, over)) {
-                        // Raised in rows that need it by their own sum (not in others, so that a row's bits depend on
-                        // no other row): what the row has so far is scaled down.
+                        // Raised in rows that need it by their own sum: what the row has so far is scaled down.
                         // By the sum's logarithm at least, so that it is 1 at most whatever this tile's scores are.
                         const float2 lf = unpair(l2);
                         const float m2 = over ? fmaxf(fmaxf(m, m + __log2f(lf.x + lf.y)), top * p.c1) : m;

@@ -4,7 +4,7 @@
 //     y = h (mean(h^2) + eps)^(-1/2) (w + off)
 // with y in BF16, or in e4m3 with a scale for each row, or left out.
 //
-// Memory bound, and with 13 instructions a value not far from bound by issue slots (75% of them with 16): x, r
+// Memory bound, and with 35 instructions issued a value not far from bound by issue slots (74% of them): x, r
 // (and a gate of every row) are read once, h and y written once, in 16-byte steps; a row stays in
 // registers through its two sums, x and r as they came.  One warp a row up to 1024 values, one CTA a row above,
 // rows that may begin anywhere as in norm.cu; rows that are not alike or have more than 16384 values are

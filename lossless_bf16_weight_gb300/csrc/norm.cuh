@@ -55,9 +55,9 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float a, float b) {
 }
 
 // The 8-bit form of a row from u = h * w (exact in fp32: 8 x 8 significant
-// bits) and its largest magnitude.  1 / rms stands in y and in the scale and
-// cancels in y / scale = u * (448 / max |u|), so a code depends on two
-// roundings only.  A row whose scale is the smallest (max |y| below 448 *
+// bits; with an offset of the weights the sum and the product are rounded) and its largest magnitude.  1 / rms stands in y
+// and in the scale and cancels in y / scale = u * (448 / max |u|), so a code depends on no sum over the row and on
+// two roundings beside those of u.  A row whose scale is the smallest (max |y| below 448 *
 // 2^-126) takes y times 2^126; one that is not finite, or whose u is not, has a
 // NaN scale.
 struct RowScale {

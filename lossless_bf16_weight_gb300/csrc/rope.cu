@@ -11,7 +11,8 @@
 //
 // Measured: 32 + 8 heads of 128, 8143 tokens 28.8 us (5.9 TB/s, 0.86 of a copy): with two heads a lane
 // on their way and 64 registers a thread; with one 31, with three 30, with three CTAs an SM instead of four 32,
-// with warps of 8 rounds instead of all heads 31.  16 + 16 heads of 64, 8620 tokens (in L2) 10.9 us; one token 1.7.
+// with warps of 8 rounds instead of all heads 31.  16 + 16 heads of 64, 8620 tokens (in L2) 10.9 us; one token 2.1
+// (32 + 8 heads of 128 on three axes 2.4).
 #include "kernels.h"
 #include "kv4_host.h"
 #include "rope.cuh"
