@@ -830,7 +830,7 @@ def attention(q, k, v, out, start, ws, kv_start=None, scale: float = 0.0, causal
         if lse.dtype is not _types()[3]:
             raise UwError(UW_ERR_SHAPE, "%s (lse is not fp32)" % what)
         _refuse(_short((lse, 4 * n * hq, "lse")), what)
-        if lse.dim() > 1 and lse.shape[-1] != hq:
+        if lse.dim() > 1 and lse.shape[-1] != hq and min(n, hq) > 1:
             raise UwError(UW_ERR_SHAPE, "%s (lse is %s, its rows are not of %d heads)" % (what, tuple(lse.shape), hq))
     _here(what, q, k, v, out, start, kv_start, lse, ws)
     _check(load().uw_attention(start.data_ptr(), None if kv_start is None else kv_start.data_ptr(), seqs, n, m, qr, hq, kr,

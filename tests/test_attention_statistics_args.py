@@ -16,3 +16,10 @@ def test_shape_of_the_statistics(uw):
         with pytest.raises(RuntimeError) as e:
             uw.attention(**good, lse=lse)
         assert e.value.status == want, tuple(lse.shape)
+    # one head, or one token: either order is the same
+    one = dict(good, q=q[:, :1], k=k[:, :1], v=k[:, :1], out=q[:, :1])
+    few = dict(good, q=q[:1], k=k[:1], v=k[:1], out=q[:1])
+    for args, lse in ((one, torch.zeros(1, 7)), (one, torch.zeros(7, 1)), (few, torch.zeros(4, 1)), (few, torch.zeros(1, 4))):
+        with pytest.raises(RuntimeError) as e:
+            uw.attention(**args, lse=lse)
+        assert e.value.status == INVALID, tuple(lse.shape)
