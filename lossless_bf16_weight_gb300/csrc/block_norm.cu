@@ -291,7 +291,8 @@ cudaError_t launch_rows(const BlockParams &p, cudaStream_t st) {
         // Up to two rows an SM: as many threads as a row has steps (257 x 5120 to 8 bits 3.9 us, half as many
         // 4.4, a quarter 6.5).  More: what keeps the most loads on their way, by CTAs of an SM and registers
         // (8191 x 4096 42.4 us with 5 CTAs of 256 threads, 45.4 with 4; 4000 x 8192 43.5 with 3 of 512, 42.4 with 4 of 256
-        // and twice the steps a thread, 56.8 when values were converted one by one; 2000 x 16384 45.3 with 2, with one and early weights 59.8).
+        // and twice the steps a thread, 56.8 when values were converted one by one; 2000 x 16384 45.3 with 2, with one and
+        // early weights 59.8).
         if (vecs <= 1024 && p.n <= 2 * sm_count())
             return run(block_cta_kernel<1, k8, false, false, 1024, 1>, 1);
         if (vecs <= 512)
